@@ -371,6 +371,147 @@ flce_status flce_forward_noalloc(const void* X, const void* W, const int64_t* la
                                  float* loss, float* lse, int64_t* n_valid, int* device_error,
                                  flce_stream_t stream);
 
+/*
+ * ------------------------------------------------------------------------
+ * Operators around the LM head: the norm in front of it, 8-bit operands with
+ * block scales, the head's product on them, and the processing of its logits
+ * before a token is picked.  The conventions above hold (caller's buffers and
+ * stream, no synchronisation, no state); these entry points report no device
+ * error.
+ *
+ * 8-bit values are e4m3 (finite, largest 448), one byte each, with one float
+ * scale per block of 128 columns and 1 or 128 rows: a value stands for
+ * byte * scale.  A block's scale is a / 448 with a = max(|v|, 2^-100) over it,
+ * and its bytes are e4m3(v * (448 / a)), rounded to nearest even; the last
+ * block of a row (or of the rows) may be short.  A NaN stays a NaN byte and
+ * does not raise a; an infinity makes its block's scale infinite.
+ */
+typedef enum { FLCE_BF16 = 0, FLCE_F32 = 1 } flce_dtype;
+
+/*
+ * Root-mean-square norm with the residual's addition, row by row:
+ *
+ *     h = x + residual            (h = x without a residual)
+ *     y = h * rstd * weight       rstd = 1 / sqrt(mean(h^2) + eps)
+ *
+ * in FP32; y and h are rounded to the element type once, and y is formed from
+ * the unrounded h.
+ *   x, residual  device [N][H] of `dtype`, rows ldx / ldr elements apart
+ *                (residual may be NULL).
+ *   weight       device [H] of `weight_dtype`.
+ *   y            device [N][H] of `dtype`.
+ *   h_out        device [N][H] of `dtype`: the rounded sum, or NULL.  It may be
+ *                x or residual itself (same address, rows H apart).
+ *   rstd         device float [N], or NULL.
+ * 1 <= H <= 65536.  Any alignment that the element type allows (16-byte
+ * aligned rows are faster).  No output may otherwise overlap an input or
+ * another output.
+ */
+flce_status flce_rms_norm_forward(const void* x, int64_t ldx, const void* residual, int64_t ldr,
+                                  const void* weight, int64_t N, int64_t H, float eps,
+                                  flce_dtype dtype, flce_dtype weight_dtype, void* y, void* h_out,
+                                  float* rstd, flce_stream_t stream);
+
+/*
+ * The same norm with y in 8 bits, from its unrounded FP32 values:
+ *   q      device [N][H] e4m3.
+ *   scale  device float [N][ceil(H / 128)]: one per row and 128 columns.
+ */
+flce_status flce_rms_norm_fp8(const void* x, int64_t ldx, const void* residual, int64_t ldr,
+                              const void* weight, int64_t N, int64_t H, float eps,
+                              flce_dtype dtype, flce_dtype weight_dtype, void* q, float* scale,
+                              void* h_out, flce_stream_t stream);
+
+/*
+ * Backward of flce_rms_norm_forward, with g = dy * weight:
+ *
+ *     dx = rstd * (g - h * rstd^2 * mean(g * h)) + dh     (of x and of residual)
+ *     dweight = sum over rows of dy * h * rstd
+ *
+ *   dy         device [N][H] of `dtype`.
+ *   dh         device [N][H] of `dtype`: gradient of h_out, or NULL.
+ *   h          device [N][H] of `dtype`, rows ldh apart: h_out (x without a
+ *              residual); rstd device float [N], as written by the forward.
+ *   dx         device [N][H] of `dtype`, or NULL.
+ *   dweight    device [H] of `weight_dtype`, or NULL.
+ *   workspace  device, 256-byte aligned, flce_rms_norm_workspace_size(N, H)
+ *              bytes: FP32 partial sums of dweight, added in a fixed order.
+ * No output may overlap an input, the workspace or the other output.
+ */
+flce_status flce_rms_norm_backward(const void* dy, const void* dh, const void* h, int64_t ldh,
+                                   const void* weight, const float* rstd, int64_t N, int64_t H,
+                                   flce_dtype dtype, flce_dtype weight_dtype, void* dx,
+                                   void* dweight, void* workspace, size_t workspace_bytes,
+                                   flce_stream_t stream);
+size_t flce_rms_norm_workspace_size(int64_t N, int64_t H);
+
+/*
+ * x [R][K] (`dtype`, rows ldx elements apart) in 8 bits with one scale per
+ * block_rows x 128 block, block_rows 1 (activations) or 128 (weights):
+ *   q      device [R][K] e4m3;  scale  device float [ceil(R / block_rows)][ceil(K / 128)].
+ */
+flce_status flce_quantize_fp8(const void* x, int64_t ldx, int64_t R, int64_t K, flce_dtype dtype,
+                              int block_rows, void* q, float* scale, flce_stream_t stream);
+
+/*
+ * y = A B^T on 8-bit operands, for a linear layer or LM head whose weight is
+ * kept in 8 bits (serving; the training path is flce_forward / flce_backward
+ * on the bf16 weight):
+ *
+ *   y[m][v] = sum over blocks j of K of  a_scale[m][j] * b_scale[v / 128][j]
+ *                                        * sum over k in block j of A[m][k] B[v][k]
+ *
+ *   A        device e4m3 [M][K], rows lda bytes apart; a_scale float
+ *            [M][ceil(K / 128)] (block_rows 1).
+ *   B        device e4m3 [V][K], rows ldb bytes apart; b_scale float
+ *            [ceil(V / 128)][ceil(K / 128)] (block_rows 128).
+ *   y        device [M][V] of out_dtype, rows ldy elements apart.
+ * A block's products are summed in FP32 by the tensor cores, the scaled blocks
+ * in FP32, and the sum is rounded once.  K, lda and ldb are multiples of 16, A
+ * and B 16-byte aligned; K <= 65536.
+ */
+flce_status flce_matmul_fp8(const void* A, int64_t lda, const float* a_scale, const void* B,
+                            int64_t ldb, const float* b_scale, int64_t M, int64_t V, int64_t K,
+                            void* y, int64_t ldy, flce_dtype out_dtype, flce_stream_t stream);
+
+/*
+ * Logits before a token is picked.  Per row b and column v, with c = how often
+ * v occurs among the row's generated tokens and seen = v occurs in its prompt
+ * or among them:
+ *
+ *     l = logits[b][v]
+ *     seen:  l = l > 0 ? l / repetition[b] : l * repetition[b]
+ *     l = l - frequency[b] * c - presence[b] * (c > 0)
+ *     l = l + bias_values[b][i]    where bias_ids[b][i] == v (the last such i)
+ *     l = -infinity                where v is not allowed
+ *
+ *   logits     device [B][V] of `dtype`, rows ld_logits apart.
+ *   out        device [B][V] of `out_dtype`, rows ld_out apart; may be logits
+ *              itself (same address, type and row distance; columns that
+ *              nothing applies to are then not touched), else no overlap.
+ *   tokens     device int32, or int64 with tokens_int64, [B][L], rows ld_tokens
+ *              apart: the first prompt_lengths[b] (NULL: none) of the first
+ *              lengths[b] (NULL: L) entries are the prompt's, the rest are
+ *              generated.  Lengths are clamped to [0, L].  Ids outside [0, V)
+ *              do not count.  NULL with L = 0.
+ *   repetition, frequency, presence   device float [B], each may be NULL.
+ *   bias_ids   device int32 (int64 with bias_int64) [B][n_bias], bias_values
+ *              float [B][n_bias]; ids outside [0, V) are skipped.  NULL with
+ *              n_bias = 0; n_bias <= 65535.
+ *   allowed    device int32 [B][>= ceil(V / 32)], rows ld_allowed words apart,
+ *              or NULL: bit v % 32 of word v / 32 is set where v is allowed.
+ * A row without an allowed column is -infinity throughout.
+ */
+flce_status flce_process_logits(const void* logits, int64_t ld_logits, flce_dtype dtype,
+                                int64_t B, int64_t V, const void* tokens, int64_t ld_tokens,
+                                int tokens_int64, int64_t L, const int32_t* lengths,
+                                const int32_t* prompt_lengths, const float* repetition,
+                                const float* frequency, const float* presence,
+                                const void* bias_ids, int bias_int64, const float* bias_values,
+                                int64_t n_bias, const int32_t* allowed, int64_t ld_allowed,
+                                void* out, int64_t ld_out, flce_dtype out_dtype,
+                                flce_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

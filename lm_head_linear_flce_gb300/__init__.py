@@ -28,6 +28,8 @@ __all__ = [
     "flce_logits", "flce_forward_vocab_shard", "flce_merge_vocab_shards",
     "flce_backward_vocab_shard", "flce_downcast_bf16",
     "linear_cross_entropy", "STATUS",
+    "flce_rms_norm", "flce_rms_norm_backward", "rms_norm", "rms_norm_fp8", "quantize_fp8",
+    "matmul_fp8", "process_logits",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -451,3 +453,7 @@ def linear_cross_entropy(hidden, weight, labels, ignore_index=-100, shift=False,
         labels = labels.reshape(B * S)
     return _FusedLinearCE.apply(hidden.contiguous(), weight.contiguous(), labels.contiguous(),
                                 seq_len, ignore_index, shift, reduction)
+
+
+from .head_ops import (flce_rms_norm, flce_rms_norm_backward, matmul_fp8,  # noqa: E402
+                       process_logits, quantize_fp8, rms_norm, rms_norm_fp8)

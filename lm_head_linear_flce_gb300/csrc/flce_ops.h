@@ -1,0 +1,44 @@
+// Host-side helpers shared by the entry points of the operators around the LM
+// head (norm, 8-bit operands and their product, logits processing).
+#pragma once
+
+#include <cstdint>
+#include <cuda_runtime.h>
+
+#include "../../include/flce.h"
+
+namespace flce {
+
+constexpr int kScaleGroup = 128;          // columns that share a scale
+constexpr float kFp8Max = 448.f;          // largest e4m3 value
+constexpr float kAmaxMin = 0x1p-100f;     // floor of a block's max |v|: its scale stays normal
+constexpr int64_t kMaxRowElems = 1 << 16; // longest norm row / contraction
+
+// FLCE_OK and the SM count of the current device, if it is an sm_103 one.
+flce_status check_device(int* sms);
+
+inline bool valid_dtype(flce_dtype t) { return t == FLCE_BF16 || t == FLCE_F32; }
+inline size_t dtype_bytes(flce_dtype t) { return t == FLCE_F32 ? 4 : 2; }
+inline bool aligned_to(const void* p, size_t a) {
+  return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0;
+}
+
+// Bytes from the first to the last element of a [rows][cols] matrix.
+inline size_t span_bytes(int64_t rows, int64_t cols, int64_t ld, size_t elem) {
+  if (rows <= 0 || cols <= 0) return 0;
+  return (static_cast<size_t>(rows - 1) * static_cast<size_t>(ld) + static_cast<size_t>(cols)) *
+         elem;
+}
+
+struct Range {
+  const void* p;
+  size_t n;
+};
+
+// Whether two byte ranges share a byte (a null range shares none).
+inline bool ranges_overlap(const Range& a, const Range& b) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+  return a.p && b.p && a.n > 0 && b.n > 0 && x < y + b.n && y < x + a.n;
+}
+
+}  // namespace flce
