@@ -1,82 +1,626 @@
-// Matrix product on 8-bit operands with block scales (flce_matmul_fp8).
+// Matrix product on 8-bit operands with block scales (flce_matmul_fp8):
+//
+//   y[m][v] = sum_j sa[m][j] * sb[v / 128][j] * P_j[m][v],
+//   P_j     = the products of block j (128 columns of K), in FP32.
+//
+// The scales differ from block to block of K, so a block's sum P_j is formed by
+// itself in tensor memory (four K = 32 MMAs, the first not accumulating) and the
+// epilogue warps, which hold the FP32 result in registers, read it and add
+// sa * sb * P_j while the tensor cores run the next block into the other
+// accumulator.
 #include <cuda_bf16.h>
-#include <cuda_fp8.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
+#include <atomic>
+
+#include "flce_fp8_device.cuh"
 #include "flce_internal.h"
 #include "flce_ops.h"
 
 namespace flce {
 namespace {
 
-constexpr int kTile = 64;  // output rows and columns per block
-constexpr int kKStep = 32; // K per shared-memory step (4 steps per scale block)
+constexpr int kKB = 128;      // bytes (= columns of K) per pipeline stage: one scale block
+constexpr int kMmaK8 = 32;    // K per MMA
 
-__device__ __forceinline__ float e4m3_to_f(uint8_t b) {
-  __nv_fp8_e4m3 v;
-  v.__x = b;
-  return static_cast<float>(v);
-}
+// ------------------------------------------------ many rows: CTA pairs
+// A tile is 256 rows of A x 256 rows of B on a 2-CTA cluster (each CTA stages
+// 128 rows of either, 32 KB a stage, and holds 128 x 256 of the result).  Eight
+// epilogue warps per CTA: two per TMEM lane quarter, 128 columns each, so that
+// the result is 128 registers a thread.  Three warpgroups: the first (TMA, MMA)
+// hands registers to the two of the epilogue; 384 threads launch with 168 each,
+// 64512 in all = 128 * 56 + 256 * 224.
+constexpr int kPairThreads = 384;  // warp 0 TMA, warp 1 MMA, warps 4..11 epilogue
+constexpr int kPairEpi = 8;
+constexpr int kPairLeanRegs = 56;
+constexpr int kPairEpiRegs = 224;
+constexpr int kPairStages = 6;
+constexpr int kPairStageBytes = 2 * 128 * kKB;
+constexpr int kPairSmem = kPairStages * kPairStageBytes + kPairEpi * kStageBufBytes + 1024 + 256;
+constexpr uint16_t kBoth = 0x3;
 
-__device__ __forceinline__ void store_out(float* p, float v) { *p = v; }
-__device__ __forceinline__ void store_out(__nv_bfloat16* p, float v) {
-  *p = __float2bfloat16_rn(v);
-}
+struct Fp8Args {
+  int M, V, G;        // G: blocks of 128 columns of K
+  int tiles_m, tiles_v;
+  const float* a_scale;
+  const float* b_scale;
+  void* y;
+  int64_t ldy;
+  int tma_store;      // y's rows are 16-byte aligned
+  unsigned long long wait_limit_ns;
+};
 
-// 64 x 64 outputs per block of 256 threads, 4 x 4 per thread; each 128-column
-// block of K is summed by itself, then scaled into the result.
-template <class O>
-__global__ void __launch_bounds__(256)
-    matmul_fp8_kernel(const uint8_t* __restrict__ A, int64_t lda,
-                      const float* __restrict__ a_scale, const uint8_t* __restrict__ B,
-                      int64_t ldb, const float* __restrict__ b_scale, int64_t M, int64_t V, int K,
-                      O* __restrict__ y, int64_t ldy) {
-  __shared__ float as[kKStep][kTile + 1], bs[kKStep][kTile + 1];
-  const int64_t v0 = static_cast<int64_t>(blockIdx.x) * kTile;
-  const int64_t m0 = static_cast<int64_t>(blockIdx.y) * kTile;
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  const int groups = (K + kScaleGroup - 1) / kScaleGroup;
-  float acc[4][4] = {};
-  for (int j = 0; j < groups; ++j) {
-    float part[4][4] = {};
-    for (int k0 = j * kScaleGroup; k0 < min(K, (j + 1) * kScaleGroup); k0 += kKStep) {
-      for (int i = threadIdx.x; i < kTile * kKStep; i += 256) {
-        const int k = i % kKStep, r = i / kKStep;
-        const bool in_k = k0 + k < K;
-        as[k][r] = in_k && m0 + r < M ? e4m3_to_f(A[(m0 + r) * lda + k0 + k]) : 0.f;
-        bs[k][r] = in_k && v0 + r < V ? e4m3_to_f(B[(v0 + r) * ldb + k0 + k]) : 0.f;
-      }
-      __syncthreads();
-#pragma unroll
-      for (int k = 0; k < kKStep; ++k) {
-        float a[4], b[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) a[i] = as[k][ty * 4 + i];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) b[i] = bs[k][tx + 16 * i];
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int n = 0; n < 4; ++n) part[i][n] = fmaf(a[i], b[n], part[i][n]);
-      }
-      __syncthreads();
-    }
-    const float sb = b_scale[v0 / kScaleGroup * groups + j];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int64_t m = m0 + ty * 4 + i;
-      const float s = m < M ? a_scale[m * groups + j] * sb : 0.f;
-#pragma unroll
-      for (int n = 0; n < 4; ++n) acc[i][n] = fmaf(s, part[i][n], acc[i][n]);
+struct Ring {
+  uint32_t idx = 0, phase = 0;
+  __device__ void advance(uint32_t n) {
+    if (++idx == n) {
+      idx = 0;
+      phase ^= 1u;
     }
   }
+};
+
+// The four MMAs of one 128-byte K block: operands are 128-byte-swizzled, 8-row
+// groups 1024 bytes apart, a K step 32 bytes along the swizzled row (2 in the
+// descriptor's units of 16).  Descriptors of the first K step; their address
+// field does not carry, so a step is an addition.
+template <int M, int N, bool PAIR>
+__device__ __forceinline__ void mma_block(uint32_t d, uint64_t ad, uint64_t bd) {
+  constexpr uint32_t idesc = instr_desc_e4m3(M, N);
+  constexpr uint64_t kStep = kMmaK8 / 16;
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int n = 0; n < 4; ++n) {
-      const int64_t m = m0 + ty * 4 + i, v = v0 + tx + 16 * n;
-      if (m < M && v < V) store_out(y + m * ldy + v, acc[i][n]);
+  for (int k = 0; k < kKB / kMmaK8; ++k) {
+    if (PAIR) mma_e4m3_pair(d, ad + kStep * k, bd + kStep * k, idesc, k > 0);
+    else mma_e4m3_single(d, ad + kStep * k, bd + kStep * k, idesc, k > 0);
+  }
+}
+
+// Waits (bounded, whatever the abort flag says) until the stages in `issued`
+// have received their last loads: no CTA may exit with copies in flight.
+template <int STAGES>
+__device__ void drain_stages(uint32_t full, uint32_t issued, const Ring& pipe, WaitCtx w) {
+  volatile uint32_t never = 0u;
+  w.abort = &never;
+  for (int i = 0; i < STAGES; ++i)
+    if (issued & (1u << i))
+      wait_parity(full + 8 * i, static_cast<uint32_t>(i) < pipe.idx ? pipe.phase : pipe.phase ^ 1u,
+                  w);
+}
+
+__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
+  __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<uint32_t*>(&h);
+}
+
+// One warp's 32 rows x 128 bytes of the result, already in its staging buffer
+// (128-byte-swizzled rows), to global memory.
+template <class O>
+__device__ __forceinline__ void store_chunk(const Fp8Args& a, const CUtensorMap* ty, uint32_t buf,
+                                            int row0, int col0, int lane) {
+  constexpr int kCols = 128 / static_cast<int>(sizeof(O));
+  // a TMA store writes whole 16-byte pieces, also where V ends inside one
+  if (a.tma_store && (col0 + kCols <= a.V || a.V * sizeof(O) % 16 == 0)) {
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+      tma_store_2d(ty, buf, col0, row0);
+      bulk_commit();
     }
+    return;
+  }
+  __syncwarp();
+  for (int r = 0; r < 32 && row0 + r < a.M; ++r) {
+#pragma unroll
+    for (int c = lane; c < kCols; c += 32) {
+      const uint32_t at =
+          buf + r * 128 + (((c * sizeof(O) / 16) ^ (r & 7)) << 4) + (c * sizeof(O)) % 16;
+      O* dst = static_cast<O*>(a.y) + static_cast<int64_t>(row0 + r) * a.ldy + col0 + c;
+      if (col0 + c < a.V) {
+        if (sizeof(O) == 4) {
+          uint32_t v;
+          asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+          *reinterpret_cast<uint32_t*>(dst) = v;
+        } else {
+          uint16_t v;
+          asm volatile("ld.shared.b16 %0, [%1];" : "=h"(v) : "r"(at) : "memory");
+          *reinterpret_cast<uint16_t*>(dst) = v;
+        }
+      }
+    }
+  }
+  __syncwarp();
+}
+
+template <class O>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
+    flce_fp8_pair_kernel(const __grid_constant__ CUtensorMap ta,
+                         const __grid_constant__ CUtensorMap tb,
+                         const __grid_constant__ CUtensorMap ty, const Fp8Args a) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t a_base = (raw + 1023u) & ~1023u;
+  const uint32_t b_base = a_base + kPairStages * 128 * kKB;
+  const uint32_t staging = b_base + kPairStages * 128 * kKB;
+  const uint32_t full = staging + kPairEpi * kStageBufBytes;
+  const uint32_t done = full + 8 * kPairStages;
+  const uint32_t tempty = done + 8 * kPairStages;
+  const uint32_t drain = tempty + 16;
+  auto* slot = reinterpret_cast<uint32_t*>(smem_raw + (drain + 8 - raw));
+  volatile uint32_t* abort_flag = slot + 1;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  const int rank = static_cast<int>(cluster_ctarank());
+  const bool leader = rank == 0;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kPairStages; ++i) {
+      mbar_init(full + 8 * i, 1);  // the leader's producer, for both CTAs' bytes
+      mbar_init(done + 8 * i, 1);  // the leader's multicast commit
+    }
+    for (int i = 0; i < 2; ++i)
+      mbar_init(tempty + 8 * i, 2 * kPairEpi);  // every epilogue warp of both CTAs
+    mbar_init(drain, 1);
+    *abort_flag = 0u;
+    fence_barrier_init();
+    fence_proxy_async_smem();
+    tma_prefetch_desc(&ta);
+    tma_prefetch_desc(&tb);
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(smem_u32(slot), kTmemCols);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();  // no CTA signals its peer's barriers before they are set up
+  tc_fence_after();
+  const uint32_t tmem = *slot;
+  const WaitCtx w{abort_flag, nullptr, a.wait_limit_ns};
+  const int tiles = a.tiles_m * a.tiles_v;
+  const int first = blockIdx.x >> 1, step = gridDim.x >> 1;
+
+  // The roles are branches of their own so that each is compiled for its share
+  // of the registers.
+  if (warp < 4) {
+    regs_release<kPairLeanRegs>();
+    if (warp == 0 && lane == 0) {
+      Ring pipe;
+      uint32_t issued = 0;
+      const uint64_t keep = l2_policy_evict_last();
+      bool ok = true;
+      for (int t = first; t < tiles && ok; t += step) {
+        const int arow = (t % a.tiles_m) * 256 + 128 * rank;
+        const int brow = (t / a.tiles_m) * 256 + 128 * rank;
+        for (int j = 0; j < a.G; ++j) {
+          ok = wait_parity(done + 8 * pipe.idx, pipe.phase ^ 1u, w);
+          if (!ok) break;
+          const uint32_t bar = full + 8 * pipe.idx;
+          if (leader) mbar_arrive_expect_tx(bar, 2 * kPairStageBytes);
+          const uint32_t bar_c = mapa_shared(bar, 0);
+          tma_load_2d_pair_hint(a_base + pipe.idx * 128 * kKB, &ta, j * kKB, arow, bar_c, keep);
+          tma_load_2d_pair(b_base + pipe.idx * 128 * kKB, &tb, j * kKB, brow, bar_c);
+          issued |= 1u << pipe.idx;
+          pipe.advance(kPairStages);
+        }
+      }
+      if (leader) drain_stages<kPairStages>(full, issued, pipe, w);
+    } else if (warp == 1 && leader) {
+      // The whole warp runs the loop, so that its values stay uniform; one lane
+      // issues.  A stage and an accumulator are both one block of K, so one
+      // commit per block, on the stage's barrier, tells the producers that the
+      // stage is free and the epilogue that the accumulator is there.
+      const uint64_t ad0 = smem_desc_sw128(a_base, 0, 1024);
+      const uint64_t bd0 = smem_desc_sw128(b_base, 0, 1024);
+      Ring pipe, acc;
+      bool ok = true;
+      for (int t = first; t < tiles && ok; t += step) {
+        for (int j = 0; j < a.G; ++j) {
+          ok = wait_parity(full + 8 * pipe.idx, pipe.phase, w) &&
+               wait_parity(tempty + 8 * acc.idx, acc.phase ^ 1u, w);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          tc_fence_after();
+          if (elect_one()) {
+            const uint64_t at = static_cast<uint64_t>(pipe.idx) * (128 * kKB / 16);
+            mma_block<256, 256, true>(tmem + acc.idx * kAccCols, ad0 + at, bd0 + at);
+            mma_commit_pair_multicast(done + 8 * pipe.idx, kBoth);
+          }
+          __syncwarp();
+          pipe.advance(kPairStages);
+          acc.advance(2);
+        }
+      }
+      // every issued MMA completes before tensor memory is released
+      if (elect_one()) {
+        mma_commit_pair(drain);
+        WaitCtx wd = w;
+        volatile uint32_t never = 0u;
+        wd.abort = &never;
+        wait_parity(drain, 0u, wd);
+      }
+      __syncwarp();
+    }
+  } else {
+    regs_acquire<kPairEpiRegs>();
+    const int q = warp & 3, half = (warp - 4) >> 2;
+    const uint32_t buf = staging + (warp - 4) * kStageBufBytes;
+    Ring pipe, acc;
+    bool ok = true;
+    for (int t = first; t < tiles && ok; t += step) {
+      const int row0 = (t % a.tiles_m) * 256 + 128 * rank + q * 32;
+      const int col0 = (t / a.tiles_m) * 256 + 128 * half;
+      const int row = row0 + lane;
+      const float* sa = a.a_scale + static_cast<int64_t>(min(row, a.M - 1)) * a.G;
+      // a half past V has no scale block of its own; its columns are not stored
+      const float* sb = a.b_scale + static_cast<int64_t>(min(col0, a.V - 1) / kScaleGroup) * a.G;
+      uint64_t r[64];
+#pragma unroll
+      for (int i = 0; i < 64; ++i) r[i] = 0;
+      // scales are fetched two blocks ahead of their use
+      float sa0 = sa[0], sb0 = sb[0], sa1 = sa[min(1, a.G - 1)], sb1 = sb[min(1, a.G - 1)];
+      for (int j = 0; j < a.G; ++j) {
+        const float s = sa0 * sb0;
+        sa0 = sa1;
+        sb0 = sb1;
+        const int jn = min(j + 2, a.G - 1);
+        sa1 = sa[jn];
+        sb1 = sb[jn];
+        ok = wait_parity_inline(done + 8 * pipe.idx, pipe.phase, w);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t tbase = tmem + (static_cast<uint32_t>(q * 32) << 16) +
+                               acc.idx * kAccCols + half * 128;
+        const uint32_t su = __float_as_uint(s);
+        const uint64_t s2 = pack_f32x2(su, su);
+        uint32_t v[2][16];  // the next 16 columns load while these are added
+        tmem_ld_begin(tbase, v[0]);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          uint32_t(&x)[16] = v[c & 1];
+          tmem_wait(x);
+          if (c < 7) {
+            tmem_ld_begin(tbase + 16 * (c + 1), v[(c + 1) & 1]);
+          } else {  // everything is read: hand the accumulator back
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_remote(mapa_shared(tempty + 8 * acc.idx, 0));
+          }
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            r[8 * c + i] = fma_f32x2(s2, pack_f32x2(x[2 * i], x[2 * i + 1]), r[8 * c + i]);
+        }
+        pipe.advance(kPairStages);
+        acc.advance(2);
+      }
+      if (!ok) break;
+      constexpr int kWords = 32;                  // 128 bytes of one row per chunk
+      constexpr int kPairs = sizeof(O) == 2 ? 32 : 16;  // register pairs per chunk
+#pragma unroll
+      for (int c = 0; c < 64 / kPairs; ++c) {
+        const int x = col0 + c * 2 * kPairs;
+        if (x >= a.V) break;  // warp-uniform
+        uint32_t o[kWords];
+#pragma unroll
+        for (int i = 0; i < kPairs; ++i) {
+          float lo, hi;
+          unpack_f32x2(r[c * kPairs + i], lo, hi);
+          if (sizeof(O) == 2) {
+            o[i] = pack_bf16x2(lo, hi);
+          } else {
+            o[2 * i] = __float_as_uint(lo);
+            o[2 * i + 1] = __float_as_uint(hi);
+          }
+        }
+        if (lane == 0) bulk_wait_read<0>();  // the buffer's last store has left it
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          st_shared_v4(buf + lane * 128 + ((i ^ (lane & 7)) << 4),
+                       make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]));
+        store_chunk<O>(a, &ty, buf, row0, x, lane);
+      }
+    }
+    if (lane == 0) bulk_wait_all();
+    __syncwarp();
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc_pair(tmem, kTmemCols);
+}
+
+// ------------------------------------------------ few rows: B streamed
+// With at most 128 rows of A the product is bound by reading B once.  The roles
+// of the operands are swapped: 128 rows of B are the MMA's M, the rows of A
+// (padded to NP) its N, so nothing of the tensor cores' work is wasted on
+// padding to 128 rows of A.  One CTA per SM; the ring keeps about 190 KB of B in
+// flight.  With fewer tiles of B than SMs, a cluster of `splits` CTAs shares a
+// tile, each taking a contiguous part of K; the parts are added in rank order
+// through distributed shared memory.
+constexpr int kRowThreads = 192;  // warp 0 TMA, warp 1 MMA, warps 2..5 epilogue
+
+template <int NP>
+struct RowShape {
+  static constexpr int kStageBytes = 128 * kKB + NP * kKB;
+  static constexpr int kStages = NP <= 16 ? 12 : NP <= 32 ? 11 : NP <= 64 ? 9 : 6;
+  static constexpr int kAccs = 4;                     // accumulators of NP columns
+  static constexpr int kTmem = NP * kAccs < 32 ? 32 : NP * kAccs;
+  static constexpr int kScaleBytes = 4 * 2 * NP * 4;  // two buffers per epilogue warp
+  static constexpr int kSmem = kStages * kStageBytes + kScaleBytes + 1024 + 512;
+};
+
+template <int NP, class O>
+__global__ void __launch_bounds__(kRowThreads, 1)
+    flce_fp8_rows_kernel(const __grid_constant__ CUtensorMap ta,
+                         const __grid_constant__ CUtensorMap tb, const Fp8Args a,
+                         const int splits) {
+  using S = RowShape<NP>;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;  // stage i: B rows, then A rows
+  const uint32_t scales = base + S::kStages * S::kStageBytes;
+  const uint32_t full = scales + S::kScaleBytes;
+  const uint32_t empty = full + 8 * S::kStages;
+  const uint32_t tfull = empty + 8 * S::kStages;
+  const uint32_t tempty = tfull + 8 * S::kAccs;
+  const uint32_t drain = tempty + 8 * S::kAccs;
+  auto* slot = reinterpret_cast<uint32_t*>(smem_raw + (drain + 8 - raw));
+  volatile uint32_t* abort_flag = slot + 1;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < S::kStages; ++i) {
+      mbar_init(full + 8 * i, 1);
+      mbar_init(empty + 8 * i, 1);
+    }
+    for (int i = 0; i < S::kAccs; ++i) {
+      mbar_init(tfull + 8 * i, 1);
+      mbar_init(tempty + 8 * i, 4);
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0u;
+    fence_barrier_init();
+    fence_proxy_async_smem();
+    tma_prefetch_desc(&ta);
+    tma_prefetch_desc(&tb);
+  }
+  if (warp == 1) {
+    tmem_alloc_single(smem_u32(slot), S::kTmem);
+    tmem_relinquish_single();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *slot;
+  const WaitCtx w{abort_flag, nullptr, a.wait_limit_ns};
+  const int part = splits > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+  const int j0 = static_cast<int>(static_cast<int64_t>(a.G) * part / splits);
+  const int j1 = static_cast<int>(static_cast<int64_t>(a.G) * (part + 1) / splits);
+  const int first = static_cast<int>(blockIdx.x) / splits;
+  const int step = static_cast<int>(gridDim.x) / splits;
+  bool ok = true;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      Ring pipe;
+      uint32_t issued = 0;
+      const uint64_t keep = l2_policy_evict_last(), once = l2_policy_evict_first();
+      for (int t = first; t < a.tiles_v && ok; t += step) {
+        for (int j = j0; j < j1; ++j) {
+          ok = wait_parity(empty + 8 * pipe.idx, pipe.phase ^ 1u, w);
+          if (!ok) break;
+          const uint32_t bar = full + 8 * pipe.idx;
+          const uint32_t sb = base + pipe.idx * S::kStageBytes;
+          mbar_arrive_expect_tx(bar, S::kStageBytes);
+          tma_load_2d_hint(sb, &tb, j * kKB, t * 128, bar, once);
+          tma_load_2d_hint(sb + 128 * kKB, &ta, j * kKB, 0, bar, keep);
+          issued |= 1u << pipe.idx;
+          pipe.advance(S::kStages);
+        }
+      }
+      drain_stages<S::kStages>(full, issued, pipe, w);
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      Ring pipe, acc;
+      for (int t = first; t < a.tiles_v && ok; t += step) {
+        for (int j = j0; j < j1; ++j) {
+          ok = wait_parity(tempty + 8 * acc.idx, acc.phase ^ 1u, w) &&
+               wait_parity(full + 8 * pipe.idx, pipe.phase, w);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t sb = base + pipe.idx * S::kStageBytes;
+          mma_block<128, NP, false>(tmem + acc.idx * NP, smem_desc_sw128(sb, 0, 1024),
+                                    smem_desc_sw128(sb + 128 * kKB, 0, 1024));
+          mma_commit_single(empty + 8 * pipe.idx);
+          mma_commit_single(tfull + 8 * acc.idx);
+          pipe.advance(S::kStages);
+          acc.advance(S::kAccs);
+        }
+      }
+      mma_commit_single(drain);
+      WaitCtx wd = w;
+      volatile uint32_t never = 0u;
+      wd.abort = &never;
+      wait_parity(drain, 0u, wd);
+    }
+  }
+
+  const int q = warp & 3;
+  constexpr int kSa = (NP + 31) / 32;  // scales of A a lane fetches per block
+  float r[NP];
+  if (warp >= 2) {
+    auto* my_scales =
+        reinterpret_cast<float*>(smem_raw + (scales - raw)) + (warp - 2) * 2 * NP;
+    Ring acc;
+    // the last tile's result stays in registers when K is split (one tile each)
+    for (int t = first; t < a.tiles_v && ok; t += step) {
+      const int v = t * 128 + q * 32 + lane;
+      const float* sb = a.b_scale + static_cast<int64_t>(t) * a.G;
+#pragma unroll
+      for (int n = 0; n < NP; ++n) r[n] = 0.f;
+      float sa[kSa], sbj = 0.f;
+      auto fetch = [&](int j) {
+        sbj = sb[j];
+#pragma unroll
+        for (int i = 0; i < kSa; ++i) {
+          const int n = i * 32 + lane;
+          sa[i] = n < a.M ? a.a_scale[static_cast<int64_t>(n) * a.G + j] : 0.f;
+        }
+      };
+      if (j0 < j1) fetch(j0);
+      for (int j = j0; j < j1; ++j) {
+        // this block's scales into the warp's buffer, the next ones on their way
+        float* s = my_scales + (j & 1) * NP;
+#pragma unroll
+        for (int i = 0; i < kSa; ++i)
+          if (NP % 32 == 0 || i * 32 + lane < NP) s[i * 32 + lane] = sa[i] * sbj;
+        __syncwarp();
+        if (j + 1 < j1) fetch(j + 1);
+        ok = wait_parity_inline(tfull + 8 * acc.idx, acc.phase, w);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t tbase = tmem + (static_cast<uint32_t>(q * 32) << 16) + acc.idx * NP;
+        constexpr int kC = NP < 32 ? 16 : 32;
+#pragma unroll
+        for (int c = 0; c < NP / kC; ++c) {
+          uint32_t p[kC];
+          tmem_ld_begin(tbase + kC * c, p);
+          tmem_wait(p);
+#pragma unroll
+          for (int i = 0; i < kC / 4; ++i) {
+            const float4 f = *reinterpret_cast<const float4*>(s + kC * c + 4 * i);
+            float* d = r + kC * c + 4 * i;
+            d[0] = fmaf(f.x, __uint_as_float(p[4 * i]), d[0]);
+            d[1] = fmaf(f.y, __uint_as_float(p[4 * i + 1]), d[1]);
+            d[2] = fmaf(f.z, __uint_as_float(p[4 * i + 2]), d[2]);
+            d[3] = fmaf(f.w, __uint_as_float(p[4 * i + 3]), d[3]);
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(tempty + 8 * acc.idx);
+        acc.advance(S::kAccs);
+      }
+      if (!ok) break;
+      if (splits == 1 && v < a.V) {
+        O* y = static_cast<O*>(a.y) + v;
+#pragma unroll
+        for (int n = 0; n < NP; ++n)
+          if (n < a.M) {
+            if constexpr (sizeof(O) == 2) y[n * a.ldy] = __float2bfloat16_rn(r[n]);
+            else y[n * a.ldy] = r[n];
+          }
+      }
+    }
+  }
+  if (splits > 1) {
+    // Every role has finished with the stages: their memory takes this part's
+    // result, [NP][128] floats, and each CTA adds a share of the columns of all
+    // parts.
+    __syncthreads();
+    const uint32_t mine = base;
+    if (warp >= 2) {
+#pragma unroll
+      for (int n = 0; n < NP; ++n)
+        asm volatile("st.shared.f32 [%0], %1;" ::"r"(mine + 4u * (n * 128 + q * 32 + lane)),
+                     "f"(r[n])
+                     : "memory");
+    }
+    cluster_sync_all();
+    const int v = first * 128 + q * 32 + lane;
+    if (warp >= 2 && ok && v < a.V && first < a.tiles_v) {
+      for (int n = part; n < a.M; n += splits) {
+        float sum = 0.f;
+        for (int p = 0; p < splits; ++p) {
+          float x;
+          asm volatile("ld.shared::cluster.f32 %0, [%1];"
+                       : "=f"(x)
+                       : "r"(mapa_shared(mine + 4u * (n * 128 + q * 32 + lane), p))
+                       : "memory");
+          sum += x;
+        }
+        O* y = static_cast<O*>(a.y) + n * a.ldy + v;
+        if constexpr (sizeof(O) == 2) *y = __float2bfloat16_rn(sum);
+        else *y = sum;
+      }
+    }
+    cluster_sync_all();  // no CTA leaves while its part is still read
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc_single(tmem, S::kTmem);
+}
+
+// ------------------------------------------------------------- launching
+constexpr int kMaxDevices = 64;
+struct Prepared {
+  std::atomic<int> done[kMaxDevices] = {};
+};
+
+// Raises the kernel's shared-memory limit on the device's first launch.
+cudaError_t prepare(const void* kernel, int smem, Prepared* p) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const bool cached = dev >= 0 && dev < kMaxDevices;
+  if (cached && p->done[dev].load(std::memory_order_acquire)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e == cudaSuccess && cached) p->done[dev].store(1, std::memory_order_release);
+  return e;
+}
+
+template <class O>
+cudaError_t launch_pair(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& ty,
+                        const Fp8Args& a, int sms, cudaStream_t s) {
+  static Prepared prepared;
+  auto* k = flce_fp8_pair_kernel<O>;
+  cudaError_t e = prepare(reinterpret_cast<const void*>(k), kPairSmem, &prepared);
+  if (e != cudaSuccess) return e;
+  const int64_t tiles = static_cast<int64_t>(a.tiles_m) * a.tiles_v;
+  const int pairs = static_cast<int>(std::min<int64_t>(tiles, sms / 2));
+  k<<<2 * pairs, kPairThreads, kPairSmem, s>>>(ta, tb, ty, a);
+  note_launch();
+  note_wait_limit(a.wait_limit_ns);
+  return cudaGetLastError();
+}
+
+template <int NP, class O>
+cudaError_t launch_rows(const CUtensorMap& ta, const CUtensorMap& tb, const Fp8Args& a, int sms,
+                        cudaStream_t s) {
+  static Prepared prepared;
+  auto* k = flce_fp8_rows_kernel<NP, O>;
+  cudaError_t e =
+      prepare(reinterpret_cast<const void*>(k), RowShape<NP>::kSmem, &prepared);
+  if (e != cudaSuccess) return e;
+  // As many parts of K as keep every CTA on an SM of its own, none empty.
+  int splits = 1;
+  while (splits < 8 && 2 * splits * a.tiles_v <= sms && 2 * splits <= a.G) splits *= 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(splits > 1 ? splits * a.tiles_v : std::min(a.tiles_v, sms));
+  cfg.blockDim = dim3(kRowThreads);
+  cfg.dynamicSmemBytes = RowShape<NP>::kSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = splits;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, k, ta, tb, a, splits);
+  note_launch();
+  note_wait_limit(a.wait_limit_ns);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+template <class O>
+cudaError_t launch_rows_for(const CUtensorMap& ta, const CUtensorMap& tb, const Fp8Args& a,
+                            int np, int sms, cudaStream_t s) {
+  if (np == 16) return launch_rows<16, O>(ta, tb, a, sms, s);
+  if (np == 32) return launch_rows<32, O>(ta, tb, a, sms, s);
+  if (np == 64) return launch_rows<64, O>(ta, tb, a, sms, s);
+  return launch_rows<128, O>(ta, tb, a, sms, s);
 }
 
 }  // namespace
@@ -107,22 +651,44 @@ extern "C" flce_status flce_matmul_fp8(const void* A, int64_t lda, const float* 
                        {b_scale, span_bytes(gv, gk, gk, 4)}};
   for (const Range& r : ins)
     if (ranges_overlap(yr, r)) return FLCE_ERR_INVALID_ARG;
+  const int64_t tiles_m = (M + 255) / 256, tiles_v = (V + 255) / 256;
+  if (tiles_m * tiles_v > kMaxDim) return FLCE_ERR_UNSUPPORTED_SHAPE;
   int sms = 0;
   const flce_status st = check_device(&sms);
   if (st != FLCE_OK) return st;
   const auto s = reinterpret_cast<cudaStream_t>(stream);
-  if ((M + kTile - 1) / kTile > 65535) return FLCE_ERR_UNSUPPORTED_SHAPE;
-  const dim3 grid(static_cast<unsigned>((V + kTile - 1) / kTile),
-                  static_cast<unsigned>((M + kTile - 1) / kTile));
-  const auto* a8 = static_cast<const uint8_t*>(A);
-  const auto* b8 = static_cast<const uint8_t*>(B);
-  if (out_dtype == FLCE_BF16)
-    matmul_fp8_kernel<<<grid, 256, 0, s>>>(a8, lda, a_scale, b8, ldb, b_scale, M, V,
-                                           static_cast<int>(K), static_cast<__nv_bfloat16*>(y),
-                                           ldy);
-  else
-    matmul_fp8_kernel<<<grid, 256, 0, s>>>(a8, lda, a_scale, b8, ldb, b_scale, M, V,
-                                           static_cast<int>(K), static_cast<float*>(y), ldy);
-  note_launch();
-  return cudaGetLastError() == cudaSuccess ? FLCE_OK : FLCE_ERR_CUDA;
+  Fp8Args a = {};
+  a.M = static_cast<int>(M);
+  a.V = static_cast<int>(V);
+  a.G = static_cast<int>(gk);
+  a.a_scale = a_scale;
+  a.b_scale = b_scale;
+  a.y = y;
+  a.ldy = ldy;
+  a.wait_limit_ns = wait_limit_ns();
+  constexpr CUtensorMapDataType kU8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
+  CUtensorMap ta, tb;
+  if (!make_tmap(&tb, B, K, V, ldb, kKB, 128, kU8)) return FLCE_ERR_CUDA;
+  cudaError_t err;
+  if (M <= 128) {
+    const int np = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
+    a.tiles_v = static_cast<int>(gv);
+    if (!make_tmap(&ta, A, K, M, lda, kKB, np, kU8)) return FLCE_ERR_CUDA;
+    err = out_dtype == FLCE_BF16 ? launch_rows_for<__nv_bfloat16>(ta, tb, a, np, sms, s)
+                                 : launch_rows_for<float>(ta, tb, a, np, sms, s);
+  } else {
+    a.tiles_m = static_cast<int>(tiles_m);
+    a.tiles_v = static_cast<int>(tiles_v);
+    a.tma_store = aligned_to(y, 16) && ldy * e % 16 == 0;
+    CUtensorMap ty = tb;  // not used without TMA stores
+    if (!make_tmap(&ta, A, K, M, lda, kKB, 128, kU8)) return FLCE_ERR_CUDA;
+    if (a.tma_store &&
+        !make_tmap(&ty, y, V, M, ldy * e, 128 / e, 32,
+                   out_dtype == FLCE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                          : CU_TENSOR_MAP_DATA_TYPE_FLOAT32))
+      return FLCE_ERR_CUDA;
+    err = out_dtype == FLCE_BF16 ? launch_pair<__nv_bfloat16>(ta, tb, ty, a, sms, s)
+                                 : launch_pair<float>(ta, tb, ty, a, sms, s);
+  }
+  return err == cudaSuccess ? FLCE_OK : FLCE_ERR_CUDA;
 }

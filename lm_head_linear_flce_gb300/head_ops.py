@@ -237,7 +237,9 @@ def matmul_fp8(a, a_scale, b, b_scale, out_dtype=torch.bfloat16):
     a: float8_e4m3fn [..., K] with a_scale float32 [..., ceil(K / 128)], as
     rms_norm_fp8 or quantize_fp8(block_rows=1) give them; b: float8_e4m3fn
     [V, K] with b_scale float32 [ceil(V / 128), ceil(K / 128)], as
-    quantize_fp8(W) gives them.  K must be a multiple of 16.  No gradient."""
+    quantize_fp8(W) gives them.  K must be a multiple of 16.  As with
+    flce_logits, where V is no multiple of 8 the result is a view of rows padded
+    to one (16-byte rows).  No gradient."""
     _cuda("a", a, (_FP8,))
     dev = a.device
     _cuda("b", b, (_FP8,), dev)
@@ -262,10 +264,11 @@ def matmul_fp8(a, a_scale, b, b_scale, out_dtype=torch.bfloat16):
             am, lda = am.clone(memory_format=torch.contiguous_format), K
         if (ldb | bm.data_ptr()) % 16:
             bm, ldb = bm.clone(memory_format=torch.contiguous_format), K
-    y = torch.empty(*a.shape[:-1], V, dtype=out_dtype, device=dev)
+    ld = (V + 7) // 8 * 8
+    y = torch.empty(*a.shape[:-1], ld, dtype=out_dtype, device=dev)
     _call("flce_matmul_fp8", dev, am.data_ptr(), lda, a_scale.data_ptr(), bm.data_ptr(), ldb,
-          b_scale.data_ptr(), M, V, K, y.data_ptr(), V, _DTYPE[out_dtype])
-    return y
+          b_scale.data_ptr(), M, V, K, y.data_ptr(), ld, _DTYPE[out_dtype])
+    return y if ld == V else y[..., :V]
 
 
 _IDS = (torch.int32, torch.int64)
