@@ -271,22 +271,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                                acc.idx * kAccCols + half * 128;
         const uint32_t su = __float_as_uint(s);
         const uint64_t s2 = pack_f32x2(su, su);
-        uint32_t v[2][16];  // the next 16 columns load while these are added
-        tmem_ld_begin(tbase, v[0]);
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          uint32_t(&x)[16] = v[c & 1];
-          tmem_wait(x);
-          if (c < 7) {
-            tmem_ld_begin(tbase + 16 * (c + 1), v[(c + 1) & 1]);
-          } else {  // everything is read: hand the accumulator back
+        for (int c = 0; c < 2; ++c) {
+          uint32_t x[64];
+          tmem_ld(tbase + 64 * c, x);
+          if (c == 1) {
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive_remote(mapa_shared(tempty + 8 * acc.idx, 0));
           }
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            r[8 * c + i] = fma_f32x2(s2, pack_f32x2(x[2 * i], x[2 * i + 1]), r[8 * c + i]);
+          for (int i = 0; i < 32; ++i)
+            r[32 * c + i] = fma_f32x2(s2, pack_f32x2(x[2 * i], x[2 * i + 1]), r[32 * c + i]);
         }
         pipe.advance(kPairStages);
         acc.advance(2);
@@ -484,8 +480,7 @@ __global__ void __launch_bounds__(kRowThreads, 1)
 #pragma unroll
         for (int c = 0; c < NP / kC; ++c) {
           uint32_t p[kC];
-          tmem_ld_begin(tbase + kC * c, p);
-          tmem_wait(p);
+          tmem_ld(tbase + kC * c, p);
 #pragma unroll
           for (int i = 0; i < kC / 4; ++i) {
             const float4 f = *reinterpret_cast<const float4*>(s + kC * c + 4 * i);

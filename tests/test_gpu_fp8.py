@@ -137,7 +137,7 @@ def test_writes_stay_inside_and_repeat_bit_for_bit():
             a, sa, b, sb = operands(M, V, K, seed=6)
             ldy = V + 3
             buf = torch.full((M + 2, ldy), 7.0, dtype=out, device="cuda")
-            head_ops._call("flce_matmul_fp8", a.device, a.data_ptr(), K, sa.data_ptr(),
+            head_ops._call("flce_matmul_fp8", a.get_device(), a.data_ptr(), K, sa.data_ptr(),
                            b.data_ptr(), K, sb.data_ptr(), M, V, K, buf[1:].data_ptr(), ldy,
                            head_ops._DTYPE[out])
             y = flce.matmul_fp8(a, sa, b, sb, out_dtype=out)
