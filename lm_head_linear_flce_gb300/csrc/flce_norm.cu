@@ -12,8 +12,9 @@
 namespace flce {
 namespace {
 
-constexpr int kNormThreads = 256;
-constexpr int kDwRows = 64;  // rows per partial sum of dweight
+constexpr int kNormThreads = 256;   // of the kernels for rows past kMaxHeld, and the quantiser
+constexpr int kMaxHeld = 16384;     // longest row held in registers (1024 threads x 16 values)
+constexpr int kDwRows = 64;         // rows per partial sum of dweight beyond that
 
 __device__ __forceinline__ float to_f(float v) { return v; }
 __device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
@@ -52,7 +53,320 @@ __device__ float block_sum(float v) {
 __device__ __forceinline__ uint8_t to_e4m3(float v) {
   return __nv_cvt_float_to_fp8(v, __NV_SATFINITE, __NV_E4M3);
 }
+__device__ __forceinline__ uint32_t pack_e4m3(float a, float b, float c, float d) {
+  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
+  return lo | hi << 16;
+}
 
+// ------------------------------------------------------- rows in registers
+// A row is a block's (or, with 32 threads a row, a warp's), read once and held
+// in registers between the sum of squares and the output.  A thread holds P
+// slots of E elements:
+//   VEC  H a multiple of E = 16 / sizeof(T): E consecutive columns, slot s of
+//        thread t being piece t + s * threads, loaded as 16 bytes where the
+//        rows are `aligned`; 16 (bf16) or 32 (float32) neighbouring lanes make a
+//        group of 128 columns.  The same threads add the same columns in either
+//        case, so that a view's alignment does not change the result;
+//   else E = 4 columns 32 apart, a warp and slot being one group: rows of any
+//        length, still read whole lines at a time.
+template <class T, bool VEC>
+struct Slots {
+  static constexpr int kE = VEC ? 16 / static_cast<int>(sizeof(T)) : 4;
+  static constexpr int kLanes = VEC ? kScaleGroup / kE : 32;  // lanes of a scale group
+  __device__ static int first(int s) {  // column of the slot's first element
+    const int t = threadIdx.x + s * blockDim.x;
+    return VEC ? t * kE : (t >> 5) * kScaleGroup + (t & 31);
+  }
+  static constexpr int kStep = VEC ? 1 : 32;  // columns between a slot's elements
+};
+
+template <class T, bool VEC>
+__device__ __forceinline__ void load_slot(const T* __restrict__ row, int c, int H, bool aligned,
+                                          float (&v)[Slots<T, VEC>::kE]) {
+  constexpr int kE = Slots<T, VEC>::kE;
+  if constexpr (VEC) {
+    // H is a multiple of E: a piece lies inside the row or past it
+    if (!aligned) {
+#pragma unroll
+      for (int i = 0; i < kE; ++i) v[i] = c < H ? to_f(row[c + i]) : 0.f;
+      return;
+    }
+    uint4 p = make_uint4(0, 0, 0, 0);
+    if (c < H) p = *reinterpret_cast<const uint4*>(row + c);
+    if constexpr (sizeof(T) == 4) {
+      v[0] = __uint_as_float(p.x);
+      v[1] = __uint_as_float(p.y);
+      v[2] = __uint_as_float(p.z);
+      v[3] = __uint_as_float(p.w);
+    } else {
+      const uint32_t w[4] = {p.x, p.y, p.z, p.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[2 * i] = __uint_as_float(w[i] << 16);
+        v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < kE; ++i) v[i] = c + 32 * i < H ? to_f(row[c + 32 * i]) : 0.f;
+  }
+}
+
+template <class T, bool VEC>
+__device__ __forceinline__ void store_slot(T* __restrict__ row, int c, int H, bool aligned,
+                                           const float (&v)[Slots<T, VEC>::kE]) {
+  constexpr int kE = Slots<T, VEC>::kE;
+  if constexpr (VEC) {
+    if (c >= H) return;
+    if (!aligned) {
+#pragma unroll
+      for (int i = 0; i < kE; ++i) row[c + i] = from_f<T>(v[i]);
+      return;
+    }
+    uint4 p;
+    if constexpr (sizeof(T) == 4) {
+      p = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
+                     __float_as_uint(v[3]));
+    } else {
+      uint32_t w[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+        w[i] = *reinterpret_cast<uint32_t*>(&h);
+      }
+      p = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    *reinterpret_cast<uint4*>(row + c) = p;
+  } else {
+#pragma unroll
+    for (int i = 0; i < kE; ++i)
+      if (c + 32 * i < H) row[c + 32 * i] = from_f<T>(v[i]);
+  }
+}
+
+// The weight's elements of a slot (of either type).
+template <class T, bool VEC>
+__device__ __forceinline__ void load_weight(const void* __restrict__ w, int w_f32, int c, int H,
+                                            bool aligned, float (&v)[Slots<T, VEC>::kE]) {
+  constexpr int kE = Slots<T, VEC>::kE;
+  if constexpr (VEC) {
+    if (c >= H) {
+#pragma unroll
+      for (int i = 0; i < kE; ++i) v[i] = 0.f;
+    } else if (!aligned) {
+#pragma unroll
+      for (int i = 0; i < kE; ++i)
+        v[i] = w_f32 ? static_cast<const float*>(w)[c + i]
+                     : to_f(static_cast<const __nv_bfloat16*>(w)[c + i]);
+    } else if (w_f32) {
+#pragma unroll
+      for (int i = 0; i < kE / 4; ++i) {
+        const float4 p = reinterpret_cast<const float4*>(static_cast<const float*>(w) + c)[i];
+        v[4 * i] = p.x;
+        v[4 * i + 1] = p.y;
+        v[4 * i + 2] = p.z;
+        v[4 * i + 3] = p.w;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kE / 4; ++i) {
+        const uint2 p = reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(w) + c)[i];
+        v[4 * i] = __uint_as_float(p.x << 16);
+        v[4 * i + 1] = __uint_as_float(p.x & 0xffff0000u);
+        v[4 * i + 2] = __uint_as_float(p.y << 16);
+        v[4 * i + 3] = __uint_as_float(p.y & 0xffff0000u);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < kE; ++i) {
+      const int k = c + 32 * i;
+      v[i] = k >= H ? 0.f
+             : w_f32 ? static_cast<const float*>(w)[k]
+                     : to_f(static_cast<const __nv_bfloat16*>(w)[k]);
+    }
+  }
+}
+
+// Sum over the threads of a row (blockDim.x of them), the same on every one.
+// `part`: 2 x 32 floats, used in turn by `phase`, so that one barrier a sum is
+// enough.
+__device__ __forceinline__ float row_sum(float v, float* part, int phase) {
+  v = warp_sum(v);
+  if (blockDim.x == 32) return v;
+  float* p = part + 32 * phase;
+  if ((threadIdx.x & 31) == 0) p[threadIdx.x >> 5] = v;
+  __syncthreads();
+  const int lane = threadIdx.x & 31;
+  return warp_sum(lane < static_cast<int>(blockDim.x >> 5) ? p[lane] : 0.f);
+}
+
+// Bytes bound it: 16-byte loads of every value once, all of a row's in flight
+// at once.
+template <class T, bool FP8, bool VEC, int P>
+__global__ void __launch_bounds__(1024)
+    norm_fwd_held_kernel(const T* x, int64_t ldx, const T* residual, int64_t ldr,
+                         const void* __restrict__ weight, int w_f32, bool aligned, int64_t N, int H,
+                         float eps, T* y, uint8_t* q, float* scale, T* h_out, float* rstd) {
+  using S = Slots<T, VEC>;
+  __shared__ float part[64];
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
+  if (row >= N) return;  // a whole warp (rows share a block only as warps)
+  float h[P][S::kE];
+#pragma unroll
+  for (int s = 0; s < P; ++s) load_slot<T, VEC>(x + row * ldx, S::first(s), H, aligned, h[s]);
+  if (residual) {
+#pragma unroll
+    for (int s = 0; s < P; ++s) {
+      float r[S::kE];
+      load_slot<T, VEC>(residual + row * ldr, S::first(s), H, aligned, r);
+#pragma unroll
+      for (int i = 0; i < S::kE; ++i) h[s][i] += r[i];
+    }
+  }
+  float ss = 0.f;
+#pragma unroll
+  for (int s = 0; s < P; ++s)
+#pragma unroll
+    for (int i = 0; i < S::kE; ++i) ss = fmaf(h[s][i], h[s][i], ss);
+  if (h_out) {
+#pragma unroll
+    for (int s = 0; s < P; ++s) store_slot<T, VEC>(h_out + row * H, S::first(s), H, aligned, h[s]);
+  }
+  const float r = rsqrtf(row_sum(ss, part, 0) / static_cast<float>(H) + eps);
+  if (rstd && threadIdx.x == 0) rstd[row] = r;
+  const int groups = (H + kScaleGroup - 1) / kScaleGroup;
+#pragma unroll
+  for (int s = 0; s < P; ++s) {
+    const int c = S::first(s);
+    float w[S::kE];
+    load_weight<T, VEC>(weight, w_f32, c, H, aligned, w);
+#pragma unroll
+    for (int i = 0; i < S::kE; ++i) h[s][i] = h[s][i] * r * w[i];
+    if constexpr (!FP8) {
+      store_slot<T, VEC>(y + row * H, c, H, aligned, h[s]);
+    } else {
+      float a = 0.f;
+#pragma unroll
+      for (int i = 0; i < S::kE; ++i) a = fmaxf(a, fabsf(h[s][i]));
+#pragma unroll
+      for (int o = S::kLanes / 2; o > 0; o >>= 1)
+        a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+      a = fmaxf(a, kAmaxMin);
+      const float inv = kFp8Max / a;
+      uint8_t* qr = q + row * H;
+      if constexpr (VEC) {
+        uint32_t b[S::kE / 4];
+#pragma unroll
+        for (int i = 0; i < S::kE / 4; ++i)
+          b[i] = pack_e4m3(h[s][4 * i] * inv, h[s][4 * i + 1] * inv, h[s][4 * i + 2] * inv,
+                           h[s][4 * i + 3] * inv);
+        if (c < H && !aligned) {
+#pragma unroll
+          for (int i = 0; i < S::kE; ++i) qr[c + i] = static_cast<uint8_t>(b[i / 4] >> 8 * (i % 4));
+        } else if (c < H) {
+          if constexpr (S::kE == 8) *reinterpret_cast<uint2*>(qr + c) = make_uint2(b[0], b[1]);
+          else *reinterpret_cast<uint32_t*>(qr + c) = b[0];
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < S::kE; ++i)
+          if (c + 32 * i < H) qr[c + 32 * i] = to_e4m3(h[s][i] * inv);
+      }
+      const int g = c / kScaleGroup;
+      if ((threadIdx.x & (S::kLanes - 1)) == 0 && g < groups) scale[row * groups + g] = a / kFp8Max;
+    }
+  }
+}
+
+// dx of a row and this block's share of dweight in one pass over dy, h (and
+// dh): a block walks rows blockIdx.x, + gridDim.x, ... with the weight and the
+// sums of its columns in registers, and leaves one partial sum per column.
+template <class T, bool VEC, int P, int THREADS>
+__global__ void __launch_bounds__(THREADS)
+    norm_bwd_held_kernel(const T* __restrict__ dy, const T* __restrict__ dh,
+                         const T* __restrict__ h, int64_t ldh, const void* __restrict__ weight,
+                         int w_f32, bool aligned, const float* __restrict__ rstd, int64_t N,
+                         int H, T* __restrict__ dx, float* __restrict__ dw_part) {
+  using S = Slots<T, VEC>;
+  __shared__ float part[64];
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.y;
+  float w[P][S::kE], dw[P][S::kE];
+#pragma unroll
+  for (int s = 0; s < P; ++s) {
+    load_weight<T, VEC>(weight, w_f32, S::first(s), H, aligned, w[s]);
+#pragma unroll
+    for (int i = 0; i < S::kE; ++i) dw[s][i] = 0.f;
+  }
+  const float inv_h = 1.f / static_cast<float>(H);
+  int phase = 0;
+  for (int64_t row = first; row < N; row += step, phase ^= 1) {
+    float g[P][S::kE], v[P][S::kE];
+    const float r = rstd[row];
+#pragma unroll
+    for (int s = 0; s < P; ++s) load_slot<T, VEC>(dy + row * H, S::first(s), H, aligned, g[s]);
+#pragma unroll
+    for (int s = 0; s < P; ++s) load_slot<T, VEC>(h + row * ldh, S::first(s), H, aligned, v[s]);
+    float dot = 0.f;
+#pragma unroll
+    for (int s = 0; s < P; ++s)
+#pragma unroll
+      for (int i = 0; i < S::kE; ++i) {
+        const float d = g[s][i];
+        dw[s][i] = fmaf(d * v[s][i], r, dw[s][i]);
+        g[s][i] = d * w[s][i];
+        dot = fmaf(g[s][i], v[s][i], dot);
+      }
+    if (!dx) continue;
+    const float k = r * r * (row_sum(dot, part, phase) * inv_h);
+#pragma unroll
+    for (int s = 0; s < P; ++s) {
+      const int c = S::first(s);
+#pragma unroll
+      for (int i = 0; i < S::kE; ++i) g[s][i] = r * (g[s][i] - v[s][i] * k);
+      if (dh) {
+        float e[S::kE];
+        load_slot<T, VEC>(dh + row * H, c, H, aligned, e);
+#pragma unroll
+        for (int i = 0; i < S::kE; ++i) g[s][i] += e[i];
+      }
+      store_slot<T, VEC>(dx + row * H, c, H, aligned, g[s]);
+    }
+  }
+  if (!dw_part) return;
+#pragma unroll
+  for (int s = 0; s < P; ++s) {
+    const int c = S::first(s);
+    float* p = dw_part + first * H;
+#pragma unroll
+    for (int i = 0; i < S::kE; ++i)
+      if (c + i * S::kStep < H) p[c + i * S::kStep] = dw[s][i];
+  }
+}
+
+// dweight = the partial sums, added in order: 32 columns a block, each of its
+// eight warps taking every eighth partial, then the warps in order.
+template <class W>
+__global__ void __launch_bounds__(256)
+    norm_dw_sum_kernel(const float* __restrict__ part, int64_t parts, int H, W* __restrict__ dw) {
+  __shared__ float sums[8][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int c = blockIdx.x * 32 + lane;
+  float s = 0.f;
+  if (c < H) {
+#pragma unroll 8
+    for (int64_t p = warp; p < parts; p += 8) s += part[p * H + c];
+  }
+  sums[warp][lane] = s;
+  __syncthreads();
+  if (warp != 0 || c >= H) return;
+  for (int k = 1; k < 8; ++k) s += sums[k][lane];
+  dw[c] = from_f<W>(s);
+}
+
+// ----------------------------------------------------- rows past kMaxHeld
 // A block per row; a warp per group of 128 columns in the second pass.
 template <class T, class W, bool FP8>
 __global__ void __launch_bounds__(kNormThreads)
@@ -117,7 +431,7 @@ __global__ void __launch_bounds__(kNormThreads)
   }
 }
 
-// Partial sums of dweight over kDwRows rows, then their sum in order.
+// Partial sums of dweight over kDwRows rows.
 template <class T>
 __global__ void __launch_bounds__(kNormThreads)
     norm_bwd_dw_kernel(const T* __restrict__ dy, const T* __restrict__ h, int64_t ldh,
@@ -133,25 +447,125 @@ __global__ void __launch_bounds__(kNormThreads)
   part[static_cast<int64_t>(blockIdx.x) * H + c] = s;
 }
 
-template <class W>
-__global__ void __launch_bounds__(kNormThreads)
-    norm_dw_sum_kernel(const float* __restrict__ part, int64_t parts, int H, W* __restrict__ dw) {
-  const int c = blockIdx.x * kNormThreads + threadIdx.x;
-  if (c >= H) return;
-  float s = 0.f;
-  for (int64_t p = 0; p < parts; ++p) s += part[p * H + c];
-  dw[c] = from_f<W>(s);
-}
-
-// One block of block_rows x 128 elements per thread block.
+// 128 x 128 blocks of a matrix with 16-byte rows: a thread block reads a block
+// once into registers (16 values of bf16, 4 of float32 a load, all in flight),
+// takes the maximum and writes it.
 template <class T>
 __global__ void __launch_bounds__(kNormThreads)
-    quantize_kernel(const T* __restrict__ x, int64_t ldx, int64_t R, int K, int block_rows,
+    quantize_tile_kernel(const T* __restrict__ x, int64_t ldx, int64_t R, int K,
+                         uint8_t* __restrict__ q, float* __restrict__ scale) {
+  constexpr int kE = 16 / static_cast<int>(sizeof(T));
+  constexpr int kCols = kScaleGroup / kE;             // pieces of a row of the block
+  constexpr int kRowStep = kNormThreads / kCols;
+  constexpr int kN = kScaleGroup / kRowStep;          // pieces a thread holds
+  __shared__ float part[kNormThreads / 32];
+  const int64_t r0 = static_cast<int64_t>(blockIdx.x) * kScaleGroup + threadIdx.x / kCols;
+  const int c = blockIdx.y * kScaleGroup + threadIdx.x % kCols * kE;
+  uint4 v[kN];
+#pragma unroll
+  for (int i = 0; i < kN; ++i) {
+    const int64_t r = r0 + i * kRowStep;
+    v[i] = make_uint4(0, 0, 0, 0);
+    if (r < R && c < K) v[i] = *reinterpret_cast<const uint4*>(x + r * ldx + c);
+  }
+  float a = 0.f;
+#pragma unroll
+  for (int i = 0; i < kN; ++i) {
+    const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (sizeof(T) == 4) {
+        a = fmaxf(a, fabsf(__uint_as_float(w[k])));
+      } else {
+        a = fmaxf(a, fabsf(__uint_as_float(w[k] << 16)));
+        a = fmaxf(a, fabsf(__uint_as_float(w[k] & 0xffff0000u)));
+      }
+    }
+  }
+  a = warp_max(a);
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = a;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kNormThreads / 32; ++w) a = fmaxf(a, part[w]);
+  a = fmaxf(a, kAmaxMin);
+  const float inv = kFp8Max / a;
+#pragma unroll
+  for (int i = 0; i < kN; ++i) {
+    const int64_t r = r0 + i * kRowStep;
+    if (r >= R || c >= K) continue;
+    const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+    if constexpr (sizeof(T) == 4) {
+      *reinterpret_cast<uint32_t*>(q + r * K + c) =
+          pack_e4m3(__uint_as_float(w[0]) * inv, __uint_as_float(w[1]) * inv,
+                    __uint_as_float(w[2]) * inv, __uint_as_float(w[3]) * inv);
+    } else {
+      uint32_t o[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        o[k] = pack_e4m3(__uint_as_float(w[2 * k] << 16) * inv,
+                         __uint_as_float(w[2 * k] & 0xffff0000u) * inv,
+                         __uint_as_float(w[2 * k + 1] << 16) * inv,
+                         __uint_as_float(w[2 * k + 1] & 0xffff0000u) * inv);
+      *reinterpret_cast<uint2*>(q + r * K + c) = make_uint2(o[0], o[1]);
+    }
+  }
+  if (threadIdx.x == 0)
+    scale[static_cast<int64_t>(blockIdx.x) * gridDim.y + blockIdx.y] = a / kFp8Max;
+}
+
+// 1 x 128 groups: a half warp (bf16) or warp (float32, or unaligned rows, 4
+// columns 32 apart a lane) per group.
+template <class T, bool VEC>
+__global__ void __launch_bounds__(kNormThreads)
+    quantize_rows_kernel(const T* __restrict__ x, int64_t ldx, int64_t R, int K,
+                         uint8_t* __restrict__ q, float* __restrict__ scale) {
+  using S = Slots<T, VEC>;
+  constexpr int kPer = kNormThreads / S::kLanes;  // groups per thread block
+  const int groups = (K + kScaleGroup - 1) / kScaleGroup;
+  const int64_t u = static_cast<int64_t>(blockIdx.x) * kPer + threadIdx.x / S::kLanes;
+  const int64_t row = u / groups;
+  const int g = static_cast<int>(u % groups);
+  const int l = threadIdx.x % S::kLanes;
+  // a group past the last row takes part in the shuffles with zeros
+  const int c = row < R ? g * kScaleGroup + (VEC ? l * S::kE : l) : K;
+  float v[S::kE];
+  load_slot<T, VEC>(x + (row < R ? row : 0) * ldx, c, K, true, v);
+  float a = 0.f;
+#pragma unroll
+  for (int i = 0; i < S::kE; ++i) a = fmaxf(a, fabsf(v[i]));
+#pragma unroll
+  for (int o = S::kLanes / 2; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+  a = fmaxf(a, kAmaxMin);
+  const float inv = kFp8Max / a;
+  if (row >= R) return;
+  uint8_t* qr = q + row * K;
+  if constexpr (VEC) {
+    if (c < K) {
+      uint32_t b[S::kE / 4];
+#pragma unroll
+      for (int i = 0; i < S::kE / 4; ++i)
+        b[i] = pack_e4m3(v[4 * i] * inv, v[4 * i + 1] * inv, v[4 * i + 2] * inv,
+                         v[4 * i + 3] * inv);
+      if constexpr (S::kE == 8) *reinterpret_cast<uint2*>(qr + c) = make_uint2(b[0], b[1]);
+      else *reinterpret_cast<uint32_t*>(qr + c) = b[0];
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < S::kE; ++i)
+      if (c + 32 * i < K) qr[c + 32 * i] = to_e4m3(v[i] * inv);
+  }
+  if (l == 0) scale[u] = a / kFp8Max;
+}
+
+// 128 x 128 blocks of unaligned rows, read twice.
+template <class T>
+__global__ void __launch_bounds__(kNormThreads)
+    quantize_kernel(const T* __restrict__ x, int64_t ldx, int64_t R, int K,
                     uint8_t* __restrict__ q, float* __restrict__ scale) {
   __shared__ float part[kNormThreads / 32];
-  const int64_t r0 = static_cast<int64_t>(blockIdx.x) * block_rows;
+  const int64_t r0 = static_cast<int64_t>(blockIdx.x) * kScaleGroup;
   const int c = blockIdx.y * kScaleGroup + (threadIdx.x & (kScaleGroup - 1));
-  const int64_t r1 = min(R, r0 + block_rows);
+  const int64_t r1 = min(R, r0 + kScaleGroup);
   float a = 0.f;
   if (c < K)
     for (int64_t r = r0 + threadIdx.x / kScaleGroup; r < r1; r += kNormThreads / kScaleGroup)
@@ -205,54 +619,203 @@ bool norm_outputs_apart(const void* x, int64_t ldx, const void* residual, int64_
   return !ranges_overlap(a, b) && !ranges_overlap(a, h) && !ranges_overlap(b, h);
 }
 
-template <class T, class W, bool FP8>
-cudaError_t run_norm_fwd(const void* x, int64_t ldx, const void* residual, int64_t ldr,
-                         const void* weight, int64_t N, int64_t H, float eps, void* y, void* q,
-                         float* scale, void* h_out, float* rstd, cudaStream_t s) {
-  norm_fwd_kernel<T, W, FP8><<<static_cast<unsigned>(N), kNormThreads, 0, s>>>(
-      static_cast<const T*>(x), ldx, static_cast<const T*>(residual), ldr,
-      static_cast<const W*>(weight), static_cast<int>(H), eps, static_cast<T*>(y),
-      static_cast<uint8_t*>(q), scale, static_cast<T*>(h_out), rstd);
+// How a row of H columns is spread over threads.  Few rows: as many threads as
+// there are slots, for latency.  Many: a few slots a thread (16 values), so that
+// more rows are in flight on an SM; short rows share a block, a warp each.
+struct RowPlan {
+  int threads, slots, rows;  // threads a row, slots a thread, rows a block
+};
+RowPlan plan_rows(int64_t N, int64_t H, int elems, bool vec) {
+  const int64_t units = vec ? (H + elems - 1) / elems
+                            : (H + kScaleGroup - 1) / kScaleGroup * 32;  // slots of a row
+  const int most = 16 / elems;  // slots a thread may hold
+  const bool few = N <= 304;    // at most two rows an SM
+  int slots = 1;
+  while (slots < most && units > (few ? 1024 : 32) * slots) slots *= 2;
+  int64_t threads = (units + slots - 1) / slots;
+  threads = std::max<int64_t>((threads + 31) / 32 * 32, 32);
+  return {static_cast<int>(threads), slots, threads == 32 && !few ? 8 : 1};
+}
+
+// Partial sums of dweight: a block's rows at a time.  A fixed number, so that
+// the order of additions depends on the sizes alone: four blocks of up to 256
+// threads, two of 512 or one larger on each of 152 SMs.
+int64_t held_parts(int64_t N, const RowPlan& p) {
+  const int64_t blocks = p.threads <= 256 ? 608 : p.threads <= 512 ? 304 : 152;
+  return std::min<int64_t>((N + p.rows - 1) / p.rows, blocks) * p.rows;
+}
+int64_t dw_parts(int64_t N, int64_t H) {
+  if (H > kMaxHeld) return (N + kDwRows - 1) / kDwRows;
+  // whichever plan the call's types and alignment lead to
+  return std::max({held_parts(N, plan_rows(N, H, 8, true)), held_parts(N, plan_rows(N, H, 4, true)),
+                   held_parts(N, plan_rows(N, H, 4, false))});
+}
+
+struct FwdArgs {
+  const void* x;
+  int64_t ldx;
+  const void* residual;
+  int64_t ldr;
+  const void* weight;
+  int w_f32;
+  int64_t N;
+  int H;
+  float eps;
+  void* y;
+  void* q;
+  float* scale;
+  void* h_out;
+  float* rstd;
+};
+
+template <class T, bool FP8, bool VEC, int P>
+void launch_fwd_held(const RowPlan& p, bool aligned, const FwdArgs& a, cudaStream_t s) {
+  const unsigned blocks = static_cast<unsigned>((a.N + p.rows - 1) / p.rows);
+  norm_fwd_held_kernel<T, FP8, VEC, P><<<blocks, dim3(p.threads, p.rows), 0, s>>>(
+      static_cast<const T*>(a.x), a.ldx, static_cast<const T*>(a.residual), a.ldr, a.weight,
+      a.w_f32, aligned, a.N, a.H, a.eps, static_cast<T*>(a.y), static_cast<uint8_t*>(a.q), a.scale,
+      static_cast<T*>(a.h_out), a.rstd);
+}
+
+// Whether every row's pieces are 16-byte aligned.
+template <class T>
+bool fwd_aligned(const FwdArgs& a) {
+  const int e = 16 / sizeof(T);
+  return a.ldx % e == 0 && a.ldr % e == 0 && aligned_to(a.x, 16) &&
+         aligned_to(a.residual, 16) && aligned_to(a.weight, 16) && aligned_to(a.y, 16) &&
+         aligned_to(a.q, 8) && aligned_to(a.h_out, 16);
+}
+
+template <class T, bool FP8>
+cudaError_t run_norm_fwd(const FwdArgs& a, cudaStream_t s) {
+  if (a.H > kMaxHeld) {
+    const auto launch = [&](auto w) {
+      using W = decltype(w);
+      norm_fwd_kernel<T, W, FP8><<<static_cast<unsigned>(a.N), kNormThreads, 0, s>>>(
+          static_cast<const T*>(a.x), a.ldx, static_cast<const T*>(a.residual), a.ldr,
+          static_cast<const W*>(a.weight), a.H, a.eps, static_cast<T*>(a.y),
+          static_cast<uint8_t*>(a.q), a.scale, static_cast<T*>(a.h_out), a.rstd);
+    };
+    if (a.w_f32) launch(float{});
+    else launch(__nv_bfloat16{});
+  } else if (a.H % Slots<T, true>::kE == 0) {
+    constexpr int kE = Slots<T, true>::kE;
+    const bool al = fwd_aligned<T>(a);
+    const RowPlan p = plan_rows(a.N, a.H, kE, true);
+    if (p.slots == 1) launch_fwd_held<T, FP8, true, 1>(p, al, a, s);
+    else if (p.slots == 2) launch_fwd_held<T, FP8, true, 2>(p, al, a, s);
+    else if constexpr (kE == 4) launch_fwd_held<T, FP8, true, 4>(p, al, a, s);
+  } else {
+    const RowPlan p = plan_rows(a.N, a.H, 4, false);
+    if (p.slots == 1) launch_fwd_held<T, FP8, false, 1>(p, false, a, s);
+    else if (p.slots == 2) launch_fwd_held<T, FP8, false, 2>(p, false, a, s);
+    else launch_fwd_held<T, FP8, false, 4>(p, false, a, s);
+  }
   note_launch();
   return cudaGetLastError();
 }
 
-template <bool FP8, class... A>
-cudaError_t norm_fwd_by_type(flce_dtype t, flce_dtype w, A... a) {
-  if (t == FLCE_BF16)
-    return w == FLCE_BF16 ? run_norm_fwd<__nv_bfloat16, __nv_bfloat16, FP8>(a...)
-                          : run_norm_fwd<__nv_bfloat16, float, FP8>(a...);
-  return w == FLCE_BF16 ? run_norm_fwd<float, __nv_bfloat16, FP8>(a...)
-                        : run_norm_fwd<float, float, FP8>(a...);
+struct BwdArgsN {
+  const void* dy;
+  const void* dh;
+  const void* h;
+  int64_t ldh;
+  const void* weight;
+  int w_f32;
+  const float* rstd;
+  int64_t N;
+  int H;
+  void* dx;
+  void* dweight;
+  float* part;
+};
+
+template <class T, bool VEC, int P>
+void launch_bwd_held(const RowPlan& p, bool aligned, int64_t parts, const BwdArgsN& a,
+                     cudaStream_t s) {
+  // with up to 256 threads the sums and both rows fit the register file
+  auto* k = p.threads * p.rows <= 256 ? norm_bwd_held_kernel<T, VEC, P, 256>
+                                      : norm_bwd_held_kernel<T, VEC, P, 1024>;
+  k<<<static_cast<unsigned>(parts / p.rows), dim3(p.threads, p.rows), 0, s>>>(
+      static_cast<const T*>(a.dy), static_cast<const T*>(a.dh), static_cast<const T*>(a.h), a.ldh,
+      a.weight, a.w_f32, aligned, a.rstd, a.N, a.H, static_cast<T*>(a.dx),
+      a.dweight ? a.part : nullptr);
 }
 
-int64_t dw_parts(int64_t N) { return (N + kDwRows - 1) / kDwRows; }
-
-template <class T, class W>
-cudaError_t run_norm_bwd(const void* dy, const void* dh, const void* h, int64_t ldh,
-                         const void* weight, const float* rstd, int64_t N, int64_t H, void* dx,
-                         void* dweight, void* ws, cudaStream_t s) {
-  const int cols = static_cast<int>((H + kNormThreads - 1) / kNormThreads);
-  if (dx && N > 0) {
-    norm_bwd_dx_kernel<T, W><<<static_cast<unsigned>(N), kNormThreads, 0, s>>>(
-        static_cast<const T*>(dy), static_cast<const T*>(dh), static_cast<const T*>(h), ldh,
-        static_cast<const W*>(weight), rstd, static_cast<int>(H), static_cast<T*>(dx));
-    note_launch();
-  }
-  if (dweight) {
-    const int64_t parts = dw_parts(N);
-    float* part = static_cast<float*>(ws);
-    if (parts > 0) {
-      norm_bwd_dw_kernel<T><<<dim3(static_cast<unsigned>(parts), cols), kNormThreads, 0, s>>>(
-          static_cast<const T*>(dy), static_cast<const T*>(h), ldh, rstd, N,
-          static_cast<int>(H), part);
+template <class T>
+cudaError_t run_norm_bwd(const BwdArgsN& a, cudaStream_t s) {
+  int64_t parts = 0;
+  if (a.N > 0 && a.H > kMaxHeld) {
+    parts = dw_parts(a.N, a.H);
+    const unsigned cols = static_cast<unsigned>((a.H + kNormThreads - 1) / kNormThreads);
+    const T* dy = static_cast<const T*>(a.dy);
+    const T* h = static_cast<const T*>(a.h);
+    if (a.dx) {
+      const auto launch = [&](auto w) {
+        using W = decltype(w);
+        norm_bwd_dx_kernel<T, W><<<static_cast<unsigned>(a.N), kNormThreads, 0, s>>>(
+            dy, static_cast<const T*>(a.dh), h, a.ldh, static_cast<const W*>(a.weight), a.rstd,
+            a.H, static_cast<T*>(a.dx));
+      };
+      if (a.w_f32) launch(float{});
+      else launch(__nv_bfloat16{});
       note_launch();
     }
-    norm_dw_sum_kernel<W><<<cols, kNormThreads, 0, s>>>(part, parts, static_cast<int>(H),
-                                                        static_cast<W*>(dweight));
+    if (a.dweight) {
+      norm_bwd_dw_kernel<T><<<dim3(static_cast<unsigned>(parts), cols), kNormThreads, 0, s>>>(
+          dy, h, a.ldh, a.rstd, a.N, a.H, a.part);
+      note_launch();
+    }
+  } else if (a.N > 0 && (a.dx || a.dweight)) {
+    constexpr int kE = Slots<T, true>::kE;
+    const bool vec = a.H % kE == 0;
+    const bool al = a.ldh % kE == 0 && aligned_to(a.dy, 16) && aligned_to(a.dh, 16) &&
+                    aligned_to(a.h, 16) && aligned_to(a.weight, 16) && aligned_to(a.dx, 16);
+    const RowPlan p = plan_rows(a.N, a.H, vec ? kE : 4, vec);
+    parts = held_parts(a.N, p);
+    if (vec) {
+      if (p.slots == 1) launch_bwd_held<T, true, 1>(p, al, parts, a, s);
+      else if (p.slots == 2) launch_bwd_held<T, true, 2>(p, al, parts, a, s);
+      else if constexpr (kE == 4) launch_bwd_held<T, true, 4>(p, al, parts, a, s);
+    } else {
+      if (p.slots == 1) launch_bwd_held<T, false, 1>(p, al, parts, a, s);
+      else if (p.slots == 2) launch_bwd_held<T, false, 2>(p, al, parts, a, s);
+      else launch_bwd_held<T, false, 4>(p, al, parts, a, s);
+    }
+    note_launch();
+  }
+  if (a.dweight) {
+    const unsigned blocks = static_cast<unsigned>((a.H + 31) / 32);
+    if (a.w_f32)
+      norm_dw_sum_kernel<<<blocks, 256, 0, s>>>(a.part, parts, a.H, static_cast<float*>(a.dweight));
+    else
+      norm_dw_sum_kernel<<<blocks, 256, 0, s>>>(a.part, parts, a.H,
+                                                static_cast<__nv_bfloat16*>(a.dweight));
     note_launch();
   }
   return cudaGetLastError();
+}
+
+template <class T>
+void run_quantize(const void* xp, int64_t ldx, int64_t R, int64_t K64, int block_rows, void* qp,
+                  float* scale, cudaStream_t s) {
+  const T* x = static_cast<const T*>(xp);
+  auto* q = static_cast<uint8_t*>(qp);
+  const int K = static_cast<int>(K64), e = 16 / sizeof(T);
+  const int64_t gk = (K + kScaleGroup - 1) / kScaleGroup;
+  const bool vec = K % e == 0 && ldx % e == 0 && aligned_to(x, 16) && aligned_to(q, 8);
+  if (block_rows == 1) {
+    const int lanes = vec ? Slots<T, true>::kLanes : Slots<T, false>::kLanes;
+    const int per = kNormThreads / lanes;
+    const auto blocks = static_cast<unsigned>((R * gk + per - 1) / per);
+    if (vec) quantize_rows_kernel<T, true><<<blocks, kNormThreads, 0, s>>>(x, ldx, R, K, q, scale);
+    else quantize_rows_kernel<T, false><<<blocks, kNormThreads, 0, s>>>(x, ldx, R, K, q, scale);
+    return;
+  }
+  const dim3 grid(static_cast<unsigned>((R + kScaleGroup - 1) / kScaleGroup),
+                  static_cast<unsigned>(gk));
+  if (vec) quantize_tile_kernel<T><<<grid, kNormThreads, 0, s>>>(x, ldx, R, K, q, scale);
+  else quantize_kernel<T><<<grid, kNormThreads, 0, s>>>(x, ldx, R, K, q, scale);
 }
 
 }  // namespace
@@ -277,11 +840,12 @@ flce_status flce_rms_norm_forward(const void* x, int64_t ldx, const void* residu
     return FLCE_ERR_INVALID_ARG;
   int sms = 0;
   if ((st = check_device(&sms)) != FLCE_OK) return st;
-  return norm_fwd_by_type<false>(dtype, weight_dtype, x, ldx, residual, ldr, weight, N, H, eps, y,
-                                 static_cast<void*>(nullptr), static_cast<float*>(nullptr), h_out,
-                                 rstd, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
-             ? FLCE_OK
-             : FLCE_ERR_CUDA;
+  const FwdArgs a = {x, ldx, residual, ldr, weight, weight_dtype == FLCE_F32, N,
+                     static_cast<int>(H), eps, y, nullptr, nullptr, h_out, rstd};
+  const auto s = reinterpret_cast<cudaStream_t>(stream);
+  const cudaError_t err = dtype == FLCE_BF16 ? run_norm_fwd<__nv_bfloat16, false>(a, s)
+                                             : run_norm_fwd<float, false>(a, s);
+  return err == cudaSuccess ? FLCE_OK : FLCE_ERR_CUDA;
 }
 
 flce_status flce_rms_norm_fp8(const void* x, int64_t ldx, const void* residual, int64_t ldr,
@@ -300,17 +864,17 @@ flce_status flce_rms_norm_fp8(const void* x, int64_t ldx, const void* residual, 
     return FLCE_ERR_INVALID_ARG;
   int sms = 0;
   if ((st = check_device(&sms)) != FLCE_OK) return st;
-  return norm_fwd_by_type<true>(dtype, weight_dtype, x, ldx, residual, ldr, weight, N, H, eps,
-                                static_cast<void*>(nullptr), q, scale, h_out,
-                                static_cast<float*>(nullptr),
-                                reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
-             ? FLCE_OK
-             : FLCE_ERR_CUDA;
+  const FwdArgs a = {x, ldx, residual, ldr, weight, weight_dtype == FLCE_F32, N,
+                     static_cast<int>(H), eps, nullptr, q, scale, h_out, nullptr};
+  const auto s = reinterpret_cast<cudaStream_t>(stream);
+  const cudaError_t err = dtype == FLCE_BF16 ? run_norm_fwd<__nv_bfloat16, true>(a, s)
+                                             : run_norm_fwd<float, true>(a, s);
+  return err == cudaSuccess ? FLCE_OK : FLCE_ERR_CUDA;
 }
 
 size_t flce_rms_norm_workspace_size(int64_t N, int64_t H) {
   if (N < 0 || H <= 0 || H > kMaxRowElems || N > kMaxRows) return 0;
-  const size_t n = static_cast<size_t>(dw_parts(N)) * static_cast<size_t>(H) * 4;
+  const size_t n = static_cast<size_t>(dw_parts(N, H)) * static_cast<size_t>(H) * 4;
   return std::max<size_t>((n + 255) / 256 * 256, 256);
 }
 
@@ -346,18 +910,10 @@ flce_status flce_rms_norm_backward(const void* dy, const void* dh, const void* h
   const flce_status st = check_device(&sms);
   if (st != FLCE_OK) return st;
   const auto s = reinterpret_cast<cudaStream_t>(stream);
-  const bool wb = weight_dtype == FLCE_BF16;
-  cudaError_t err;
-  if (dtype == FLCE_BF16)
-    err = wb ? run_norm_bwd<__nv_bfloat16, __nv_bfloat16>(dy, dh, h, ldh, weight, rstd, N, H, dx,
-                                                          dweight, workspace, s)
-             : run_norm_bwd<__nv_bfloat16, float>(dy, dh, h, ldh, weight, rstd, N, H, dx, dweight,
-                                                  workspace, s);
-  else
-    err = wb ? run_norm_bwd<float, __nv_bfloat16>(dy, dh, h, ldh, weight, rstd, N, H, dx, dweight,
-                                                  workspace, s)
-             : run_norm_bwd<float, float>(dy, dh, h, ldh, weight, rstd, N, H, dx, dweight,
-                                          workspace, s);
+  const BwdArgsN a = {dy, dh, h, ldh, weight, weight_dtype == FLCE_F32, rstd, N,
+                      static_cast<int>(H), dx, dweight, static_cast<float*>(workspace)};
+  const cudaError_t err =
+      dtype == FLCE_BF16 ? run_norm_bwd<__nv_bfloat16>(a, s) : run_norm_bwd<float>(a, s);
   return err == cudaSuccess ? FLCE_OK : FLCE_ERR_CUDA;
 }
 
@@ -378,15 +934,9 @@ flce_status flce_quantize_fp8(const void* x, int64_t ldx, int64_t R, int64_t K, 
   const flce_status st = check_device(&sms);
   if (st != FLCE_OK) return st;
   const auto s = reinterpret_cast<cudaStream_t>(stream);
-  const dim3 grid(static_cast<unsigned>(gr), static_cast<unsigned>(gk));
-  if (dtype == FLCE_BF16)
-    quantize_kernel<<<grid, kNormThreads, 0, s>>>(static_cast<const __nv_bfloat16*>(x), ldx, R,
-                                                  static_cast<int>(K), block_rows,
-                                                  static_cast<uint8_t*>(q), scale);
-  else
-    quantize_kernel<<<grid, kNormThreads, 0, s>>>(static_cast<const float*>(x), ldx, R,
-                                                  static_cast<int>(K), block_rows,
-                                                  static_cast<uint8_t*>(q), scale);
+  if (block_rows == 1 && gr * gk > kMaxRows) return FLCE_ERR_UNSUPPORTED_SHAPE;
+  if (dtype == FLCE_BF16) run_quantize<__nv_bfloat16>(x, ldx, R, K, block_rows, q, scale, s);
+  else run_quantize<float>(x, ldx, R, K, block_rows, q, scale, s);
   note_launch();
   return cudaGetLastError() == cudaSuccess ? FLCE_OK : FLCE_ERR_CUDA;
 }
