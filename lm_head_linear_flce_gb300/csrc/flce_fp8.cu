@@ -329,8 +329,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 // With at most 128 rows of A the product is bound by reading B once.  The roles
 // of the operands are swapped: 128 rows of B are the MMA's M, the rows of A
 // (padded to NP) its N, so nothing of the tensor cores' work is wasted on
-// padding to 128 rows of A.  One CTA per SM; the ring keeps about 190 KB of B in
-// flight.  With fewer tiles of B than SMs, a cluster of `splits` CTAs shares a
+// padding to 128 rows of A.  Two CTAs per SM (one at NP = 128), whose rings keep
+// about 160 KB of B in flight: a tile's first loads and last stores overlap the
+// other CTA's stream, and 153 to 304 tiles run at once instead of in two rounds.  With fewer tiles of B than SMs, a cluster of `splits` CTAs shares a
 // tile, each taking a contiguous part of K; the parts are added in rank order
 // through distributed shared memory.
 constexpr int kRowThreads = 192;  // warp 0 TMA, warp 1 MMA, warps 2..5 epilogue
@@ -338,7 +339,8 @@ constexpr int kRowThreads = 192;  // warp 0 TMA, warp 1 MMA, warps 2..5 epilogue
 template <int NP>
 struct RowShape {
   static constexpr int kStageBytes = 128 * kKB + NP * kKB;
-  static constexpr int kStages = NP <= 16 ? 12 : NP <= 32 ? 11 : NP <= 64 ? 9 : 6;
+  static constexpr int kPerSm = NP <= 64 ? 2 : 1;  // CTAs per SM
+  static constexpr int kStages = NP <= 16 ? 6 : NP <= 32 ? 5 : NP <= 64 ? 4 : 6;
   static constexpr int kAccs = 4;                     // accumulators of NP columns
   static constexpr int kTmem = NP * kAccs < 32 ? 32 : NP * kAccs;
   static constexpr int kScaleBytes = 4 * 2 * NP * 4;  // two buffers per epilogue warp
@@ -346,7 +348,7 @@ struct RowShape {
 };
 
 template <int NP, class O>
-__global__ void __launch_bounds__(kRowThreads, 1)
+__global__ void __launch_bounds__(kRowThreads, RowShape<NP>::kPerSm)
     flce_fp8_rows_kernel(const __grid_constant__ CUtensorMap ta,
                          const __grid_constant__ CUtensorMap tb, const Fp8Args a,
                          const int splits) {
@@ -588,11 +590,12 @@ cudaError_t launch_rows(const CUtensorMap& ta, const CUtensorMap& tb, const Fp8A
   cudaError_t e =
       prepare(reinterpret_cast<const void*>(k), RowShape<NP>::kSmem, &prepared);
   if (e != cudaSuccess) return e;
-  // As many parts of K as keep every CTA on an SM of its own, none empty.
+  // As many parts of K as the device has room for, none empty.
+  const int room = RowShape<NP>::kPerSm * sms;
   int splits = 1;
-  while (splits < 8 && 2 * splits * a.tiles_v <= sms && 2 * splits <= a.G) splits *= 2;
+  while (splits < 8 && 2 * splits * a.tiles_v <= room && 2 * splits <= a.G) splits *= 2;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(splits > 1 ? splits * a.tiles_v : std::min(a.tiles_v, sms));
+  cfg.gridDim = dim3(splits > 1 ? splits * a.tiles_v : std::min(a.tiles_v, room));
   cfg.blockDim = dim3(kRowThreads);
   cfg.dynamicSmemBytes = RowShape<NP>::kSmem;
   cfg.stream = s;

@@ -81,36 +81,46 @@ struct Slots {
   static constexpr int kStep = VEC ? 1 : 32;  // columns between a slot's elements
 };
 
+// A slot's elements as loaded (zero past the row), and as floats.
+template <class T, bool VEC>
+struct Piece {
+  static constexpr int kE = Slots<T, VEC>::kE;
+  uint32_t w[kE * sizeof(T) / 4];
+
+  __device__ __forceinline__ void load(const T* __restrict__ row, int c, int H, bool aligned) {
+    if constexpr (VEC) {
+      // H is a multiple of E: a piece lies inside the row or past it
+      if (aligned) {
+        uint4 p = make_uint4(0, 0, 0, 0);
+        if (c < H) p = *reinterpret_cast<const uint4*>(row + c);
+        w[0] = p.x, w[1] = p.y, w[2] = p.z, w[3] = p.w;
+        return;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kE; ++i) {
+      const int k = c + i * Slots<T, VEC>::kStep;
+      if constexpr (sizeof(T) == 4) {
+        w[i] = k < H ? __float_as_uint(row[k]) : 0u;
+      } else {
+        const uint32_t u = k < H ? __bfloat16_as_ushort(row[k]) : 0u;
+        w[i / 2] = i % 2 ? w[i / 2] | u << 16 : u;
+      }
+    }
+  }
+  __device__ __forceinline__ void floats(float (&v)[kE]) const {
+#pragma unroll
+    for (int i = 0; i < kE; ++i)
+      v[i] = __uint_as_float(sizeof(T) == 4 ? w[i] : i % 2 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
+  }
+};
+
 template <class T, bool VEC>
 __device__ __forceinline__ void load_slot(const T* __restrict__ row, int c, int H, bool aligned,
                                           float (&v)[Slots<T, VEC>::kE]) {
-  constexpr int kE = Slots<T, VEC>::kE;
-  if constexpr (VEC) {
-    // H is a multiple of E: a piece lies inside the row or past it
-    if (!aligned) {
-#pragma unroll
-      for (int i = 0; i < kE; ++i) v[i] = c < H ? to_f(row[c + i]) : 0.f;
-      return;
-    }
-    uint4 p = make_uint4(0, 0, 0, 0);
-    if (c < H) p = *reinterpret_cast<const uint4*>(row + c);
-    if constexpr (sizeof(T) == 4) {
-      v[0] = __uint_as_float(p.x);
-      v[1] = __uint_as_float(p.y);
-      v[2] = __uint_as_float(p.z);
-      v[3] = __uint_as_float(p.w);
-    } else {
-      const uint32_t w[4] = {p.x, p.y, p.z, p.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        v[2 * i] = __uint_as_float(w[i] << 16);
-        v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-      }
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < kE; ++i) v[i] = c + 32 * i < H ? to_f(row[c + 32 * i]) : 0.f;
-  }
+  Piece<T, VEC> p;
+  p.load(row, c, H, aligned);
+  p.floats(v);
 }
 
 template <class T, bool VEC>
@@ -302,13 +312,36 @@ __global__ void __launch_bounds__(THREADS)
   }
   const float inv_h = 1.f / static_cast<float>(H);
   int phase = 0;
+  // the next row's values are on their way while a row is summed and written
+  // (where the registers allow: with 1024 threads a row is fetched when its turn
+  // comes)
+  constexpr bool kAhead = THREADS <= 512;
+  Piece<T, VEC> ny[P], nh[P], ne[P];
+  float nr = 0.f;
+  const auto fetch = [&](int64_t row) {
+    if (row >= N) return;
+    nr = rstd[row];
+#pragma unroll
+    for (int s = 0; s < P; ++s) {
+      const int c = S::first(s);
+      ny[s].load(dy + row * H, c, H, aligned);
+      nh[s].load(h + row * ldh, c, H, aligned);
+      if (dh && dx) ne[s].load(dh + row * H, c, H, aligned);
+    }
+  };
+  if (kAhead) fetch(first);
   for (int64_t row = first; row < N; row += step, phase ^= 1) {
+    if (!kAhead) fetch(row);
     float g[P][S::kE], v[P][S::kE];
-    const float r = rstd[row];
+    Piece<T, VEC> e[P];
+    const float r = nr;
 #pragma unroll
-    for (int s = 0; s < P; ++s) load_slot<T, VEC>(dy + row * H, S::first(s), H, aligned, g[s]);
-#pragma unroll
-    for (int s = 0; s < P; ++s) load_slot<T, VEC>(h + row * ldh, S::first(s), H, aligned, v[s]);
+    for (int s = 0; s < P; ++s) {
+      ny[s].floats(g[s]);
+      nh[s].floats(v[s]);
+      e[s] = ne[s];
+    }
+    if (kAhead) fetch(row + step);
     float dot = 0.f;
 #pragma unroll
     for (int s = 0; s < P; ++s)
@@ -323,16 +356,15 @@ __global__ void __launch_bounds__(THREADS)
     const float k = r * r * (row_sum(dot, part, phase) * inv_h);
 #pragma unroll
     for (int s = 0; s < P; ++s) {
-      const int c = S::first(s);
 #pragma unroll
       for (int i = 0; i < S::kE; ++i) g[s][i] = r * (g[s][i] - v[s][i] * k);
       if (dh) {
-        float e[S::kE];
-        load_slot<T, VEC>(dh + row * H, c, H, aligned, e);
+        float t[S::kE];
+        e[s].floats(t);
 #pragma unroll
-        for (int i = 0; i < S::kE; ++i) g[s][i] += e[i];
+        for (int i = 0; i < S::kE; ++i) g[s][i] += t[i];
       }
-      store_slot<T, VEC>(dx + row * H, c, H, aligned, g[s]);
+      store_slot<T, VEC>(dx + row * H, S::first(s), H, aligned, g[s]);
     }
   }
   if (!dw_part) return;
@@ -347,22 +379,23 @@ __global__ void __launch_bounds__(THREADS)
 }
 
 // dweight = the partial sums, added in order: 32 columns a block, each of its
-// eight warps taking every eighth partial, then the warps in order.
+// 32 warps taking every 32nd partial, then the warps in order.
+constexpr int kSumWarps = 32;
 template <class W>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(32 * kSumWarps)
     norm_dw_sum_kernel(const float* __restrict__ part, int64_t parts, int H, W* __restrict__ dw) {
-  __shared__ float sums[8][32];
+  __shared__ float sums[kSumWarps][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
   float s = 0.f;
   if (c < H) {
 #pragma unroll 8
-    for (int64_t p = warp; p < parts; p += 8) s += part[p * H + c];
+    for (int64_t p = warp; p < parts; p += kSumWarps) s += part[p * H + c];
   }
   sums[warp][lane] = s;
   __syncthreads();
   if (warp != 0 || c >= H) return;
-  for (int k = 1; k < 8; ++k) s += sums[k][lane];
+  for (int k = 1; k < kSumWarps; ++k) s += sums[k][lane];
   dw[c] = from_f<W>(s);
 }
 
@@ -451,7 +484,7 @@ __global__ void __launch_bounds__(kNormThreads)
 // once into registers (16 values of bf16, 4 of float32 a load, all in flight),
 // takes the maximum and writes it.
 template <class T>
-__global__ void __launch_bounds__(kNormThreads)
+__global__ void __launch_bounds__(kNormThreads, 3)
     quantize_tile_kernel(const T* __restrict__ x, int64_t ldx, int64_t R, int K,
                          uint8_t* __restrict__ q, float* __restrict__ scale) {
   constexpr int kE = 16 / static_cast<int>(sizeof(T));
@@ -733,9 +766,9 @@ struct BwdArgsN {
 template <class T, bool VEC, int P>
 void launch_bwd_held(const RowPlan& p, bool aligned, int64_t parts, const BwdArgsN& a,
                      cudaStream_t s) {
-  // with up to 256 threads the sums and both rows fit the register file
-  auto* k = p.threads * p.rows <= 256 ? norm_bwd_held_kernel<T, VEC, P, 256>
-                                      : norm_bwd_held_kernel<T, VEC, P, 1024>;
+  auto* k = p.threads * p.rows <= 256   ? norm_bwd_held_kernel<T, VEC, P, 256>
+            : p.threads * p.rows <= 512 ? norm_bwd_held_kernel<T, VEC, P, 512>
+                                        : norm_bwd_held_kernel<T, VEC, P, 1024>;
   k<<<static_cast<unsigned>(parts / p.rows), dim3(p.threads, p.rows), 0, s>>>(
       static_cast<const T*>(a.dy), static_cast<const T*>(a.dh), static_cast<const T*>(a.h), a.ldh,
       a.weight, a.w_f32, aligned, a.rstd, a.N, a.H, static_cast<T*>(a.dx),
@@ -787,9 +820,9 @@ cudaError_t run_norm_bwd(const BwdArgsN& a, cudaStream_t s) {
   if (a.dweight) {
     const unsigned blocks = static_cast<unsigned>((a.H + 31) / 32);
     if (a.w_f32)
-      norm_dw_sum_kernel<<<blocks, 256, 0, s>>>(a.part, parts, a.H, static_cast<float*>(a.dweight));
+      norm_dw_sum_kernel<<<blocks, 32 * kSumWarps, 0, s>>>(a.part, parts, a.H, static_cast<float*>(a.dweight));
     else
-      norm_dw_sum_kernel<<<blocks, 256, 0, s>>>(a.part, parts, a.H,
+      norm_dw_sum_kernel<<<blocks, 32 * kSumWarps, 0, s>>>(a.part, parts, a.H,
                                                 static_cast<__nv_bfloat16*>(a.dweight));
     note_launch();
   }
