@@ -12,7 +12,6 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
-#include <atomic>
 
 #include "flce_fp8_device.cuh"
 #include "flce_internal.h"
@@ -550,29 +549,12 @@ __global__ void __launch_bounds__(kRowThreads, RowShape<NP>::kPerSm)
 }
 
 // ------------------------------------------------------------- launching
-constexpr int kMaxDevices = 64;
-struct Prepared {
-  std::atomic<int> done[kMaxDevices] = {};
-};
-
-// Raises the kernel's shared-memory limit on the device's first launch.
-cudaError_t prepare(const void* kernel, int smem, Prepared* p) {
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  const bool cached = dev >= 0 && dev < kMaxDevices;
-  if (cached && p->done[dev].load(std::memory_order_acquire)) return cudaSuccess;
-  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e == cudaSuccess && cached) p->done[dev].store(1, std::memory_order_release);
-  return e;
-}
-
 template <class O>
 cudaError_t launch_pair(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& ty,
                         const Fp8Args& a, int sms, cudaStream_t s) {
-  static Prepared prepared;
+  static SmemLimit limit;
   auto* k = flce_fp8_pair_kernel<O>;
-  cudaError_t e = prepare(reinterpret_cast<const void*>(k), kPairSmem, &prepared);
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(k), kPairSmem, &limit);
   if (e != cudaSuccess) return e;
   const int64_t tiles = static_cast<int64_t>(a.tiles_m) * a.tiles_v;
   const int pairs = static_cast<int>(std::min<int64_t>(tiles, sms / 2));
@@ -585,10 +567,10 @@ cudaError_t launch_pair(const CUtensorMap& ta, const CUtensorMap& tb, const CUte
 template <int NP, class O>
 cudaError_t launch_rows(const CUtensorMap& ta, const CUtensorMap& tb, const Fp8Args& a, int sms,
                         cudaStream_t s) {
-  static Prepared prepared;
+  static SmemLimit limit;
   auto* k = flce_fp8_rows_kernel<NP, O>;
   cudaError_t e =
-      prepare(reinterpret_cast<const void*>(k), RowShape<NP>::kSmem, &prepared);
+      allow_smem(reinterpret_cast<const void*>(k), RowShape<NP>::kSmem, &limit);
   if (e != cudaSuccess) return e;
   // As many parts of K as the device has room for, none empty.
   const int room = RowShape<NP>::kPerSm * sms;

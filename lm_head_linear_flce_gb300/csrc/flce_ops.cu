@@ -1,8 +1,6 @@
 // Host-side helpers shared by the operators around the LM head (flce_ops.h).
 #include "flce_ops.h"
 
-#include <atomic>
-
 namespace flce {
 namespace {
 
@@ -30,31 +28,15 @@ flce_status check_device(int* sms) {
   return (v & 1) ? FLCE_OK : FLCE_ERR_UNSUPPORTED_DEVICE;
 }
 
-bool make_tmap_sw64(CUtensorMap* m, const void* ptr, uint64_t inner, uint64_t outer,
-                    uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer,
-                    CUtensorMapDataType dtype) {
-  using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                              const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                              const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-  static const Encode encode = [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
-                                         &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
-      return static_cast<Encode>(nullptr);
-    return reinterpret_cast<Encode>(p);
-  }();
-  if (!encode) return false;
-  cuuint64_t dims[2] = {inner, outer};
-  cuuint64_t strides[1] = {row_bytes};
-  cuuint32_t box[2] = {box_inner, box_outer};
-  cuuint32_t ones[2] = {1, 1};
-  return encode(m, dtype, 2, const_cast<void*>(ptr), dims, strides, box, ones,
-                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
-                CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+cudaError_t allow_smem(const void* kernel, int smem, SmemLimit* limit) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const bool cached = dev >= 0 && dev < 64;
+  if (cached && limit->set[dev].load(std::memory_order_acquire)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e == cudaSuccess && cached) limit->set[dev].store(1, std::memory_order_release);
+  return e;
 }
 
 }  // namespace flce

@@ -2,8 +2,8 @@
 // head (norm, 8-bit operands and their product, logits processing).
 #pragma once
 
+#include <atomic>
 #include <cstdint>
-#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include "../../include/flce.h"
@@ -18,12 +18,13 @@ constexpr int64_t kMaxRowElems = 1 << 16; // longest norm row / contraction
 // FLCE_OK and the SM count of the current device, if it is an sm_103 one.
 flce_status check_device(int* sms);
 
-// 2-D tensor map over a row-major [outer][inner] matrix (rows `row_bytes`
-// apart) with 64-byte swizzle: the 16-byte piece p of a box's 64-byte row r lies
-// at piece p ^ (r / 2 % 4).  False if the CUDA driver rejects it.
-bool make_tmap_sw64(CUtensorMap* m, const void* ptr, uint64_t inner, uint64_t outer,
-                    uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer,
-                    CUtensorMapDataType dtype);
+// Raises a kernel's dynamic shared-memory limit to `smem`, on its first launch
+// on a device; one SmemLimit per kernel.  Atomic: racing first launches set the
+// same attribute.
+struct SmemLimit {
+  std::atomic<int> set[64] = {};
+};
+cudaError_t allow_smem(const void* kernel, int smem, SmemLimit* limit);
 
 inline bool valid_dtype(flce_dtype t) { return t == FLCE_BF16 || t == FLCE_F32; }
 inline size_t dtype_bytes(flce_dtype t) { return t == FLCE_F32 ? 4 : 2; }

@@ -4,6 +4,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "flce_internal.h"
 #include "flce_ops.h"
@@ -44,146 +45,164 @@ __device__ __forceinline__ int64_t id_at(const void* p, int is64, int64_t i) {
 // "in the prompt": 16 bits where the history is shorter than 2^15 (half the
 // shared memory, so twice the columns a block), else 32.  With biases, 16 more
 // bits hold 1 + the largest index of the column's entries.
-constexpr int kWin = 8;    // consecutive columns a thread takes at a time
-constexpr int kBatch = 4;  // windows a thread has in flight
+constexpr int kWin = 4;  // consecutive columns a thread takes at a time: neighbouring lanes
+                         // then read and write whole lines in either type
 
 template <bool WIDE>
 struct Counts {
+  static constexpr uint32_t kPrompt = WIDE ? 0x80000000u : 0x8000u;
   uint32_t* words;
   __device__ void add(int c, bool prompt) {
-    if constexpr (WIDE) {
-      if (prompt) atomicOr(words + c, 0x80000000u);
-      else atomicAdd(words + c, 1u);
-    } else {
-      const int sh = 16 * (c & 1);
-      if (prompt) atomicOr(words + (c >> 1), 0x8000u << sh);
-      else atomicAdd(words + (c >> 1), 1u << sh);
-    }
+    const int sh = WIDE ? 0 : 16 * (c & 1);
+    uint32_t* w = words + (WIDE ? c : c >> 1);
+    if (prompt) atomicOr(w, kPrompt << sh);
+    else atomicAdd(w, 1u << sh);
   }
-  // Counters of the window at c (a multiple of kWin); false if all are zero.
-  __device__ bool window(int c, uint32_t (&n)[kWin]) const {
-    if constexpr (WIDE) {
-      const uint4 p = *reinterpret_cast<const uint4*>(words + c);
-      const uint4 q = *reinterpret_cast<const uint4*>(words + c + 4);
-      n[0] = p.x, n[1] = p.y, n[2] = p.z, n[3] = p.w;
-      n[4] = q.x, n[5] = q.y, n[6] = q.z, n[7] = q.w;
-      return (p.x | p.y | p.z | p.w | q.x | q.y | q.z | q.w) != 0;
-    } else {
-      const uint4 p = *reinterpret_cast<const uint4*>(words + (c >> 1));
-      const uint32_t w[4] = {p.x, p.y, p.z, p.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) n[2 * i] = w[i] & 0xffffu, n[2 * i + 1] = w[i] >> 16;
-      return (p.x | p.y | p.z | p.w) != 0;
-    }
+  // The window's counters, at c (a multiple of kWin).
+  using Packed = typename std::conditional<WIDE, uint4, uint2>::type;
+  __device__ Packed window(int c) const {
+    return *reinterpret_cast<const Packed*>(words + (WIDE ? c : c >> 1));
   }
-  static constexpr uint32_t kPrompt = WIDE ? 0x80000000u : 0x8000u;
 };
+__device__ __forceinline__ bool any(const uint4& p) { return (p.x | p.y | p.z | p.w) != 0; }
+__device__ __forceinline__ bool any(const uint2& p) { return (p.x | p.y) != 0; }
+__device__ __forceinline__ void unpack(const uint4& p, uint32_t (&n)[kWin]) {
+  n[0] = p.x, n[1] = p.y, n[2] = p.z, n[3] = p.w;
+}
+__device__ __forceinline__ void unpack(const uint2& p, uint32_t (&n)[kWin]) {
+  n[0] = p.x & 0xffffu, n[1] = p.x >> 16, n[2] = p.y & 0xffffu, n[3] = p.y >> 16;
+}
 
-// Eight consecutive logits as loaded, and as floats.
-template <class T>
-struct Raw {
-  uint4 p[sizeof(T) / 2];
-};
-__device__ __forceinline__ void floats(const Raw<float>& r, float (&v)[kWin]) {
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    v[4 * i] = __uint_as_float(r.p[i].x);
-    v[4 * i + 1] = __uint_as_float(r.p[i].y);
-    v[4 * i + 2] = __uint_as_float(r.p[i].z);
-    v[4 * i + 3] = __uint_as_float(r.p[i].w);
-  }
+// Four consecutive logits as loaded, and as floats.
+__device__ __forceinline__ uint4 load_raw(const float* p) {
+  return *reinterpret_cast<const uint4*>(p);
 }
-__device__ __forceinline__ void floats(const Raw<__nv_bfloat16>& r, float (&v)[kWin]) {
-  const uint32_t w[4] = {r.p[0].x, r.p[0].y, r.p[0].z, r.p[0].w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] = __uint_as_float(w[i] << 16);
-    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-  }
+__device__ __forceinline__ uint2 load_raw(const __nv_bfloat16* p) {
+  return *reinterpret_cast<const uint2*>(p);
 }
-template <class T>
-__device__ __forceinline__ Raw<T> load_raw(const T* p) {
-  Raw<T> r;
-#pragma unroll
-  for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i)
-    r.p[i] = reinterpret_cast<const uint4*>(p)[i];
-  return r;
+__device__ __forceinline__ void floats(const uint4& r, float (&v)[kWin]) {
+  v[0] = __uint_as_float(r.x), v[1] = __uint_as_float(r.y);
+  v[2] = __uint_as_float(r.z), v[3] = __uint_as_float(r.w);
+}
+__device__ __forceinline__ void floats(const uint2& r, float (&v)[kWin]) {
+  v[0] = __uint_as_float(r.x << 16), v[1] = __uint_as_float(r.x & 0xffff0000u);
+  v[2] = __uint_as_float(r.y << 16), v[3] = __uint_as_float(r.y & 0xffff0000u);
 }
 __device__ __forceinline__ void store_window(float* p, const float (&v)[kWin]) {
-  reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-  reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+  *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
 }
 __device__ __forceinline__ void store_window(__nv_bfloat16* p, const float (&v)[kWin]) {
-  uint32_t w[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-    w[i] = *reinterpret_cast<uint32_t*>(&h);
-  }
-  *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+  __nv_bfloat162 a = __floats2bfloat162_rn(v[0], v[1]), b = __floats2bfloat162_rn(v[2], v[3]);
+  *reinterpret_cast<uint2*>(p) =
+      make_uint2(*reinterpret_cast<uint32_t*>(&a), *reinterpret_cast<uint32_t*>(&b));
 }
 __device__ __forceinline__ float load_f(const float* p) { return *p; }
 __device__ __forceinline__ float load_f(const __nv_bfloat16* p) { return __bfloat162float(*p); }
 __device__ __forceinline__ void store_f(float* p, float v) { *p = v; }
 __device__ __forceinline__ void store_f(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 
+// Windows a thread has on their way, in slots of its own in shared memory:
+// 64 bytes a thread, 64 KB an SM, all the time.
+template <class T>
+constexpr int kRing = 16 / static_cast<int>(sizeof(T));
+
+template <int BYTES>
+__device__ __forceinline__ void copy_async(void* dst, const void* src) {
+  const uint32_t d = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
+  asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(d), "l"(src), "n"(BYTES)
+               : "memory");
+}
+
+// Mask words a block of `cols` columns may touch, with one to spare for the
+// word behind a window's first, in steps of 16 bytes.
+__host__ __device__ constexpr int mask_words(int cols) { return (cols / 32 + 3 + 3) / 4 * 4; }
+
 template <class T, class O, bool WIDE, bool BIAS, int THREADS>
-__global__ void __launch_bounds__(THREADS)
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS)
     process_kernel(const T* logits, O* out, const ProcessArgs a) {
   extern __shared__ __align__(16) uint32_t smem[];
   const int64_t b = blockIdx.y;
-  const int64_t v0 = static_cast<int64_t>(blockIdx.x) * a.cols;
-  const int cols = static_cast<int>(min(int64_t{a.cols}, a.V - v0));
+  const int v0 = static_cast<int>(blockIdx.x) * a.cols;  // V <= 2^30
+  const int cols = min(a.cols, static_cast<int>(a.V) - v0);
   const T* in_row = logits + b * a.ld_logits + v0;
   O* out_row = out + b * a.ld_out + v0;
   // Windows start `shift` columns before the block's first, where both rows are
-  // 16-byte aligned; if no shift does that, every window goes column by column.
-  constexpr int kEI = 16 / static_cast<int>(sizeof(T)), kEO = 16 / static_cast<int>(sizeof(O));
-  const int mi = static_cast<int>(reinterpret_cast<uintptr_t>(in_row) / sizeof(T) % kEI);
-  const int mo = static_cast<int>(reinterpret_cast<uintptr_t>(out_row) / sizeof(O) % kEO);
-  const int shift = kEI > kEO ? mi : mo;
-  const bool vec = (mi - shift) % kEI == 0 && (mo - shift) % kEO == 0;
+  // aligned to one; if that differs, every window goes column by column.
+  const auto misaligned = [](const auto* p) {
+    return static_cast<int>(reinterpret_cast<uintptr_t>(p) / sizeof(*p) % kWin);
+  };
+  const int shift = misaligned(in_row);
+  const bool vec = shift == misaligned(out_row);
   const int windows = (shift + cols + kWin - 1) / kWin;
-  // a window wholly inside the block's columns
-  const auto whole = [&](int k) {
-    return vec && kWin * k >= shift && kWin * (k + 1) - shift <= cols;
-  };
+  // windows [w_lo, w_hi) lie wholly inside the block's columns
+  const int w_lo = vec ? (shift + kWin - 1) / kWin : windows;
+  const int w_hi = vec ? (shift + cols) / kWin : windows;
 
-  Raw<T> raw[kBatch];
-  const auto fetch = [&](int k0) {
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      const int k = k0 + i * THREADS;
-      if (k < windows && whole(k)) raw[i] = load_raw(in_row + kWin * k - shift);
-    }
-  };
-  if (!a.in_place) fetch(threadIdx.x);
-
-  // counters, then bias indices, one per window column
-  const int slots = windows * kWin;
-  Counts<WIDE> counts{smem};
-  uint32_t* bias = smem + (WIDE ? slots : slots / 2);
-  const int words = (WIDE ? slots : slots / 2) + (BIAS ? slots / 2 : 0);
-  for (int i = threadIdx.x; i < words / 4; i += THREADS)
-    reinterpret_cast<uint4*>(smem)[i] = make_uint4(0, 0, 0, 0);
-  __syncthreads();
-  int64_t len = a.lengths ? a.lengths[b] : a.L;
-  len = max(int64_t{0}, min(len, a.L));
+  // What depends on nothing else is asked for at once: the row's scalars and the
+  // thread's first windows.
+  const int64_t len0 = a.lengths ? a.lengths[b] : a.L;
   const int64_t prompt = a.prompt_lengths ? a.prompt_lengths[b] : 0;
-  constexpr int kIds = 8;  // ids a thread has in flight
-  for (int64_t i0 = threadIdx.x; i0 < len; i0 += THREADS * kIds) {
-    int64_t id[kIds];
+  const float rep = a.repetition ? a.repetition[b] : 1.f;
+  const float freq = a.frequency ? a.frequency[b] : 0.f;
+  const float pres = a.presence ? a.presence[b] : 0.f;
+
+  // Shared memory: the ring, the block's mask words, counters, bias indices
+  // (the latter two one per window column).
+  using Raw = decltype(load_raw(in_row));
+  Raw* ring = reinterpret_cast<Raw*>(smem) + threadIdx.x;  // this thread's slots, THREADS apart
+  uint32_t* mask = smem + kRing<T> * THREADS * sizeof(Raw) / 4;
+  const int slots = (windows * kWin + 7) / 8 * 8;
+  Counts<WIDE> counts{mask + mask_words(a.cols)};
+  uint32_t* bias = counts.words + (WIDE ? slots : slots / 2);
+  const int words = (WIDE ? slots : slots / 2) + (BIAS ? slots / 2 : 0);
+  // The thread's window k (if it is whole) into the ring; one group per window.
+  const auto fetch = [&](int k, int slot) {
+    if (k >= w_lo && k < w_hi && !a.in_place)
+      copy_async<sizeof(Raw)>(ring + slot * THREADS, in_row + kWin * k - shift);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+#pragma unroll
+  for (int i = 0; i < kRing<T>; ++i) fetch(threadIdx.x + i * THREADS, i);
+
+  // mask word i holds columns 32 (v0 / 32 + i) and on
+  const int first_word = v0 >> 5;
+  if (a.allowed) {
+    const int* m = a.allowed + b * a.ld_allowed;
+    const int last = static_cast<int>((a.V - 1) >> 5);
+    for (int i = threadIdx.x; i < mask_words(a.cols); i += THREADS)
+      mask[i] = first_word + i <= last ? static_cast<uint32_t>(m[first_word + i]) : 0u;
+  }
+  for (int i = threadIdx.x; i < words / 4; i += THREADS)
+    reinterpret_cast<uint4*>(counts.words)[i] = make_uint4(0, 0, 0, 0);
+  __syncthreads();
+  const int64_t len = max(int64_t{0}, min(len0, a.L));
+  constexpr int kIds = 8;
+  int id[kIds];  // relative to v0; negative: none
+  const auto fetch_ids = [&](int64_t i0) {
 #pragma unroll
     for (int u = 0; u < kIds; ++u) {
       const int64_t i = i0 + u * THREADS;
-      id[u] = i < len ? id_at(a.tokens, a.tokens_int64, b * a.ld_tokens + i) : -1;
+      id[u] = -1;
+      if (i >= len) continue;
+      if (a.tokens_int64) {
+        const int64_t t = static_cast<const int64_t*>(a.tokens)[b * a.ld_tokens + i] - v0;
+        id[u] = t >= 0 && t < cols ? static_cast<int>(t) : -1;
+      } else {
+        const int t = static_cast<const int*>(a.tokens)[b * a.ld_tokens + i];
+        id[u] = t >= 0 ? t - v0 : -1;
+      }
     }
+  };
+  // the next ids are on their way while these are counted
+  fetch_ids(threadIdx.x);
+  for (int64_t i0 = threadIdx.x; i0 < len; i0 += THREADS * kIds) {
+    int now[kIds];
 #pragma unroll
-    for (int u = 0; u < kIds; ++u) {
-      const int64_t c = id[u] - v0;
-      if (id[u] >= 0 && c >= 0 && c < cols)
-        counts.add(static_cast<int>(c) + shift, i0 + u * THREADS < prompt);
-    }
+    for (int u = 0; u < kIds; ++u) now[u] = id[u];
+    fetch_ids(i0 + THREADS * kIds);
+#pragma unroll
+    for (int u = 0; u < kIds; ++u)
+      if (now[u] >= 0 && now[u] < cols) counts.add(now[u] + shift, i0 + u * THREADS < prompt);
   }
   if constexpr (BIAS) {
     for (int i = threadIdx.x; i < a.n_bias; i += THREADS) {
@@ -203,67 +222,60 @@ __global__ void __launch_bounds__(THREADS)
   }
   __syncthreads();
 
-  const float rep = a.repetition ? a.repetition[b] : 1.f;
-  const float freq = a.frequency ? a.frequency[b] : 0.f;
-  const float pres = a.presence ? a.presence[b] : 0.f;
-  const int* mask = a.allowed ? a.allowed + b * a.ld_allowed : nullptr;
-  // One column: its counter n, bias entry e (0: none) and whether it is allowed.
-  const auto apply = [&](float l, uint32_t n, uint32_t e, bool ok) {
+  // One column with its counter n and bias entry e (0: none).
+  const auto apply = [&](float l, uint32_t n, uint32_t e) {
     if (n) {
       l = l > 0.f ? l / rep : l * rep;
       const uint32_t c = n & ~Counts<WIDE>::kPrompt;
       l -= freq * static_cast<float>(c) + (c ? pres : 0.f);
     }
     if (BIAS && e) l += a.bias_values[b * a.n_bias + e - 1];
-    return ok ? l : -INFINITY;
+    return l;
   };
-  for (int k0 = threadIdx.x; k0 < windows; k0 += THREADS * kBatch) {
-    if (!a.in_place && k0 != static_cast<int>(threadIdx.x)) fetch(k0);
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      const int k = k0 + i * THREADS;
-      if (k >= windows) break;
-      const int c0 = kWin * k;  // the window's first counter
-      uint32_t n[kWin];
-      bool plain = !counts.window(c0, n);
-      uint32_t e[kWin] = {};
-      if constexpr (BIAS) {
-        const uint4 p = *reinterpret_cast<const uint4*>(bias + (c0 >> 1));
-        const uint32_t w[4] = {p.x, p.y, p.z, p.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) e[2 * j] = w[j] & 0xffffu, e[2 * j + 1] = w[j] >> 16;
-        plain = plain && (p.x | p.y | p.z | p.w) == 0;
-      }
-      const int64_t v = v0 + c0 - shift;  // the window's first column
-      if (whole(k)) {
-        uint32_t ok = 0xffu;
-        if (mask) {
-          const int sh = static_cast<int>(v & 31);
-          ok = static_cast<uint32_t>(mask[v >> 5]) >> sh;
-          if (sh > 32 - kWin) ok |= static_cast<uint32_t>(mask[(v >> 5) + 1]) << (32 - sh);
-          ok &= 0xffu;
-        }
-        plain = plain && ok == 0xffu;
-        if (a.in_place && plain) continue;  // nothing applies: not touched
-        if (a.in_place) raw[i] = load_raw(in_row + c0 - shift);
+  int slot = 0;
+  for (int k = threadIdx.x; k < windows; k += THREADS) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kRing<T> - 1) : "memory");
+    const int c0 = kWin * k;  // the window's first counter
+    const auto n4 = counts.window(c0);
+    uint2 e4 = make_uint2(0, 0);
+    if constexpr (BIAS) e4 = *reinterpret_cast<const uint2*>(bias + (c0 >> 1));
+    const bool some = any(n4) || (BIAS && any(e4));
+    uint32_t ok = 0xfu;  // which of the window's columns are allowed
+    if (a.allowed) {
+      // the first window may begin up to three columns before the block
+      const int bit = v0 + c0 - shift - 32 * first_word, w = max(bit, 0) >> 5;
+      ok = bit < 0 ? mask[0] << -bit : __funnelshift_r(mask[w], mask[w + 1], bit & 31);
+    }
+    if (k >= w_lo && k < w_hi) {
+      if (!(a.in_place && !some && (ok & 0xfu) == 0xfu)) {  // in place: not touched
         float l[kWin];
-        floats(raw[i], l);
-        if (!plain) {
+        floats(a.in_place ? load_raw(in_row + c0 - shift) : ring[slot * THREADS], l);
+        if (some) {
+          uint32_t n[kWin], e[kWin];
+          unpack(n4, n);
+          unpack(e4, e);
 #pragma unroll
-          for (int j = 0; j < kWin; ++j) l[j] = apply(l[j], n[j], e[j], ok >> j & 1);
+          for (int j = 0; j < kWin; ++j) l[j] = apply(l[j], n[j], e[j]);
         }
+#pragma unroll
+        for (int j = 0; j < kWin; ++j) l[j] = ok >> j & 1 ? l[j] : -INFINITY;
         store_window(out_row + c0 - shift, l);
-      } else {
+      }
+    } else {
+      uint32_t n[kWin], e[kWin];
+      unpack(n4, n);
+      unpack(e4, e);
 #pragma unroll
-        for (int j = 0; j < kWin; ++j) {
-          const int c = c0 - shift + j;
-          if (c < 0 || c >= cols) continue;
-          const bool ok = !mask || (mask[(v + j) >> 5] >> ((v + j) & 31) & 1);
-          store_f(out_row + c, apply(load_f(in_row + c), n[j], e[j], ok));
-        }
+      for (int j = 0; j < kWin; ++j) {
+        const int c = c0 - shift + j;
+        if (c < 0 || c >= cols) continue;
+        store_f(out_row + c, ok >> j & 1 ? apply(load_f(in_row + c), n[j], e[j]) : -INFINITY);
       }
     }
+    fetch(k + kRing<T> * THREADS, slot);
+    slot = slot + 1 == kRing<T> ? 0 : slot + 1;
   }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
 // Shared memory a block may take: two blocks an SM.
@@ -271,13 +283,13 @@ constexpr int kMaxSmem = 100 * 1024;
 
 template <class T, class O, bool WIDE, bool BIAS, int THREADS>
 cudaError_t launch_process(const void* logits, void* out, int64_t B, const ProcessArgs& a,
-                           int smem, cudaStream_t s) {
+                           int counters, cudaStream_t s) {
+  // (the shift's window: 16 columns of counters more, in steps of 8)
+  const int smem = 64 * THREADS + 4 * mask_words(a.cols) + (a.cols + 16) * counters;
   auto* k = process_kernel<T, O, WIDE, BIAS, THREADS>;
-  if (smem > 48 * 1024) {
-    const cudaError_t e =
-        cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
-    if (e != cudaSuccess) return e;
-  }
+  static SmemLimit limit;
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(k), kMaxSmem, &limit);
+  if (e != cudaSuccess) return e;
   const dim3 grid(static_cast<unsigned>((a.V + a.cols - 1) / a.cols), static_cast<unsigned>(B));
   k<<<grid, THREADS, smem, s>>>(static_cast<const T*>(logits), static_cast<O*>(out), a);
   note_launch();
@@ -289,29 +301,30 @@ cudaError_t run_process(const void* logits, void* out, int64_t B, ProcessArgs a,
                         cudaStream_t s) {
   const bool wide = a.L >= 32768, bias = a.n_bias > 0;
   const int per_col = (wide ? 4 : 2) + (bias ? 2 : 0);
-  // Columns a block: two blocks for every SM if the batch gives that, since
-  // every block of a row reads the row's history; at least 1024, and at most
-  // what shared memory holds (less the windows' shift).
-  const int64_t most = kMaxSmem / per_col - 2 * kWin;
-  int64_t cols = (B * a.V + 2 * sms - 1) / (2 * sms);
+  // Columns a block.  Every block of a row reads the row's history, so a block
+  // has four columns for each entry where the batch is large enough; but no
+  // fewer than 2 blocks an SM, no more than 8, at least 1024 columns, and at
+  // most what shared memory holds.
+  const int64_t ring = 512 * 64;  // kRing windows for each thread, at most
+  const int64_t most = (kMaxSmem - ring) * 8 / (8 * per_col + 1) - 128, all = B * a.V;
+  int64_t cols = std::max((all + 8 * sms - 1) / (8 * sms), 4 * a.L);
+  cols = std::min(cols, (all + 2 * sms - 1) / (2 * sms));
   cols = std::min(std::max<int64_t>(cols, 1024), most);
   const int64_t blocks = (a.V + cols - 1) / cols;
   cols = std::min(((a.V + blocks - 1) / blocks + 63) / 64 * 64, most / 64 * 64);
   a.cols = static_cast<int>(cols);
-  // one window more for the shift; in steps of 16 bytes
-  const int smem = static_cast<int>((cols + 2 * kWin) / kWin * kWin * per_col + 15) / 16 * 16;
   const bool small = cols <= 4096;
   if (wide && bias)
-    return small ? launch_process<T, O, true, true, 256>(logits, out, B, a, smem, s)
-                 : launch_process<T, O, true, true, 512>(logits, out, B, a, smem, s);
+    return small ? launch_process<T, O, true, true, 256>(logits, out, B, a, per_col, s)
+                 : launch_process<T, O, true, true, 512>(logits, out, B, a, per_col, s);
   if (wide)
-    return small ? launch_process<T, O, true, false, 256>(logits, out, B, a, smem, s)
-                 : launch_process<T, O, true, false, 512>(logits, out, B, a, smem, s);
+    return small ? launch_process<T, O, true, false, 256>(logits, out, B, a, per_col, s)
+                 : launch_process<T, O, true, false, 512>(logits, out, B, a, per_col, s);
   if (bias)
-    return small ? launch_process<T, O, false, true, 256>(logits, out, B, a, smem, s)
-                 : launch_process<T, O, false, true, 512>(logits, out, B, a, smem, s);
-  return small ? launch_process<T, O, false, false, 256>(logits, out, B, a, smem, s)
-               : launch_process<T, O, false, false, 512>(logits, out, B, a, smem, s);
+    return small ? launch_process<T, O, false, true, 256>(logits, out, B, a, per_col, s)
+                 : launch_process<T, O, false, true, 512>(logits, out, B, a, per_col, s);
+  return small ? launch_process<T, O, false, false, 256>(logits, out, B, a, per_col, s)
+               : launch_process<T, O, false, false, 512>(logits, out, B, a, per_col, s);
 }
 
 }  // namespace
