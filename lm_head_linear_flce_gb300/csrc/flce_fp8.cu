@@ -325,29 +325,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 }
 
 // ------------------------------------------------ few rows: B streamed
-// With at most 128 rows of A the product is bound by reading B once.  The roles
+// With at most 64 rows of A the product is bound by reading B once.  The roles
 // of the operands are swapped: 128 rows of B are the MMA's M, the rows of A
 // (padded to NP) its N, so nothing of the tensor cores' work is wasted on
-// padding to 128 rows of A.  Two CTAs per SM (one at NP = 128), whose rings keep
-// about 160 KB of B in flight: a tile's first loads and last stores overlap the
-// other CTA's stream, and 153 to 304 tiles run at once instead of in two rounds.  With fewer tiles of B than SMs, a cluster of `splits` CTAs shares a
-// tile, each taking a contiguous part of K; the parts are added in rank order
-// through distributed shared memory.
-constexpr int kRowThreads = 192;  // warp 0 TMA, warp 1 MMA, warps 2..5 epilogue
-
+// padding to 128 rows of A.  Two CTAs per SM, whose rings keep about 190 KB in
+// flight: a tile's first loads and last stores overlap the other CTA's stream,
+// and 153 to 304 tiles run at once instead of in two rounds.  With fewer tiles
+// of B than there is room for, a cluster of `splits` CTAs shares a tile, each
+// taking a contiguous part of K; the parts are added in rank order through
+// distributed shared memory.
+//
+// A column's scale differs from lane to lane here (it is a row of A), so each
+// block costs the epilogue a scale per element from shared memory; measured
+// with 151936 x 4096, that holds the HBM rate up to NP = 64 (104 us for 64 rows)
+// and not beyond (177 us at NP = 128, where the pair kernel takes 126).
 template <int NP>
 struct RowShape {
+  static constexpr int kThreads = 192;  // warp 0 TMA, warp 1 MMA, warps 2..5 epilogue
   static constexpr int kStageBytes = 128 * kKB + NP * kKB;
-  static constexpr int kPerSm = NP <= 64 ? 2 : 1;  // CTAs per SM
-  static constexpr int kStages = NP <= 16 ? 6 : NP <= 32 ? 5 : NP <= 64 ? 4 : 6;
+  static constexpr int kStages = NP <= 16 ? 6 : NP <= 32 ? 5 : 4;
   static constexpr int kAccs = 4;                     // accumulators of NP columns
-  static constexpr int kTmem = NP * kAccs < 32 ? 32 : NP * kAccs;
+  static constexpr int kTmem = NP * kAccs;
   static constexpr int kScaleBytes = 4 * 2 * NP * 4;  // two buffers per epilogue warp
   static constexpr int kSmem = kStages * kStageBytes + kScaleBytes + 1024 + 512;
 };
+constexpr int kRowsPerSm = 2;  // CTAs per SM
 
 template <int NP, class O>
-__global__ void __launch_bounds__(kRowThreads, RowShape<NP>::kPerSm)
+__global__ void __launch_bounds__(RowShape<NP>::kThreads, kRowsPerSm)
     flce_fp8_rows_kernel(const __grid_constant__ CUtensorMap ta,
                          const __grid_constant__ CUtensorMap tb, const Fp8Args a,
                          const int splits) {
@@ -357,22 +362,18 @@ __global__ void __launch_bounds__(kRowThreads, RowShape<NP>::kPerSm)
   const uint32_t base = (raw + 1023u) & ~1023u;  // stage i: B rows, then A rows
   const uint32_t scales = base + S::kStages * S::kStageBytes;
   const uint32_t full = scales + S::kScaleBytes;
-  const uint32_t empty = full + 8 * S::kStages;
-  const uint32_t tfull = empty + 8 * S::kStages;
-  const uint32_t tempty = tfull + 8 * S::kAccs;
+  const uint32_t done = full + 8 * S::kStages;
+  const uint32_t tempty = done + 8 * S::kStages;
   const uint32_t drain = tempty + 8 * S::kAccs;
   auto* slot = reinterpret_cast<uint32_t*>(smem_raw + (drain + 8 - raw));
   volatile uint32_t* abort_flag = slot + 1;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < S::kStages; ++i) {
-      mbar_init(full + 8 * i, 1);
-      mbar_init(empty + 8 * i, 1);
+      mbar_init(full + 8 * i, 1);  // the producer, for the stage's bytes
+      mbar_init(done + 8 * i, 1);  // the MMAs' commit: stage free, accumulator there
     }
-    for (int i = 0; i < S::kAccs; ++i) {
-      mbar_init(tfull + 8 * i, 1);
-      mbar_init(tempty + 8 * i, 4);
-    }
+    for (int i = 0; i < S::kAccs; ++i) mbar_init(tempty + 8 * i, 4);
     mbar_init(drain, 1);
     *abort_flag = 0u;
     fence_barrier_init();
@@ -403,7 +404,7 @@ __global__ void __launch_bounds__(kRowThreads, RowShape<NP>::kPerSm)
       const uint64_t keep = l2_policy_evict_last(), once = l2_policy_evict_first();
       for (int t = first; t < a.tiles_v && ok; t += step) {
         for (int j = j0; j < j1; ++j) {
-          ok = wait_parity(empty + 8 * pipe.idx, pipe.phase ^ 1u, w);
+          ok = wait_parity(done + 8 * pipe.idx, pipe.phase ^ 1u, w);
           if (!ok) break;
           const uint32_t bar = full + 8 * pipe.idx;
           const uint32_t sb = base + pipe.idx * S::kStageBytes;
@@ -417,63 +418,81 @@ __global__ void __launch_bounds__(kRowThreads, RowShape<NP>::kPerSm)
       drain_stages<S::kStages>(full, issued, pipe, w);
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      Ring pipe, acc;
-      for (int t = first; t < a.tiles_v && ok; t += step) {
-        for (int j = j0; j < j1; ++j) {
-          ok = wait_parity(tempty + 8 * acc.idx, acc.phase ^ 1u, w) &&
-               wait_parity(full + 8 * pipe.idx, pipe.phase, w);
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t sb = base + pipe.idx * S::kStageBytes;
-          mma_block<128, NP, false>(tmem + acc.idx * NP, smem_desc_sw128(sb, 0, 1024),
-                                    smem_desc_sw128(sb + 128 * kKB, 0, 1024));
-          mma_commit_single(empty + 8 * pipe.idx);
-          mma_commit_single(tfull + 8 * acc.idx);
-          pipe.advance(S::kStages);
-          acc.advance(S::kAccs);
+    // as in the pair kernel: the whole warp in the loop, one lane issuing, one
+    // commit a block
+    const uint64_t bd0 = smem_desc_sw128(base, 0, 1024);
+    const uint64_t ad0 = smem_desc_sw128(base + 128 * kKB, 0, 1024);
+    Ring pipe, acc;
+    for (int t = first; t < a.tiles_v && ok; t += step) {
+      for (int j = j0; j < j1; ++j) {
+        ok = wait_parity(full + 8 * pipe.idx, pipe.phase, w) &&
+             wait_parity(tempty + 8 * acc.idx, acc.phase ^ 1u, w);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one()) {
+          const uint64_t at = static_cast<uint64_t>(pipe.idx) * (S::kStageBytes / 16);
+          mma_block<128, NP, false>(tmem + acc.idx * NP, bd0 + at, ad0 + at);
+          mma_commit_single(done + 8 * pipe.idx);
         }
+        __syncwarp();
+        pipe.advance(S::kStages);
+        acc.advance(S::kAccs);
       }
+    }
+    if (elect_one()) {
       mma_commit_single(drain);
       WaitCtx wd = w;
       volatile uint32_t never = 0u;
       wd.abort = &never;
       wait_parity(drain, 0u, wd);
     }
+    __syncwarp();
   }
 
+  // Epilogue warps: TMEM lane quarter q, a row of B a thread.
   const int q = warp & 3;
   constexpr int kSa = (NP + 31) / 32;  // scales of A a lane fetches per block
   float r[NP];
   if (warp >= 2) {
-    auto* my_scales =
-        reinterpret_cast<float*>(smem_raw + (scales - raw)) + (warp - 2) * 2 * NP;
-    Ring acc;
+    auto* my_scales = reinterpret_cast<float*>(smem_raw + (scales - raw)) + (warp - 2) * 2 * NP;
+    Ring pipe, acc;
     // the last tile's result stays in registers when K is split (one tile each)
     for (int t = first; t < a.tiles_v && ok; t += step) {
       const int v = t * 128 + q * 32 + lane;
       const float* sb = a.b_scale + static_cast<int64_t>(t) * a.G;
 #pragma unroll
       for (int n = 0; n < NP; ++n) r[n] = 0.f;
-      float sa[kSa], sbj = 0.f;
-      auto fetch = [&](int j) {
-        sbj = sb[j];
+      // scales are fetched kAhead blocks before their use: a miss costs more than
+      // a block takes
+      constexpr int kAhead = 4;
+      float sa[kAhead][kSa], sbj[kAhead];
+      const auto fetch = [&](int slot, int j) {
+        j = min(j, j1 - 1);
+        sbj[slot] = sb[j];
 #pragma unroll
         for (int i = 0; i < kSa; ++i) {
           const int n = i * 32 + lane;
-          sa[i] = n < a.M ? a.a_scale[static_cast<int64_t>(n) * a.G + j] : 0.f;
+          sa[slot][i] = n < a.M ? a.a_scale[static_cast<int64_t>(n) * a.G + j] : 0.f;
         }
       };
-      if (j0 < j1) fetch(j0);
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) fetch(i, j0 + i);
       for (int j = j0; j < j1; ++j) {
-        // this block's scales into the warp's buffer, the next ones on their way
+        // this block's scales into the warp's buffer, the queue moves up
         float* s = my_scales + (j & 1) * NP;
 #pragma unroll
         for (int i = 0; i < kSa; ++i)
-          if (NP % 32 == 0 || i * 32 + lane < NP) s[i * 32 + lane] = sa[i] * sbj;
+          if (NP % 32 == 0 || i * 32 + lane < NP) s[i * 32 + lane] = sa[0][i] * sbj[0];
         __syncwarp();
-        if (j + 1 < j1) fetch(j + 1);
-        ok = wait_parity_inline(tfull + 8 * acc.idx, acc.phase, w);
+#pragma unroll
+        for (int k = 0; k + 1 < kAhead; ++k) {
+          sbj[k] = sbj[k + 1];
+#pragma unroll
+          for (int i = 0; i < kSa; ++i) sa[k][i] = sa[k + 1][i];
+        }
+        fetch(kAhead - 1, j + kAhead);
+        ok = wait_parity_inline(done + 8 * pipe.idx, pipe.phase, w);
         if (!ok) break;
         tc_fence_after();
         const uint32_t tbase = tmem + (static_cast<uint32_t>(q * 32) << 16) + acc.idx * NP;
@@ -494,7 +513,8 @@ __global__ void __launch_bounds__(kRowThreads, RowShape<NP>::kPerSm)
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(tempty + 8 * acc.idx);
+        if (lane == 0) mbar_arrive_remote(tempty + 8 * acc.idx);
+        pipe.advance(S::kStages);
         acc.advance(S::kAccs);
       }
       if (!ok) break;
@@ -549,6 +569,8 @@ __global__ void __launch_bounds__(kRowThreads, RowShape<NP>::kPerSm)
 }
 
 // ------------------------------------------------------------- launching
+constexpr int kFewRows = 64;  // rows of A up to which B is streamed past them
+
 template <class O>
 cudaError_t launch_pair(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& ty,
                         const Fp8Args& a, int sms, cudaStream_t s) {
@@ -573,12 +595,12 @@ cudaError_t launch_rows(const CUtensorMap& ta, const CUtensorMap& tb, const Fp8A
       allow_smem(reinterpret_cast<const void*>(k), RowShape<NP>::kSmem, &limit);
   if (e != cudaSuccess) return e;
   // As many parts of K as the device has room for, none empty.
-  const int room = RowShape<NP>::kPerSm * sms;
+  const int room = kRowsPerSm * sms;
   int splits = 1;
   while (splits < 8 && 2 * splits * a.tiles_v <= room && 2 * splits <= a.G) splits *= 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(splits > 1 ? splits * a.tiles_v : std::min(a.tiles_v, room));
-  cfg.blockDim = dim3(kRowThreads);
+  cfg.blockDim = dim3(RowShape<NP>::kThreads);
   cfg.dynamicSmemBytes = RowShape<NP>::kSmem;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -599,8 +621,7 @@ cudaError_t launch_rows_for(const CUtensorMap& ta, const CUtensorMap& tb, const 
                             int np, int sms, cudaStream_t s) {
   if (np == 16) return launch_rows<16, O>(ta, tb, a, sms, s);
   if (np == 32) return launch_rows<32, O>(ta, tb, a, sms, s);
-  if (np == 64) return launch_rows<64, O>(ta, tb, a, sms, s);
-  return launch_rows<128, O>(ta, tb, a, sms, s);
+  return launch_rows<64, O>(ta, tb, a, sms, s);
 }
 
 }  // namespace
@@ -650,8 +671,8 @@ extern "C" flce_status flce_matmul_fp8(const void* A, int64_t lda, const float* 
   CUtensorMap ta, tb;
   if (!make_tmap(&tb, B, K, V, ldb, kKB, 128, kU8)) return FLCE_ERR_CUDA;
   cudaError_t err;
-  if (M <= 128) {
-    const int np = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
+  if (M <= kFewRows) {
+    const int np = M <= 16 ? 16 : M <= 32 ? 32 : 64;
     a.tiles_v = static_cast<int>(gv);
     if (!make_tmap(&ta, A, K, M, lda, kKB, np, kU8)) return FLCE_ERR_CUDA;
     err = out_dtype == FLCE_BF16 ? launch_rows_for<__nv_bfloat16>(ta, tb, a, np, sms, s)
