@@ -14,6 +14,10 @@ namespace {
 
 constexpr int kNormThreads = 256;   // of the kernels for rows past kMaxHeld, and the quantiser
 constexpr int kMaxHeld = 16384;     // longest row held in registers (1024 threads x 16 values)
+constexpr int kBwdAhead = 2;        // rows the backward has in shared memory or on their way
+// the backward's threads on an SM: a thread of P = 4 float32 pieces holds 80 registers
+template <class T>
+constexpr int kBwdThreads = sizeof(T) == 4 ? 512 : 1024;
 constexpr int kDwRows = 64;         // rows per partial sum of dweight beyond that
 
 __device__ __forceinline__ float to_f(float v) { return v; }
@@ -107,6 +111,9 @@ struct Piece {
         w[i / 2] = i % 2 ? w[i / 2] | u << 16 : u;
       }
     }
+  }
+  __device__ __forceinline__ void set(const uint4& p) {
+    if constexpr (VEC) w[0] = p.x, w[1] = p.y, w[2] = p.z, w[3] = p.w;
   }
   __device__ __forceinline__ void floats(float (&v)[kE]) const {
 #pragma unroll
@@ -290,17 +297,29 @@ __global__ void __launch_bounds__(1024)
   }
 }
 
+__device__ __forceinline__ void copy_async16(void* dst, const void* src) {
+  const uint32_t d = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(src) : "memory");
+}
+
 // dx of a row and this block's share of dweight in one pass over dy, h (and
 // dh): a block walks rows blockIdx.x, + gridDim.x, ... with the weight and the
 // sums of its columns in registers, and leaves one partial sum per column.
-template <class T, bool VEC, int P, int THREADS>
-__global__ void __launch_bounds__(THREADS)
+//
+// AHEAD: the rows' pieces come through shared memory, kBwdAhead rows at a time,
+// each thread's own in slots that only it touches: the rows in flight cost no
+// registers, and a row is read there twice (sum, then dx) instead of being held
+// over the sum.  Without it (rows not aligned to 16 bytes, or too long for the
+// slots) a row is loaded when its turn comes.
+template <class T, bool VEC, int P, int THREADS, bool AHEAD>
+__global__ void __launch_bounds__(THREADS, AHEAD && THREADS <= 512 ? kBwdThreads<T> / THREADS : 1)
     norm_bwd_held_kernel(const T* __restrict__ dy, const T* __restrict__ dh,
                          const T* __restrict__ h, int64_t ldh, const void* __restrict__ weight,
-                         int w_f32, bool aligned, const float* __restrict__ rstd, int64_t N,
-                         int H, T* __restrict__ dx, float* __restrict__ dw_part) {
+                         int w_f32, bool aligned, const float* __restrict__ rstd, int64_t N, int H,
+                         T* __restrict__ dx, float* __restrict__ dw_part) {
   using S = Slots<T, VEC>;
   __shared__ float part[64];
+  extern __shared__ __align__(16) uint4 ring[];  // [kBwdAhead][3][P][threads of the block]
   const int64_t first = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
   const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.y;
   float w[P][S::kE], dw[P][S::kE];
@@ -311,62 +330,85 @@ __global__ void __launch_bounds__(THREADS)
     for (int i = 0; i < S::kE; ++i) dw[s][i] = 0.f;
   }
   const float inv_h = 1.f / static_cast<float>(H);
-  int phase = 0;
-  // the next row's values are on their way while a row is summed and written
-  // (where the registers allow: with 1024 threads a row is fetched when its turn
-  // comes)
-  constexpr bool kAhead = THREADS <= 512;
-  Piece<T, VEC> ny[P], nh[P], ne[P];
-  float nr = 0.f;
-  const auto fetch = [&](int64_t row) {
-    if (row >= N) return;
-    nr = rstd[row];
-#pragma unroll
-    for (int s = 0; s < P; ++s) {
-      const int c = S::first(s);
-      ny[s].load(dy + row * H, c, H, aligned);
-      nh[s].load(h + row * ldh, c, H, aligned);
-      if (dh && dx) ne[s].load(dh + row * H, c, H, aligned);
-    }
+  const bool with_dh = dh && dx;
+  const int threads = blockDim.x * blockDim.y, tid = threadIdx.y * blockDim.x + threadIdx.x;
+  const auto slot = [&](int stage, int array, int s) {
+    return ring + ((stage * 3 + array) * P + s) * threads + tid;
   };
-  if (kAhead) fetch(first);
-  for (int64_t row = first; row < N; row += step, phase ^= 1) {
-    if (!kAhead) fetch(row);
-    float g[P][S::kE], v[P][S::kE];
-    Piece<T, VEC> e[P];
-    const float r = nr;
+  const auto fetch = [&](int64_t row, int stage) {
+    if (row < N) {
 #pragma unroll
-    for (int s = 0; s < P; ++s) {
-      ny[s].floats(g[s]);
-      nh[s].floats(v[s]);
-      e[s] = ne[s];
+      for (int s = 0; s < P; ++s) {
+        const int c = S::first(s);
+        if (c >= H) continue;  // (stays zero)
+        copy_async16(slot(stage, 0, s), dy + row * H + c);
+        copy_async16(slot(stage, 1, s), h + row * ldh + c);
+        if (with_dh) copy_async16(slot(stage, 2, s), dh + row * H + c);
+      }
     }
-    if (kAhead) fetch(row + step);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  if constexpr (AHEAD) {
+    for (int i = 0; i < kBwdAhead * 3 * P; ++i) ring[i * threads + tid] = make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int i = 0; i < kBwdAhead; ++i) fetch(first + i * step, i);
+  }
+  int stage = 0, phase = 0;
+  for (int64_t row = first; row < N; row += step, phase ^= 1) {
+    const float r = rstd[row];
+    Piece<T, VEC> held[3][P];  // without AHEAD
+    const auto piece = [&](int array, int s) {
+      Piece<T, VEC> p = held[array][s];
+      if constexpr (AHEAD) p.set(*slot(stage, array, s));
+      return p;
+    };
+    if constexpr (AHEAD) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(kBwdAhead - 1) : "memory");
+    } else {
+#pragma unroll
+      for (int s = 0; s < P; ++s) {
+        const int c = S::first(s);
+        held[0][s].load(dy + row * H, c, H, aligned);
+        held[1][s].load(h + row * ldh, c, H, aligned);
+        if (with_dh) held[2][s].load(dh + row * H, c, H, aligned);
+      }
+    }
     float dot = 0.f;
 #pragma unroll
-    for (int s = 0; s < P; ++s)
+    for (int s = 0; s < P; ++s) {
+      float d[S::kE], v[S::kE];
+      piece(0, s).floats(d);
+      piece(1, s).floats(v);
 #pragma unroll
       for (int i = 0; i < S::kE; ++i) {
-        const float d = g[s][i];
-        dw[s][i] = fmaf(d * v[s][i], r, dw[s][i]);
-        g[s][i] = d * w[s][i];
-        dot = fmaf(g[s][i], v[s][i], dot);
+        const float t = d[i] * v[i];
+        dw[s][i] = fmaf(t, r, dw[s][i]);
+        dot = fmaf(t, w[s][i], dot);
       }
-    if (!dx) continue;
-    const float k = r * r * (row_sum(dot, part, phase) * inv_h);
+    }
+    if (dx) {
+      const float k = r * r * (row_sum(dot, part, phase) * inv_h);
 #pragma unroll
-    for (int s = 0; s < P; ++s) {
+      for (int s = 0; s < P; ++s) {
+        float d[S::kE], v[S::kE];
+        piece(0, s).floats(d);
+        piece(1, s).floats(v);
 #pragma unroll
-      for (int i = 0; i < S::kE; ++i) g[s][i] = r * (g[s][i] - v[s][i] * k);
-      if (dh) {
-        float t[S::kE];
-        e[s].floats(t);
+        for (int i = 0; i < S::kE; ++i) d[i] = r * (d[i] * w[s][i] - v[i] * k);
+        if (with_dh) {
+          piece(2, s).floats(v);
 #pragma unroll
-        for (int i = 0; i < S::kE; ++i) g[s][i] += t[i];
+          for (int i = 0; i < S::kE; ++i) d[i] += v[i];
+        }
+        store_slot<T, VEC>(dx + row * H, S::first(s), H, aligned, d);
       }
-      store_slot<T, VEC>(dx + row * H, S::first(s), H, aligned, g[s]);
+    }
+    if constexpr (AHEAD) {
+      fetch(row + kBwdAhead * step, stage);
+      stage = stage + 1 == kBwdAhead ? 0 : stage + 1;
     }
   }
+  if constexpr (AHEAD) asm volatile("cp.async.wait_group 0;" ::: "memory");
   if (!dw_part) return;
 #pragma unroll
   for (int s = 0; s < P; ++s) {
@@ -670,18 +712,30 @@ RowPlan plan_rows(int64_t N, int64_t H, int elems, bool vec) {
   return {static_cast<int>(threads), slots, threads == 32 && !few ? 8 : 1};
 }
 
+// The backward's threads a row: up to 256 before a thread takes more slots.
+RowPlan plan_bwd(int64_t N, int64_t H, int elems, bool vec) {
+  RowPlan p = plan_rows(N, H, elems, vec);
+  while (p.slots > 1 && p.rows == 1 && p.threads <= 128) {
+    p.slots /= 2;
+    p.threads *= 2;
+  }
+  return p;
+}
+
 // Partial sums of dweight: a block's rows at a time.  A fixed number, so that
-// the order of additions depends on the sizes alone: four blocks of up to 256
-// threads, two of 512 or one larger on each of 152 SMs.
-int64_t held_parts(int64_t N, const RowPlan& p) {
-  const int64_t blocks = p.threads <= 256 ? 608 : p.threads <= 512 ? 304 : 152;
+// the order of additions depends on the sizes and the type alone: the blocks
+// that 152 SMs hold at once.
+int64_t held_parts(int64_t N, const RowPlan& p, size_t elem_bytes) {
+  const int64_t threads = p.threads * p.rows;
+  const int64_t blocks = 152 * std::max<int64_t>((elem_bytes == 4 ? 512 : 1024) /
+                                                     (threads <= 256 ? 256 : threads <= 512 ? 512 : 1024), 1);
   return std::min<int64_t>((N + p.rows - 1) / p.rows, blocks) * p.rows;
 }
 int64_t dw_parts(int64_t N, int64_t H) {
   if (H > kMaxHeld) return (N + kDwRows - 1) / kDwRows;
-  // whichever plan the call's types and alignment lead to
-  return std::max({held_parts(N, plan_rows(N, H, 8, true)), held_parts(N, plan_rows(N, H, 4, true)),
-                   held_parts(N, plan_rows(N, H, 4, false))});
+  // whichever plan the call's types lead to
+  return std::max({held_parts(N, plan_bwd(N, H, 8, true), 2), held_parts(N, plan_bwd(N, H, 4, true), 4),
+                   held_parts(N, plan_bwd(N, H, 4, false), 2)});
 }
 
 struct FwdArgs {
@@ -764,15 +818,30 @@ struct BwdArgsN {
 };
 
 template <class T, bool VEC, int P>
-void launch_bwd_held(const RowPlan& p, bool aligned, int64_t parts, const BwdArgsN& a,
-                     cudaStream_t s) {
-  auto* k = p.threads * p.rows <= 256   ? norm_bwd_held_kernel<T, VEC, P, 256>
-            : p.threads * p.rows <= 512 ? norm_bwd_held_kernel<T, VEC, P, 512>
-                                        : norm_bwd_held_kernel<T, VEC, P, 1024>;
-  k<<<static_cast<unsigned>(parts / p.rows), dim3(p.threads, p.rows), 0, s>>>(
-      static_cast<const T*>(a.dy), static_cast<const T*>(a.dh), static_cast<const T*>(a.h), a.ldh,
-      a.weight, a.w_f32, aligned, a.rstd, a.N, a.H, static_cast<T*>(a.dx),
-      a.dweight ? a.part : nullptr);
+cudaError_t launch_bwd_held(const RowPlan& p, bool aligned, int64_t parts,
+                            const BwdArgsN& a, cudaStream_t s) {
+  constexpr int kMost = 200 * 1024;
+  const int threads = p.threads * p.rows, ring = kBwdAhead * 3 * P * threads * 16;
+  const auto launch = [&](auto* k, int smem) {
+    k<<<static_cast<unsigned>(parts / p.rows), dim3(p.threads, p.rows), smem, s>>>(
+        static_cast<const T*>(a.dy), static_cast<const T*>(a.dh), static_cast<const T*>(a.h),
+        a.ldh, a.weight, a.w_f32, aligned, a.rstd, a.N, a.H, static_cast<T*>(a.dx),
+        a.dweight ? a.part : nullptr);
+    return cudaGetLastError();
+  };
+  if constexpr (VEC) {
+    if (aligned && ring <= kMost) {
+      auto* k = threads <= 256   ? norm_bwd_held_kernel<T, VEC, P, 256, true>
+                : threads <= 512 ? norm_bwd_held_kernel<T, VEC, P, 512, true>
+                                 : norm_bwd_held_kernel<T, VEC, P, 1024, true>;
+      static SmemLimit limits[3];  // one for each of them
+      const cudaError_t e = allow_smem(reinterpret_cast<const void*>(k), kMost,
+                                       &limits[threads <= 256 ? 0 : threads <= 512 ? 1 : 2]);
+      return e != cudaSuccess ? e : launch(k, ring);
+    }
+  }
+  return threads <= 512 ? launch(norm_bwd_held_kernel<T, VEC, P, 512, false>, 0)
+                        : launch(norm_bwd_held_kernel<T, VEC, P, 1024, false>, 0);
 }
 
 template <class T>
@@ -804,17 +873,19 @@ cudaError_t run_norm_bwd(const BwdArgsN& a, cudaStream_t s) {
     const bool vec = a.H % kE == 0;
     const bool al = a.ldh % kE == 0 && aligned_to(a.dy, 16) && aligned_to(a.dh, 16) &&
                     aligned_to(a.h, 16) && aligned_to(a.weight, 16) && aligned_to(a.dx, 16);
-    const RowPlan p = plan_rows(a.N, a.H, vec ? kE : 4, vec);
-    parts = held_parts(a.N, p);
+    const RowPlan p = plan_bwd(a.N, a.H, vec ? kE : 4, vec);
+    parts = held_parts(a.N, p, sizeof(T));
+    cudaError_t e = cudaSuccess;
     if (vec) {
-      if (p.slots == 1) launch_bwd_held<T, true, 1>(p, al, parts, a, s);
-      else if (p.slots == 2) launch_bwd_held<T, true, 2>(p, al, parts, a, s);
-      else if constexpr (kE == 4) launch_bwd_held<T, true, 4>(p, al, parts, a, s);
+      if (p.slots == 1) e = launch_bwd_held<T, true, 1>(p, al, parts, a, s);
+      else if (p.slots == 2) e = launch_bwd_held<T, true, 2>(p, al, parts, a, s);
+      else if constexpr (kE == 4) e = launch_bwd_held<T, true, 4>(p, al, parts, a, s);
     } else {
-      if (p.slots == 1) launch_bwd_held<T, false, 1>(p, al, parts, a, s);
-      else if (p.slots == 2) launch_bwd_held<T, false, 2>(p, al, parts, a, s);
-      else launch_bwd_held<T, false, 4>(p, al, parts, a, s);
+      if (p.slots == 1) e = launch_bwd_held<T, false, 1>(p, al, parts, a, s);
+      else if (p.slots == 2) e = launch_bwd_held<T, false, 2>(p, al, parts, a, s);
+      else e = launch_bwd_held<T, false, 4>(p, al, parts, a, s);
     }
+    if (e != cudaSuccess) return e;
     note_launch();
   }
   if (a.dweight) {
