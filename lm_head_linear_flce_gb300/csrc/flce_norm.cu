@@ -597,9 +597,9 @@ __global__ void __launch_bounds__(kNormThreads)
   using S = Slots<T, VEC>;
   constexpr int kPer = kNormThreads / S::kLanes;  // groups per thread block
   const int groups = (K + kScaleGroup - 1) / kScaleGroup;
-  const int64_t u = static_cast<int64_t>(blockIdx.x) * kPer + threadIdx.x / S::kLanes;
-  const int64_t row = u / groups;
-  const int g = static_cast<int>(u % groups);
+  const uint32_t u = blockIdx.x * kPer + threadIdx.x / S::kLanes;  // (the host bounds their number)
+  const int64_t row = u / static_cast<uint32_t>(groups);
+  const int g = static_cast<int>(u % static_cast<uint32_t>(groups));
   const int l = threadIdx.x % S::kLanes;
   // a group past the last row takes part in the shuffles with zeros
   const int c = row < R ? g * kScaleGroup + (VEC ? l * S::kE : l) : K;

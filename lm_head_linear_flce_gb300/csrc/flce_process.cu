@@ -42,9 +42,18 @@ __device__ __forceinline__ int64_t id_at(const void* p, int is64, int64_t i) {
 // so that they arrive under it.
 //
 // A column's counter is its number of generated occurrences, and a top bit for
-// "in the prompt": 16 bits where the history is shorter than 2^15 (half the
-// shared memory, so twice the columns a block), else 32.  With biases, 16 more
-// bits hold 1 + the largest index of the column's entries.
+// "in the prompt".  16 bits do for a history of up to 2^15 (half the shared
+// memory, so twice the columns a block): with a prompt at least one token is not
+// generated and the count stays below the bit, without one no bit is set and all
+// sixteen are the count.  Longer histories take 32.
+//
+// Biases: up to kBiasList entries a row, a block lists those of its columns and
+// applies them after its windows, from the logit read beforehand; the list costs
+// no shared memory per column.  More entries go by an index per column, 1 + the
+// largest of the column's entries.
+constexpr int kNoBias = 0, kListedBias = 1, kIndexedBias = 2;
+constexpr int kBiasList = 512;
+
 constexpr int kWin = 4;  // consecutive columns a thread takes at a time: neighbouring lanes
                          // then read and write whole lines in either type
 
@@ -57,6 +66,9 @@ struct Counts {
     uint32_t* w = words + (WIDE ? c : c >> 1);
     if (prompt) atomicOr(w, kPrompt << sh);
     else atomicAdd(w, 1u << sh);
+  }
+  __device__ uint32_t at(int c) const {
+    return WIDE ? words[c] : words[c >> 1] >> 16 * (c & 1) & 0xffffu;
   }
   // The window's counters, at c (a multiple of kWin).
   using Packed = typename std::conditional<WIDE, uint4, uint2>::type;
@@ -117,7 +129,7 @@ __device__ __forceinline__ void copy_async(void* dst, const void* src) {
 // word behind a window's first, in steps of 16 bytes.
 __host__ __device__ constexpr int mask_words(int cols) { return (cols / 32 + 3 + 3) / 4 * 4; }
 
-template <class T, class O, bool WIDE, bool BIAS, int THREADS>
+template <class T, class O, bool WIDE, int BIAS, int THREADS>
 __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
     process_kernel(const T* logits, O* out, const ProcessArgs a) {
   extern __shared__ __align__(16) uint32_t smem[];
@@ -146,15 +158,18 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
   const float freq = a.frequency ? a.frequency[b] : 0.f;
   const float pres = a.presence ? a.presence[b] : 0.f;
 
-  // Shared memory: the ring, the block's mask words, counters, bias indices
-  // (the latter two one per window column).
+  // Shared memory: the ring, the block's bias list, its mask words, counters,
+  // bias indices (the last two one per window column).
   using Raw = decltype(load_raw(in_row));
   Raw* ring = reinterpret_cast<Raw*>(smem) + threadIdx.x;  // this thread's slots, THREADS apart
-  uint32_t* mask = smem + kRing<T> * THREADS * sizeof(Raw) / 4;
+  uint32_t* listed = smem + kRing<T> * THREADS * sizeof(Raw) / 4;  // column << 16 | entry
+  auto* before = reinterpret_cast<float*>(listed + kBiasList);      // its logit
+  __shared__ int n_listed;
+  uint32_t* mask = listed + (BIAS == kListedBias ? 2 * kBiasList : 0);
   const int slots = (windows * kWin + 7) / 8 * 8;
   Counts<WIDE> counts{mask + mask_words(a.cols)};
   uint32_t* bias = counts.words + (WIDE ? slots : slots / 2);
-  const int words = (WIDE ? slots : slots / 2) + (BIAS ? slots / 2 : 0);
+  const int words = (WIDE ? slots : slots / 2) + (BIAS == kIndexedBias ? slots / 2 : 0);
   // The thread's window k (if it is whole) into the ring; one group per window.
   const auto fetch = [&](int k, int slot) {
     if (k >= w_lo && k < w_hi && !a.in_place)
@@ -174,6 +189,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
   }
   for (int i = threadIdx.x; i < words / 4; i += THREADS)
     reinterpret_cast<uint4*>(counts.words)[i] = make_uint4(0, 0, 0, 0);
+  if (threadIdx.x == 0) n_listed = 0;
   __syncthreads();
   const int64_t len = max(int64_t{0}, min(len0, a.L));
   constexpr int kIds = 8;
@@ -204,10 +220,16 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
     for (int u = 0; u < kIds; ++u)
       if (now[u] >= 0 && now[u] < cols) counts.add(now[u] + shift, i0 + u * THREADS < prompt);
   }
-  if constexpr (BIAS) {
+  if constexpr (BIAS != kNoBias) {
     for (int i = threadIdx.x; i < a.n_bias; i += THREADS) {
       const int64_t v = id_at(a.bias_ids, a.bias_int64, b * a.n_bias + i);
       if (v < v0 || v - v0 >= cols) continue;
+      if constexpr (BIAS == kListedBias) {
+        const int at = atomicAdd(&n_listed, 1), c = static_cast<int>(v - v0);
+        listed[at] = static_cast<uint32_t>(c) << 16 | static_cast<uint32_t>(i);
+        before[at] = load_f(in_row + c);
+        continue;
+      }
       // the largest index stays, in whatever order the threads come
       const int c = static_cast<int>(v - v0) + shift, sh = 16 * (c & 1);
       uint32_t* w = bias + (c >> 1);
@@ -223,13 +245,14 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
   __syncthreads();
 
   // One column with its counter n and bias entry e (0: none).
+  const uint32_t count_bits = WIDE || prompt > 0 ? ~Counts<WIDE>::kPrompt : ~0u;
   const auto apply = [&](float l, uint32_t n, uint32_t e) {
     if (n) {
       l = l > 0.f ? l / rep : l * rep;
-      const uint32_t c = n & ~Counts<WIDE>::kPrompt;
+      const uint32_t c = n & count_bits;
       l -= freq * static_cast<float>(c) + (c ? pres : 0.f);
     }
-    if (BIAS && e) l += a.bias_values[b * a.n_bias + e - 1];
+    if (BIAS != kNoBias && e) l += a.bias_values[b * a.n_bias + e - 1];
     return l;
   };
   int slot = 0;
@@ -238,8 +261,8 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
     const int c0 = kWin * k;  // the window's first counter
     const auto n4 = counts.window(c0);
     uint2 e4 = make_uint2(0, 0);
-    if constexpr (BIAS) e4 = *reinterpret_cast<const uint2*>(bias + (c0 >> 1));
-    const bool some = any(n4) || (BIAS && any(e4));
+    if constexpr (BIAS == kIndexedBias) e4 = *reinterpret_cast<const uint2*>(bias + (c0 >> 1));
+    const bool some = any(n4) || (BIAS == kIndexedBias && any(e4));
     uint32_t ok = 0xfu;  // which of the window's columns are allowed
     if (a.allowed) {
       // the first window may begin up to three columns before the block
@@ -276,16 +299,31 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
     slot = slot + 1 == kRing<T> ? 0 : slot + 1;
   }
   asm volatile("cp.async.wait_group 0;" ::: "memory");
+  if constexpr (BIAS == kListedBias) {
+    __syncthreads();  // the block's windows are written
+    for (int i = threadIdx.x; i < n_listed; i += THREADS) {
+      const uint32_t mine = listed[i];
+      bool last = true;  // of the entries with this column
+      for (int k = 0; k < n_listed; ++k)
+        last = last && !(listed[k] > mine && listed[k] >> 16 == mine >> 16);
+      if (!last) continue;
+      const int c = static_cast<int>(mine >> 16), bit = v0 + c - 32 * first_word;
+      const bool ok = !a.allowed || (mask[bit >> 5] >> (bit & 31) & 1);
+      const float l = apply(before[i], counts.at(c + shift), (mine & 0xffffu) + 1);
+      store_f(out_row + c, ok ? l : -INFINITY);
+    }
+  }
 }
 
 // Shared memory a block may take: two blocks an SM.
-constexpr int kMaxSmem = 100 * 1024;
+constexpr int kMaxSmem = 113 * 1024;
 
-template <class T, class O, bool WIDE, bool BIAS, int THREADS>
+template <class T, class O, bool WIDE, int BIAS, int THREADS>
 cudaError_t launch_process(const void* logits, void* out, int64_t B, const ProcessArgs& a,
                            int counters, cudaStream_t s) {
   // (the shift's window: 16 columns of counters more, in steps of 8)
-  const int smem = 64 * THREADS + 4 * mask_words(a.cols) + (a.cols + 16) * counters;
+  const int smem = 64 * THREADS + (BIAS == kListedBias ? 8 * kBiasList : 0) +
+                   4 * mask_words(a.cols) + (a.cols + 16) * counters;
   auto* k = process_kernel<T, O, WIDE, BIAS, THREADS>;
   static SmemLimit limit;
   const cudaError_t e = allow_smem(reinterpret_cast<const void*>(k), kMaxSmem, &limit);
@@ -299,32 +337,32 @@ cudaError_t launch_process(const void* logits, void* out, int64_t B, const Proce
 template <class T, class O>
 cudaError_t run_process(const void* logits, void* out, int64_t B, ProcessArgs a, int sms,
                         cudaStream_t s) {
-  const bool wide = a.L >= 32768, bias = a.n_bias > 0;
-  const int per_col = (wide ? 4 : 2) + (bias ? 2 : 0);
-  // Columns a block.  Every block of a row reads the row's history, so a block
-  // has four columns for each entry where the batch is large enough; but no
-  // fewer than 2 blocks an SM, no more than 8, at least 1024 columns, and at
-  // most what shared memory holds.
-  const int64_t ring = 512 * 64;  // kRing windows for each thread, at most
-  const int64_t most = (kMaxSmem - ring) * 8 / (8 * per_col + 1) - 128, all = B * a.V;
-  int64_t cols = std::max((all + 8 * sms - 1) / (8 * sms), 4 * a.L);
-  cols = std::min(cols, (all + 2 * sms - 1) / (2 * sms));
-  cols = std::min(std::max<int64_t>(cols, 1024), most);
-  const int64_t blocks = (a.V + cols - 1) / cols;
-  cols = std::min(((a.V + blocks - 1) / blocks + 63) / 64 * 64, most / 64 * 64);
-  a.cols = static_cast<int>(cols);
-  const bool small = cols <= 4096;
-  if (wide && bias)
-    return small ? launch_process<T, O, true, true, 256>(logits, out, B, a, per_col, s)
-                 : launch_process<T, O, true, true, 512>(logits, out, B, a, per_col, s);
-  if (wide)
-    return small ? launch_process<T, O, true, false, 256>(logits, out, B, a, per_col, s)
-                 : launch_process<T, O, true, false, 512>(logits, out, B, a, per_col, s);
-  if (bias)
-    return small ? launch_process<T, O, false, true, 256>(logits, out, B, a, per_col, s)
-                 : launch_process<T, O, false, true, 512>(logits, out, B, a, per_col, s);
-  return small ? launch_process<T, O, false, false, 256>(logits, out, B, a, per_col, s)
-               : launch_process<T, O, false, false, 512>(logits, out, B, a, per_col, s);
+  const bool wide = a.L > 32768;
+  const int bias = a.n_bias == 0 ? kNoBias : a.n_bias <= kBiasList ? kListedBias : kIndexedBias;
+  const int per_col = (wide ? 4 : 2) + (bias == kIndexedBias ? 2 : 0);
+  // Blocks a row.  Every one reads the row's history, so there are only as many
+  // as give a block four columns for each entry, and no more than 8 an SM (of at
+  // least 1024 columns); but as many as fill the SMs, two each, and as shared
+  // memory asks for.
+  const int64_t fixed = 512 * 64 + 8 * kBiasList + 1024;  // ring, list, rounding
+  const int64_t most = (kMaxSmem - fixed) * 8 / (8 * per_col + 1) / 64 * 64, all = B * a.V;
+  const auto blocks_of = [&](int64_t cols) { return (a.V + cols - 1) / cols; };
+  const int64_t wanted = std::max<int64_t>({(all + 8 * sms - 1) / (8 * sms), 4 * a.L, 1024});
+  const int64_t fill = std::min(std::max<int64_t>(2 * sms / B, 1), blocks_of(1024));
+  const int64_t blocks = std::max({blocks_of(wanted), fill, blocks_of(most)});
+  a.cols = static_cast<int>(std::min((blocks_of(blocks) + 63) / 64 * 64, most));
+  const auto launch = [&](auto w, auto bm) {
+    constexpr bool kW = decltype(w)::value;
+    constexpr int kB = decltype(bm)::value;
+    return a.cols <= 4096 ? launch_process<T, O, kW, kB, 256>(logits, out, B, a, per_col, s)
+                          : launch_process<T, O, kW, kB, 512>(logits, out, B, a, per_col, s);
+  };
+  const auto by_bias = [&](auto w) {
+    return bias == kNoBias       ? launch(w, std::integral_constant<int, kNoBias>{})
+           : bias == kListedBias ? launch(w, std::integral_constant<int, kListedBias>{})
+                                 : launch(w, std::integral_constant<int, kIndexedBias>{});
+  };
+  return wide ? by_bias(std::true_type{}) : by_bias(std::false_type{});
 }
 
 }  // namespace
