@@ -147,3 +147,14 @@ def test_python_layer_refuses_wrong_tensors():
         with pytest.raises(ValueError, match="CUDA tensor"):
             call()
     assert ctypes.sizeof(ctypes.c_void_p) == 8
+
+
+def test_calls_raise_without_the_native_module(monkeypatch, tmp_path):
+    monkeypatch.setattr(flce, "library_path", str(tmp_path / "libflce.so"))
+    monkeypatch.setattr(head_ops, "_module", None)
+    x, w = torch.zeros(2, 64, dtype=torch.bfloat16), torch.ones(64)
+    for call in (lambda: flce.rms_norm(x, w), lambda: flce.rms_norm_fp8(x, w),
+                 lambda: flce.quantize_fp8(x), lambda: flce.process_logits(x),
+                 lambda: flce.matmul_fp8(x, w, x, w)):
+        with pytest.raises(RuntimeError, match="no fallback"):
+            call()
