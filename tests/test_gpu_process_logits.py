@@ -162,6 +162,71 @@ def test_non_finite_logits_and_empty_rows():
     assert e.shape == (0, 64)
 
 
+def fast_oracle(z, k):
+    """The definition, vectorised over a row (checked against the entry by entry
+    one below): for batches of millions of columns."""
+    out = z.double().numpy().copy()
+    B, V = out.shape
+    for b in range(B):
+        tok = k["tokens"][b, :int(k["lengths"][b])].numpy().astype(np.int64)
+        ok = (tok >= 0) & (tok < V)
+        gen = ok & (np.arange(len(tok)) >= int(k["prompt_lengths"][b]))
+        seen = np.unique(tok[ok])
+        r = float(k["repetition_penalty"][b])
+        out[b, seen] = np.where(out[b, seen] > 0, out[b, seen] / r, out[b, seen] * r)
+        ids, times = np.unique(tok[gen], return_counts=True)
+        out[b, ids] -= float(k["frequency_penalty"][b]) * times + float(k["presence_penalty"][b])
+        if k.get("bias_ids") is not None:
+            last = {int(v): i for i, v in enumerate(k["bias_ids"][b].tolist()) if 0 <= v < V}
+            for v, i in last.items():
+                out[b, v] += float(k["bias_values"][b, i])
+        if k.get("allowed") is not None:
+            w = k["allowed"][b].numpy().astype("<i4").view(np.uint8)
+            out[b, np.unpackbits(w, bitorder="little")[:V] == 0] = -np.inf
+    return out
+
+
+def test_fast_oracle_is_the_definition():
+    z, k = case(5, 3001, 200, 7, BF, seed=11)
+    a, b = oracle(z, k), fast_oracle(z, k)
+    assert np.array_equal(np.isfinite(a), np.isfinite(b))
+    fin = np.isfinite(a)
+    assert np.allclose(a[fin], b[fin], rtol=1e-14, atol=1e-14)
+
+
+@pytest.mark.parametrize("dt,odt", [(BF, F32), (F32, F32), (BF, BF), (F32, BF)])
+@pytest.mark.parametrize("B,V,L,nb,mask", [(30, 152064, 300, 300, True), (33, 128255, 3000, 0, True),
+                                           (70, 60001, 20, 5, False), (9, 500000, 33000, 20, True),
+                                           (40, 110000, 700, 600, True), (500, 8500, 32768, 3, True),
+                                           (32, 131072, 0, 0, True), (5, 1000003, 100, 1, False)])
+def test_large_batches(B, V, L, nb, mask, dt, odt):
+    """Millions of columns: aligned and unaligned rows, histories around 2^15,
+    more biases than a list holds, in place too where the types allow."""
+    z, k = case(B, V, L, nb, dt, torch.int64 if nb % 2 else torch.int32, seed=B)
+    if not mask:
+        k["allowed"] = None
+    want = fast_oracle(z, k)
+    kk = {n: None if t is None else t.cuda() for n, t in k.items()}
+    zz = z.cuda()
+    got = flce.process_logits(zz, out_dtype=odt, **kk)
+    size = np.abs(z.double().numpy()).max() * 2 + L * 2 + 40
+    g = got.double().cpu().numpy()
+    fin = np.isfinite(want)
+    assert np.array_equal(fin, np.isfinite(g))
+    tol = 5 * 2.0 ** -24 * size + (1.01 * 2.0 ** -8 * np.abs(want[fin]) if odt == BF else 0)
+    assert (np.abs(g[fin] - want[fin]) <= tol).all()
+    if dt == odt:
+        assert flce.process_logits(zz, out=zz, **kk) is zz
+        assert torch.equal(zz, got)
+        wide = torch.full((B, V + 7), 3.0, dtype=dt, device="cuda")
+        wide[:, 2:V + 2] = z.cuda()
+        view = wide[:, 2:V + 2]
+        flce.process_logits(view, out=view, **kk)
+        assert torch.equal(view, got)
+        assert (wide[:, :2] == 3).all() and (wide[:, V + 2:] == 3).all()
+    del kk, zz, got
+
+
 def test_side_stream_and_graph():
     z, k = case(4, 40000, 3000, 5, BF, seed=4)
     want = run(z, k)
