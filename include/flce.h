@@ -468,7 +468,10 @@ flce_status flce_quantize_fp8(const void* x, int64_t ldx, int64_t R, int64_t K, 
  *   y        device [M][V] of out_dtype, rows ldy elements apart.
  * A block's products are summed in FP32 by the tensor cores, the scaled blocks
  * in FP32, and the sum is rounded once.  K, lda and ldb are multiples of 16, A
- * and B 16-byte aligned; K <= 65536.
+ * and B 16-byte aligned; K <= 65536.  The tensor cores lose at most about 2^-16
+ * of a block's sum of |products| (measured on random operands: 1e-7 of the
+ * result).  As in flce_logits, a wait that runs out (flce_set_wait_limit_ns)
+ * ends the call with y incomplete.
  */
 flce_status flce_matmul_fp8(const void* A, int64_t lda, const float* a_scale, const void* B,
                             int64_t ldb, const float* b_scale, int64_t M, int64_t V, int64_t K,

@@ -633,6 +633,7 @@ extern "C" flce_status flce_matmul_fp8(const void* A, int64_t lda, const float* 
                                        const void* B, int64_t ldb, const float* b_scale, int64_t M,
                                        int64_t V, int64_t K, void* y, int64_t ldy,
                                        flce_dtype out_dtype, flce_stream_t stream) {
+  OpRange range("flce_matmul_fp8");
   constexpr int64_t kMaxDim = (int64_t{1} << 31) - 1024;
   if (M < 0 || V <= 0 || K <= 0 || !valid_dtype(out_dtype)) return FLCE_ERR_INVALID_ARG;
   if (K % 16 != 0 || K > kMaxRowElems || M > kMaxDim || V > kMaxDim)

@@ -5,6 +5,7 @@
 #include <atomic>
 #include <cstdint>
 #include <cuda_runtime.h>
+#include <nvtx3/nvToolsExt.h>
 
 #include "../../include/flce.h"
 
@@ -17,6 +18,15 @@ constexpr int64_t kMaxRowElems = 1 << 16; // longest norm row / contraction
 
 // FLCE_OK and the SM count of the current device, if it is an sm_103 one.
 flce_status check_device(int* sms);
+
+// NVTX range over the host side of one call (a pointer check when no tool is
+// attached).
+struct OpRange {
+  explicit OpRange(const char* name) { nvtxRangePushA(name); }
+  ~OpRange() { nvtxRangePop(); }
+  OpRange(const OpRange&) = delete;
+  OpRange& operator=(const OpRange&) = delete;
+};
 
 // Raises a kernel's dynamic shared-memory limit to `smem`, on its first launch
 // on a device; one SmemLimit per kernel.  Atomic: racing first launches set the

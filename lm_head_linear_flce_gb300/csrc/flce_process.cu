@@ -341,13 +341,13 @@ cudaError_t run_process(const void* logits, void* out, int64_t B, ProcessArgs a,
   const int bias = a.n_bias == 0 ? kNoBias : a.n_bias <= kBiasList ? kListedBias : kIndexedBias;
   const int per_col = (wide ? 4 : 2) + (bias == kIndexedBias ? 2 : 0);
   // Blocks a row.  Every one reads the row's history, so there are only as many
-  // as give a block four columns for each entry, and no more than 4 an SM (of at
+  // as give a block four columns for each entry, and no more than 6 an SM (of at
   // least 1024 columns); but as many as fill the SMs, two each, and as shared
   // memory asks for.
   const int64_t fixed = 512 * 64 + 8 * kBiasList + 1024;  // ring, list, rounding
   const int64_t most = (kMaxSmem - fixed) * 8 / (8 * per_col + 1) / 64 * 64, all = B * a.V;
   const auto blocks_of = [&](int64_t cols) { return (a.V + cols - 1) / cols; };
-  const int64_t wanted = std::max<int64_t>({(all + 4 * sms - 1) / (4 * sms), 4 * a.L, 1024});
+  const int64_t wanted = std::max<int64_t>({(all + 6 * sms - 1) / (6 * sms), 4 * a.L, 1024});
   const int64_t fill = std::min(std::max<int64_t>(2 * sms / B, 1), blocks_of(1024));
   const int64_t blocks = std::max({blocks_of(wanted), fill, blocks_of(most)});
   a.cols = static_cast<int>(std::min((blocks_of(blocks) + 63) / 64 * 64, most));
@@ -377,6 +377,7 @@ extern "C" flce_status flce_process_logits(
     const float* presence, const void* bias_ids, int bias_int64, const float* bias_values,
     int64_t n_bias, const int32_t* allowed, int64_t ld_allowed, void* out, int64_t ld_out,
     flce_dtype out_dtype, flce_stream_t stream) {
+  OpRange range("flce_process_logits");
   if (B < 0 || V <= 0 || L < 0 || n_bias < 0 || !valid_dtype(dtype) || !valid_dtype(out_dtype))
     return FLCE_ERR_INVALID_ARG;
   if (B > 65535 || V > (int64_t{1} << 30) || L >= (int64_t{1} << 31) || n_bias > 65535)
@@ -436,8 +437,9 @@ extern "C" flce_status flce_process_logits(
   const auto s = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t err;
   if (dtype == FLCE_BF16)
-    err = out_dtype == FLCE_BF16 ? run_process<__nv_bfloat16, __nv_bfloat16>(logits, out, B, a, sms, s)
-                                 : run_process<__nv_bfloat16, float>(logits, out, B, a, sms, s);
+    err = out_dtype == FLCE_BF16
+              ? run_process<__nv_bfloat16, __nv_bfloat16>(logits, out, B, a, sms, s)
+              : run_process<__nv_bfloat16, float>(logits, out, B, a, sms, s);
   else
     err = out_dtype == FLCE_BF16 ? run_process<float, __nv_bfloat16>(logits, out, B, a, sms, s)
                                  : run_process<float, float>(logits, out, B, a, sms, s);

@@ -84,7 +84,9 @@ struct OnDevice {
             c10::cuda::getCurrentCUDAStream(t.get_device()).stream())) {}
 };
 
-PyObject* wrap(Tensor t) { return t.defined() ? THPVariable_Wrap(std::move(t)) : Py_NewRef(Py_None); }
+PyObject* wrap(Tensor t) {
+  return t.defined() ? THPVariable_Wrap(std::move(t)) : Py_NewRef(Py_None);
+}
 template <class... T>
 PyObject* answer(flce_status st, T&&... t) {
   if (st != FLCE_OK) return PyLong_FromLong(st);
