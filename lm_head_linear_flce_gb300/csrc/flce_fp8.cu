@@ -173,6 +173,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   cluster_sync_all();  // no CTA signals its peer's barriers before they are set up
   tc_fence_after();
   const uint32_t tmem = *slot;
+  griddep_launch_dependents();
+  griddep_wait();  // set up; from here on global memory is read and written
   const WaitCtx w{abort_flag, nullptr, a.wait_limit_ns};
   const int tiles = a.tiles_m * a.tiles_v;
   const int first = blockIdx.x >> 1, step = gridDim.x >> 1;
@@ -389,6 +391,8 @@ __global__ void __launch_bounds__(RowShape<NP>::kThreads, kRowsPerSm)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *slot;
+  griddep_launch_dependents();
+  griddep_wait();
   const WaitCtx w{abort_flag, nullptr, a.wait_limit_ns};
   const int part = splits > 1 ? static_cast<int>(cluster_ctarank()) : 0;
   const int j0 = static_cast<int>(static_cast<int64_t>(a.G) * part / splits);
@@ -580,10 +584,10 @@ cudaError_t launch_pair(const CUtensorMap& ta, const CUtensorMap& tb, const CUte
   if (e != cudaSuccess) return e;
   const int64_t tiles = static_cast<int64_t>(a.tiles_m) * a.tiles_v;
   const int pairs = static_cast<int>(std::min<int64_t>(tiles, sms / 2));
-  k<<<2 * pairs, kPairThreads, kPairSmem, s>>>(ta, tb, ty, a);
+  e = launch_overlapped(k, dim3(2 * pairs), dim3(kPairThreads), kPairSmem, s, 1, ta, tb, ty, a);
   note_launch();
   note_wait_limit(a.wait_limit_ns);
-  return cudaGetLastError();
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 template <int NP, class O>
@@ -598,19 +602,9 @@ cudaError_t launch_rows(const CUtensorMap& ta, const CUtensorMap& tb, const Fp8A
   const int room = kRowsPerSm * sms;
   int splits = 1;
   while (splits < 8 && 2 * splits * a.tiles_v <= room && 2 * splits <= a.G) splits *= 2;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(splits > 1 ? splits * a.tiles_v : std::min(a.tiles_v, room));
-  cfg.blockDim = dim3(RowShape<NP>::kThreads);
-  cfg.dynamicSmemBytes = RowShape<NP>::kSmem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = splits;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, k, ta, tb, a, splits);
+  e = launch_overlapped(k, dim3(splits > 1 ? splits * a.tiles_v : std::min(a.tiles_v, room)),
+                        dim3(RowShape<NP>::kThreads), RowShape<NP>::kSmem, s, splits, ta, tb, a,
+                        splits);
   note_launch();
   note_wait_limit(a.wait_limit_ns);
   return e != cudaSuccess ? e : cudaGetLastError();

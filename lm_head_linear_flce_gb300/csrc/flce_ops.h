@@ -36,6 +36,32 @@ struct SmemLimit {
 };
 cudaError_t allow_smem(const void* kernel, int smem, SmemLimit* limit);
 
+// Launches `kernel` so that it may start while the stream's previous kernel
+// ends: its blocks take the places that become free, set themselves up and wait
+// (griddep_wait, before their first access of global memory) until that kernel
+// is complete.  Only where that kernel allows it (griddep_launch_dependents, or
+// at its end); after anything else this is a plain launch.  cluster: CTAs per
+// cluster, where the kernel does not fix it.
+template <class... P, class... A>
+cudaError_t launch_overlapped(void (*kernel)(P...), dim3 grid, dim3 block, int smem,
+                              cudaStream_t s, int cluster, const A&... args) {
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
+
 inline bool valid_dtype(flce_dtype t) { return t == FLCE_BF16 || t == FLCE_F32; }
 inline size_t dtype_bytes(flce_dtype t) { return t == FLCE_F32 ? 4 : 2; }
 inline bool aligned_to(const void* p, size_t a) {

@@ -6,6 +6,7 @@
 #include <algorithm>
 #include <type_traits>
 
+#include "flce_device.cuh"
 #include "flce_internal.h"
 #include "flce_ops.h"
 
@@ -133,6 +134,8 @@ template <class T, class O, bool WIDE, int BIAS, int THREADS>
 __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
     process_kernel(const T* logits, O* out, const ProcessArgs a) {
   extern __shared__ __align__(16) uint32_t smem[];
+  griddep_launch_dependents();
+  griddep_wait();
   const int64_t b = blockIdx.y;
   const int v0 = static_cast<int>(blockIdx.x) * a.cols;  // V <= 2^30
   const int cols = min(a.cols, static_cast<int>(a.V) - v0);
@@ -329,9 +332,10 @@ cudaError_t launch_process(const void* logits, void* out, int64_t B, const Proce
   const cudaError_t e = allow_smem(reinterpret_cast<const void*>(k), kMaxSmem, &limit);
   if (e != cudaSuccess) return e;
   const dim3 grid(static_cast<unsigned>((a.V + a.cols - 1) / a.cols), static_cast<unsigned>(B));
-  k<<<grid, THREADS, smem, s>>>(static_cast<const T*>(logits), static_cast<O*>(out), a);
+  const cudaError_t e2 = launch_overlapped(k, grid, dim3(THREADS), smem, s, 1,
+                                           static_cast<const T*>(logits), static_cast<O*>(out), a);
   note_launch();
-  return cudaGetLastError();
+  return e2 != cudaSuccess ? e2 : cudaGetLastError();
 }
 
 template <class T, class O>
