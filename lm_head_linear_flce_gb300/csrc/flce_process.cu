@@ -114,16 +114,68 @@ __device__ __forceinline__ float load_f(const __nv_bfloat16* p) { return __bfloa
 __device__ __forceinline__ void store_f(float* p, float v) { *p = v; }
 __device__ __forceinline__ void store_f(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 
-// Windows a thread has on their way, in slots of its own in shared memory:
-// 64 bytes a thread, 64 KB an SM, all the time.
-template <class T>
-constexpr int kRing = 16 / static_cast<int>(sizeof(T));
+// Windows a thread has on their way, in slots of its own in shared memory, in
+// bytes: 64 KB an SM with four small blocks there, 48 KB with two large ones,
+// which need the room for counters.
+template <int THREADS>
+constexpr int kRingBytes = THREADS <= 256 ? 64 : 48;
+template <class T, int THREADS>
+constexpr int kRing = kRingBytes<THREADS> / (kWin * static_cast<int>(sizeof(T)));
 
 template <int BYTES>
 __device__ __forceinline__ void copy_async(void* dst, const void* src) {
   const uint32_t d = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
   asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(d), "l"(src), "n"(BYTES)
                : "memory");
+}
+
+// The column of an id relative to v0, all others (negative ids among them) as a
+// number that no block has columns for.
+__device__ __forceinline__ uint32_t column(int t, int v0) {
+  return static_cast<uint32_t>(t) - static_cast<uint32_t>(v0);
+}
+__device__ __forceinline__ uint32_t column(int64_t t, int v0) {
+  const uint64_t c = static_cast<uint64_t>(t) - static_cast<uint64_t>(v0);
+  return c >> 32 ? ~0u : static_cast<uint32_t>(c);
+}
+
+// f(column, i) for each i < len of a row's history, THREADS threads together: 16
+// bytes at a time, kIdLoads of them on their way while as many are counted.
+constexpr int kIdLoads = 4;
+template <int THREADS, class I, class F>
+__device__ __forceinline__ void each_id(const I* t, int64_t len, int v0, const F& f) {
+  constexpr int kPer = 16 / sizeof(I);
+  const int64_t head = min(len, static_cast<int64_t>(
+                                    (0 - reinterpret_cast<uintptr_t>(t)) / sizeof(I) % kPer));
+  const int64_t packs = (len - head) / kPer, tail = head + packs * kPer;
+  const int edges = static_cast<int>(head + len - tail);
+  if (threadIdx.x < edges) {
+    const int64_t i = threadIdx.x < head ? threadIdx.x : tail + threadIdx.x - head;
+    f(column(t[i], v0), i);
+  }
+  const uint4* p = reinterpret_cast<const uint4*>(t + head);
+  uint4 next[kIdLoads];
+  const auto fetch = [&](int64_t k0) {
+#pragma unroll
+    for (int u = 0; u < kIdLoads; ++u)
+      if (k0 + u * THREADS < packs) next[u] = p[k0 + u * THREADS];
+  };
+  fetch(threadIdx.x);
+  for (int64_t k0 = threadIdx.x; k0 < packs; k0 += THREADS * kIdLoads) {
+    uint4 now[kIdLoads];
+#pragma unroll
+    for (int u = 0; u < kIdLoads; ++u) now[u] = next[u];
+    fetch(k0 + THREADS * kIdLoads);
+#pragma unroll
+    for (int u = 0; u < kIdLoads; ++u) {
+      const int64_t k = k0 + u * THREADS;
+      if (k >= packs) break;
+      alignas(16) I ids[kPer];
+      *reinterpret_cast<uint4*>(ids) = now[u];
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) f(column(ids[j], v0), head + k * kPer + j);
+    }
+  }
 }
 
 // Mask words a block of `cols` columns may touch, with one to spare for the
@@ -134,6 +186,7 @@ template <class T, class O, bool WIDE, int BIAS, int THREADS>
 __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
     process_kernel(const T* logits, O* out, const ProcessArgs a) {
   extern __shared__ __align__(16) uint32_t smem[];
+  constexpr int kSlots = kRing<T, THREADS>;
   griddep_launch_dependents();
   griddep_wait();
   const int64_t b = blockIdx.y;
@@ -165,7 +218,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
   // bias indices (the last two one per window column).
   using Raw = decltype(load_raw(in_row));
   Raw* ring = reinterpret_cast<Raw*>(smem) + threadIdx.x;  // this thread's slots, THREADS apart
-  uint32_t* listed = smem + kRing<T> * THREADS * sizeof(Raw) / 4;  // column << 16 | entry
+  uint32_t* listed = smem + kSlots * THREADS * sizeof(Raw) / 4;  // column << 16 | entry
   auto* before = reinterpret_cast<float*>(listed + kBiasList);      // its logit
   __shared__ int n_listed;
   uint32_t* mask = listed + (BIAS == kListedBias ? 2 * kBiasList : 0);
@@ -180,7 +233,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
 #pragma unroll
-  for (int i = 0; i < kRing<T>; ++i) fetch(threadIdx.x + i * THREADS, i);
+  for (int i = 0; i < kSlots; ++i) fetch(threadIdx.x + i * THREADS, i);
 
   // mask word i holds columns 32 (v0 / 32 + i) and on
   const int first_word = v0 >> 5;
@@ -195,34 +248,12 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
   if (threadIdx.x == 0) n_listed = 0;
   __syncthreads();
   const int64_t len = max(int64_t{0}, min(len0, a.L));
-  constexpr int kIds = 8;
-  int id[kIds];  // relative to v0; negative: none
-  const auto fetch_ids = [&](int64_t i0) {
-#pragma unroll
-    for (int u = 0; u < kIds; ++u) {
-      const int64_t i = i0 + u * THREADS;
-      id[u] = -1;
-      if (i >= len) continue;
-      if (a.tokens_int64) {
-        const int64_t t = static_cast<const int64_t*>(a.tokens)[b * a.ld_tokens + i] - v0;
-        id[u] = t >= 0 && t < cols ? static_cast<int>(t) : -1;
-      } else {
-        const int t = static_cast<const int*>(a.tokens)[b * a.ld_tokens + i];
-        id[u] = t >= 0 ? t - v0 : -1;
-      }
-    }
+  const auto count = [&](uint32_t c, int64_t i) {  // entry i, c columns behind v0
+    if (c < static_cast<uint32_t>(cols)) counts.add(static_cast<int>(c) + shift, i < prompt);
   };
-  // the next ids are on their way while these are counted
-  fetch_ids(threadIdx.x);
-  for (int64_t i0 = threadIdx.x; i0 < len; i0 += THREADS * kIds) {
-    int now[kIds];
-#pragma unroll
-    for (int u = 0; u < kIds; ++u) now[u] = id[u];
-    fetch_ids(i0 + THREADS * kIds);
-#pragma unroll
-    for (int u = 0; u < kIds; ++u)
-      if (now[u] >= 0 && now[u] < cols) counts.add(now[u] + shift, i0 + u * THREADS < prompt);
-  }
+  if (a.tokens_int64)
+    each_id<THREADS>(static_cast<const int64_t*>(a.tokens) + b * a.ld_tokens, len, v0, count);
+  else each_id<THREADS>(static_cast<const int*>(a.tokens) + b * a.ld_tokens, len, v0, count);
   if constexpr (BIAS != kNoBias) {
     for (int i = threadIdx.x; i < a.n_bias; i += THREADS) {
       const int64_t v = id_at(a.bias_ids, a.bias_int64, b * a.n_bias + i);
@@ -260,7 +291,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
   };
   int slot = 0;
   for (int k = threadIdx.x; k < windows; k += THREADS) {
-    asm volatile("cp.async.wait_group %0;" ::"n"(kRing<T> - 1) : "memory");
+    asm volatile("cp.async.wait_group %0;" ::"n"(kSlots - 1) : "memory");
     const int c0 = kWin * k;  // the window's first counter
     const auto n4 = counts.window(c0);
     uint2 e4 = make_uint2(0, 0);
@@ -298,8 +329,8 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
         store_f(out_row + c, ok >> j & 1 ? apply(load_f(in_row + c), n[j], e[j]) : -INFINITY);
       }
     }
-    fetch(k + kRing<T> * THREADS, slot);
-    slot = slot + 1 == kRing<T> ? 0 : slot + 1;
+    fetch(k + kSlots * THREADS, slot);
+    slot = slot + 1 == kSlots ? 0 : slot + 1;
   }
   asm volatile("cp.async.wait_group 0;" ::: "memory");
   if constexpr (BIAS == kListedBias) {
@@ -325,7 +356,7 @@ template <class T, class O, bool WIDE, int BIAS, int THREADS>
 cudaError_t launch_process(const void* logits, void* out, int64_t B, const ProcessArgs& a,
                            int counters, cudaStream_t s) {
   // (the shift's window: 16 columns of counters more, in steps of 8)
-  const int smem = 64 * THREADS + (BIAS == kListedBias ? 8 * kBiasList : 0) +
+  const int smem = kRingBytes<THREADS> * THREADS + (BIAS == kListedBias ? 8 * kBiasList : 0) +
                    4 * mask_words(a.cols) + (a.cols + 16) * counters;
   auto* k = process_kernel<T, O, WIDE, BIAS, THREADS>;
   static SmemLimit limit;
@@ -344,17 +375,22 @@ cudaError_t run_process(const void* logits, void* out, int64_t B, ProcessArgs a,
   const bool wide = a.L > 32768;
   const int bias = a.n_bias == 0 ? kNoBias : a.n_bias <= kBiasList ? kListedBias : kIndexedBias;
   const int per_col = (wide ? 4 : 2) + (bias == kIndexedBias ? 2 : 0);
-  // Blocks a row.  Every one reads the row's history, so there are only as many
-  // as give a block four columns for each entry, and no more than 6 an SM (of at
-  // least 1024 columns); but as many as fill the SMs, two each, and as shared
-  // memory asks for.
-  const int64_t fixed = 512 * 64 + 8 * kBiasList + 1024;  // ring, list, rounding
-  const int64_t most = (kMaxSmem - fixed) * 8 / (8 * per_col + 1) / 64 * 64, all = B * a.V;
-  const auto blocks_of = [&](int64_t cols) { return (a.V + cols - 1) / cols; };
-  const int64_t wanted = std::max<int64_t>({(all + 6 * sms - 1) / (6 * sms), 4 * a.L, 1024});
-  const int64_t fill = std::min(std::max<int64_t>(2 * sms / B, 1), blocks_of(1024));
-  const int64_t blocks = std::max({blocks_of(wanted), fill, blocks_of(most)});
-  a.cols = static_cast<int>(std::min((blocks_of(blocks) + 63) / 64 * 64, most));
+  // Blocks a row, n.  Every one reads the row's history.  Two blocks share an SM,
+  // so that the SMs take ceil(B n / 2 SMs) turns, each about as long as a block's
+  // columns, half its history's length (an id costs about half a column) and the
+  // time of some 512 columns for its start.  Taken is the n with the least of
+  // that, of those whose blocks have 1024 columns and fit into shared memory.
+  const int64_t fixed = 512 * kRingBytes<512> + 8 * kBiasList + 1024;  // ring, list, rounding
+  const int64_t most = (kMaxSmem - fixed) * 8 / (8 * per_col + 1) / 64 * 64;
+  const auto cols_of = [&](int64_t n) { return ((a.V + n - 1) / n + 63) / 64 * 64; };
+  int64_t blocks = (a.V + most - 1) / most, best = INT64_MAX;
+  const int64_t least = blocks;
+  for (int64_t n = least; n == least || (n * 1024 <= a.V + 1023 && n <= 4 * sms); ++n) {
+    const int64_t turns = (B * n + 2 * sms - 1) / (2 * sms);
+    const int64_t cost = turns * (cols_of(n) + a.L / 2 + 512);
+    if (cost < best) best = cost, blocks = n;
+  }
+  a.cols = static_cast<int>(std::min(cols_of(blocks), most));
   const auto launch = [&](auto w, auto bm) {
     constexpr bool kW = decltype(w)::value;
     constexpr int kB = decltype(bm)::value;
