@@ -114,9 +114,13 @@ __device__ __forceinline__ float load_f(const __nv_bfloat16* p) { return __bfloa
 __device__ __forceinline__ void store_f(float* p, float v) { *p = v; }
 __device__ __forceinline__ void store_f(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 
+// Blocks that share an SM, shared memory permitting.
+template <int THREADS>
+constexpr int kPerSm = THREADS <= 256 ? 4 : 3;
+
 // Windows a thread has on their way, in slots of its own in shared memory, in
-// bytes: 64 KB an SM with four small blocks there, 48 KB with two large ones,
-// which need the room for counters.
+// bytes: 64 KB an SM with four small blocks there, 72 or 48 KB with three or two
+// large ones, which need the room for counters.
 template <int THREADS>
 constexpr int kRingBytes = THREADS <= 256 ? 64 : 48;
 template <class T, int THREADS>
@@ -140,11 +144,13 @@ __device__ __forceinline__ uint32_t column(int64_t t, int v0) {
 }
 
 // f(column, i) for each i < len of a row's history, THREADS threads together: 16
-// bytes at a time, kIdLoads of them on their way while as many are counted.
-constexpr int kIdLoads = 4;
+// bytes at a time, kIdLoads of them on their way while as many are counted (as
+// many as registers allow: four in blocks of 512 spill, 37 us for 35).
+template <int THREADS>
+constexpr int kIdLoads = THREADS <= 256 ? 4 : 2;
 template <int THREADS, class I, class F>
 __device__ __forceinline__ void each_id(const I* t, int64_t len, int v0, const F& f) {
-  constexpr int kPer = 16 / sizeof(I);
+  constexpr int kPer = 16 / sizeof(I), kLoads = kIdLoads<THREADS>;
   const int64_t head = min(len, static_cast<int64_t>(
                                     (0 - reinterpret_cast<uintptr_t>(t)) / sizeof(I) % kPer));
   const int64_t packs = (len - head) / kPer, tail = head + packs * kPer;
@@ -154,20 +160,20 @@ __device__ __forceinline__ void each_id(const I* t, int64_t len, int v0, const F
     f(column(t[i], v0), i);
   }
   const uint4* p = reinterpret_cast<const uint4*>(t + head);
-  uint4 next[kIdLoads];
+  uint4 next[kLoads];
   const auto fetch = [&](int64_t k0) {
 #pragma unroll
-    for (int u = 0; u < kIdLoads; ++u)
+    for (int u = 0; u < kLoads; ++u)
       if (k0 + u * THREADS < packs) next[u] = p[k0 + u * THREADS];
   };
   fetch(threadIdx.x);
-  for (int64_t k0 = threadIdx.x; k0 < packs; k0 += THREADS * kIdLoads) {
-    uint4 now[kIdLoads];
+  for (int64_t k0 = threadIdx.x; k0 < packs; k0 += THREADS * kLoads) {
+    uint4 now[kLoads];
 #pragma unroll
-    for (int u = 0; u < kIdLoads; ++u) now[u] = next[u];
-    fetch(k0 + THREADS * kIdLoads);
+    for (int u = 0; u < kLoads; ++u) now[u] = next[u];
+    fetch(k0 + THREADS * kLoads);
 #pragma unroll
-    for (int u = 0; u < kIdLoads; ++u) {
+    for (int u = 0; u < kLoads; ++u) {
       const int64_t k = k0 + u * THREADS;
       if (k >= packs) break;
       alignas(16) I ids[kPer];
@@ -183,7 +189,7 @@ __device__ __forceinline__ void each_id(const I* t, int64_t len, int v0, const F
 __host__ __device__ constexpr int mask_words(int cols) { return (cols / 32 + 3 + 3) / 4 * 4; }
 
 template <class T, class O, bool WIDE, int BIAS, int THREADS>
-__global__ void __launch_bounds__(THREADS, 1024 / THREADS)
+__global__ void __launch_bounds__(THREADS, kPerSm<THREADS>)
     process_kernel(const T* logits, O* out, const ProcessArgs a) {
   extern __shared__ __align__(16) uint32_t smem[];
   constexpr int kSlots = kRing<T, THREADS>;
@@ -349,8 +355,10 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
   }
 }
 
-// Shared memory a block may take: two blocks an SM.
-constexpr int kMaxSmem = 113 * 1024;
+// Shared memory an SM has for its blocks, and that a block may take: two an SM.
+constexpr int kSmSmem = 227 * 1024, kMaxSmem = 113 * 1024;
+// Columns that a block of 256 threads takes at most; more take 512.
+constexpr int kSmallCols = 4096;
 
 template <class T, class O, bool WIDE, int BIAS, int THREADS>
 cudaError_t launch_process(const void* logits, void* out, int64_t B, const ProcessArgs& a,
@@ -375,26 +383,37 @@ cudaError_t run_process(const void* logits, void* out, int64_t B, ProcessArgs a,
   const bool wide = a.L > 32768;
   const int bias = a.n_bias == 0 ? kNoBias : a.n_bias <= kBiasList ? kListedBias : kIndexedBias;
   const int per_col = (wide ? 4 : 2) + (bias == kIndexedBias ? 2 : 0);
-  // Blocks a row, n.  Every one reads the row's history.  Two blocks share an SM,
-  // so that the SMs take ceil(B n / 2 SMs) turns, each about as long as a block's
-  // columns, half its history's length (an id costs about half a column) and the
-  // time of some 512 columns for its start.  Taken is the n with the least of
-  // that, of those whose blocks have 1024 columns and fit into shared memory.
-  const int64_t fixed = 512 * kRingBytes<512> + 8 * kBiasList + 1024;  // ring, list, rounding
-  const int64_t most = (kMaxSmem - fixed) * 8 / (8 * per_col + 1) / 64 * 64;
+  // Blocks a row, n.  `per` of them share an SM, so that the SMs take
+  // ceil(B n / (per SMs)) turns, each as long as a block's columns, the row's
+  // history, which every block reads (an id costs a quarter of a column, and a
+  // quarter more for each block that reads beside it), and a start worth some
+  // 4096 columns.  Taken is the n with the least of that, of those that fill
+  // their turns; blocks have 1024 columns at least and fit into shared memory.
+  // (8 x 152064 bf16, histories of 32768: 1 block an SM 11 us, 2 13, 4 16; without
+  // histories 2 blocks 4.2 us, 1 4.9, 4 5.5.)
+  const auto smem_of = [&](int64_t cols) {  // of a block with 512 threads
+    return 512 * kRingBytes<512> + 8 * kBiasList + 1024 + cols * (8 * per_col + 1) / 8;
+  };
+  const int64_t most = (kMaxSmem - smem_of(0)) * 8 / (8 * per_col + 1) / 64 * 64;
   const auto cols_of = [&](int64_t n) { return ((a.V + n - 1) / n + 63) / 64 * 64; };
-  int64_t blocks = (a.V + most - 1) / most, best = INT64_MAX;
-  const int64_t least = blocks;
-  for (int64_t n = least; n == least || (n * 1024 <= a.V + 1023 && n <= 4 * sms); ++n) {
-    const int64_t turns = (B * n + 2 * sms - 1) / (2 * sms);
-    const int64_t cost = turns * (cols_of(n) + a.L / 2 + 512);
+  const int64_t least = (a.V + most - 1) / most, finest = std::max(least, (a.V + 1023) / 1024);
+  int64_t blocks = least, best = INT64_MAX;
+  for (int64_t fill = 1; fill <= 24; ++fill) {  // blocks an SM, all turns together
+    const int64_t n = std::clamp<int64_t>(fill * sms / B, least, finest);
+    const int64_t cols = cols_of(n);
+    const int64_t per = cols <= kSmallCols ? kPerSm<256>
+                                           : std::min<int64_t>(kPerSm<512>, kSmSmem / smem_of(cols));
+    const int64_t at_once = std::min(per, (B * n + sms - 1) / sms);
+    const int64_t turn = cols + a.L / 4 * (at_once + 1) + 4096;
+    const int64_t cost = (B * n + per * sms - 1) / (per * sms) * turn;
     if (cost < best) best = cost, blocks = n;
+    if (n == finest) break;
   }
   a.cols = static_cast<int>(std::min(cols_of(blocks), most));
   const auto launch = [&](auto w, auto bm) {
     constexpr bool kW = decltype(w)::value;
     constexpr int kB = decltype(bm)::value;
-    return a.cols <= 4096 ? launch_process<T, O, kW, kB, 256>(logits, out, B, a, per_col, s)
+    return a.cols <= kSmallCols ? launch_process<T, O, kW, kB, 256>(logits, out, B, a, per_col, s)
                           : launch_process<T, O, kW, kB, 512>(logits, out, B, a, per_col, s);
   };
   const auto by_bias = [&](auto w) {

@@ -116,3 +116,45 @@ def test_example_runs():
                        capture_output=True, text=True, timeout=300)
     assert r.returncode == 0, r.stdout + r.stderr
     assert "training: loss" in r.stdout and "decoded:" in r.stdout
+
+
+@pytest.mark.parametrize("B", [1, 40, 200])
+def test_calls_in_a_row_wait_for_one_another(B):
+    """Each call reads what the one before wrote, in memory used again and again,
+    with no synchronisation between them: the same bits as with one after every
+    call."""
+    H, V, L, steps = 640, 4016, 9, 30
+    g = torch.Generator().manual_seed(B)
+    x = torch.randn(B, H, generator=g).to(BF).cuda()
+    w = (1 + 0.2 * torch.randn(H, generator=g)).to(BF).cuda()
+    Wq, Ws = flce.quantize_fp8((0.05 * torch.randn(V, H, generator=g)).to(BF).cuda())
+    back, bs = flce.quantize_fp8((0.05 * torch.randn(H, V, generator=g)).to(BF).cuda())
+    tok = torch.randint(0, V, (B, L), generator=g).cuda()
+    fp = torch.full((B,), 0.5).cuda()
+
+    def chain(wait):
+        stream = x.clone()
+        for _ in range(steps):
+            q, s = flce.rms_norm_fp8(stream, w)
+            wait()
+            z = flce.matmul_fp8(q, s, Wq, Ws, out_dtype=torch.float32)
+            wait()
+            flce.process_logits(z, tokens=tok, frequency_penalty=fp, out=z)
+            wait()
+            zq, zs = flce.quantize_fp8(z, block_rows=1)
+            wait()
+            y = flce.matmul_fp8(zq, zs, back, bs)
+            wait()
+            y, h, rstd = flce.flce_rms_norm(y, w, residual=stream)
+            wait()
+            stream, dw = flce.flce_rms_norm_backward(y, h, w, rstd)
+            wait()
+            stream = flce.flce_rms_norm(stream, dw)[0]
+        torch.cuda.synchronize()
+        return stream, z
+
+    want = chain(torch.cuda.synchronize)
+    for _ in range(3):
+        got = chain(lambda: None)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert torch.isfinite(want[0].float()).all() and want[0].float().abs().max() > 0

@@ -227,6 +227,20 @@ def test_large_batches(B, V, L, nb, mask, dt, odt):
     del kk, zz, got
 
 
+@pytest.mark.parametrize("ids", [torch.int32, torch.int64])
+@pytest.mark.parametrize("offset", [0, 1, 2, 3])
+def test_histories_of_every_start_and_length(offset, ids):
+    # rows that begin anywhere in their 16 bytes and end anywhere in the next ones
+    z, k = case(40, 300, 37, 0, ids=ids, seed=offset)
+    wide = torch.full((40, 41 + offset), 5, dtype=ids)
+    wide[:, offset:offset + 37] = k["tokens"]
+    k["lengths"] = torch.arange(40).clamp(max=37).int()
+    k["prompt_lengths"] = k["lengths"] // 2
+    on_gpu = {n: None if t is None else t.cuda() for n, t in k.items()}
+    on_gpu["tokens"] = wide.cuda()[:, offset:offset + 37]
+    check(flce.process_logits(z.cuda(), **on_gpu), z, k)
+
+
 def test_side_stream_and_graph():
     z, k = case(4, 40000, 3000, 5, BF, seed=4)
     want = run(z, k)
