@@ -30,6 +30,16 @@ constexpr int kMmaK8 = 32;    // K per MMA
 // the result is 128 registers a thread.  Three warpgroups: the first (TMA, MMA)
 // hands registers to the two of the epilogue; 384 threads launch with 168 each,
 // 64512 in all = 128 * 56 + 256 * 224.
+//
+// Bound by the tensor cores, and in a loop of seconds by the board's power:
+// 4096 x 152064 x 3584 to bf16 takes 1.53 to 1.63 ms (2.7 to 2.9 PFLOP/s) by
+// itself, 1.68 ms in a loop; 256 x 151936 x 4096 to float32 takes 141 us, 5.5 TB/s.
+// A block's scales change with every 128 columns of K, so its products go through
+// registers (packed fma) before the next block may add to them; the two 256-column
+// accumulators fill TMEM and hide that.  Also measured, 4096 x 152064 x 3584
+// against 2.7 to 2.9 PFLOP/s: three accumulators of 160 columns 2.2, sixteen epilogue
+// warps 1.9, accumulators in halves 1.5; a second staging buffer for the stores and
+// scales fetched a tile ahead changed nothing.
 constexpr int kPairThreads = 384;  // warp 0 TMA, warp 1 MMA, warps 4..11 epilogue
 constexpr int kPairEpi = 8;
 constexpr int kPairLeanRegs = 56;
@@ -338,16 +348,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 // distributed shared memory.
 //
 // A column's scale differs from lane to lane here (it is a row of A), so each
-// block costs the epilogue a scale per element from shared memory; measured
-// with 151936 x 4096, that holds the HBM rate up to NP = 64 (104 us for 64 rows)
-// and not beyond (177 us at NP = 128, where the pair kernel takes 126).
+// block costs the epilogue a scale per element from shared memory.  Of 151936 x
+// 4096 bytes: 8 rows 93.5 us (6.7 TB/s), 32 103, 48 105, 64 110, each to float32;
+// NP = 128 took 177 where the pair kernel takes 126.  NP = 48 is worth having
+// where the rows of A start inside a 128-byte line and so cost two reads each:
+// 37 x 32003 x 2064 19.7 us, padded to 64 21.8.
 template <int NP>
 struct RowShape {
   static constexpr int kThreads = 192;  // warp 0 TMA, warp 1 MMA, warps 2..5 epilogue
   static constexpr int kStageBytes = 128 * kKB + NP * kKB;
   static constexpr int kStages = NP <= 16 ? 6 : NP <= 32 ? 5 : 4;
   static constexpr int kAccs = 4;                     // accumulators of NP columns
-  static constexpr int kTmem = NP * kAccs;
+  static constexpr int kTmem = NP == 48 ? 256 : NP * kAccs;  // a power of two
+  // a stage's barrier serves for its accumulator too, so at most kStages are ahead
+  static_assert(kStages >= kAccs);
   static constexpr int kScaleBytes = 4 * 2 * NP * 4;  // two buffers per epilogue warp
   static constexpr int kSmem = kStages * kStageBytes + kScaleBytes + 1024 + 512;
 };
@@ -500,7 +514,7 @@ __global__ void __launch_bounds__(RowShape<NP>::kThreads, kRowsPerSm)
         if (!ok) break;
         tc_fence_after();
         const uint32_t tbase = tmem + (static_cast<uint32_t>(q * 32) << 16) + acc.idx * NP;
-        constexpr int kC = NP < 32 ? 16 : 32;
+        constexpr int kC = NP % 32 ? 16 : 32;
 #pragma unroll
         for (int c = 0; c < NP / kC; ++c) {
           uint32_t p[kC];
@@ -614,6 +628,7 @@ template <class O>
 cudaError_t launch_rows_for(const CUtensorMap& ta, const CUtensorMap& tb, const Fp8Args& a,
                             int np, int sms, cudaStream_t s) {
   if (np == 16) return launch_rows<16, O>(ta, tb, a, sms, s);
+  if (np == 48) return launch_rows<48, O>(ta, tb, a, sms, s);
   if (np == 32) return launch_rows<32, O>(ta, tb, a, sms, s);
   return launch_rows<64, O>(ta, tb, a, sms, s);
 }
@@ -667,7 +682,7 @@ extern "C" flce_status flce_matmul_fp8(const void* A, int64_t lda, const float* 
   if (!make_tmap(&tb, B, K, V, ldb, kKB, 128, kU8)) return FLCE_ERR_CUDA;
   cudaError_t err;
   if (M <= kFewRows) {
-    const int np = M <= 16 ? 16 : M <= 32 ? 32 : 64;
+    const int np = M <= 16 ? 16 : M <= 32 ? 32 : M <= 48 ? 48 : 64;
     a.tiles_v = static_cast<int>(gv);
     if (!make_tmap(&ta, A, K, M, lda, kKB, np, kU8)) return FLCE_ERR_CUDA;
     err = out_dtype == FLCE_BF16 ? launch_rows_for<__nv_bfloat16>(ta, tb, a, np, sms, s)

@@ -61,6 +61,20 @@ def test_matches_the_float64_product(M, V, K, out):
     check(y, a, sa, b, sb, out)
 
 
+def test_every_number_of_rows():
+    # each padding of the rows, filled, one below and one above; rows of 144 bytes
+    g = torch.Generator().manual_seed(3)
+    V, K = 259, 144
+    b, sb = flce.quantize_fp8(torch.randn(V, K, generator=g).cuda())
+    x = torch.randn(70, K, generator=g).cuda()
+    whole = flce.quantize_fp8(x, block_rows=1)
+    want, mag = ref.matmul_fp8(f64(whole[0]), f64(whole[1]), f64(b), f64(sb))
+    for M in range(1, 71):
+        y = f64(flce.matmul_fp8(whole[0][:M], whole[1][:M], b, sb, out_dtype=F32))
+        assert y.shape == (M, V)
+        assert (np.abs(y - want[:M]) <= 2.0 ** -15 * mag[:M]).all(), M
+
+
 @pytest.mark.parametrize("M", [1, 7, 40, 90, 300, 1100])
 def test_every_scale_reaches_its_block(M):
     """Exact case: operands of ones, scales powers of two that name their place;
