@@ -40,13 +40,19 @@ constexpr int kMmaK8 = 32;    // K per MMA
 // against 2.7 to 2.9 PFLOP/s: three accumulators of 160 columns 2.2, sixteen epilogue
 // warps 1.9, accumulators in halves 1.5; a second staging buffer for the stores and
 // scales fetched a tile ahead changed nothing.
-constexpr int kPairThreads = 384;  // warp 0 TMA, warp 1 MMA, warps 4..11 epilogue
-constexpr int kPairEpi = 8;
-constexpr int kPairLeanRegs = 56;
-constexpr int kPairEpiRegs = 224;
-constexpr int kPairStages = 6;
-constexpr int kPairStageBytes = 2 * 128 * kKB;
-constexpr int kPairSmem = kPairStages * kPairStageBytes + kPairEpi * kStageBufBytes + 1024 + 256;
+constexpr int kTileThreads = 384;  // warp 0 TMA, warp 1 MMA, warps 4..11 epilogue
+constexpr int kTileEpi = 8;
+constexpr int kTileLeanRegs = 56;
+constexpr int kTileEpiRegs = 224;
+template <bool PAIR>
+struct TileShape {
+  static constexpr int kRows = PAIR ? 256 : 128;   // rows of A, 256 of B
+  static constexpr int kBBytes = (PAIR ? 128 : 256) * kKB;  // of B in this CTA's stage
+  static constexpr int kStageBytes = 128 * kKB + kBBytes;
+  static constexpr int kStages = PAIR ? 6 : 4;
+  static constexpr int kSmem = kStages * kStageBytes + kTileEpi * kStageBufBytes + 1024 + 256;
+  static_assert(kStages >= 2);  // accumulators: a stage's barrier serves for its own
+};
 constexpr uint16_t kBoth = 0x3;
 
 struct Fp8Args {
@@ -141,32 +147,33 @@ __device__ __forceinline__ void store_chunk(const Fp8Args& a, const CUtensorMap*
   __syncwarp();
 }
 
-template <class O>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
-    flce_fp8_pair_kernel(const __grid_constant__ CUtensorMap ta,
+template <class O, bool PAIR>
+__global__ void __launch_bounds__(kTileThreads, 1)
+    flce_fp8_tile_kernel(const __grid_constant__ CUtensorMap ta,
                          const __grid_constant__ CUtensorMap tb,
                          const __grid_constant__ CUtensorMap ty, const Fp8Args a) {
+  using S = TileShape<PAIR>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t a_base = (raw + 1023u) & ~1023u;
-  const uint32_t b_base = a_base + kPairStages * 128 * kKB;
-  const uint32_t staging = b_base + kPairStages * 128 * kKB;
-  const uint32_t full = staging + kPairEpi * kStageBufBytes;
-  const uint32_t done = full + 8 * kPairStages;
-  const uint32_t tempty = done + 8 * kPairStages;
+  const uint32_t b_base = a_base + S::kStages * 128 * kKB;
+  const uint32_t staging = b_base + S::kStages * S::kBBytes;
+  const uint32_t full = staging + kTileEpi * kStageBufBytes;
+  const uint32_t done = full + 8 * S::kStages;
+  const uint32_t tempty = done + 8 * S::kStages;
   const uint32_t drain = tempty + 16;
   auto* slot = reinterpret_cast<uint32_t*>(smem_raw + (drain + 8 - raw));
   volatile uint32_t* abort_flag = slot + 1;
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-  const int rank = static_cast<int>(cluster_ctarank());
+  const int rank = PAIR ? static_cast<int>(cluster_ctarank()) : 0;
   const bool leader = rank == 0;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kPairStages; ++i) {
+    for (int i = 0; i < S::kStages; ++i) {
       mbar_init(full + 8 * i, 1);  // the leader's producer, for both CTAs' bytes
       mbar_init(done + 8 * i, 1);  // the leader's multicast commit
     }
     for (int i = 0; i < 2; ++i)
-      mbar_init(tempty + 8 * i, 2 * kPairEpi);  // every epilogue warp of both CTAs
+      mbar_init(tempty + 8 * i, (PAIR ? 2 : 1) * kTileEpi);  // every epilogue warp
     mbar_init(drain, 1);
     *abort_flag = 0u;
     fence_barrier_init();
@@ -175,45 +182,57 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     tma_prefetch_desc(&tb);
   }
   if (warp == 1) {
-    tmem_alloc_pair(smem_u32(slot), kTmemCols);
-    tmem_relinquish_pair();
+    if (PAIR) {
+      tmem_alloc_pair(smem_u32(slot), kTmemCols);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc_single(smem_u32(slot), kTmemCols);
+      tmem_relinquish_single();
+    }
   }
   tc_fence_before();
   __syncthreads();
-  cluster_sync_all();  // no CTA signals its peer's barriers before they are set up
+  if (PAIR) cluster_sync_all();  // no CTA signals its peer's barriers before they are set up
   tc_fence_after();
   const uint32_t tmem = *slot;
   griddep_launch_dependents();
   griddep_wait();  // set up; from here on global memory is read and written
   const WaitCtx w{abort_flag, nullptr, a.wait_limit_ns};
   const int tiles = a.tiles_m * a.tiles_v;
-  const int first = blockIdx.x >> 1, step = gridDim.x >> 1;
+  const int first = blockIdx.x >> PAIR, step = gridDim.x >> PAIR;
 
   // The roles are branches of their own so that each is compiled for its share
   // of the registers.
   if (warp < 4) {
-    regs_release<kPairLeanRegs>();
+    regs_release<kTileLeanRegs>();
     if (warp == 0 && lane == 0) {
       Ring pipe;
       uint32_t issued = 0;
-      const uint64_t keep = l2_policy_evict_last();
+      const uint64_t keep = l2_policy_evict_last(), once = l2_policy_evict_first();
       bool ok = true;
       for (int t = first; t < tiles && ok; t += step) {
-        const int arow = (t % a.tiles_m) * 256 + 128 * rank;
+        const int arow = (t % a.tiles_m) * S::kRows + 128 * rank;
         const int brow = (t / a.tiles_m) * 256 + 128 * rank;
         for (int j = 0; j < a.G; ++j) {
           ok = wait_parity(done + 8 * pipe.idx, pipe.phase ^ 1u, w);
           if (!ok) break;
           const uint32_t bar = full + 8 * pipe.idx;
-          if (leader) mbar_arrive_expect_tx(bar, 2 * kPairStageBytes);
-          const uint32_t bar_c = mapa_shared(bar, 0);
-          tma_load_2d_pair_hint(a_base + pipe.idx * 128 * kKB, &ta, j * kKB, arow, bar_c, keep);
-          tma_load_2d_pair(b_base + pipe.idx * 128 * kKB, &tb, j * kKB, brow, bar_c);
+          const uint32_t as = a_base + pipe.idx * 128 * kKB, bs = b_base + pipe.idx * S::kBBytes;
+          if (leader) mbar_arrive_expect_tx(bar, (PAIR ? 2 : 1) * S::kStageBytes);
+          if (PAIR) {
+            const uint32_t bar_c = mapa_shared(bar, 0);
+            tma_load_2d_pair_hint(as, &ta, j * kKB, arow, bar_c, keep);
+            tma_load_2d_pair(bs, &tb, j * kKB, brow, bar_c);
+          } else {
+            tma_load_2d_hint(bs, &tb, j * kKB, brow, bar, once);
+            tma_load_2d_hint(bs + 128 * kKB, &tb, j * kKB, brow + 128, bar, once);
+            tma_load_2d_hint(as, &ta, j * kKB, arow, bar, keep);
+          }
           issued |= 1u << pipe.idx;
-          pipe.advance(kPairStages);
+          pipe.advance(S::kStages);
         }
       }
-      if (leader) drain_stages<kPairStages>(full, issued, pipe, w);
+      if (leader) drain_stages<S::kStages>(full, issued, pipe, w);
     } else if (warp == 1 && leader) {
       // The whole warp runs the loop, so that its values stay uniform; one lane
       // issues.  A stage and an accumulator are both one block of K, so one
@@ -231,18 +250,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           if (!ok) break;
           tc_fence_after();
           if (elect_one()) {
-            const uint64_t at = static_cast<uint64_t>(pipe.idx) * (128 * kKB / 16);
-            mma_block<256, 256, true>(tmem + acc.idx * kAccCols, ad0 + at, bd0 + at);
-            mma_commit_pair_multicast(done + 8 * pipe.idx, kBoth);
+            const uint64_t ad = ad0 + static_cast<uint64_t>(pipe.idx) * (128 * kKB / 16);
+            const uint64_t bd = bd0 + static_cast<uint64_t>(pipe.idx) * (S::kBBytes / 16);
+            mma_block<S::kRows, 256, PAIR>(tmem + acc.idx * kAccCols, ad, bd);
+            if (PAIR) mma_commit_pair_multicast(done + 8 * pipe.idx, kBoth);
+            else mma_commit_single(done + 8 * pipe.idx);
           }
           __syncwarp();
-          pipe.advance(kPairStages);
+          pipe.advance(S::kStages);
           acc.advance(2);
         }
       }
       // every issued MMA completes before tensor memory is released
       if (elect_one()) {
-        mma_commit_pair(drain);
+        if (PAIR) mma_commit_pair(drain);
+        else mma_commit_single(drain);
         WaitCtx wd = w;
         volatile uint32_t never = 0u;
         wd.abort = &never;
@@ -251,13 +273,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       __syncwarp();
     }
   } else {
-    regs_acquire<kPairEpiRegs>();
+    regs_acquire<kTileEpiRegs>();
     const int q = warp & 3, half = (warp - 4) >> 2;
+    const uint32_t hand_back = PAIR ? mapa_shared(tempty, 0) : tempty;
     const uint32_t buf = staging + (warp - 4) * kStageBufBytes;
     Ring pipe, acc;
     bool ok = true;
     for (int t = first; t < tiles && ok; t += step) {
-      const int row0 = (t % a.tiles_m) * 256 + 128 * rank + q * 32;
+      const int row0 = (t % a.tiles_m) * S::kRows + 128 * rank + q * 32;
       const int col0 = (t / a.tiles_m) * 256 + 128 * half;
       const int row = row0 + lane;
       const float* sa = a.a_scale + static_cast<int64_t>(min(row, a.M - 1)) * a.G;
@@ -289,13 +312,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           if (c == 1) {
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive_remote(mapa_shared(tempty + 8 * acc.idx, 0));
+            if (lane == 0) mbar_arrive_remote(hand_back + 8 * acc.idx);
           }
 #pragma unroll
           for (int i = 0; i < 32; ++i)
             r[32 * c + i] = fma_f32x2(s2, pack_f32x2(x[2 * i], x[2 * i + 1]), r[32 * c + i]);
         }
-        pipe.advance(kPairStages);
+        pipe.advance(S::kStages);
         acc.advance(2);
       }
       if (!ok) break;
@@ -331,9 +354,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
-  cluster_sync_all();
+  if (PAIR) cluster_sync_all();
   tc_fence_after();
-  if (warp == 1) tmem_dealloc_pair(tmem, kTmemCols);
+  if (warp == 1) {
+    if (PAIR) tmem_dealloc_pair(tmem, kTmemCols);
+    else tmem_dealloc_single(tmem, kTmemCols);
+  }
 }
 
 // ------------------------------------------------ few rows: B streamed
@@ -588,20 +614,30 @@ __global__ void __launch_bounds__(RowShape<NP>::kThreads, kRowsPerSm)
 
 // ------------------------------------------------------------- launching
 constexpr int kFewRows = 64;  // rows of A up to which B is streamed past them
+constexpr int kSingleRows = 128;  // and up to which a tile is one CTA's
 
-template <class O>
-cudaError_t launch_pair(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& ty,
-                        const Fp8Args& a, int sms, cudaStream_t s) {
+template <bool PAIR, class O>
+cudaError_t launch_tiles(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& ty,
+                         const Fp8Args& a, int sms, cudaStream_t s) {
+  constexpr int kCtas = PAIR ? 2 : 1, kSmem = TileShape<PAIR>::kSmem;
   static SmemLimit limit;
-  auto* k = flce_fp8_pair_kernel<O>;
-  cudaError_t e = allow_smem(reinterpret_cast<const void*>(k), kPairSmem, &limit);
+  auto* k = flce_fp8_tile_kernel<O, PAIR>;
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(k), kSmem, &limit);
   if (e != cudaSuccess) return e;
   const int64_t tiles = static_cast<int64_t>(a.tiles_m) * a.tiles_v;
-  const int pairs = static_cast<int>(std::min<int64_t>(tiles, sms / 2));
-  e = launch_overlapped(k, dim3(2 * pairs), dim3(kPairThreads), kPairSmem, s, 1, ta, tb, ty, a);
+  const int at_once = static_cast<int>(std::min<int64_t>(tiles, sms / kCtas));
+  e = launch_overlapped(k, dim3(kCtas * at_once), dim3(kTileThreads), kSmem, s, kCtas, ta, tb, ty,
+                        a);
   note_launch();
   note_wait_limit(a.wait_limit_ns);
   return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+template <class O>
+cudaError_t launch_tiles_for(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& ty,
+                             const Fp8Args& a, bool pair, int sms, cudaStream_t s) {
+  return pair ? launch_tiles<true, O>(ta, tb, ty, a, sms, s)
+              : launch_tiles<false, O>(ta, tb, ty, a, sms, s);
 }
 
 template <int NP, class O>
@@ -688,7 +724,8 @@ extern "C" flce_status flce_matmul_fp8(const void* A, int64_t lda, const float* 
     err = out_dtype == FLCE_BF16 ? launch_rows_for<__nv_bfloat16>(ta, tb, a, np, sms, s)
                                  : launch_rows_for<float>(ta, tb, a, np, sms, s);
   } else {
-    a.tiles_m = static_cast<int>(tiles_m);
+    const bool pair = M > kSingleRows;
+    a.tiles_m = static_cast<int>(tiles_m);  // 1 without pairs
     a.tiles_v = static_cast<int>(tiles_v);
     a.tma_store = aligned_to(y, 16) && ldy * e % 16 == 0;
     CUtensorMap ty = tb;  // not used without TMA stores
@@ -698,8 +735,8 @@ extern "C" flce_status flce_matmul_fp8(const void* A, int64_t lda, const float* 
                    out_dtype == FLCE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
                                           : CU_TENSOR_MAP_DATA_TYPE_FLOAT32))
       return FLCE_ERR_CUDA;
-    err = out_dtype == FLCE_BF16 ? launch_pair<__nv_bfloat16>(ta, tb, ty, a, sms, s)
-                                 : launch_pair<float>(ta, tb, ty, a, sms, s);
+    err = out_dtype == FLCE_BF16 ? launch_tiles_for<__nv_bfloat16>(ta, tb, ty, a, pair, sms, s)
+                                 : launch_tiles_for<float>(ta, tb, ty, a, pair, sms, s);
   }
   return err == cudaSuccess ? FLCE_OK : FLCE_ERR_CUDA;
 }
