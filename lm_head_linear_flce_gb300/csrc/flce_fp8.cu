@@ -23,35 +23,43 @@ namespace {
 constexpr int kKB = 128;      // bytes (= columns of K) per pipeline stage: one scale block
 constexpr int kMmaK8 = 32;    // K per MMA
 
-// ------------------------------------------------ many rows: CTA pairs
+// ------------------------------------------------ many rows: tiles
 // A tile is 256 rows of A x 256 rows of B on a 2-CTA cluster (each CTA stages
-// 128 rows of either, 32 KB a stage, and holds 128 x 256 of the result).  Eight
-// epilogue warps per CTA: two per TMEM lane quarter, 128 columns each, so that
-// the result is 128 registers a thread.  Three warpgroups: the first (TMA, MMA)
-// hands registers to the two of the epilogue; 384 threads launch with 168 each,
-// 64512 in all = 128 * 56 + 256 * 224.
+// 128 rows of either, 32 KB a stage, and holds 128 x 256 of the result), or 128
+// rows of A x 256 or 128 of B on a CTA by itself.  Eight epilogue warps per CTA:
+// two per TMEM lane quarter, half of the columns each, so that the result is 128
+// registers a thread at most.  Three warpgroups: the first (TMA, MMA) hands
+// registers to the two of the epilogue; 384 threads launch with 168 each, 64512
+// in all = 128 * 56 + 256 * 224.
 //
-// Bound by the tensor cores, and in a loop of seconds by the board's power:
-// 4096 x 152064 x 3584 to bf16 takes 1.53 to 1.63 ms (2.7 to 2.9 PFLOP/s) by
-// itself, 1.68 ms in a loop; 256 x 151936 x 4096 to float32 takes 141 us, 5.5 TB/s.
 // A block's scales change with every 128 columns of K, so its products go through
-// registers (packed fma) before the next block may add to them; the two 256-column
-// accumulators fill TMEM and hide that.  Also measured, 4096 x 152064 x 3584
-// against 2.7 to 2.9 PFLOP/s: three accumulators of 160 columns 2.2, sixteen epilogue
-// warps 1.9, accumulators in halves 1.5; a second staging buffer for the stores and
-// scales fetched a tile ahead changed nothing.
+// registers (packed fma) before the next block may add to them; accumulators that
+// fill TMEM, two of 256 columns or four of 128, hide that.
+//
+// Bound by the tensor cores, and in a loop of seconds by the board's power: pairs
+// take 1.53 to 1.63 ms for 4096 x 152064 x 3584 to bf16 (2.7 to 2.9 PFLOP/s), 1.68
+// ms in a loop.  Up to 128 rows it is bound by reading B, of which a CTA by
+// itself has 32 KB a block under way where one of a pair has 16: 128 x 151936 x
+// 4096 to float32 takes 112 us (6.2 TB/s), with pairs 127.  Also measured, pairs at
+// 4096 x 152064 x 3584: three accumulators of 160 columns 2.2 PFLOP/s, sixteen
+// epilogue warps 1.9, accumulators in halves 1.5; a second staging buffer for the
+// stores and scales fetched a tile ahead changed nothing.
 constexpr int kTileThreads = 384;  // warp 0 TMA, warp 1 MMA, warps 4..11 epilogue
 constexpr int kTileEpi = 8;
 constexpr int kTileLeanRegs = 56;
 constexpr int kTileEpiRegs = 224;
-template <bool PAIR>
+template <bool PAIR, int N>
 struct TileShape {
-  static constexpr int kRows = PAIR ? 256 : 128;   // rows of A, 256 of B
-  static constexpr int kBBytes = (PAIR ? 128 : 256) * kKB;  // of B in this CTA's stage
+  static constexpr int kRows = PAIR ? 256 : 128;      // rows of A, N of B
+  static constexpr int kBRows = PAIR ? N / 2 : N;     // of B in this CTA's stage
+  static constexpr int kBBytes = kBRows * kKB;
   static constexpr int kStageBytes = 128 * kKB + kBBytes;
-  static constexpr int kStages = PAIR ? 6 : 4;
+  static constexpr int kStages = 192 * 1024 / kStageBytes;
+  static constexpr int kAccs = kTmemCols / N;
+  static constexpr int kCols = N / 2;                 // of an epilogue warp
   static constexpr int kSmem = kStages * kStageBytes + kTileEpi * kStageBufBytes + 1024 + 256;
-  static_assert(kStages >= 2);  // accumulators: a stage's barrier serves for its own
+  // a stage's barrier serves for its accumulator too, so at most kStages are ahead
+  static_assert(kStages >= kAccs);
 };
 constexpr uint16_t kBoth = 0x3;
 
@@ -147,12 +155,12 @@ __device__ __forceinline__ void store_chunk(const Fp8Args& a, const CUtensorMap*
   __syncwarp();
 }
 
-template <class O, bool PAIR>
+template <class O, bool PAIR, int N>
 __global__ void __launch_bounds__(kTileThreads, 1)
     flce_fp8_tile_kernel(const __grid_constant__ CUtensorMap ta,
                          const __grid_constant__ CUtensorMap tb,
                          const __grid_constant__ CUtensorMap ty, const Fp8Args a) {
-  using S = TileShape<PAIR>;
+  using S = TileShape<PAIR, N>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t a_base = (raw + 1023u) & ~1023u;
@@ -161,7 +169,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   const uint32_t full = staging + kTileEpi * kStageBufBytes;
   const uint32_t done = full + 8 * S::kStages;
   const uint32_t tempty = done + 8 * S::kStages;
-  const uint32_t drain = tempty + 16;
+  const uint32_t drain = tempty + 8 * S::kAccs;
   auto* slot = reinterpret_cast<uint32_t*>(smem_raw + (drain + 8 - raw));
   volatile uint32_t* abort_flag = slot + 1;
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -172,7 +180,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       mbar_init(full + 8 * i, 1);  // the leader's producer, for both CTAs' bytes
       mbar_init(done + 8 * i, 1);  // the leader's multicast commit
     }
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < S::kAccs; ++i)
       mbar_init(tempty + 8 * i, (PAIR ? 2 : 1) * kTileEpi);  // every epilogue warp
     mbar_init(drain, 1);
     *abort_flag = 0u;
@@ -212,7 +220,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       bool ok = true;
       for (int t = first; t < tiles && ok; t += step) {
         const int arow = (t % a.tiles_m) * S::kRows + 128 * rank;
-        const int brow = (t / a.tiles_m) * 256 + 128 * rank;
+        const int brow = (t / a.tiles_m) * N + S::kBRows * rank;
         for (int j = 0; j < a.G; ++j) {
           ok = wait_parity(done + 8 * pipe.idx, pipe.phase ^ 1u, w);
           if (!ok) break;
@@ -224,8 +232,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             tma_load_2d_pair_hint(as, &ta, j * kKB, arow, bar_c, keep);
             tma_load_2d_pair(bs, &tb, j * kKB, brow, bar_c);
           } else {
-            tma_load_2d_hint(bs, &tb, j * kKB, brow, bar, once);
-            tma_load_2d_hint(bs + 128 * kKB, &tb, j * kKB, brow + 128, bar, once);
+#pragma unroll
+            for (int i = 0; i < S::kBRows; i += 128)
+              tma_load_2d_hint(bs + i * kKB, &tb, j * kKB, brow + i, bar, once);
             tma_load_2d_hint(as, &ta, j * kKB, arow, bar, keep);
           }
           issued |= 1u << pipe.idx;
@@ -252,13 +261,13 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           if (elect_one()) {
             const uint64_t ad = ad0 + static_cast<uint64_t>(pipe.idx) * (128 * kKB / 16);
             const uint64_t bd = bd0 + static_cast<uint64_t>(pipe.idx) * (S::kBBytes / 16);
-            mma_block<S::kRows, 256, PAIR>(tmem + acc.idx * kAccCols, ad, bd);
+            mma_block<S::kRows, N, PAIR>(tmem + acc.idx * N, ad, bd);
             if (PAIR) mma_commit_pair_multicast(done + 8 * pipe.idx, kBoth);
             else mma_commit_single(done + 8 * pipe.idx);
           }
           __syncwarp();
           pipe.advance(S::kStages);
-          acc.advance(2);
+          acc.advance(S::kAccs);
         }
       }
       // every issued MMA completes before tensor memory is released
@@ -281,14 +290,14 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     bool ok = true;
     for (int t = first; t < tiles && ok; t += step) {
       const int row0 = (t % a.tiles_m) * S::kRows + 128 * rank + q * 32;
-      const int col0 = (t / a.tiles_m) * 256 + 128 * half;
+      const int col0 = (t / a.tiles_m) * N + S::kCols * half;
       const int row = row0 + lane;
       const float* sa = a.a_scale + static_cast<int64_t>(min(row, a.M - 1)) * a.G;
       // a half past V has no scale block of its own; its columns are not stored
       const float* sb = a.b_scale + static_cast<int64_t>(min(col0, a.V - 1) / kScaleGroup) * a.G;
-      uint64_t r[64];
+      uint64_t r[S::kCols / 2];
 #pragma unroll
-      for (int i = 0; i < 64; ++i) r[i] = 0;
+      for (int i = 0; i < S::kCols / 2; ++i) r[i] = 0;
       // scales are fetched two blocks ahead of their use
       float sa0 = sa[0], sb0 = sb[0], sa1 = sa[min(1, a.G - 1)], sb1 = sb[min(1, a.G - 1)];
       for (int j = 0; j < a.G; ++j) {
@@ -302,14 +311,14 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         if (!ok) break;
         tc_fence_after();
         const uint32_t tbase = tmem + (static_cast<uint32_t>(q * 32) << 16) +
-                               acc.idx * kAccCols + half * 128;
+                               acc.idx * N + half * S::kCols;
         const uint32_t su = __float_as_uint(s);
         const uint64_t s2 = pack_f32x2(su, su);
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
+        for (int c = 0; c < S::kCols / 64; ++c) {
           uint32_t x[64];
           tmem_ld(tbase + 64 * c, x);
-          if (c == 1) {
+          if (c + 1 == S::kCols / 64) {
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive_remote(hand_back + 8 * acc.idx);
@@ -319,13 +328,13 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             r[32 * c + i] = fma_f32x2(s2, pack_f32x2(x[2 * i], x[2 * i + 1]), r[32 * c + i]);
         }
         pipe.advance(S::kStages);
-        acc.advance(2);
+        acc.advance(S::kAccs);
       }
       if (!ok) break;
       constexpr int kWords = 32;                  // 128 bytes of one row per chunk
       constexpr int kPairs = sizeof(O) == 2 ? 32 : 16;  // register pairs per chunk
 #pragma unroll
-      for (int c = 0; c < 64 / kPairs; ++c) {
+      for (int c = 0; c < S::kCols / 2 / kPairs; ++c) {
         const int x = col0 + c * 2 * kPairs;
         if (x >= a.V) break;  // warp-uniform
         uint32_t o[kWords];
@@ -363,7 +372,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 }
 
 // ------------------------------------------------ few rows: B streamed
-// With at most 64 rows of A the product is bound by reading B once.  The roles
+// With few rows of A the product is bound by reading B once.  The roles
 // of the operands are swapped: 128 rows of B are the MMA's M, the rows of A
 // (padded to NP) its N, so nothing of the tensor cores' work is wasted on
 // padding to 128 rows of A.  Two CTAs per SM, whose rings keep about 190 KB in
@@ -376,7 +385,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 // A column's scale differs from lane to lane here (it is a row of A), so each
 // block costs the epilogue a scale per element from shared memory.  Of 151936 x
 // 4096 bytes: 8 rows 93.5 us (6.7 TB/s), 32 103, 48 105, 64 110, each to float32;
-// NP = 128 took 177 where the pair kernel takes 126.  NP = 48 is worth having
+// NP = 128 took 177 where tiles take 112.  NP = 48 is worth having
 // where the rows of A start inside a 128-byte line and so cost two reads each:
 // 37 x 32003 x 2064 19.7 us, padded to 64 21.8.
 template <int NP>
@@ -462,7 +471,7 @@ __global__ void __launch_bounds__(RowShape<NP>::kThreads, kRowsPerSm)
       drain_stages<S::kStages>(full, issued, pipe, w);
     }
   } else if (warp == 1) {
-    // as in the pair kernel: the whole warp in the loop, one lane issuing, one
+    // as in the tile kernel: the whole warp in the loop, one lane issuing, one
     // commit a block
     const uint64_t bd0 = smem_desc_sw128(base, 0, 1024);
     const uint64_t ad0 = smem_desc_sw128(base + 128 * kKB, 0, 1024);
@@ -613,15 +622,20 @@ __global__ void __launch_bounds__(RowShape<NP>::kThreads, kRowsPerSm)
 }
 
 // ------------------------------------------------------------- launching
-constexpr int kFewRows = 64;  // rows of A up to which B is streamed past them
-constexpr int kSingleRows = 128;  // and up to which a tile is one CTA's
+// Rows of A up to which B is streamed past them: 48, and 64 where the tiles of B
+// are so few that K is split (64 x 4000 x 4096: 10.4 us, in tiles 11.4; 64 x 32003 x
+// 2064 20.0, in tiles 17.1).
+constexpr int kFewRows = 48, kFewRowsSplit = 64;
 
-template <bool PAIR, class O>
+template <bool PAIR, int N, class O>
 cudaError_t launch_tiles(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& ty,
-                         const Fp8Args& a, int sms, cudaStream_t s) {
-  constexpr int kCtas = PAIR ? 2 : 1, kSmem = TileShape<PAIR>::kSmem;
+                         Fp8Args a, int sms, cudaStream_t s) {
+  using S = TileShape<PAIR, N>;
+  constexpr int kCtas = PAIR ? 2 : 1, kSmem = S::kSmem;
+  a.tiles_m = (a.M + S::kRows - 1) / S::kRows;
+  a.tiles_v = (a.V + N - 1) / N;
   static SmemLimit limit;
-  auto* k = flce_fp8_tile_kernel<O, PAIR>;
+  auto* k = flce_fp8_tile_kernel<O, PAIR, N>;
   cudaError_t e = allow_smem(reinterpret_cast<const void*>(k), kSmem, &limit);
   if (e != cudaSuccess) return e;
   const int64_t tiles = static_cast<int64_t>(a.tiles_m) * a.tiles_v;
@@ -635,9 +649,19 @@ cudaError_t launch_tiles(const CUtensorMap& ta, const CUtensorMap& tb, const CUt
 
 template <class O>
 cudaError_t launch_tiles_for(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& ty,
-                             const Fp8Args& a, bool pair, int sms, cudaStream_t s) {
-  return pair ? launch_tiles<true, O>(ta, tb, ty, a, sms, s)
-              : launch_tiles<false, O>(ta, tb, ty, a, sms, s);
+                             const Fp8Args& a, int sms, cudaStream_t s) {
+  // Rounds of tiles, times what a round takes: a pair's tile 16, a CTA's of 256
+  // columns 16.5, of 128 columns 11 (4096 x 4000 bytes: 65 rows 15.6, 15.6 and
+  // 11.4 us; 256 x 151936 x 4096 137, 146 and 165; 300 x 151936 x 4096, whose last
+  // pairs would be half empty, 232, 196 and 228).
+  const auto rounds = [&](int64_t m, int64_t n, int64_t at_once) {
+    return ((a.M + m - 1) / m * ((a.V + n - 1) / n) + at_once - 1) / at_once;
+  };
+  const int64_t pair = 32 * rounds(256, 256, sms / 2), single = 33 * rounds(128, 256, sms),
+                narrow = 22 * rounds(128, 128, sms);
+  if (narrow < std::min(pair, single)) return launch_tiles<false, 128, O>(ta, tb, ty, a, sms, s);
+  return single < pair ? launch_tiles<false, 256, O>(ta, tb, ty, a, sms, s)
+                       : launch_tiles<true, 256, O>(ta, tb, ty, a, sms, s);
 }
 
 template <int NP, class O>
@@ -698,8 +722,7 @@ extern "C" flce_status flce_matmul_fp8(const void* A, int64_t lda, const float* 
                        {b_scale, span_bytes(gv, gk, gk, 4)}};
   for (const Range& r : ins)
     if (ranges_overlap(yr, r)) return FLCE_ERR_INVALID_ARG;
-  const int64_t tiles_m = (M + 255) / 256, tiles_v = (V + 255) / 256;
-  if (tiles_m * tiles_v > kMaxDim) return FLCE_ERR_UNSUPPORTED_SHAPE;
+  if ((M + 127) / 128 * gv > kMaxDim) return FLCE_ERR_UNSUPPORTED_SHAPE;
   int sms = 0;
   const flce_status st = check_device(&sms);
   if (st != FLCE_OK) return st;
@@ -717,16 +740,13 @@ extern "C" flce_status flce_matmul_fp8(const void* A, int64_t lda, const float* 
   CUtensorMap ta, tb;
   if (!make_tmap(&tb, B, K, V, ldb, kKB, 128, kU8)) return FLCE_ERR_CUDA;
   cudaError_t err;
-  if (M <= kFewRows) {
+  if (M <= (gv <= sms ? kFewRowsSplit : kFewRows)) {
     const int np = M <= 16 ? 16 : M <= 32 ? 32 : M <= 48 ? 48 : 64;
     a.tiles_v = static_cast<int>(gv);
     if (!make_tmap(&ta, A, K, M, lda, kKB, np, kU8)) return FLCE_ERR_CUDA;
     err = out_dtype == FLCE_BF16 ? launch_rows_for<__nv_bfloat16>(ta, tb, a, np, sms, s)
                                  : launch_rows_for<float>(ta, tb, a, np, sms, s);
   } else {
-    const bool pair = M > kSingleRows;
-    a.tiles_m = static_cast<int>(tiles_m);  // 1 without pairs
-    a.tiles_v = static_cast<int>(tiles_v);
     a.tma_store = aligned_to(y, 16) && ldy * e % 16 == 0;
     CUtensorMap ty = tb;  // not used without TMA stores
     if (!make_tmap(&ta, A, K, M, lda, kKB, 128, kU8)) return FLCE_ERR_CUDA;
@@ -735,8 +755,8 @@ extern "C" flce_status flce_matmul_fp8(const void* A, int64_t lda, const float* 
                    out_dtype == FLCE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
                                           : CU_TENSOR_MAP_DATA_TYPE_FLOAT32))
       return FLCE_ERR_CUDA;
-    err = out_dtype == FLCE_BF16 ? launch_tiles_for<__nv_bfloat16>(ta, tb, ty, a, pair, sms, s)
-                                 : launch_tiles_for<float>(ta, tb, ty, a, pair, sms, s);
+    err = out_dtype == FLCE_BF16 ? launch_tiles_for<__nv_bfloat16>(ta, tb, ty, a, sms, s)
+                                 : launch_tiles_for<float>(ta, tb, ty, a, sms, s);
   }
   return err == cudaSuccess ? FLCE_OK : FLCE_ERR_CUDA;
 }

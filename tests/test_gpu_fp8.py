@@ -61,6 +61,15 @@ def test_matches_the_float64_product(M, V, K, out):
     check(y, a, sa, b, sb, out)
 
 
+# several tiles for every CTA or pair, of each kind of tile
+@pytest.mark.parametrize("M,V,K", [(60, 20003, 144), (90, 20001, 160), (300, 20099, 272),
+                                   (250, 39001, 144), (130, 10007, 400), (1000, 9001, 128)])
+def test_many_tiles(M, V, K):
+    a, sa, b, sb = operands(M, V, K, 5, 1.0)
+    for out in (BF, F32):
+        check(flce.matmul_fp8(a, sa, b, sb, out_dtype=out), a, sa, b, sb, out)
+
+
 def test_every_number_of_rows():
     # each padding of the rows, filled, one below and one above; rows of 144 bytes
     g = torch.Generator().manual_seed(3)
