@@ -62,11 +62,20 @@ template <bool WIDE>
 struct Counts {
   static constexpr uint32_t kPrompt = WIDE ? 0x80000000u : 0x8000u;
   uint32_t* words;
-  __device__ void add(int c, bool prompt) {
-    const int sh = WIDE ? 0 : 16 * (c & 1);
-    uint32_t* w = words + (WIDE ? c : c >> 1);
-    if (prompt) atomicOr(w, kPrompt << sh);
-    else atomicAdd(w, 1u << sh);
+  // Adds one to counter c, or sets its prompt bit; nothing if not `mine`.  (Both
+  // updates under predicates: 128 ids of a warp rarely take one way.)
+  __device__ __forceinline__ void add(uint32_t c, bool mine, bool prompt) const {
+    const uint32_t w = static_cast<uint32_t>(__cvta_generic_to_shared(words)) +
+                       (WIDE ? 4 * c : (2 * c & ~3u));
+    const uint32_t sh = WIDE ? 0 : 16 * (c & 1);
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %0, 0;\n\t"
+        "setp.ne.u32 q, %1, 0;\n\t"
+        "@p red.shared.add.u32 [%2], %3;\n\t"
+        "@q red.shared.or.b32 [%2], %4;\n\t}" ::"r"(static_cast<uint32_t>(mine && !prompt)),
+        "r"(static_cast<uint32_t>(mine && prompt)), "r"(w), "r"(1u << sh), "r"(kPrompt << sh)
+        : "memory");
   }
   __device__ uint32_t at(int c) const {
     return WIDE ? words[c] : words[c >> 1] >> 16 * (c & 1) & 0xffffu;
@@ -149,32 +158,32 @@ __device__ __forceinline__ uint32_t column(int64_t t, int v0) {
 template <int THREADS>
 constexpr int kIdLoads = THREADS <= 256 ? 4 : 2;
 template <int THREADS, class I, class F>
-__device__ __forceinline__ void each_id(const I* t, int64_t len, int v0, const F& f) {
+__device__ __forceinline__ void each_id(const I* t, int len, int v0, const F& f) {
   constexpr int kPer = 16 / sizeof(I), kLoads = kIdLoads<THREADS>;
-  const int64_t head = min(len, static_cast<int64_t>(
-                                    (0 - reinterpret_cast<uintptr_t>(t)) / sizeof(I) % kPer));
-  const int64_t packs = (len - head) / kPer, tail = head + packs * kPer;
-  const int edges = static_cast<int>(head + len - tail);
-  if (threadIdx.x < edges) {
-    const int64_t i = threadIdx.x < head ? threadIdx.x : tail + threadIdx.x - head;
+  const int tid = threadIdx.x;
+  const int head =
+      min(len, static_cast<int>((0 - reinterpret_cast<uintptr_t>(t)) / sizeof(I) % kPer));
+  const int packs = (len - head) / kPer, tail = head + packs * kPer;
+  if (tid < head + len - tail) {
+    const int i = tid < head ? tid : tail + tid - head;
     f(column(t[i], v0), i);
   }
   const uint4* p = reinterpret_cast<const uint4*>(t + head);
   uint4 next[kLoads];
-  const auto fetch = [&](int64_t k0) {
+  const auto fetch = [&](int k0) {  // k0 + THREADS * kLoads < 2^31 / kPer + 4096
 #pragma unroll
     for (int u = 0; u < kLoads; ++u)
       if (k0 + u * THREADS < packs) next[u] = p[k0 + u * THREADS];
   };
-  fetch(threadIdx.x);
-  for (int64_t k0 = threadIdx.x; k0 < packs; k0 += THREADS * kLoads) {
+  fetch(tid);
+  for (int k0 = tid; k0 < packs; k0 += THREADS * kLoads) {
     uint4 now[kLoads];
 #pragma unroll
     for (int u = 0; u < kLoads; ++u) now[u] = next[u];
     fetch(k0 + THREADS * kLoads);
 #pragma unroll
     for (int u = 0; u < kLoads; ++u) {
-      const int64_t k = k0 + u * THREADS;
+      const int k = k0 + u * THREADS;
       if (k >= packs) break;
       alignas(16) I ids[kPer];
       *reinterpret_cast<uint4*>(ids) = now[u];
@@ -215,7 +224,7 @@ __global__ void __launch_bounds__(THREADS, kPerSm<THREADS>)
   // What depends on nothing else is asked for at once: the row's scalars and the
   // thread's first windows.
   const int64_t len0 = a.lengths ? a.lengths[b] : a.L;
-  const int64_t prompt = a.prompt_lengths ? a.prompt_lengths[b] : 0;
+  const int prompt = a.prompt_lengths ? a.prompt_lengths[b] : 0;
   const float rep = a.repetition ? a.repetition[b] : 1.f;
   const float freq = a.frequency ? a.frequency[b] : 0.f;
   const float pres = a.presence ? a.presence[b] : 0.f;
@@ -232,14 +241,17 @@ __global__ void __launch_bounds__(THREADS, kPerSm<THREADS>)
   Counts<WIDE> counts{mask + mask_words(a.cols)};
   uint32_t* bias = counts.words + (WIDE ? slots : slots / 2);
   const int words = (WIDE ? slots : slots / 2) + (BIAS == kIndexedBias ? slots / 2 : 0);
-  // The thread's window k (if it is whole) into the ring; one group per window.
-  const auto fetch = [&](int k, int slot) {
-    if (k >= w_lo && k < w_hi && !a.in_place)
-      copy_async<sizeof(Raw)>(ring + slot * THREADS, in_row + kWin * k - shift);
+  // A thread's whole windows are k0 and every THREADS on; one group per window.
+  const int k0 = w_lo + threadIdx.x;
+  const int w_fetch = a.in_place ? 0 : w_hi;
+  const T* src = in_row - shift + kWin * k0;
+  const auto fetch = [&](const T* from, int k, Raw* slot) {
+    if (k < w_fetch) copy_async<sizeof(Raw)>(slot, from);
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
 #pragma unroll
-  for (int i = 0; i < kSlots; ++i) fetch(threadIdx.x + i * THREADS, i);
+  for (int i = 0; i < kSlots; ++i)
+    fetch(src + i * kWin * THREADS, k0 + i * THREADS, ring + i * THREADS);
 
   // mask word i holds columns 32 (v0 / 32 + i) and on
   const int first_word = v0 >> 5;
@@ -253,9 +265,9 @@ __global__ void __launch_bounds__(THREADS, kPerSm<THREADS>)
     reinterpret_cast<uint4*>(counts.words)[i] = make_uint4(0, 0, 0, 0);
   if (threadIdx.x == 0) n_listed = 0;
   __syncthreads();
-  const int64_t len = max(int64_t{0}, min(len0, a.L));
-  const auto count = [&](uint32_t c, int64_t i) {  // entry i, c columns behind v0
-    if (c < static_cast<uint32_t>(cols)) counts.add(static_cast<int>(c) + shift, i < prompt);
+  const int len = static_cast<int>(max(int64_t{0}, min(len0, a.L)));
+  const auto count = [&](uint32_t c, int i) {  // entry i, c columns behind v0
+    counts.add(c + shift, c < static_cast<uint32_t>(cols), i < prompt);
   };
   if (a.tokens_int64)
     each_id<THREADS>(static_cast<const int64_t*>(a.tokens) + b * a.ld_tokens, len, v0, count);
@@ -284,59 +296,64 @@ __global__ void __launch_bounds__(THREADS, kPerSm<THREADS>)
   }
   __syncthreads();
 
-  // One column with its counter n and bias entry e (0: none).
+  // One column with its counter n and bias entry e (0: none).  The division is by
+  // a row's one penalty: its reciprocal, unless that is near the type's ends.
   const uint32_t count_bits = WIDE || prompt > 0 ? ~Counts<WIDE>::kPrompt : ~0u;
+  const float inverse = 1.f / rep;
+  const bool tame = rep > 1e-30f && rep < 1e30f;
   const auto apply = [&](float l, uint32_t n, uint32_t e) {
-    if (n) {
-      l = l > 0.f ? l / rep : l * rep;
-      const uint32_t c = n & count_bits;
-      l -= freq * static_cast<float>(c) + (c ? pres : 0.f);
-    }
+    const uint32_t c = n & count_bits;
+    const float up = tame ? l * inverse : l / rep;
+    const float x = (l > 0.f ? up : l * rep) - fmaf(freq, static_cast<float>(c), c ? pres : 0.f);
+    if (n) l = x;
     if (BIAS != kNoBias && e) l += a.bias_values[b * a.n_bias + e - 1];
     return l;
   };
-  int slot = 0;
-  for (int k = threadIdx.x; k < windows; k += THREADS) {
+  const int bit0 = v0 - shift - 32 * first_word;  // of a window's column 0, at k = 0
+  // Columns of windows that are not whole, or all where the rows' alignments differ.
+  const int edges = (windows - (w_hi - w_lo)) * kWin;
+  for (int i = threadIdx.x; i < edges; i += THREADS) {
+    const int k = i / kWin < w_lo ? i / kWin : i / kWin - w_lo + w_hi;
+    const int at = kWin * k + i % kWin, c = at - shift, bit = bit0 + at;
+    if (c < 0 || c >= cols) continue;
+    uint32_t e = 0;
+    if constexpr (BIAS == kIndexedBias) e = bias[at >> 1] >> 16 * (at & 1) & 0xffffu;
+    const bool ok = !a.allowed || (mask[bit >> 5] >> (bit & 31) & 1);
+    store_f(out_row + c, ok ? apply(load_f(in_row + c), counts.at(at), e) : -INFINITY);
+  }
+  Raw* slot = ring;
+  O* dst = out_row - shift + kWin * k0;
+  for (int k = k0; k < w_hi; k += THREADS) {
     asm volatile("cp.async.wait_group %0;" ::"n"(kSlots - 1) : "memory");
-    const int c0 = kWin * k;  // the window's first counter
-    const auto n4 = counts.window(c0);
+    const auto n4 = counts.window(kWin * k);
     uint2 e4 = make_uint2(0, 0);
-    if constexpr (BIAS == kIndexedBias) e4 = *reinterpret_cast<const uint2*>(bias + (c0 >> 1));
+    if constexpr (BIAS == kIndexedBias) e4 = *reinterpret_cast<const uint2*>(bias + kWin / 2 * k);
     const bool some = any(n4) || (BIAS == kIndexedBias && any(e4));
     uint32_t ok = 0xfu;  // which of the window's columns are allowed
     if (a.allowed) {
-      // the first window may begin up to three columns before the block
-      const int bit = v0 + c0 - shift - 32 * first_word, w = max(bit, 0) >> 5;
-      ok = bit < 0 ? mask[0] << -bit : __funnelshift_r(mask[w], mask[w + 1], bit & 31);
+      const int bit = bit0 + kWin * k, w = bit >> 5;
+      ok = __funnelshift_r(mask[w], mask[w + 1], bit & 31) & 0xfu;
     }
-    if (k >= w_lo && k < w_hi) {
-      if (!(a.in_place && !some && (ok & 0xfu) == 0xfu)) {  // in place: not touched
-        float l[kWin];
-        floats(a.in_place ? load_raw(in_row + c0 - shift) : ring[slot * THREADS], l);
-        if (some) {
-          uint32_t n[kWin], e[kWin];
-          unpack(n4, n);
-          unpack(e4, e);
+    if (!(a.in_place && !some && ok == 0xfu)) {  // in place: not touched
+      float l[kWin];
+      floats(a.in_place ? load_raw(src) : *slot, l);
+      if (some) {
+        uint32_t n[kWin], e[kWin];
+        unpack(n4, n);
+        unpack(e4, e);
 #pragma unroll
-          for (int j = 0; j < kWin; ++j) l[j] = apply(l[j], n[j], e[j]);
-        }
+        for (int j = 0; j < kWin; ++j) l[j] = apply(l[j], n[j], e[j]);
+      }
+      if (ok != 0xfu) {
 #pragma unroll
         for (int j = 0; j < kWin; ++j) l[j] = ok >> j & 1 ? l[j] : -INFINITY;
-        store_window(out_row + c0 - shift, l);
       }
-    } else {
-      uint32_t n[kWin], e[kWin];
-      unpack(n4, n);
-      unpack(e4, e);
-#pragma unroll
-      for (int j = 0; j < kWin; ++j) {
-        const int c = c0 - shift + j;
-        if (c < 0 || c >= cols) continue;
-        store_f(out_row + c, ok >> j & 1 ? apply(load_f(in_row + c), n[j], e[j]) : -INFINITY);
-      }
+      store_window(dst, l);
     }
-    fetch(k + kSlots * THREADS, slot);
-    slot = slot + 1 == kSlots ? 0 : slot + 1;
+    fetch(src + kSlots * kWin * THREADS, k + kSlots * THREADS, slot);
+    slot = slot == ring + (kSlots - 1) * THREADS ? ring : slot + THREADS;
+    src += kWin * THREADS;
+    dst += kWin * THREADS;
   }
   asm volatile("cp.async.wait_group 0;" ::: "memory");
   if constexpr (BIAS == kListedBias) {
