@@ -407,13 +407,15 @@ cudaError_t run_process(const void* logits, void* out, int64_t B, ProcessArgs a,
   const int bias = a.n_bias == 0 ? kNoBias : a.n_bias <= kBiasList ? kListedBias : kIndexedBias;
   const int per_col = (wide ? 4 : 2) + (bias == kIndexedBias ? 2 : 0);
   // Blocks a row, n.  `per` of them share an SM, so that the SMs take
-  // ceil(B n / (per SMs)) turns, each as long as a block's columns, the row's
-  // history, which every block reads (an id costs a quarter of a column, and a
-  // quarter more for each block that reads beside it), and a start worth some
-  // 4096 columns.  Taken is the n with the least of that, of those that fill
-  // their turns; blocks have 1024 columns at least and fit into shared memory.
-  // (8 x 152064 bf16, histories of 32768: 1 block an SM 11 us, 2 13, 4 16; without
-  // histories 2 blocks 4.2 us, 1 4.9, 4 5.5.)
+  // ceil(B n / (per SMs)) turns.  A turn is as long as a block's columns, three
+  // tenths more for each block beside it; for each of its blocks the row's history,
+  // which every block reads (an id costs about a column), and some 1024 columns of
+  // setting up; and a start of some 2048.  Taken is the n with the least of that, of
+  // those that fill their turns; blocks have 1024 columns at least and fit into
+  // shared memory.  (Timed for 1 to 1024 rows and histories of up to 32768 this n is
+  // 2% slower than the best one on average, 24% at worst.  16 x 152064 bf16,
+  // histories of 32768: 1 block an SM 11.3 us, 2 14.5, 4 16.8; 8 rows without
+  // histories: 4.2, 3.6, 4.2.)
   const auto smem_of = [&](int64_t cols) {  // of a block with 512 threads
     return 512 * kRingBytes<512> + 8 * kBiasList + 1024 + cols * (8 * per_col + 1) / 8;
   };
@@ -427,7 +429,7 @@ cudaError_t run_process(const void* logits, void* out, int64_t B, ProcessArgs a,
     const int64_t per = cols <= kSmallCols ? kPerSm<256>
                                            : std::min<int64_t>(kPerSm<512>, kSmSmem / smem_of(cols));
     const int64_t at_once = std::min(per, (B * n + sms - 1) / sms);
-    const int64_t turn = cols + a.L / 4 * (at_once + 1) + 4096;
+    const int64_t turn = cols + cols * 3 * (at_once - 1) / 10 + at_once * (a.L + 1024) + 2048;
     const int64_t cost = (B * n + per * sms - 1) / (per * sms) * turn;
     if (cost < best) best = cost, blocks = n;
     if (n == finest) break;
