@@ -199,6 +199,39 @@ __device__ __forceinline__ void each_id(const I* t, int len, int v0, const F& f)
   }
 }
 
+// The windows of a block of `cols` columns, the first starting `shift` columns
+// before them: `all` of them, of which [lo, hi) lie wholly inside (none where
+// `whole` is false, or where the columns do not fill one).
+struct Windows {
+  int all, lo, hi;
+};
+__host__ __device__ constexpr Windows windows_of(int shift, int cols, bool whole) {
+  const int all = (shift + cols + kWin - 1) / kWin;
+  if (!whole) return {all, all, all};
+  const int lo = (shift + kWin - 1) / kWin, hi = (shift + cols) / kWin;
+  return {all, lo, hi > lo ? hi : lo};
+}
+// The e-th window that is not whole.
+__host__ __device__ constexpr int edge_window(const Windows& w, int e) {
+  return e < w.lo ? e : e - w.lo + w.hi;
+}
+// Every window comes up once, as an edge or as a whole one: in place, a column
+// that two threads take is a race.
+constexpr bool each_window_once() {
+  for (int whole = 0; whole < 2; ++whole)
+    for (int shift = 0; shift < kWin; ++shift)
+      for (int cols = 1; cols <= 5 * kWin; ++cols) {
+        const Windows w = windows_of(shift, cols, whole);
+        for (int k = 0; k < w.all; ++k) {
+          int times = w.lo <= k && k < w.hi;
+          for (int e = 0; e < w.all - (w.hi - w.lo); ++e) times += edge_window(w, e) == k;
+          if (times != 1) return false;
+        }
+      }
+  return true;
+}
+static_assert(each_window_once());
+
 // Mask words a block of `cols` columns may touch, with one to spare for the
 // word behind a window's first, in steps of 16 bytes.
 __host__ __device__ constexpr int mask_words(int cols) { return (cols / 32 + 3 + 3) / 4 * 4; }
@@ -222,10 +255,8 @@ __global__ void __launch_bounds__(THREADS, kPerSm<THREADS>)
   };
   const int shift = misaligned(in_row);
   const bool vec = shift == misaligned(out_row);
-  const int windows = (shift + cols + kWin - 1) / kWin;
-  // windows [w_lo, w_hi) lie wholly inside the block's columns
-  const int w_lo = vec ? (shift + kWin - 1) / kWin : windows;
-  const int w_hi = vec ? (shift + cols) / kWin : windows;
+  const Windows win = windows_of(shift, cols, vec);
+  const int windows = win.all, w_lo = win.lo, w_hi = win.hi;
 
   // What depends on nothing else is asked for at once: the row's scalars and the
   // thread's first windows.
@@ -319,7 +350,7 @@ __global__ void __launch_bounds__(THREADS, kPerSm<THREADS>)
   // Columns of windows that are not whole, or all where the rows' alignments differ.
   const int edges = (windows - (w_hi - w_lo)) * kWin;
   for (int i = threadIdx.x; i < edges; i += THREADS) {
-    const int k = i / kWin < w_lo ? i / kWin : i / kWin - w_lo + w_hi;
+    const int k = edge_window(win, i / kWin);
     const int at = kWin * k + i % kWin, c = at - shift, bit = bit0 + at;
     if (c < 0 || c >= cols) continue;
     uint32_t e = 0;

@@ -277,3 +277,24 @@ def test_refusals():
     buf = torch.zeros(6, 100, device="cuda")
     with pytest.raises(flce.FlceError):  # a shifted overlap
         flce.process_logits(buf[0:3], out=buf[1:4])
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("offset", [0, 1, 2, 3])
+@pytest.mark.parametrize("V", [1, 2, 3, 5, 1025, 2050, 4097, 8194, 40001])
+def test_narrow_blocks_in_place(V, offset, dt):
+    """Rows, or a row's last block, of fewer columns than a window, starting
+    anywhere in one: each column is penalised once."""
+    B, L = 5, 12
+    z, k = case(B, V, L, 2, dt, seed=V + offset)
+    k["allowed"] = None
+    k["tokens"][:, ::3] = V - 1  # the last columns among them
+    k["lengths"] = torch.full((B,), L, dtype=torch.int32)
+    k["prompt_lengths"] = torch.arange(B, dtype=torch.int32)
+    wide = torch.full((B, (V + offset + 11) // 4 * 4), 5.0, dtype=dt, device="cuda")
+    view = wide[:, offset:offset + V]
+    view.copy_(z)
+    flce.process_logits(view, out=view, **{n: None if t is None else t.cuda()
+                                           for n, t in k.items()})
+    check(view, z, k)
+    assert (wide[:, :offset] == 5).all() and (wide[:, offset + V:] == 5).all()
