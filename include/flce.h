@@ -478,6 +478,18 @@ flce_status flce_matmul_fp8(const void* A, int64_t lda, const float* a_scale, co
                             void* y, int64_t ldy, flce_dtype out_dtype, flce_stream_t stream);
 
 /*
+ * Self-test of the product's bounded waits: flce_matmul_fp8 whose CTAs stop
+ * loading after `stop_after` (>= 0) blocks of K each, so that where a CTA has
+ * more to do its waits run out after `limit_ns`; the kernel then returns
+ * cleanly, with y incomplete.
+ */
+flce_status flce_selftest_matmul_fp8_timeout(int64_t stop_after, int64_t limit_ns, const void* A,
+                                             int64_t lda, const float* a_scale, const void* B,
+                                             int64_t ldb, const float* b_scale, int64_t M,
+                                             int64_t V, int64_t K, void* y, int64_t ldy,
+                                             flce_dtype out_dtype, flce_stream_t stream);
+
+/*
  * Logits before a token is picked.  Per row b and column v, with c = how often
  * v occurs among the row's generated tokens and seen = v occurs in its prompt
  * or among them:

@@ -72,6 +72,7 @@ struct Fp8Args {
   int64_t ldy;
   int tma_store;      // y's rows are 16-byte aligned
   unsigned long long wait_limit_ns;
+  int64_t stop_after;  // self-test: blocks of K that a CTA loads before it stops; -1: all
 };
 
 struct Ring {
@@ -216,13 +217,14 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     if (warp == 0 && lane == 0) {
       Ring pipe;
       uint32_t issued = 0;
+      int64_t loaded = 0;
       const uint64_t keep = l2_policy_evict_last(), once = l2_policy_evict_first();
       bool ok = true;
       for (int t = first; t < tiles && ok; t += step) {
         const int arow = (t % a.tiles_m) * S::kRows + 128 * rank;
         const int brow = (t / a.tiles_m) * N + S::kBRows * rank;
         for (int j = 0; j < a.G; ++j) {
-          ok = wait_parity(done + 8 * pipe.idx, pipe.phase ^ 1u, w);
+          ok = loaded++ != a.stop_after && wait_parity(done + 8 * pipe.idx, pipe.phase ^ 1u, w);
           if (!ok) break;
           const uint32_t bar = full + 8 * pipe.idx;
           const uint32_t as = a_base + pipe.idx * 128 * kKB, bs = b_base + pipe.idx * S::kBBytes;
@@ -307,7 +309,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const int jn = min(j + 2, a.G - 1);
         sa1 = sa[jn];
         sb1 = sb[jn];
-        ok = wait_parity_inline(done + 8 * pipe.idx, pipe.phase, w);
+        ok = wait_parity_warp(done + 8 * pipe.idx, pipe.phase, w);
         if (!ok) break;
         tc_fence_after();
         const uint32_t tbase = tmem + (static_cast<uint32_t>(q * 32) << 16) +
@@ -454,10 +456,11 @@ __global__ void __launch_bounds__(RowShape<NP>::kThreads, kRowsPerSm)
     if (lane == 0) {
       Ring pipe;
       uint32_t issued = 0;
+      int64_t loaded = 0;
       const uint64_t keep = l2_policy_evict_last(), once = l2_policy_evict_first();
       for (int t = first; t < a.tiles_v && ok; t += step) {
         for (int j = j0; j < j1; ++j) {
-          ok = wait_parity(done + 8 * pipe.idx, pipe.phase ^ 1u, w);
+          ok = loaded++ != a.stop_after && wait_parity(done + 8 * pipe.idx, pipe.phase ^ 1u, w);
           if (!ok) break;
           const uint32_t bar = full + 8 * pipe.idx;
           const uint32_t sb = base + pipe.idx * S::kStageBytes;
@@ -545,7 +548,7 @@ __global__ void __launch_bounds__(RowShape<NP>::kThreads, kRowsPerSm)
           for (int i = 0; i < kSa; ++i) sa[k][i] = sa[k + 1][i];
         }
         fetch(kAhead - 1, j + kAhead);
-        ok = wait_parity_inline(done + 8 * pipe.idx, pipe.phase, w);
+        ok = wait_parity_warp(done + 8 * pipe.idx, pipe.phase, w);
         if (!ok) break;
         tc_fence_after();
         const uint32_t tbase = tmem + (static_cast<uint32_t>(q * 32) << 16) + acc.idx * NP;
@@ -693,16 +696,11 @@ cudaError_t launch_rows_for(const CUtensorMap& ta, const CUtensorMap& tb, const 
   return launch_rows<64, O>(ta, tb, a, sms, s);
 }
 
-}  // namespace
-}  // namespace flce
-
-using namespace flce;
-
-extern "C" flce_status flce_matmul_fp8(const void* A, int64_t lda, const float* a_scale,
-                                       const void* B, int64_t ldb, const float* b_scale, int64_t M,
-                                       int64_t V, int64_t K, void* y, int64_t ldy,
-                                       flce_dtype out_dtype, flce_stream_t stream) {
-  OpRange range("flce_matmul_fp8");
+flce_status matmul_fp8(const char* name, const void* A, int64_t lda, const float* a_scale,
+                       const void* B, int64_t ldb, const float* b_scale, int64_t M, int64_t V,
+                       int64_t K, void* y, int64_t ldy, flce_dtype out_dtype,
+                       unsigned long long limit_ns, int64_t stop_after, flce_stream_t stream) {
+  OpRange range(name);
   constexpr int64_t kMaxDim = (int64_t{1} << 31) - 1024;
   if (M < 0 || V <= 0 || K <= 0 || !valid_dtype(out_dtype)) return FLCE_ERR_INVALID_ARG;
   if (K % 16 != 0 || K > kMaxRowElems || M > kMaxDim || V > kMaxDim)
@@ -735,7 +733,8 @@ extern "C" flce_status flce_matmul_fp8(const void* A, int64_t lda, const float* 
   a.b_scale = b_scale;
   a.y = y;
   a.ldy = ldy;
-  a.wait_limit_ns = wait_limit_ns();
+  a.wait_limit_ns = limit_ns;
+  a.stop_after = stop_after;
   constexpr CUtensorMapDataType kU8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
   CUtensorMap ta, tb;
   if (!make_tmap(&tb, B, K, V, ldb, kKB, 128, kU8)) return FLCE_ERR_CUDA;
@@ -760,3 +759,30 @@ extern "C" flce_status flce_matmul_fp8(const void* A, int64_t lda, const float* 
   }
   return err == cudaSuccess ? FLCE_OK : FLCE_ERR_CUDA;
 }
+
+}  // namespace
+}  // namespace flce
+
+using namespace flce;
+
+extern "C" {
+
+flce_status flce_matmul_fp8(const void* A, int64_t lda, const float* a_scale, const void* B,
+                            int64_t ldb, const float* b_scale, int64_t M, int64_t V, int64_t K,
+                            void* y, int64_t ldy, flce_dtype out_dtype, flce_stream_t stream) {
+  return matmul_fp8("flce_matmul_fp8", A, lda, a_scale, B, ldb, b_scale, M, V, K, y, ldy,
+                    out_dtype, wait_limit_ns(), -1, stream);
+}
+
+flce_status flce_selftest_matmul_fp8_timeout(int64_t stop_after, int64_t limit_ns, const void* A,
+                                             int64_t lda, const float* a_scale, const void* B,
+                                             int64_t ldb, const float* b_scale, int64_t M,
+                                             int64_t V, int64_t K, void* y, int64_t ldy,
+                                             flce_dtype out_dtype, flce_stream_t stream) {
+  if (stop_after < 0 || limit_ns <= 0) return FLCE_ERR_INVALID_ARG;
+  return matmul_fp8("flce_selftest_matmul_fp8_timeout", A, lda, a_scale, B, ldb, b_scale, M, V, K,
+                    y, ldy, out_dtype, static_cast<unsigned long long>(limit_ns), stop_after,
+                    stream);
+}
+
+}  // extern "C"

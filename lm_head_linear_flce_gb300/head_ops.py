@@ -40,6 +40,8 @@ _ARGS = {
     "flce_rms_norm_workspace_size": [_I64, _I64],
     "flce_quantize_fp8": [_P, _I64, _I64, _I64, _INT, _INT, _P, _P, _P],
     "flce_matmul_fp8": [_P, _I64, _P, _P, _I64, _P, _I64, _I64, _I64, _P, _I64, _INT, _P],
+    "flce_selftest_matmul_fp8_timeout": [_I64, _I64, _P, _I64, _P, _P, _I64, _P, _I64, _I64, _I64,
+                                         _P, _I64, _INT, _P],
     "flce_process_logits": [_P, _I64, _INT, _I64, _I64, _P, _I64, _INT, _I64, _P, _P, _P, _P, _P,
                             _P, _INT, _P, _I64, _P, _I64, _P, _I64, _INT, _P],
 }

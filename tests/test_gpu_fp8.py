@@ -199,3 +199,33 @@ def test_refusals():
             call()
     with pytest.raises(flce.FlceError):  # K is not a multiple of 16
         flce.matmul_fp8(a[:, :200], sa, b[:, :200], sb)
+
+
+# each kernel: rows of every padding, whole K and split; tiles of 128 and 256
+# columns on a CTA, and on a pair
+TIMEOUTS = [(5, 45000, 640), (20, 45000, 640), (40, 45000, 640), (5, 1000, 1024), (64, 1000, 1024),
+            (100, 4000, 640), (100, 45000, 640), (256, 45000, 640)]
+
+
+def stopped(M, V, K, out, stop_after, limit_ns):
+    """The product of CTAs that stop loading after `stop_after` blocks, in a
+    buffer of ones with a row and three columns to spare."""
+    from lm_head_linear_flce_gb300 import head_ops
+    a, sa, b, sb = operands(M, V, K, seed=8)
+    buf = torch.ones(M + 1, V + 3, dtype=out, device="cuda")
+    head_ops._call("flce_selftest_matmul_fp8_timeout", a.get_device(), stop_after, limit_ns,
+                   a.data_ptr(), K, sa.data_ptr(), b.data_ptr(), K, sb.data_ptr(), M, V, K,
+                   buf.data_ptr(), V + 3, head_ops._DTYPE[out])
+    torch.cuda.synchronize()
+    assert (buf[M] == 1).all() and (buf[:, V:] == 1).all()
+    return buf[:M, :V], (a, sa, b, sb)
+
+
+@pytest.mark.parametrize("stop_after", [0, 1, 3])
+@pytest.mark.parametrize("M,V,K", TIMEOUTS)
+def test_a_wait_that_runs_out_ends_the_kernel(M, V, K, stop_after):
+    for out in (BF, F32):
+        y, op = stopped(M, V, K, out, stop_after, 20_000_000)
+        # the next product is right
+        check(flce.matmul_fp8(*op, out_dtype=out)[:, :257], op[0], op[1],
+              op[2].view(torch.uint8)[:257].view(op[2].dtype), op[3][:3], out)
