@@ -100,16 +100,33 @@ __device__ __forceinline__ void mma_block(uint32_t d, uint64_t ad, uint64_t bd) 
   }
 }
 
-// Waits (bounded, whatever the abort flag says) until the stages in `issued`
-// have received their last loads: no CTA may exit with copies in flight.
+// How long a CTA that has given up waits at least for its copies and MMAs in
+// flight, however short the limit is: they take microseconds.
+constexpr unsigned long long kLandNs = 1000000;
+
+// The wait that ends a role: bounded, whatever the abort flag says.
+__device__ __forceinline__ WaitCtx last_wait(const WaitCtx& w, volatile uint32_t* never) {
+  return {never, w.err, w.limit_ns > kLandNs ? w.limit_ns : kLandNs};
+}
+
+// Waits until the stages in `issued` have received their last loads: no CTA may
+// exit with copies in flight.
 template <int STAGES>
-__device__ void drain_stages(uint32_t full, uint32_t issued, const Ring& pipe, WaitCtx w) {
+__device__ void drain_stages(uint32_t full, uint32_t issued, const Ring& pipe, const WaitCtx& w0) {
   volatile uint32_t never = 0u;
-  w.abort = &never;
+  const WaitCtx w = last_wait(w0, &never);
   for (int i = 0; i < STAGES; ++i)
     if (issued & (1u << i))
       wait_parity(full + 8 * i, static_cast<uint32_t>(i) < pipe.idx ? pipe.phase : pipe.phase ^ 1u,
                   w);
+}
+
+// The same for the CTA of a pair whose loads complete on its peer's barriers,
+// which it cannot wait for: it gives them time.  Only after it has given up;
+// otherwise the peer's wait covers them.
+__device__ __noinline__ void let_copies_land() {
+  const uint64_t t0 = global_timer_ns();
+  for (int i = 0; i < 100000 && global_timer_ns() - t0 < kLandNs; ++i) __nanosleep(1000);
 }
 
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
@@ -244,6 +261,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         }
       }
       if (leader) drain_stages<S::kStages>(full, issued, pipe, w);
+      else if (!ok) let_copies_land();
     } else if (warp == 1 && leader) {
       // The whole warp runs the loop, so that its values stay uniform; one lane
       // issues.  A stage and an accumulator are both one block of K, so one
@@ -276,10 +294,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       if (elect_one()) {
         if (PAIR) mma_commit_pair(drain);
         else mma_commit_single(drain);
-        WaitCtx wd = w;
         volatile uint32_t never = 0u;
-        wd.abort = &never;
-        wait_parity(drain, 0u, wd);
+        wait_parity(drain, 0u, last_wait(w, &never));
       }
       __syncwarp();
     }
@@ -498,10 +514,8 @@ __global__ void __launch_bounds__(RowShape<NP>::kThreads, kRowsPerSm)
     }
     if (elect_one()) {
       mma_commit_single(drain);
-      WaitCtx wd = w;
       volatile uint32_t never = 0u;
-      wd.abort = &never;
-      wait_parity(drain, 0u, wd);
+      wait_parity(drain, 0u, last_wait(w, &never));
     }
     __syncwarp();
   }

@@ -229,3 +229,14 @@ def test_a_wait_that_runs_out_ends_the_kernel(M, V, K, stop_after):
         # the next product is right
         check(flce.matmul_fp8(*op, out_dtype=out)[:, :257], op[0], op[1],
               op[2].view(torch.uint8)[:257].view(op[2].dtype), op[3][:3], out)
+
+
+@pytest.mark.parametrize("M,V,K", TIMEOUTS)
+def test_a_short_limit_leaves_nothing_in_flight(M, V, K):
+    """Kernels that give up at once, right before one that takes their place on
+    the SMs: its stages are its own."""
+    for stop_after in (0, 1, 2, 3, 4):
+        y, op = stopped(M, V, K, F32, stop_after, 1)
+        for _ in range(2):
+            check(flce.matmul_fp8(*op, out_dtype=F32)[:, :257], op[0], op[1],
+                  op[2].view(torch.uint8)[:257].view(op[2].dtype), op[3][:3], F32)
