@@ -269,8 +269,9 @@ const char* flce_status_string(flce_status status);
 /*
  * Limit, in nanoseconds, on every wait inside the library's kernels (default
  * 2e9), flce_forward_noalloc's included; it applies to calls made after it is
- * set.  A wait that runs out records FLCE_ERR_TIMEOUT and its kernel returns
- * early.  Values <= 0 restore the default.  Process-wide.
+ * set.  A wait that runs out records FLCE_ERR_TIMEOUT, where the call has an
+ * error word, and its kernel returns early.  Values <= 0 restore the default.
+ * Process-wide.
  */
 void flce_set_wait_limit_ns(int64_t limit_ns);
 
@@ -470,8 +471,8 @@ flce_status flce_quantize_fp8(const void* x, int64_t ldx, int64_t R, int64_t K, 
  * in FP32, and the sum is rounded once.  K, lda and ldb are multiples of 16, A
  * and B 16-byte aligned; K <= 65536.  The tensor cores lose at most about 2^-16
  * of a block's sum of |products| (measured on random operands: 1e-7 of the
- * result).  As in flce_logits, a wait that runs out (flce_set_wait_limit_ns)
- * ends the call with y incomplete.
+ * result).  A wait that runs out (flce_set_wait_limit_ns) ends the kernel early,
+ * with NaN in every element of y that it had not finished.
  */
 flce_status flce_matmul_fp8(const void* A, int64_t lda, const float* a_scale, const void* B,
                             int64_t ldb, const float* b_scale, int64_t M, int64_t V, int64_t K,
@@ -481,7 +482,7 @@ flce_status flce_matmul_fp8(const void* A, int64_t lda, const float* a_scale, co
  * Self-test of the product's bounded waits: flce_matmul_fp8 whose CTAs stop
  * loading after `stop_after` (>= 0) blocks of K each, so that where a CTA has
  * more to do its waits run out after `limit_ns`; the kernel then returns
- * cleanly, with y incomplete.
+ * cleanly, with NaN in what it had not finished.
  */
 flce_status flce_selftest_matmul_fp8_timeout(int64_t stop_after, int64_t limit_ns, const void* A,
                                              int64_t lda, const float* a_scale, const void* B,

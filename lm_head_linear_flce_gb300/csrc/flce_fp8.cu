@@ -129,6 +129,9 @@ __device__ __noinline__ void let_copies_land() {
   for (int i = 0; i < 100000 && global_timer_ns() - t0 < kLandNs; ++i) __nanosleep(1000);
 }
 
+// What a result is where a wait has run out before it was complete.
+constexpr uint32_t kNotComplete = 0x7fc00000u;  // NaN
+
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<uint32_t*>(&h);
@@ -306,7 +309,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     const uint32_t buf = staging + (warp - 4) * kStageBufBytes;
     Ring pipe, acc;
     bool ok = true;
-    for (int t = first; t < tiles && ok; t += step) {
+    for (int t = first; t < tiles; t += step) {
       const int row0 = (t % a.tiles_m) * S::kRows + 128 * rank + q * 32;
       const int col0 = (t / a.tiles_m) * N + S::kCols * half;
       const int row = row0 + lane;
@@ -318,7 +321,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       for (int i = 0; i < S::kCols / 2; ++i) r[i] = 0;
       // scales are fetched two blocks ahead of their use
       float sa0 = sa[0], sb0 = sb[0], sa1 = sa[min(1, a.G - 1)], sb1 = sb[min(1, a.G - 1)];
-      for (int j = 0; j < a.G; ++j) {
+      for (int j = ok ? 0 : a.G; j < a.G; ++j) {
         const float s = sa0 * sb0;
         sa0 = sa1;
         sb0 = sb1;
@@ -348,7 +351,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         pipe.advance(S::kStages);
         acc.advance(S::kAccs);
       }
-      if (!ok) break;
+      if (!ok) {  // this tile, and those after it, whose blocks are not waited for
+#pragma unroll
+        for (int i = 0; i < S::kCols / 2; ++i) r[i] = pack_f32x2(kNotComplete, kNotComplete);
+      }
       constexpr int kWords = 32;                  // 128 bytes of one row per chunk
       constexpr int kPairs = sizeof(O) == 2 ? 32 : 16;  // register pairs per chunk
 #pragma unroll
@@ -528,7 +534,7 @@ __global__ void __launch_bounds__(RowShape<NP>::kThreads, kRowsPerSm)
     auto* my_scales = reinterpret_cast<float*>(smem_raw + (scales - raw)) + (warp - 2) * 2 * NP;
     Ring pipe, acc;
     // the last tile's result stays in registers when K is split (one tile each)
-    for (int t = first; t < a.tiles_v && ok; t += step) {
+    for (int t = first; t < a.tiles_v; t += step) {
       const int v = t * 128 + q * 32 + lane;
       const float* sb = a.b_scale + static_cast<int64_t>(t) * a.G;
 #pragma unroll
@@ -548,7 +554,7 @@ __global__ void __launch_bounds__(RowShape<NP>::kThreads, kRowsPerSm)
       };
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) fetch(i, j0 + i);
-      for (int j = j0; j < j1; ++j) {
+      for (int j = ok ? j0 : j1; j < j1; ++j) {
         // this block's scales into the warp's buffer, the queue moves up
         float* s = my_scales + (j & 1) * NP;
 #pragma unroll
@@ -587,7 +593,10 @@ __global__ void __launch_bounds__(RowShape<NP>::kThreads, kRowsPerSm)
         pipe.advance(S::kStages);
         acc.advance(S::kAccs);
       }
-      if (!ok) break;
+      if (!ok) {  // this tile, and those after it, whose blocks are not waited for
+#pragma unroll
+        for (int n = 0; n < NP; ++n) r[n] = __uint_as_float(kNotComplete);
+      }
       if (splits == 1 && v < a.V) {
         O* y = static_cast<O*>(a.y) + v;
 #pragma unroll
@@ -602,7 +611,7 @@ __global__ void __launch_bounds__(RowShape<NP>::kThreads, kRowsPerSm)
   if (splits > 1) {
     // Every role has finished with the stages: their memory takes this part's
     // result, [NP][128] floats, and each CTA adds a share of the columns of all
-    // parts.
+    // parts (a part that is not complete is NaN, and so are the sums).
     __syncthreads();
     const uint32_t mine = base;
     if (warp >= 2) {
@@ -614,7 +623,7 @@ __global__ void __launch_bounds__(RowShape<NP>::kThreads, kRowsPerSm)
     }
     cluster_sync_all();
     const int v = first * 128 + q * 32 + lane;
-    if (warp >= 2 && ok && v < a.V && first < a.tiles_v) {
+    if (warp >= 2 && v < a.V && first < a.tiles_v) {
       for (int n = part; n < a.M; n += splits) {
         float sum = 0.f;
         for (int p = 0; p < splits; ++p) {

@@ -174,7 +174,8 @@ def matmul_fp8(a, a_scale, b, b_scale, out_dtype=torch.bfloat16):
     [V, K] with b_scale float32 [ceil(V / 128), ceil(K / 128)], as
     quantize_fp8(W) gives them.  K must be a multiple of 16.  As with
     flce_logits, where V is no multiple of 8 the result is a view of rows padded
-    to one (16-byte rows).  No gradient."""
+    to one (16-byte rows).  No gradient.  If a wait inside the kernel runs out
+    (flce_set_wait_limit_ns), what it had not finished is NaN."""
     out = _DTYPE.get(out_dtype)
     if out is None:
         raise ValueError(f"out_dtype must be bfloat16 or float32, got {out_dtype}")

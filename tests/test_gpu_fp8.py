@@ -240,3 +240,28 @@ def test_a_short_limit_leaves_nothing_in_flight(M, V, K):
         for _ in range(2):
             check(flce.matmul_fp8(*op, out_dtype=F32)[:, :257], op[0], op[1],
                   op[2].view(torch.uint8)[:257].view(op[2].dtype), op[3][:3], F32)
+
+
+@pytest.mark.parametrize("out", [BF, F32])
+@pytest.mark.parametrize("stop_after", [0, 1, 5])
+@pytest.mark.parametrize("M,V,K", TIMEOUTS + [(5, 1000, 1104), (64, 1000, 1104), (33, 700, 2064)])
+def test_what_is_not_complete_is_nan(M, V, K, stop_after, out):
+    """Every element is NaN or right, where parts of a split K are complete and
+    others are not too, and where a CTA gives up in its second tile."""
+    y, (a, sa, b, sb) = stopped(M, V, K, out, stop_after, 20_000_000)
+    gone = torch.isnan(y)
+    want = flce.matmul_fp8(a, sa, b, sb, out_dtype=out)  # (checked by the tests above)
+    assert torch.equal(y[~gone], want[~gone])
+    G, tiles = -(-K // 128), -(-V // 128)
+    split = M <= 64 and 2 * tiles <= 304 and 2 <= G
+    if stop_after == 0:
+        assert gone.all()
+    elif split:  # parts of 1 block, or of 1 and 2: complete or not, the same for every tile
+        parts = max(p for p in (1, 2, 4, 8) if p * tiles <= 304 and p <= G)
+        assert gone.all() if -(-G // parts) > stop_after else not gone.any()
+    elif stop_after < G:
+        assert gone.all()
+    elif V == 45000:  # the first tiles are complete, the next are not
+        assert gone.any() and not gone.all()
+    else:
+        assert not gone.any()
