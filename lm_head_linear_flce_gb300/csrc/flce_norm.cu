@@ -1057,7 +1057,8 @@ flce_status flce_rms_norm_forward(const void* x, int64_t ldx, const void* residu
   flce_status st = check_norm(x, ldx, residual, ldr, weight, N, H, dtype, weight_dtype);
   if (st != FLCE_OK || N == 0) return st;
   const size_t e = dtype_bytes(dtype);
-  if (!y || !aligned_to(y, e) || !aligned_to(h_out, e)) return FLCE_ERR_INVALID_ARG;
+  if (!y || !aligned_to(y, e) || !aligned_to(h_out, e) || !aligned_to(rstd, 4))
+    return FLCE_ERR_INVALID_ARG;
   if (!norm_outputs_apart(x, ldx, residual, ldr,
                           {weight, static_cast<size_t>(H) * dtype_bytes(weight_dtype)}, N, H, e,
                           h_out, {y, span_bytes(N, H, H, e)},
@@ -1081,7 +1082,7 @@ flce_status flce_rms_norm_fp8(const void* x, int64_t ldx, const void* residual, 
   flce_status st = check_norm(x, ldx, residual, ldr, weight, N, H, dtype, weight_dtype);
   if (st != FLCE_OK || N == 0) return st;
   const size_t e = dtype_bytes(dtype);
-  if (!q || !scale || !aligned_to(h_out, e)) return FLCE_ERR_INVALID_ARG;
+  if (!q || !scale || !aligned_to(h_out, e) || !aligned_to(scale, 4)) return FLCE_ERR_INVALID_ARG;
   const int64_t groups = (H + kScaleGroup - 1) / kScaleGroup;
   if (!norm_outputs_apart(x, ldx, residual, ldr,
                           {weight, static_cast<size_t>(H) * dtype_bytes(weight_dtype)}, N, H, e,
@@ -1116,7 +1117,7 @@ flce_status flce_rms_norm_backward(const void* dy, const void* dh, const void* h
   if (N > 0 && (!dy || !h || !weight || !rstd || ldh < H)) return FLCE_ERR_INVALID_ARG;
   const size_t e = dtype_bytes(dtype), we = dtype_bytes(weight_dtype);
   if (!aligned_to(dy, e) || !aligned_to(dh, e) || !aligned_to(h, e) || !aligned_to(dx, e) ||
-      !aligned_to(weight, we) || !aligned_to(dweight, we))
+      !aligned_to(weight, we) || !aligned_to(dweight, we) || !aligned_to(rstd, 4))
     return FLCE_ERR_INVALID_ARG;
   if (dweight) {
     if (!workspace || !aligned_to(workspace, 256)) return FLCE_ERR_INVALID_ARG;
@@ -1152,7 +1153,8 @@ flce_status flce_quantize_fp8(const void* x, int64_t ldx, int64_t R, int64_t K, 
   if (K > kMaxRowElems || R > kMaxRows) return FLCE_ERR_UNSUPPORTED_SHAPE;
   if (R == 0) return FLCE_OK;
   const size_t e = dtype_bytes(dtype);
-  if (!x || !q || !scale || ldx < K || !aligned_to(x, e)) return FLCE_ERR_INVALID_ARG;
+  if (!x || !q || !scale || ldx < K || !aligned_to(x, e) || !aligned_to(scale, 4))
+    return FLCE_ERR_INVALID_ARG;
   const int64_t gr = (R + block_rows - 1) / block_rows, gk = (K + kScaleGroup - 1) / kScaleGroup;
   const Range xr = {x, span_bytes(R, K, ldx, e)}, qr = {q, span_bytes(R, K, K, 1)},
               sr = {scale, span_bytes(gr, gk, gk, 4)};

@@ -158,3 +158,19 @@ def test_calls_raise_without_the_native_module(monkeypatch, tmp_path):
                  lambda: flce.matmul_fp8(x, w, x, w)):
         with pytest.raises(RuntimeError, match="no fallback"):
             call()
+
+
+# Made-up addresses that a check does not refuse would reach the device, so these
+# too are made only where no kernel can run.
+@no_gpu
+@pytest.mark.parametrize("off", [1, 2, 3])
+def test_float_outputs_and_statistics_that_are_not_aligned(off):
+    for name in ("flce_rms_norm_forward", "flce_rms_norm_fp8"):  # rstd, and the scales
+        assert norm(name, rstd=BASE + 5 * G + off) == INVALID
+    need = fn("flce_rms_norm_workspace_size")(100, 64)
+    assert fn("flce_rms_norm_backward")(BASE, None, BASE + 2 * G, 64, BASE + 3 * G,
+                                        BASE + 4 * G + off, 100, 64, 0, 0, BASE + 5 * G,
+                                        BASE + 6 * G, BASE + 7 * G, need, None) == INVALID
+    for rows in (1, 128):
+        assert fn("flce_quantize_fp8")(BASE, 64, 10, 64, 1, rows, BASE + G, BASE + 2 * G + off,
+                                       None) == INVALID
