@@ -526,10 +526,12 @@ __global__ void __launch_bounds__(kSmallThreads)
 }
 
 // ----------------------------------------------------- rows past kMaxHeld
-// A block per row; a warp per group of 128 columns in the second pass.
+// A block per row; a warp per group of 128 columns in the second pass, where a
+// thread reads an element before it writes the sum in its place (h_out may be x or
+// residual).
 template <class T, class W, bool FP8>
 __global__ void __launch_bounds__(kNormThreads)
-    norm_fwd_kernel(const T* __restrict__ x, int64_t ldx, const T* residual, int64_t ldr,
+    norm_fwd_kernel(const T* x, int64_t ldx, const T* residual, int64_t ldr,
                     const W* __restrict__ weight, int H, float eps, T* y, uint8_t* q,
                     float* scale, T* h_out, float* rstd) {
   const int64_t row = blockIdx.x;

@@ -315,3 +315,18 @@ def test_refusals():
             call()
     with pytest.raises(flce.FlceError):  # the sum would overwrite the weight's neighbour x
         flce.rms_norm_fp8(x[1:3], w, residual_out=x[:2])
+
+
+@pytest.mark.parametrize("H", [64, 1001, 16384, 16388, 40000])
+def test_sum_in_the_place_of_x(H):
+    for dt in (BF, F32):
+        x, res, w, _, _ = case(6, H, dt, dt, seed=17)
+        for residual in (res, None):
+            want = flce.flce_rms_norm(x, w, residual=residual, residual_out=torch.empty_like(x))
+            want8 = flce.rms_norm_fp8(x, w, residual=residual, residual_out=torch.empty_like(x))
+            mine = x.clone()
+            got = flce.flce_rms_norm(mine, w, residual=residual, residual_out=mine)
+            mine = x.clone()
+            got8 = flce.rms_norm_fp8(mine, w, residual=residual, residual_out=mine)
+            for a, b in zip(want + want8, got + got8):
+                assert torch.equal(a.float(), b.float())
