@@ -116,6 +116,18 @@ def flce_rms_norm_backward(dy, h, weight, rstd, *, dh=None, need_dx=True, need_d
                "flce_rms_norm_backward")
 
 
+class _NotTwice(torch.autograd.Function):
+    """A gradient as it is; differentiating it by what it depends on raises."""
+
+    @staticmethod
+    def forward(ctx, grad, *depends_on):
+        return grad
+
+    @staticmethod
+    def backward(ctx, *_):
+        raise RuntimeError("rms_norm's gradient cannot be differentiated again")
+
+
 class _RmsNorm(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, residual, eps):
@@ -135,12 +147,19 @@ class _RmsNorm(torch.autograd.Function):
         else:
             dx, dw = flce_rms_norm_backward(dy, h, weight, rstd, dh=dh,
                                             need_dx=need[0] or need[2], need_dweight=need[1])
+            if torch.is_grad_enabled():
+                # create_graph=True: constants would lose what the gradients depend on
+                # without a word.  (torch's once_differentiable looks at dy and dh alone.)
+                h = h if need[0] or need[2] else None  # (else it is given)
+                dx = dx if dx is None else _NotTwice.apply(dx, dy, dh, h, weight)
+                dw = dw if dw is None else _NotTwice.apply(dw, dy, h)
         return (dx if need[0] else None, dw,
                 dx if ctx.has_residual and need[2] else None, None)
 
 
 def rms_norm(x, weight, eps=1e-6, residual=None):
-    """Root-mean-square norm over the last dimension, differentiable.
+    """Root-mean-square norm over the last dimension, differentiable (once: a
+    gradient taken with create_graph=True raises when it is differentiated).
 
     x: bf16 or float32 [..., H]; weight: bf16 or float32 [H].  Without a residual
     returns y = x * weight / sqrt(mean(x^2) + eps).  With one (as x) returns

@@ -330,3 +330,39 @@ def test_sum_in_the_place_of_x(H):
             got8 = flce.rms_norm_fp8(mine, w, residual=residual, residual_out=mine)
             for a, b in zip(want + want8, got + got8):
                 assert torch.equal(a.float(), b.float())
+
+
+def test_second_derivatives_are_refused():
+    """The backward is not differentiable: a loss that holds a gradient raises,
+    by whichever input it is differentiated, and does not lose the terms that go
+    through it."""
+    x, res, w, a, _ = case(4, 64, F32, F32, seed=13)
+    ones = torch.ones_like(a)
+    for residual in (None, res):
+        rstd = flce.flce_rms_norm(x, w, residual=residual)[2]
+        h = x if residual is None else x + residual
+        want = flce.flce_rms_norm_backward(a, h, w, rstd, dh=None if residual is None else ones)
+        for power in (1, 2):  # a gradient dy that is given, and one that depends on y
+            p, q = x.clone().requires_grad_(), w.clone().requires_grad_()
+            out = flce.rms_norm(p, q, residual=residual)
+            y, s = (out, None) if residual is None else out
+            loss = (y.pow(power) * (a if power == 1 else a / (2 * y.detach()))).sum()
+            got = torch.autograd.grad(loss + (0 if s is None else s.sum()), (p, q),
+                                      create_graph=True)
+            for g, t in zip(got, want):  # the gradient itself is as ever
+                assert torch.allclose(g, t, rtol=1e-5, atol=1e-5)
+            for g, by in ((got[0], p), (got[0], q), (got[1], p)):
+                with pytest.raises(RuntimeError, match="cannot be differentiated again"):
+                    torch.autograd.grad(g.square().sum() + y.sum(), by, retain_graph=True)
+        # dweight does not depend on the weight, where dy is given
+        q = w.clone().requires_grad_()
+        out = flce.rms_norm(x, q, residual=residual)
+        y = out if residual is None else out[0]
+        (g,) = torch.autograd.grad((y * a).sum(), q, create_graph=True)
+        assert torch.equal(torch.autograd.grad(g.sum() + (y * a).sum(), q)[0], g)
+    # a gradient that is used as a number, and a graph that is not differentiated again
+    p = x.clone().requires_grad_()
+    y = flce.rms_norm(p, w)
+    (g,) = torch.autograd.grad(y.sum(), p, create_graph=True)
+    (y.sum() * g.detach().sum()).backward()
+    assert torch.isfinite(p.grad).all()
