@@ -66,6 +66,12 @@ Rows rows(const Tensor& t, int64_t w) {
 }
 void* ptr(const Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; }
 
+// Tells autograd that a caller's tensor was written: what saved it for a backward
+// then raises instead of using the new values.
+void note_written(const Tensor& t) {
+  if (t.defined() && !t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+
 std::vector<int64_t> lead_and(const Tensor& t, int64_t last) {
   auto s = t.sizes().vec();
   s.back() = last;
@@ -112,7 +118,7 @@ int64_t integer(PyObject* o) {
 
 // What the norms share.
 struct Norm {
-  Tensor x, weight, residual, h;
+  Tensor x, weight, residual, h, out;  // out: residual_out, if it is given
   flce_dtype type, weight_type;
   int64_t N, H;
   Rows xr, rr;
@@ -138,7 +144,7 @@ struct Norm {
   }
   // Where the norm writes the sum: residual_out, or a new tensor if there is a residual.
   void sum_buffer(PyObject* o) {
-    h = arg(o, "residual_out");
+    h = out = arg(o, "residual_out");
     if (h.defined()) {
       check_cuda(h, "residual_out", x.get_device());
       check_type(h, "residual_out", x.scalar_type(), x.scalar_type());
@@ -162,6 +168,7 @@ PyObject* rms_norm_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const flce_status st = flce_rms_norm_forward(
       m.xr.p, m.xr.ld, m.rr.p, m.rr.ld, ptr(m.weight), m.N, m.H, static_cast<float>(number(a[2])),
       m.type, m.weight_type, ptr(y), ptr(m.h), static_cast<float*>(ptr(rstd)), on.stream);
+  if (st == FLCE_OK) note_written(m.out);
   return answer(st, std::move(y), std::move(m.h), std::move(rstd));
   END_HANDLE_TH_ERRORS
 }
@@ -178,6 +185,7 @@ PyObject* rms_norm_fp8(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const flce_status st = flce_rms_norm_fp8(
       m.xr.p, m.xr.ld, m.rr.p, m.rr.ld, ptr(m.weight), m.N, m.H, static_cast<float>(number(a[2])),
       m.type, m.weight_type, ptr(q), static_cast<float*>(ptr(scale)), ptr(m.h), on.stream);
+  if (st == FLCE_OK) note_written(m.out);
   return answer(st, std::move(q), std::move(scale), std::move(m.h));
   END_HANDLE_TH_ERRORS
 }
@@ -376,6 +384,7 @@ PyObject* process_logits(PyObject*, PyObject* const* a, Py_ssize_t n) {
       nb ? ptr(ids) : nullptr, b64, nb ? static_cast<const float*>(ptr(vals)) : nullptr, nb,
       static_cast<const int32_t*>(mr.p), mr.ld, ptr(out), B > 1 ? out.stride(0) : V, out_type,
       on.stream);
+  if (st == FLCE_OK && a[10] != Py_None) note_written(out);
   return answer(st, std::move(out));
   END_HANDLE_TH_ERRORS
 }

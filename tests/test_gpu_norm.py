@@ -366,3 +366,19 @@ def test_second_derivatives_are_refused():
     (g,) = torch.autograd.grad(y.sum(), p, create_graph=True)
     (y.sum() * g.detach().sum()).backward()
     assert torch.isfinite(p.grad).all()
+
+
+def test_a_written_tensor_counts_as_modified():
+    """Autograd sees what residual_out overwrites."""
+    x, res, w, _, _ = case(5, 64, BF, BF, seed=14)
+    y, h = flce.rms_norm(x.requires_grad_(), w, residual=res)  # h is kept for the backward
+    for call in (flce.rms_norm_fp8, flce.flce_rms_norm):
+        buf = torch.empty_like(x)
+        call(x.detach(), w, residual=res, residual_out=buf)
+        assert buf._version == 1
+    flce.rms_norm_fp8(res, w, residual=h.detach(), residual_out=h.detach())
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.float().sum().backward()
+    with torch.inference_mode():  # tensors without a version
+        buf = torch.empty_like(x)
+        assert flce.rms_norm_fp8(x, w, residual=res, residual_out=buf)[2] is buf

@@ -298,3 +298,18 @@ def test_narrow_blocks_in_place(V, offset, dt):
                                            for n, t in k.items()})
     check(view, z, k)
     assert (wide[:, :offset] == 5).all() and (wide[:, offset + V:] == 5).all()
+
+
+def test_a_written_tensor_counts_as_modified():
+    z = torch.randn(3, 64, device="cuda")
+    flce.process_logits(z, out=z)
+    assert z._version == 1
+    a = torch.randn(3, 64, device="cuda").requires_grad_()
+    b = a * 2
+    c = b.square()  # keeps b
+    flce.process_logits(b.detach(), out=b.detach())
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        c.sum().backward()
+    with torch.inference_mode():  # tensors without a version
+        z = torch.zeros(3, 64, device="cuda")
+        assert flce.process_logits(z, out=z) is z
