@@ -8,6 +8,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <c10/core/GradMode.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -66,6 +67,11 @@ Rows rows(const Tensor& t, int64_t w) {
 }
 void* ptr(const Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; }
 
+// A caller's tensor to be written: autograd would take it for what it was.
+void check_writable(const Tensor& t, const char* name) {
+  TORCH_CHECK_VALUE(!(c10::GradMode::is_enabled() && t.requires_grad()), name,
+                    " requires a gradient, and the call has none");
+}
 // Tells autograd that a caller's tensor was written: what saved it for a backward
 // then raises instead of using the new values.
 void note_written(const Tensor& t) {
@@ -150,6 +156,7 @@ struct Norm {
       check_type(h, "residual_out", x.scalar_type(), x.scalar_type());
       TORCH_CHECK_VALUE(h.sizes() == x.sizes() && h.is_contiguous(),
                         "residual_out must be contiguous, with the shape of x");
+      check_writable(h, "residual_out");
     } else if (residual.defined()) {
       h = empty(x.sizes(), x, x.scalar_type());
     }
@@ -316,6 +323,7 @@ PyObject* process_logits(PyObject*, PyObject* const* a, Py_ssize_t n) {
                       "out must be [B, V] with contiguous rows");
     TORCH_CHECK_VALUE(want < 0 || (want == FLCE_F32) == (out.scalar_type() == at::kFloat),
                       "out and out_dtype disagree");
+    check_writable(out, "out");
   } else {
     out = empty({B, V}, z,
                 want < 0 ? z.scalar_type() : want == FLCE_F32 ? at::kFloat : at::kBFloat16);

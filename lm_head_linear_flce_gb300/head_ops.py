@@ -172,7 +172,8 @@ def rms_norm_fp8(x, weight, eps=1e-6, residual=None, residual_out=None):
     """The norm with its output in 8 bits: (q, scale), or (q, scale, h) with a
     residual.  q: float8_e4m3fn [..., H]; scale: float32 [..., ceil(H / 128)],
     one per row and 128 columns; q * scale stands for y.  residual_out: where
-    to write h (may be residual itself).  No gradient."""
+    to write h (may be residual itself; it may not require a gradient).  No
+    gradient."""
     q, scale, h = _ok(_native().rms_norm_fp8(x, weight, eps, residual, residual_out),
                       "flce_rms_norm_fp8")
     return (q, scale) if h is None else (q, scale, h)
@@ -181,7 +182,8 @@ def rms_norm_fp8(x, weight, eps=1e-6, residual=None, residual_out=None):
 def quantize_fp8(x, block_rows=128):
     """x [R, K] (bf16 or float32) in 8 bits: (q, scale) with q float8_e4m3fn
     [R, K] and scale float32 [ceil(R / block_rows), ceil(K / 128)].  block_rows
-    is 128 for a weight, 1 for activations (x may then be [..., K])."""
+    is 128 for a weight, 1 for activations (x may then be [..., K]).  No
+    gradient."""
     return _ok(_native().quantize_fp8(x, block_rows), "flce_quantize_fp8")
 
 
@@ -217,7 +219,8 @@ def process_logits(logits, *, tokens=None, lengths=None, prompt_lengths=None,
     allowed[b, v // 32] (int32) is 0 becomes -inf.  Any part may be left out.
 
     logits: bf16 or float32.  Returns out (given, or new: out_dtype, default
-    that of logits); out may be logits itself."""
+    that of logits); out may be logits itself, and may not require a gradient.
+    No gradient."""
     code = -1 if out_dtype is None else _DTYPE.get(out_dtype)
     if code is None:
         raise ValueError(f"out_dtype must be bfloat16 or float32, got {out_dtype}")

@@ -382,3 +382,15 @@ def test_a_written_tensor_counts_as_modified():
     with torch.inference_mode():  # tensors without a version
         buf = torch.empty_like(x)
         assert flce.rms_norm_fp8(x, w, residual=res, residual_out=buf)[2] is buf
+
+
+def test_an_output_that_wants_a_gradient_is_refused():
+    x, res, w, _, _ = case(4, 64, BF, BF, seed=15)
+    leaf = torch.zeros_like(x).requires_grad_()
+    for out in (leaf, leaf * 1):
+        for call in (flce.rms_norm_fp8, flce.flce_rms_norm):
+            with pytest.raises(ValueError, match="gradient"):
+                call(x, w, residual=res, residual_out=out)
+    with torch.no_grad():
+        assert flce.rms_norm_fp8(x, w, residual=res, residual_out=leaf)[2] is leaf
+    assert torch.equal(leaf.detach(), (x.float() + res.float()).to(BF))

@@ -313,3 +313,12 @@ def test_a_written_tensor_counts_as_modified():
     with torch.inference_mode():  # tensors without a version
         z = torch.zeros(3, 64, device="cuda")
         assert flce.process_logits(z, out=z) is z
+
+
+def test_an_output_that_wants_a_gradient_is_refused():
+    z = torch.randn(3, 64, device="cuda").requires_grad_()
+    for out in (z, z * 1):
+        with pytest.raises(ValueError, match="gradient"):
+            flce.process_logits(z, out=out)
+    with torch.no_grad():
+        assert flce.process_logits(z, out=z) is z
