@@ -4,7 +4,8 @@ and ``_lib/_flce_torch.so``, the Python module over it.
 Each .cu file is compiled to an object in parallel, then linked with the
 static CUDA runtime (the library needs no libcudart at load time and finds
 the CUDA driver entry points it uses at run time).  The module is plain C++
-against the installed torch's headers.
+against the installed torch's headers; without torch only the library is built
+(``python lm_head_linear_flce_gb300/_build.py``).
 """
 from __future__ import annotations
 
@@ -12,6 +13,7 @@ import concurrent.futures
 import os
 import shutil
 import subprocess
+import sys
 import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -72,23 +74,45 @@ def build(verbose: bool = False, extra: list[str] | None = None) -> str:
     extra = list(extra or [])
     os.makedirs(OUT_DIR, exist_ok=True)
     objs = [os.path.join(OUT_DIR, s.replace(".cu", ".o")) for s in SOURCES]
-    module = os.path.join(OUT_DIR, "flce_torch.o")
+    module_obj = os.path.join(OUT_DIR, "flce_torch.o")
+    try:
+        import torch  # noqa: F401
+        no_torch = None
+    except ImportError as e:
+        no_torch = e
     with concurrent.futures.ThreadPoolExecutor(len(SOURCES) + 1) as ex:
         futs = [ex.submit(_compile, s, o, extra) for s, o in zip(SOURCES, objs)]
-        futs.append(ex.submit(_compile_module, module))
+        module = None if no_torch else ex.submit(_compile_module, module_obj)
         for f in futs:
             f.result()
-    tmp = LIB + ".tmp"
-    cmd = [nvcc(), *ARCH, "-shared", "-Xcompiler", "-fPIC", "-cudart", "static", *objs,
-           "-o", tmp]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, LIB)
-    _link_module(module)
+        # the library first: it needs nothing of the module's
+        tmp = LIB + ".tmp"
+        cmd = [nvcc(), *ARCH, "-shared", "-Xcompiler", "-fPIC", "-cudart", "static", *objs,
+               "-o", tmp]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+        os.replace(tmp, LIB)
+        try:
+            if module is not None:
+                module.result()
+                _link_module(module_obj)
+        except Exception:
+            _remove_module()
+            raise
+    if no_torch:
+        _remove_module()
+        print(f"built {LIB} without the Python module over it: torch cannot be imported "
+              f"({no_torch})", file=sys.stderr)
     if verbose:
         print("built", LIB)
     return LIB
+
+
+def _remove_module() -> None:
+    """No module is better than one of another library's: its calls then say so."""
+    if os.path.exists(MODULE):
+        os.remove(MODULE)
 
 
 if __name__ == "__main__":
