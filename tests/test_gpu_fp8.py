@@ -265,3 +265,19 @@ def test_what_is_not_complete_is_nan(M, V, K, stop_after, out):
         assert gone.any() and not gone.all()
     else:
         assert not gone.any()
+
+
+# (V, K): more tiles of V than places for them, so that a CTA goes on to a second
+# one; and fewer, but too many to split K.  Blocks of K that fill neither the
+# stages nor the accumulators evenly.
+@pytest.mark.parametrize("V,K", [(40003, 400), (39001, 912), (30000, 656)])
+def test_few_rows_on_a_vocabulary(V, K):
+    a, sa, b, sb = operands(48, V, K, seed=V)
+    want, mag = ref.matmul_fp8(f64(a), f64(sa), f64(b), f64(sb))
+    G = sa.shape[-1]
+    tol = (2.0 ** -16 + 3 * (G + 1) * 2.0 ** -24) * mag
+    for M in (1, 16, 17, 32, 33, 48):
+        for out in (BF, F32):
+            y = f64(flce.matmul_fp8(a[:M], sa[:M], b, sb, out_dtype=out))
+            t = tol[:M] + (1.01 * 2.0 ** -8 * np.abs(want[:M]) if out == BF else 0)
+            assert (np.abs(y - want[:M]) <= t).all(), (M, out)

@@ -158,3 +158,44 @@ def test_calls_in_a_row_wait_for_one_another(B):
         got = chain(lambda: None)
         assert all(torch.equal(a, b) for a, b in zip(got, want))
     assert torch.isfinite(want[0].float()).all() and want[0].float().abs().max() > 0
+
+
+def test_threads_with_streams_of_their_own():
+    """Four threads run decode steps at once, each on its own stream and, every
+    other one, on sizes that no thread has used before: the same bits as alone."""
+    import threading
+
+    def setup(i):
+        g = torch.Generator().manual_seed(i)
+        B, H, V = (1, 40, 100, 3)[i], 256 + 128 * i, 3001 + 1000 * i
+        x = torch.randn(B, H, generator=g).to(BF).cuda()
+        w = (1 + 0.2 * torch.randn(H, generator=g)).to(BF).cuda()
+        W = (0.05 * torch.randn(V, H, generator=g)).to(BF).cuda()
+        tok = torch.randint(0, V, (B, 30), generator=g).cuda()
+        return x, w, W, tok, torch.full((B,), 0.5, device="cuda")
+
+    def step(x, w, W, tok, fp):
+        b, bs = flce.quantize_fp8(W)
+        q, s = flce.rms_norm_fp8(x, w)
+        z = flce.matmul_fp8(q, s, b, bs)
+        y, h, rstd = flce.flce_rms_norm(x, w)
+        dx, dw = flce.flce_rms_norm_backward(y, h, w, rstd)
+        return flce.process_logits(z, tokens=tok, frequency_penalty=fp), dx, dw
+    data = [setup(i) for i in range(4)]
+    want = [step(*d) for d in data]
+    torch.cuda.synchronize()
+    wrong, start = [], threading.Barrier(4)
+
+    def work(i):
+        s = torch.cuda.Stream()
+        start.wait()
+        with torch.cuda.stream(s):
+            outs = [step(*data[i]) for _ in range(20)]
+        s.synchronize()
+        wrong.extend(i for o in outs for a, b in zip(o, want[i]) if not torch.equal(a, b))
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong

@@ -394,3 +394,26 @@ def test_an_output_that_wants_a_gradient_is_refused():
     with torch.no_grad():
         assert flce.rms_norm_fp8(x, w, residual=res, residual_out=leaf)[2] is leaf
     assert torch.equal(leaf.detach(), (x.float() + res.float()).to(BF))
+
+
+@pytest.mark.parametrize("N,H", [(5, 200), (64, 3584), (700, 4096), (9, 1001)])
+def test_bf16_gradient_against_the_forward_as_it_is(N, H):
+    """The forward norms the sum as it is, the backward takes the sum as it was
+    stored, rounded by up to e = 2^-8.  Against the gradient of the forward, that
+    is e of each place where the sum stands: r^3 |h| (|m| + mean |g h|) of dx, with
+    m = mean(g h), and r |dy h| of each term of dweight; beside the errors that the
+    backward has on the stored sum (see test_backward)."""
+    x, res, w, dy, dh = case(N, H, BF, BF, seed=16)
+    y, h, rstd = flce.flce_rms_norm(x, w, eps=EPS, residual=res)
+    dx, dw = flce.flce_rms_norm_backward(dy, h, w, rstd, dh=dh)
+    s = f64(x) + f64(res)
+    rdx, rdw = ref.rms_norm_backward(f64(dy), s, f64(w), EPS, f64(dh))
+    r = 1 / np.sqrt((s * s).mean(1, keepdims=True) + EPS)
+    g, e = f64(dy) * f64(w), 1.01 * rnd(BF)
+    m, am = (g * s).mean(1, keepdims=True), np.abs(g * s).mean(1, keepdims=True)
+    big = r * np.abs(g) + r ** 3 * np.abs(s) * am + np.abs(f64(dh))
+    tol = e * r ** 3 * np.abs(s) * (np.abs(m) + (1 + e) * am) + (sum_tol(H) + 12 * U) * big
+    assert (np.abs(f64(dx) - rdx) <= tol + e * (np.abs(rdx) + tol)).all()
+    t = np.abs(f64(dy) * s * r).sum(0)
+    tol = (e + (N / 32 + 80 + H / 256) * U) * t
+    assert (np.abs(f64(dw) - rdw) <= tol + e * (np.abs(rdw) + tol)).all()

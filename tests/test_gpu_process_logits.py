@@ -322,3 +322,43 @@ def test_an_output_that_wants_a_gradient_is_refused():
             flce.process_logits(z, out=out)
     with torch.no_grad():
         assert flce.process_logits(z, out=z) is z
+
+
+@pytest.mark.parametrize("prompt", [None, 0, 1, "all"])
+@pytest.mark.parametrize("L", [32767, 32768, 32769])
+def test_one_id_throughout_a_history_around_2_to_15(L, prompt):
+    """The largest counts that 16 bits hold, and the first that take 32: logits of
+    one, halved where seen, less the count, and their neighbours untouched."""
+    V = 1000
+    ids = torch.tensor([0, 1, 500, 501, 998, 999])
+    B = len(ids)
+    k = dict(tokens=ids[:, None].expand(B, L).contiguous(),
+             repetition_penalty=torch.full((B,), 2.0), frequency_penalty=torch.ones(B))
+    n = {None: 0, "all": L}.get(prompt, prompt)
+    if prompt is not None:
+        k["prompt_lengths"] = torch.full((B,), n, dtype=torch.int32)
+    want = torch.ones(B, V)
+    want[torch.arange(B), ids] = 0.5 - (L - n)
+    assert torch.equal(run(torch.ones(B, V), k).cpu(), want)
+    k["tokens"] = k["tokens"].int()
+    assert torch.equal(run(torch.ones(B, V), k).cpu(), want)
+
+
+@pytest.mark.parametrize("V", [3001, 30000])
+def test_long_histories_with_many_biases(V):
+    z, k = case(3, V, 33000, 700, F32, torch.int32, seed=V)
+    k["bias_ids"][:, ::5] = k["bias_ids"][:, 1:2]  # one id again and again
+    check(run(z, k), z, k)
+
+
+@pytest.mark.parametrize("B,V", [(2, 9001), (64, 9000)])
+def test_a_history_buffer_longer_than_its_histories(B, V):
+    """Rows of a buffer of 131072 ids of which up to 500 are live: the same as in
+    a buffer of 500 (other counters, other blocks)."""
+    z, k = case(B, V, 500, 4, BF, torch.int64, seed=V)
+    want = run(z, k, out_dtype=F32)
+    wide = torch.full((B, 131072), 7, dtype=torch.int64, device="cuda")
+    wide[:, :500] = k["tokens"].cuda()
+    got = flce.process_logits(z.cuda(), out_dtype=F32, **dict(
+        {n: t.cuda() for n, t in k.items()}, tokens=wide))
+    assert torch.equal(got, want)
