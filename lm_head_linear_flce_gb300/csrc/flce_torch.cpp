@@ -129,15 +129,16 @@ struct Norm {
   int64_t N, H;
   Rows xr, rr;
 
-  Norm(PyObject* xo, PyObject* wo, PyObject* ro)
-      : x(arg(xo, "x")), weight(arg(wo, "weight")), residual(arg(ro, "residual")) {
-    check_cuda(x, "x");
-    type = check_float(x, "x");
+  // `name`: what the caller calls x
+  Norm(PyObject* xo, PyObject* wo, PyObject* ro, const char* name = "x")
+      : x(arg(xo, name)), weight(arg(wo, "weight")), residual(arg(ro, "residual")) {
+    check_cuda(x, name);
+    type = check_float(x, name);
     check_cuda(weight, "weight", x.get_device());
     weight_type = check_float(weight, "weight");
     H = x.dim() ? x.size(-1) : 0;
     TORCH_CHECK_VALUE(H > 0 && weight.dim() == 1 && weight.size(0) == H,
-                      "expected x [..., H] and weight [H]");
+                      "expected ", name, " [..., H] and weight [H]");
     if (residual.defined()) {
       check_cuda(residual, "residual", x.get_device());
       check_type(residual, "residual", x.scalar_type(), x.scalar_type());
@@ -201,7 +202,7 @@ PyObject* rms_norm_fp8(PyObject*, PyObject* const* a, Py_ssize_t n) {
 PyObject* rms_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   check_count(n, 7);
-  Norm m(a[1], a[2], Py_None);
+  Norm m(a[1], a[2], Py_None, "h");
   const Tensor& h = m.x;
   Tensor dy = arg(a[0], "dy"), dh = arg(a[4], "dh"), rstd = arg(a[3], "rstd");
   const auto like_h = [&](Tensor& t, const char* name) {

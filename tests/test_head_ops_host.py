@@ -174,3 +174,11 @@ def test_float_outputs_and_statistics_that_are_not_aligned(off):
     for rows in (1, 128):
         assert fn("flce_quantize_fp8")(BASE, 64, 10, 64, 1, rows, BASE + G, BASE + 2 * G + off,
                                        None) == INVALID
+
+
+def test_the_backward_names_its_own_arguments():
+    h, w = torch.zeros(2, 64, dtype=torch.bfloat16), torch.ones(64)
+    with pytest.raises(ValueError, match="^h must be a CUDA tensor"):
+        flce.flce_rms_norm_backward(h, h, w, torch.ones(2))
+    with pytest.raises(ValueError, match="^x must be a CUDA tensor"):
+        flce.rms_norm(h, w)
