@@ -432,7 +432,9 @@ flce_status flce_rms_norm_fp8(const void* x, int64_t ldx, const void* residual, 
  *   dy         device [N][H] of `dtype`.
  *   dh         device [N][H] of `dtype`: gradient of h_out, or NULL.
  *   h          device [N][H] of `dtype`, rows ldh apart: h_out (x without a
- *              residual); rstd device float [N], as written by the forward.
+ *              residual); rstd device float [N], as written by the forward.  (h_out
+ *              is rounded, so with bf16 this is the gradient at a sum up to 2^-8
+ *              of it away from the one the forward normed.)
  *   dx         device [N][H] of `dtype`, or NULL.
  *   dweight    device [H] of `weight_dtype`, or NULL.
  *   workspace  device, 256-byte aligned, flce_rms_norm_workspace_size(N, H)
@@ -516,7 +518,9 @@ flce_status flce_selftest_matmul_fp8_timeout(int64_t stop_after, int64_t limit_n
  *              n_bias = 0; n_bias <= 65535.
  *   allowed    device int32 [B][>= ceil(V / 32)], rows ld_allowed words apart,
  *              or NULL: bit v % 32 of word v / 32 is set where v is allowed.
- * A row without an allowed column is -infinity throughout.
+ * A row without an allowed column is -infinity throughout.  B <= 65535, V <= 2^30,
+ * L < 2^31.  The division is by way of 1 / repetition where that is of ordinary size
+ * (one float rounding more).
  */
 flce_status flce_process_logits(const void* logits, int64_t ld_logits, flce_dtype dtype,
                                 int64_t B, int64_t V, const void* tokens, int64_t ld_tokens,

@@ -37,10 +37,10 @@ constexpr int kMmaK8 = 32;    // K per MMA
 // fill TMEM, two of 256 columns or four of 128, hide that.
 //
 // Bound by the tensor cores, and in a loop of seconds by the board's power: pairs
-// take 1.53 to 1.63 ms for 4096 x 152064 x 3584 to bf16 (2.7 to 2.9 PFLOP/s), 1.68
-// ms in a loop.  Up to 128 rows it is bound by reading B, of which a CTA by
-// itself has 32 KB a block under way where one of a pair has 16: 128 x 151936 x
-// 4096 to float32 takes 112 us (6.2 TB/s), with pairs 127.  Also measured, pairs at
+// take 1.43 to 1.65 ms for 4096 x 152064 x 3584 to bf16 on one board or another (2.7
+// to 3.1 PFLOP/s), 1.63 to 1.71 ms in a loop.  Up to 128 rows it is bound by reading
+// B, of which a CTA by itself has 32 KB a block under way where one of a pair has 16:
+// 128 x 151936 x 4096 to float32 takes 114 us (6.1 TB/s), with pairs 127.  Also measured, pairs at
 // 4096 x 152064 x 3584: three accumulators of 160 columns 2.2 PFLOP/s, sixteen
 // epilogue warps 1.9, accumulators in halves 1.5; a second staging buffer for the
 // stores and scales fetched a tile ahead changed nothing.
@@ -408,10 +408,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 //
 // A column's scale differs from lane to lane here (it is a row of A), so each
 // block costs the epilogue a scale per element from shared memory.  Of 151936 x
-// 4096 bytes: 8 rows 93.5 us (6.7 TB/s), 32 103, 48 105, 64 110, each to float32;
-// NP = 128 took 177 where tiles take 112.  NP = 48 is worth having
-// where the rows of A start inside a 128-byte line and so cost two reads each:
-// 37 x 32003 x 2064 19.7 us, padded to 64 21.8.
+// 4096 bytes: 8 rows 94 to 96 us (6.6 TB/s), 32 105, 48 107, each to float32; NP = 64
+// took 110 where tiles take 107, NP = 128 177 where they take 114.  NP = 48 is worth
+// having where the rows of A start inside a 128-byte line and so cost two reads each:
+// 37 x 32003 x 2064 18.3 to 19.7 us, padded to 64 21.8.
 template <int NP>
 struct RowShape {
   static constexpr int kThreads = 192;  // warp 0 TMA, warp 1 MMA, warps 2..5 epilogue

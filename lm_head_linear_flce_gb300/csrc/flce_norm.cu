@@ -226,9 +226,10 @@ __device__ __forceinline__ float row_sum(float v, float* part, int phase) {
 }
 
 // Bytes bound it: 16-byte loads of every value once, all of a row's in flight
-// at once.  8192 x 3584 bf16 with a residual: 36 us under ncu, 6.5 TB/s of the
-// 8 bytes a value (the measured copy rate is 6.8); one row with 8-bit output 3.5
-// us, launch latency and two trips to memory.
+// at once.  8192 x 3584 with a residual, call after call: bf16 41 us (5.7 TB/s of
+// its 8 bytes a value; the measured copy rate is 6.8), float32 71 (6.6); with 8-bit
+// output 43 and 66 us; one row with 8-bit output 3 us, launch latency and two trips
+// to memory.
 template <class T, bool FP8, bool VEC, int P>
 __global__ void __launch_bounds__(1024)
     norm_fwd_held_kernel(const T* x, int64_t ldx, const T* residual, int64_t ldr,
@@ -321,6 +322,12 @@ __device__ __forceinline__ void copy_async16(void* dst, const void* src) {
 // registers, and a row is read there twice (sum, then dx) instead of being held
 // over the sum.  Without it (rows not aligned to 16 bytes, or too long for the
 // slots) a row is loaded when its turn comes.
+//
+// h is the sum as the forward stored it, in T, where the forward normed the sum
+// before it was rounded: keeping that would double what the forward writes and this
+// reads.  In bf16 it is a rounding of up to 2^-8 of h in the gradients (8192 x 3584:
+// 0.0023 off the gradient in 64 bits, where the outputs' own rounding alone makes
+// 0.0017).
 //
 // 8192 x 3584 with dh, dweight's sum included: bf16 50 us (4.7 TB/s of 8 bytes a
 // value), float32 76 us (6.2 TB/s); bf16 spends twice the instructions a byte.
@@ -460,9 +467,12 @@ __global__ void __launch_bounds__(32 * kSumWarps)
 // dx needs a row's sum, dweight a column's, and neither needs the other: where
 // the inputs stay in L2, one launch does both, the first `row_blocks` blocks rows
 // (`tpr` threads each, 8 values a thread) and the others 16 columns each, over all
-// rows.  Latency bounds it: 64 x 4096 bf16 5.6 us against 7.6 for the two launches
-// above, 2048 x 64 6.2 against 8.3; 1021 x 1001 float32 8.3 against 7.5, but 13.0
-// against 14.5 us a forward and backward where the host launches them one by one.
+// rows.  Latency bounds it: 64 x 4096 bf16 4.5 us against 6.5 for the two launches
+// above, 2048 x 64 5.1 against 7.2, 512 x 4096 13.3 against 14.6.  Where the rows
+// are many or long for its two readings it is the slower kernel: 1021 x 1001 float32
+// 8.3 against 6.9 (but 13.4 against 15.5 us a forward and backward where the host
+// launches them one by one), 2048 x 1024 bf16 14.4 against 10.6, 256 x 8192 17.4
+// against 13.7.
 constexpr int kSmallThreads = 1024;
 constexpr int kSmallValues = 8;
 constexpr int kSmallCols = 16;
@@ -611,7 +621,8 @@ __global__ void __launch_bounds__(kNormThreads)
 // 128 x 128 blocks of a matrix with 16-byte rows: a thread block reads a block
 // once into registers (8 values of bf16, 4 of float32 a load, all in flight),
 // takes the maximum and writes it.  Bound by bytes, 2 + 1 a bf16 value: 152064 x
-// 3584 in 248 us, 6.6 TB/s, with three blocks an SM (two: 288 us).
+// 3584 in 248 us, 6.6 TB/s, with three blocks an SM (two: 288 us); float32 411 us,
+// 6.6 TB/s.
 template <class T>
 __global__ void __launch_bounds__(kNormThreads, 3)
     quantize_tile_kernel(const T* __restrict__ x, int64_t ldx, int64_t R, int K,
@@ -678,7 +689,8 @@ __global__ void __launch_bounds__(kNormThreads, 3)
 }
 
 // 1 x 128 groups: a half warp (bf16) or warp (float32, or unaligned rows, 4
-// columns 32 apart a lane) per group; 152064 x 3584 bf16 in 314 us, 5.2 TB/s.
+// columns 32 apart a lane) per group; 152064 x 3584 bf16 in 312 us, 5.2 TB/s,
+// float32 571 us, 4.8 TB/s.
 template <class T, bool VEC>
 __global__ void __launch_bounds__(kNormThreads)
     quantize_rows_kernel(const T* __restrict__ x, int64_t ldx, int64_t R, int K,
@@ -946,7 +958,8 @@ cudaError_t launch_bwd_held(const RowPlan& p, bool aligned, int64_t parts,
 }
 
 // Rows that norm_bwd_small_kernel takes: a column's block adds at most 64 of them
-// a warp, and 2^21 values are read twice from L2.
+// a warp, and 2^21 values are read twice from L2.  (Times on both sides: above.  By
+// the GPU's time alone the limit would be lower.)
 bool small_bwd(int64_t N, int64_t H) {
   return N <= 2048 && H <= kSmallThreads * kSmallValues && N * H <= int64_t{1} << 21;
 }

@@ -42,11 +42,15 @@ __device__ __forceinline__ int64_t id_at(const void* p, int is64, int64_t i) {
 // per bf16 -> float32 column.  The first logits are loaded before the counting,
 // so that they arrive under it.
 // One row of 152064 takes 4.2 us, a launch and three trips to memory; 256 x 128255
-// float32 with histories of 2000 47.8 us (5.6 TB/s); 64 x 151936 bf16 with masks
-// 13.5 us without histories, and 28 us with up to 32768 ids of a text's
-// distribution a row, where the ids' instructions and the row's repeated reading
-// take over.  (Counting in a kernel beside a streaming one: 62 us where this then
-// took 45; grouping a warp's equal ids before the update was slower too.)
+// float32 with histories of 2000 47.6 us (5.6 TB/s), in place 63; 64 x 151936 bf16
+// with masks 12.8 us without histories, with 2000 ids a row 14.9, to bf16 14.2, in
+// place 15.8 (no loads ahead there), and 28 us with up to 32768 ids of a text's
+// distribution a row, where the ids' instructions and the row's reading by each of
+// its four blocks take over.  Where a row starts elsewhere in its 16 bytes than its
+// output, its columns go one by one: 64 rows of 128255, 128256 apart, into rows 128255
+// apart take 31 us, into rows 128256 apart 13.5.  (Counting in a kernel beside a
+// streaming one: 62 us where this then took 45; grouping a warp's equal ids before the
+// update was slower too.)
 //
 // A column's counter is its number of generated occurrences, and a top bit for
 // "in the prompt".  16 bits do for a history of up to 2^15 (half the shared

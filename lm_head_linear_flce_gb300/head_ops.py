@@ -164,7 +164,7 @@ def rms_norm(x, weight, eps=1e-6, residual=None):
     x: bf16 or float32 [..., H]; weight: bf16 or float32 [H].  Without a residual
     returns y = x * weight / sqrt(mean(x^2) + eps).  With one (as x) returns
     (y, h): the norm of h = x + residual, and h, the new residual stream.  Sums
-    are FP32; y and h are rounded once."""
+    are FP32; y and h are rounded once.  The backward takes h as rounded."""
     return _RmsNorm.apply(x, weight, residual, eps)
 
 
@@ -193,7 +193,8 @@ def matmul_fp8(a, a_scale, b, b_scale, out_dtype=torch.bfloat16):
     a: float8_e4m3fn [..., K] with a_scale float32 [..., ceil(K / 128)], as
     rms_norm_fp8 or quantize_fp8(block_rows=1) give them; b: float8_e4m3fn
     [V, K] with b_scale float32 [ceil(V / 128), ceil(K / 128)], as
-    quantize_fp8(W) gives them.  K must be a multiple of 16.  As with
+    quantize_fp8(W) gives them.  K must be a multiple of 16; an operand whose rows
+    are not 16-byte aligned is copied, on every call.  As with
     flce_logits, where V is no multiple of 8 the result is a view of rows padded
     to one (16-byte rows).  No gradient.  If a wait inside the kernel runs out
     (flce_set_wait_limit_ns), what it had not finished is NaN."""
