@@ -182,3 +182,15 @@ def test_the_backward_names_its_own_arguments():
         flce.flce_rms_norm_backward(h, h, w, torch.ones(2))
     with pytest.raises(ValueError, match="^x must be a CUDA tensor"):
         flce.rms_norm(h, w)
+
+
+def test_matmul_selftest_refusals():
+    def call(stop_after=0, limit=1000, **kw):
+        a = dict(A=BASE, lda=256, sa=BASE + G, B=BASE + 2 * G, ldb=256, sb=BASE + 3 * G, M=4, V=100,
+                 K=256, y=BASE + 4 * G, ldy=100, dt=0)
+        a.update(kw)
+        return fn("flce_selftest_matmul_fp8_timeout")(stop_after, limit, *a.values(), None)
+    assert call(stop_after=-1) == INVALID and call(limit=0) == INVALID
+    assert call(A=None) == INVALID and call(ldy=99) == INVALID  # as the product itself
+    assert call(K=200, lda=208, ldb=208) == SHAPE
+    assert call(M=0, A=None) == 0
