@@ -449,6 +449,59 @@ flce_status flce_rms_norm_backward(const void* dy, const void* dh, const void* h
 size_t flce_rms_norm_workspace_size(int64_t N, int64_t H);
 
 /*
+ * Layer norm with the residual's addition, row by row:
+ *
+ *     h = x + residual            (h = x without a residual)
+ *     n = (h - mean) * rstd       mean = mean(h), rstd = 1 / sqrt(mean((h - mean)^2) + eps)
+ *     y = n * weight + bias       (weight 1, bias 0 where they are NULL)
+ *
+ * in FP32, the squares summed over h - mean; y and h are rounded to the element type
+ * once, and y is formed from the unrounded h.
+ *   x, residual, y, h_out   as in flce_rms_norm_forward.
+ *   weight, bias            device [H] of `weight_dtype`, each may be NULL.
+ *   mean, rstd              device float [N] each, both or neither NULL.
+ * 1 <= H <= 65536; alignment and overlap as in flce_rms_norm_forward.
+ */
+flce_status flce_layer_norm_forward(const void* x, int64_t ldx, const void* residual, int64_t ldr,
+                                    const void* weight, const void* bias, int64_t N, int64_t H,
+                                    float eps, flce_dtype dtype, flce_dtype weight_dtype, void* y,
+                                    void* h_out, float* mean, float* rstd, flce_stream_t stream);
+
+/*
+ * The same norm with y in 8 bits, from its unrounded FP32 values; q and scale as in
+ * flce_rms_norm_fp8.
+ */
+flce_status flce_layer_norm_fp8(const void* x, int64_t ldx, const void* residual, int64_t ldr,
+                                const void* weight, const void* bias, int64_t N, int64_t H,
+                                float eps, flce_dtype dtype, flce_dtype weight_dtype, void* q,
+                                float* scale, void* h_out, flce_stream_t stream);
+
+/*
+ * Backward of flce_layer_norm_forward, with g = dy * weight:
+ *
+ *     dx = rstd * (g - mean(g) - n * mean(g * n)) + dh      (of x and of residual)
+ *     dweight = sum over rows of dy * n,  dbias = sum over rows of dy
+ *
+ *   dy, dh, h, ldh   as in flce_rms_norm_backward (h: h_out, or x without a residual;
+ *                    in bf16 the rounded sum).
+ *   weight           device [H] of `weight_dtype`, or NULL (1).
+ *   mean, rstd       device float [N], as written by the forward.
+ *   dx               device [N][H] of `dtype`, or NULL.
+ *   dweight, dbias   device [H] of `weight_dtype`, each may be NULL.
+ *   workspace        device, 256-byte aligned, flce_layer_norm_workspace_size(N, H)
+ *                    bytes, where dweight or dbias is wanted: FP32 partial sums, added in
+ *                    a fixed order.
+ * No output may overlap an input, the workspace or another output.
+ */
+flce_status flce_layer_norm_backward(const void* dy, const void* dh, const void* h, int64_t ldh,
+                                     const void* weight, const float* mean, const float* rstd,
+                                     int64_t N, int64_t H, flce_dtype dtype,
+                                     flce_dtype weight_dtype, void* dx, void* dweight, void* dbias,
+                                     void* workspace, size_t workspace_bytes,
+                                     flce_stream_t stream);
+size_t flce_layer_norm_workspace_size(int64_t N, int64_t H);
+
+/*
  * x [R][K] (`dtype`, rows ldx elements apart) in 8 bits with one scale per
  * block_rows x 128 block, block_rows 1 (activations) or 128 (weights):
  *   q      device [R][K] e4m3;  scale  device float [ceil(R / block_rows)][ceil(K / 128)].

@@ -28,8 +28,9 @@ __all__ = [
     "flce_logits", "flce_forward_vocab_shard", "flce_merge_vocab_shards",
     "flce_backward_vocab_shard", "flce_downcast_bf16",
     "linear_cross_entropy", "STATUS",
-    "flce_rms_norm", "flce_rms_norm_backward", "rms_norm", "rms_norm_fp8", "quantize_fp8",
-    "matmul_fp8", "process_logits",
+    "flce_rms_norm", "flce_rms_norm_backward", "rms_norm", "rms_norm_fp8", "flce_layer_norm",
+    "flce_layer_norm_backward", "layer_norm", "layer_norm_fp8", "quantize_fp8", "matmul_fp8",
+    "process_logits",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -455,5 +456,6 @@ def linear_cross_entropy(hidden, weight, labels, ignore_index=-100, shift=False,
                                 seq_len, ignore_index, shift, reduction)
 
 
-from .head_ops import (flce_rms_norm, flce_rms_norm_backward, matmul_fp8,  # noqa: E402
-                       process_logits, quantize_fp8, rms_norm, rms_norm_fp8)
+from .head_ops import (flce_layer_norm, flce_layer_norm_backward,  # noqa: E402
+                       flce_rms_norm, flce_rms_norm_backward, layer_norm, layer_norm_fp8,
+                       matmul_fp8, process_logits, quantize_fp8, rms_norm, rms_norm_fp8)

@@ -521,8 +521,6 @@ __global__ void __launch_bounds__(kNormThreads)
       a / kFp8Max;
 }
 
-constexpr int64_t kMaxRows = (int64_t{1} << 31) - 1;
-
 // What both forward entry points check.
 flce_status check_norm(const void* x, int64_t ldx, const void* residual, int64_t ldr,
                        const void* weight, int64_t N, int64_t H, flce_dtype dtype,
@@ -537,24 +535,6 @@ flce_status check_norm(const void* x, int64_t ldx, const void* residual, int64_t
       !aligned_to(weight, dtype_bytes(weight_dtype)))
     return FLCE_ERR_INVALID_ARG;
   return FLCE_OK;
-}
-
-// No output overlaps an input or another output, but that h_out may be x or
-// residual itself.
-bool norm_outputs_apart(const void* x, int64_t ldx, const void* residual, int64_t ldr,
-                        const Range& weight, int64_t N, int64_t H, size_t e, const void* h_out,
-                        const Range& a, const Range& b) {
-  const Range ins[] = {{x, span_bytes(N, H, ldx, e)},
-                       {residual, span_bytes(N, H, ldr, e)},
-                       weight};
-  const Range h = {h_out, span_bytes(N, H, H, e)};
-  for (const Range& r : ins) {
-    if (ranges_overlap(a, r) || ranges_overlap(b, r)) return false;
-    const bool itself = h_out && r.p == h_out && r.p != weight.p &&
-                        ((r.p == x && ldx == H) || (r.p == residual && ldr == H));
-    if (!itself && ranges_overlap(h, r)) return false;
-  }
-  return !ranges_overlap(a, b) && !ranges_overlap(a, h) && !ranges_overlap(b, h);
 }
 
 // The backward's threads a row: up to 256 before a thread takes more slots.
@@ -813,10 +793,9 @@ flce_status flce_rms_norm_forward(const void* x, int64_t ldx, const void* residu
   const size_t e = dtype_bytes(dtype);
   if (!y || !aligned_to(y, e) || !aligned_to(h_out, e) || !aligned_to(rstd, 4))
     return FLCE_ERR_INVALID_ARG;
-  if (!norm_outputs_apart(x, ldx, residual, ldr,
-                          {weight, static_cast<size_t>(H) * dtype_bytes(weight_dtype)}, N, H, e,
-                          h_out, {y, span_bytes(N, H, H, e)},
-                          {rstd, static_cast<size_t>(N) * 4}))
+  if (!norm_outputs_apart(x, ldx, residual, ldr, N, H, e, h_out,
+                          {{weight, static_cast<size_t>(H) * dtype_bytes(weight_dtype)}},
+                          {{y, span_bytes(N, H, H, e)}, {rstd, static_cast<size_t>(N) * 4}}))
     return FLCE_ERR_INVALID_ARG;
   int sms = 0;
   if ((st = check_device(&sms)) != FLCE_OK) return st;
@@ -838,10 +817,9 @@ flce_status flce_rms_norm_fp8(const void* x, int64_t ldx, const void* residual, 
   const size_t e = dtype_bytes(dtype);
   if (!q || !scale || !aligned_to(h_out, e) || !aligned_to(scale, 4)) return FLCE_ERR_INVALID_ARG;
   const int64_t groups = (H + kScaleGroup - 1) / kScaleGroup;
-  if (!norm_outputs_apart(x, ldx, residual, ldr,
-                          {weight, static_cast<size_t>(H) * dtype_bytes(weight_dtype)}, N, H, e,
-                          h_out, {q, span_bytes(N, H, H, 1)},
-                          {scale, span_bytes(N, groups, groups, 4)}))
+  if (!norm_outputs_apart(x, ldx, residual, ldr, N, H, e, h_out,
+                          {{weight, static_cast<size_t>(H) * dtype_bytes(weight_dtype)}},
+                          {{q, span_bytes(N, H, H, 1)}, {scale, span_bytes(N, groups, groups, 4)}}))
     return FLCE_ERR_INVALID_ARG;
   int sms = 0;
   if ((st = check_device(&sms)) != FLCE_OK) return st;

@@ -1,5 +1,5 @@
-// What the norms' kernels share: rows held in registers, their loads, stores and
-// sums, 8-bit output, and the plan of threads a row.
+// What the norms share: rows held in registers, their loads, stores and sums,
+// 8-bit output, the plan of threads a row, and the check that outputs are apart.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -7,6 +7,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <initializer_list>
 
 #include "flce_device.cuh"
 #include "flce_ops.h"
@@ -256,6 +257,36 @@ __device__ __forceinline__ void store_quantized(const float (&v)[Slots<T, VEC>::
 __device__ __forceinline__ void copy_async16(void* dst, const void* src) {
   const uint32_t d = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(src) : "memory");
+}
+
+constexpr int64_t kMaxRows = (int64_t{1} << 31) - 1;
+
+// No output of a norm's forward (h_out, `outs`) overlaps an input (x, residual,
+// `params`) or another output, but that h_out may be x or residual itself.
+inline bool norm_outputs_apart(const void* x, int64_t ldx, const void* residual, int64_t ldr,
+                               int64_t N, int64_t H, size_t e, const void* h_out,
+                               std::initializer_list<Range> params,
+                               std::initializer_list<Range> outs) {
+  const Range ins[] = {{x, span_bytes(N, H, ldx, e)}, {residual, span_bytes(N, H, ldr, e)}};
+  const Range h = {h_out, span_bytes(N, H, H, e)};
+  for (const Range& r : ins) {
+    const bool itself = h_out && r.p == h_out &&
+                        ((r.p == x && ldx == H) || (r.p == residual && ldr == H));
+    if (!itself && ranges_overlap(h, r)) return false;
+    for (const Range& o : outs)
+      if (ranges_overlap(o, r)) return false;
+  }
+  for (const Range& r : params) {
+    if (ranges_overlap(h, r)) return false;
+    for (const Range& o : outs)
+      if (ranges_overlap(o, r)) return false;
+  }
+  for (const Range* o = outs.begin(); o != outs.end(); ++o) {
+    if (ranges_overlap(*o, h)) return false;
+    for (const Range* p = outs.begin(); p != o; ++p)
+      if (ranges_overlap(*o, *p)) return false;
+  }
+  return true;
 }
 
 // How a row of H columns is spread over threads.  Few rows: as many threads as

@@ -124,7 +124,7 @@ int64_t integer(PyObject* o) {
 
 // What the norms share.
 struct Norm {
-  Tensor x, weight, residual, h, out;  // out: residual_out, if it is given
+  Tensor x, weight, bias, residual, h, out;  // out: residual_out, if it is given
   flce_dtype type, weight_type;
   int64_t N, H;
   Rows xr, rr;
@@ -139,6 +139,34 @@ struct Norm {
     H = x.dim() ? x.size(-1) : 0;
     TORCH_CHECK_VALUE(H > 0 && weight.dim() == 1 && weight.size(0) == H,
                       "expected ", name, " [..., H] and weight [H]");
+    add_residual();
+    if (!weight.is_contiguous()) weight = weight.contiguous();
+  }
+  // The layer norm's: weight and bias may each be None.
+  Norm(PyObject* xo, PyObject* wo, PyObject* bo, PyObject* ro, const char* name)
+      : x(arg(xo, name)), weight(arg(wo, "weight")), bias(arg(bo, "bias")),
+        residual(arg(ro, "residual")) {
+    check_cuda(x, name);
+    type = check_float(x, name);
+    H = x.dim() ? x.size(-1) : 0;
+    TORCH_CHECK_VALUE(H > 0, "expected ", name, " [..., H]");
+    weight_type = type;
+    const auto param = [&](Tensor& t, const char* what) {
+      if (!t.defined()) return;
+      check_cuda(t, what, x.get_device());
+      weight_type = check_float(t, what);
+      TORCH_CHECK_VALUE(t.dim() == 1 && t.size(0) == H, what, " must be [H] where ", name,
+                        " is [..., H]");
+      if (!t.is_contiguous()) t = t.contiguous();
+    };
+    param(bias, "bias");
+    param(weight, "weight");
+    TORCH_CHECK_VALUE(!weight.defined() || !bias.defined() ||
+                          weight.scalar_type() == bias.scalar_type(),
+                      "weight and bias must have the same type");
+    add_residual();
+  }
+  void add_residual() {
     if (residual.defined()) {
       check_cuda(residual, "residual", x.get_device());
       check_type(residual, "residual", x.scalar_type(), x.scalar_type());
@@ -147,7 +175,6 @@ struct Norm {
     N = x.numel() / H;
     xr = rows(x, H);
     rr = rows(residual, H);
-    if (!weight.is_contiguous()) weight = weight.contiguous();
   }
   // Where the norm writes the sum: residual_out, or a new tensor if there is a residual.
   void sum_buffer(PyObject* o) {
@@ -230,6 +257,92 @@ PyObject* rms_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
       ptr(dy), ptr(dh), m.xr.p, m.xr.ld, ptr(m.weight), static_cast<const float*>(ptr(rstd)), m.N,
       m.H, m.type, m.weight_type, ptr(dx), ptr(dw), ptr(ws), nws, on.stream);
   return answer(st, std::move(dx), std::move(dw));
+  END_HANDLE_TH_ERRORS
+}
+
+// (x, weight, bias, eps, residual, residual_out) -> (y, h or None, mean, rstd)
+PyObject* layer_norm_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  check_count(n, 6);
+  Norm m(a[0], a[1], a[2], a[4], "x");
+  OnDevice on(m.x);
+  m.sum_buffer(a[5]);
+  Tensor y = empty(m.x.sizes(), m.x, m.x.scalar_type());
+  const auto lead = m.x.sizes().slice(0, m.x.dim() - 1);
+  Tensor mean = empty(lead, m.x, at::kFloat), rstd = empty(lead, m.x, at::kFloat);
+  const flce_status st = flce_layer_norm_forward(
+      m.xr.p, m.xr.ld, m.rr.p, m.rr.ld, ptr(m.weight), ptr(m.bias), m.N, m.H,
+      static_cast<float>(number(a[3])), m.type, m.weight_type, ptr(y), ptr(m.h),
+      static_cast<float*>(ptr(mean)), static_cast<float*>(ptr(rstd)), on.stream);
+  if (st == FLCE_OK) note_written(m.out);
+  return answer(st, std::move(y), std::move(m.h), std::move(mean), std::move(rstd));
+  END_HANDLE_TH_ERRORS
+}
+
+// (x, weight, bias, eps, residual, residual_out) -> (q, scale, h or None)
+PyObject* layer_norm_fp8(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  check_count(n, 6);
+  Norm m(a[0], a[1], a[2], a[4], "x");
+  OnDevice on(m.x);
+  m.sum_buffer(a[5]);
+  Tensor q = empty(m.x.sizes(), m.x, at::kFloat8_e4m3fn);
+  Tensor scale = empty(lead_and(m.x, (m.H + kGroup - 1) / kGroup), m.x, at::kFloat);
+  const flce_status st = flce_layer_norm_fp8(
+      m.xr.p, m.xr.ld, m.rr.p, m.rr.ld, ptr(m.weight), ptr(m.bias), m.N, m.H,
+      static_cast<float>(number(a[3])), m.type, m.weight_type, ptr(q),
+      static_cast<float*>(ptr(scale)), ptr(m.h), on.stream);
+  if (st == FLCE_OK) note_written(m.out);
+  return answer(st, std::move(q), std::move(scale), std::move(m.h));
+  END_HANDLE_TH_ERRORS
+}
+
+// (dy, h, weight, mean, rstd, dh, need_dx, need_dweight, type of dbias as the C ABI
+//  counts it or -1 for none) -> (dx or None, dweight or None, dbias or None)
+PyObject* layer_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  check_count(n, 9);
+  Norm m(a[1], a[2], Py_None, Py_None, "h");
+  const Tensor& h = m.x;
+  Tensor dy = arg(a[0], "dy"), dh = arg(a[5], "dh");
+  const Tensor mean = arg(a[3], "mean"), rstd = arg(a[4], "rstd");
+  const auto like_h = [&](Tensor& t, const char* name) {
+    check_cuda(t, name, h.get_device());
+    check_type(t, name, h.scalar_type(), h.scalar_type());
+    TORCH_CHECK_VALUE(t.sizes() == h.sizes(), name, " must have the shape of h");
+    if (!t.is_contiguous()) t = t.contiguous();
+  };
+  OnDevice on(h);
+  like_h(dy, "dy");
+  if (dh.defined()) like_h(dh, "dh");
+  for (const auto& [t, name] : {std::pair<const Tensor&, const char*>{mean, "mean"},
+                                {rstd, "rstd"}}) {
+    check_cuda(t, name, h.get_device());
+    check_type(t, name, at::kFloat, at::kFloat);
+    TORCH_CHECK_VALUE(t.sizes() == h.sizes().slice(0, h.dim() - 1) && t.is_contiguous(), name,
+                      " must be as flce_layer_norm returned it");
+  }
+  const bool need_dw = PyObject_IsTrue(a[7]);
+  TORCH_CHECK_VALUE(!need_dw || m.weight.defined(), "dweight needs weight");
+  const int64_t bias_type = integer(a[8]);
+  TORCH_CHECK_VALUE(bias_type < 0 || !m.weight.defined() || bias_type == m.weight_type,
+                    "weight and bias must have the same type");
+  if (bias_type >= 0) m.weight_type = static_cast<flce_dtype>(bias_type);
+  const at::ScalarType wt = m.weight_type == FLCE_F32 ? at::kFloat : at::kBFloat16;
+  Tensor dx, dw, db, ws;
+  size_t nws = 0;
+  if (PyObject_IsTrue(a[6])) dx = empty(h.sizes(), h, h.scalar_type());
+  if (need_dw) dw = empty({m.H}, h, wt);
+  if (bias_type >= 0) db = empty({m.H}, h, wt);
+  if (need_dw || bias_type >= 0) {
+    nws = flce_layer_norm_workspace_size(m.N, m.H);
+    ws = empty({static_cast<int64_t>(nws)}, h, at::kByte);
+  }
+  const flce_status st = flce_layer_norm_backward(
+      ptr(dy), ptr(dh), m.xr.p, m.xr.ld, ptr(m.weight), static_cast<const float*>(ptr(mean)),
+      static_cast<const float*>(ptr(rstd)), m.N, m.H, m.type, m.weight_type, ptr(dx), ptr(dw),
+      ptr(db), ptr(ws), nws, on.stream);
+  return answer(st, std::move(dx), std::move(dw), std::move(db));
   END_HANDLE_TH_ERRORS
 }
 
@@ -401,8 +514,10 @@ PyObject* process_logits(PyObject*, PyObject* const* a, Py_ssize_t n) {
 #define FLCE_METHOD(f) \
   { #f, reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(f)), METH_FASTCALL, nullptr }
 PyMethodDef kMethods[] = {FLCE_METHOD(rms_norm_forward), FLCE_METHOD(rms_norm_fp8),
-                          FLCE_METHOD(rms_norm_backward), FLCE_METHOD(quantize_fp8),
-                          FLCE_METHOD(matmul_fp8), FLCE_METHOD(process_logits),
+                          FLCE_METHOD(rms_norm_backward), FLCE_METHOD(layer_norm_forward),
+                          FLCE_METHOD(layer_norm_fp8), FLCE_METHOD(layer_norm_backward),
+                          FLCE_METHOD(quantize_fp8), FLCE_METHOD(matmul_fp8),
+                          FLCE_METHOD(process_logits),
                           {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_flce_torch", nullptr, -1, kMethods,
                        nullptr, nullptr, nullptr, nullptr};

@@ -25,8 +25,9 @@ import lm_head_linear_flce_gb300 as _pkg
 
 from . import _I64, _INT, _P, _SZ, FlceError, library
 
-__all__ = ["flce_rms_norm", "flce_rms_norm_backward", "rms_norm", "rms_norm_fp8", "quantize_fp8",
-           "matmul_fp8", "process_logits"]
+__all__ = ["flce_rms_norm", "flce_rms_norm_backward", "rms_norm", "rms_norm_fp8",
+           "flce_layer_norm", "flce_layer_norm_backward", "layer_norm", "layer_norm_fp8",
+           "quantize_fp8", "matmul_fp8", "process_logits"]
 
 _F32 = ctypes.c_float
 _DTYPE = {torch.bfloat16: 0, torch.float32: 1}
@@ -38,6 +39,13 @@ _ARGS = {
     "flce_rms_norm_backward": [_P, _P, _P, _I64, _P, _P, _I64, _I64, _INT, _INT, _P, _P, _P, _SZ,
                                _P],
     "flce_rms_norm_workspace_size": [_I64, _I64],
+    "flce_layer_norm_forward": [_P, _I64, _P, _I64, _P, _P, _I64, _I64, _F32, _INT, _INT, _P, _P,
+                                _P, _P, _P],
+    "flce_layer_norm_fp8": [_P, _I64, _P, _I64, _P, _P, _I64, _I64, _F32, _INT, _INT, _P, _P, _P,
+                            _P],
+    "flce_layer_norm_backward": [_P, _P, _P, _I64, _P, _P, _P, _I64, _I64, _INT, _INT, _P, _P, _P,
+                                 _P, _SZ, _P],
+    "flce_layer_norm_workspace_size": [_I64, _I64],
     "flce_quantize_fp8": [_P, _I64, _I64, _I64, _INT, _INT, _P, _P, _P],
     "flce_matmul_fp8": [_P, _I64, _P, _P, _I64, _P, _I64, _I64, _I64, _P, _I64, _INT, _P],
     "flce_selftest_matmul_fp8_timeout": [_I64, _I64, _P, _I64, _P, _P, _I64, _P, _I64, _I64, _I64,
@@ -120,12 +128,13 @@ class _NotTwice(torch.autograd.Function):
     """A gradient as it is; differentiating it by what it depends on raises."""
 
     @staticmethod
-    def forward(ctx, grad, *depends_on):
+    def forward(ctx, name, grad, *depends_on):
+        ctx.name = name
         return grad
 
     @staticmethod
     def backward(ctx, *_):
-        raise RuntimeError("rms_norm's gradient cannot be differentiated again")
+        raise RuntimeError(f"{ctx.name}'s gradient cannot be differentiated again")
 
 
 class _RmsNorm(torch.autograd.Function):
@@ -151,8 +160,8 @@ class _RmsNorm(torch.autograd.Function):
                 # create_graph=True: constants would lose what the gradients depend on
                 # without a word.  (torch's once_differentiable looks at dy and dh alone.)
                 h = h if need[0] or need[2] else None  # (else it is given)
-                dx = dx if dx is None else _NotTwice.apply(dx, dy, dh, h, weight)
-                dw = dw if dw is None else _NotTwice.apply(dw, dy, h)
+                dx = dx if dx is None else _NotTwice.apply("rms_norm", dx, dy, dh, h, weight)
+                dw = dw if dw is None else _NotTwice.apply("rms_norm", dw, dy, h)
         return (dx if need[0] else None, dw,
                 dx if ctx.has_residual and need[2] else None, None)
 
@@ -176,6 +185,82 @@ def rms_norm_fp8(x, weight, eps=1e-6, residual=None, residual_out=None):
     gradient."""
     q, scale, h = _ok(_native().rms_norm_fp8(x, weight, eps, residual, residual_out),
                       "flce_rms_norm_fp8")
+    return (q, scale) if h is None else (q, scale, h)
+
+
+def flce_layer_norm(x, weight=None, bias=None, *, eps=1e-5, residual=None, residual_out=None):
+    """Calls flce_layer_norm_forward; returns (y, h, mean, rstd): the norm of
+    h = x + residual (x itself without a residual), the sum, and the per-row mean and
+    1 / sqrt(variance + eps) the backward needs."""
+    y, h, mean, rstd = _ok(_native().layer_norm_forward(x, weight, bias, eps, residual,
+                                                        residual_out), "flce_layer_norm_forward")
+    return y, (x if h is None else h), mean, rstd
+
+
+def flce_layer_norm_backward(dy, h, weight, mean, rstd, *, dh=None, need_dx=True,
+                             need_dweight=True, need_dbias=True, bias_dtype=None):
+    """Calls flce_layer_norm_backward; returns (dx or None, dweight or None, dbias or
+    None).
+
+    weight may be None (then there is no dweight).  dx is the gradient of x and of the
+    residual alike; dh (or None) is the gradient that reaches h by its other uses.
+    bias_dtype: the bias's type where there is no weight (default: that of h)."""
+    code = -1
+    if need_dbias:
+        code = _DTYPE.get(bias_dtype or (weight if weight is not None else h).dtype, 2)
+    return _ok(_native().layer_norm_backward(dy, h, weight, mean, rstd, dh, need_dx,
+                                             need_dweight and weight is not None, code),
+               "flce_layer_norm_backward")
+
+
+class _LayerNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, bias, residual, eps):
+        y, h, mean, rstd = flce_layer_norm(x, weight, bias, eps=eps, residual=residual)
+        ctx.save_for_backward(h, weight, mean, rstd)
+        ctx.has_residual = residual is not None
+        ctx.bias_dtype = None if bias is None else bias.dtype
+        ctx.set_materialize_grads(False)
+        return (y, h) if ctx.has_residual else y
+
+    @staticmethod
+    def backward(ctx, dy, dh=None):
+        h, weight, mean, rstd = ctx.saved_tensors
+        need = ctx.needs_input_grad
+        if dy is None:  # only the sum was used
+            dx = dh
+            dw = db = None
+        else:
+            dx, dw, db = flce_layer_norm_backward(
+                dy, h, weight, mean, rstd, dh=dh, need_dx=need[0] or need[3],
+                need_dweight=need[1], need_dbias=need[2], bias_dtype=ctx.bias_dtype)
+            if torch.is_grad_enabled():
+                # create_graph=True: as in _RmsNorm
+                h = h if need[0] or need[3] else None
+                dx = dx if dx is None else _NotTwice.apply("layer_norm", dx, dy, dh, h, weight)
+                dw = dw if dw is None else _NotTwice.apply("layer_norm", dw, dy, h)
+                db = db if db is None else _NotTwice.apply("layer_norm", db, dy)
+        return (dx if need[0] else None, dw, db,
+                dx if ctx.has_residual and need[3] else None, None)
+
+
+def layer_norm(x, weight=None, bias=None, eps=1e-5, residual=None):
+    """Layer norm over the last dimension, differentiable (once: a gradient taken with
+    create_graph=True raises when it is differentiated).
+
+    x: bf16 or float32 [..., H]; weight and bias: bf16 or float32 [H], of one type, each
+    may be None.  Without a residual returns y = (x - mean) / sqrt(variance + eps) *
+    weight + bias.  With one (as x) returns (y, h): the norm of h = x + residual, and h,
+    the new residual stream.  Sums are FP32; y and h are rounded once.  The backward
+    takes h as rounded."""
+    return _LayerNorm.apply(x, weight, bias, residual, eps)
+
+
+def layer_norm_fp8(x, weight=None, bias=None, eps=1e-5, residual=None, residual_out=None):
+    """The layer norm with its output in 8 bits: (q, scale), or (q, scale, h) with a
+    residual; q, scale and residual_out as in rms_norm_fp8.  No gradient."""
+    q, scale, h = _ok(_native().layer_norm_fp8(x, weight, bias, eps, residual, residual_out),
+                      "flce_layer_norm_fp8")
     return (q, scale) if h is None else (q, scale, h)
 
 
