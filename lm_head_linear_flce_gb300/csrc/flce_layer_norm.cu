@@ -1,4 +1,6 @@
 // Layer norm with the residual's addition (forward, 8-bit output, backward).
+#include <type_traits>
+
 #include "flce_internal.h"
 #include "flce_norm_device.cuh"
 
@@ -7,17 +9,85 @@ namespace {
 
 constexpr int kLnDwRows = 64;  // rows per partial sum of dweight and dbias past kMaxHeld
 
-// Sums of two values over the threads of a row, the same on every one.  `part`:
-// 2 x 32 pairs, used in turn by `phase`.
-__device__ __forceinline__ float2 row_sum2(float2 v, float2* part, int phase) {
-  v.x = warp_sum(v.x);
-  v.y = warp_sum(v.y);
-  if (blockDim.x == 32) return v;
-  float2* p = part + 32 * phase;
-  if ((threadIdx.x & 31) == 0) p[threadIdx.x >> 5] = v;
-  __syncthreads();
+// Two FP32 values in one 64-bit register: one instruction works on both, and these
+// kernels are short of issue slots in bf16.
+using F2 = uint64_t;
+__device__ __forceinline__ F2 pack2(float lo, float hi) {
+  F2 d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+  return d;
+}
+__device__ __forceinline__ float2 unpack2(F2 v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ F2 both(float v) { return pack2(v, v); }
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ float sum2(F2 v) {
+  const float2 p = unpack2(v);
+  return p.x + p.y;
+}
+template <int E>
+__device__ __forceinline__ void to_pairs(const float (&v)[E], F2 (&p)[E / 2]) {
+#pragma unroll
+  for (int i = 0; i < E / 2; ++i) p[i] = pack2(v[2 * i], v[2 * i + 1]);
+}
+template <int E>
+__device__ __forceinline__ void from_pairs(const F2 (&p)[E / 2], float (&v)[E]) {
+#pragma unroll
+  for (int i = 0; i < E / 2; ++i) {
+    const float2 f = unpack2(p[i]);
+    v[2 * i] = f.x;
+    v[2 * i + 1] = f.y;
+  }
+}
+
+// Sums of two values over the warp, in five exchanges: the first half's lanes end with
+// the first one's, the others with the second's.
+__device__ __forceinline__ float warp_sum_halves(float a, float b) {
+  const bool low = (threadIdx.x & 16) == 0;
+  float v = (low ? a : b) + __shfl_xor_sync(0xffffffffu, low ? b : a, 16);
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+// Sums of two values over the threads of a row, the same on every one.  `part`: the
+// row's 2 x 32 pairs, used in turn by `phase`.  A block's rows wait for themselves
+// alone, each at a barrier of its own.
+__device__ __forceinline__ float2 row_sum2(float2 v, float (*part)[32][2], int phase) {
+  const float s = warp_sum_halves(v.x, v.y);
   const int lane = threadIdx.x & 31;
-  v = lane < static_cast<int>(blockDim.x >> 5) ? p[lane] : make_float2(0.f, 0.f);
+  if (blockDim.x == 32)
+    return make_float2(__shfl_sync(0xffffffffu, s, 0), __shfl_sync(0xffffffffu, s, 16));
+  float(*p)[2] = part[phase];
+  if ((lane & 15) == 0) p[threadIdx.x >> 5][lane >> 4] = s;
+  asm volatile("bar.sync %0, %1;" ::"r"(threadIdx.y + 1), "r"(blockDim.x) : "memory");
+  // both sums again in five exchanges where sixteen lanes hold the warps' parts
+  const int warps = static_cast<int>(blockDim.x >> 5);
+  if (warps <= 16) {
+    const int k = lane & 15;
+    float t = k < warps ? p[k][lane >> 4] : 0.f;
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+    const float u = __shfl_xor_sync(0xffffffffu, t, 16);
+    return lane < 16 ? make_float2(t, u) : make_float2(u, t);
+  }
+  v = lane < warps ? *reinterpret_cast<const float2*>(p[lane]) : make_float2(0.f, 0.f);
   return make_float2(warp_sum(v.x), warp_sum(v.y));
 }
 
@@ -27,7 +97,7 @@ __device__ __forceinline__ bool in_row(int c, int i, int H) {
   return VEC ? c < H : c + 32 * i < H;
 }
 
-// A parameter's elements of a slot, `missing` where there is none.
+// A parameter's elements of a slot, `missing` where there is none, 0 past the row.
 template <class T, bool VEC>
 __device__ __forceinline__ void load_param(const void* __restrict__ w, int w_f32, float missing,
                                            int c, int H, bool aligned,
@@ -36,76 +106,120 @@ __device__ __forceinline__ void load_param(const void* __restrict__ w, int w_f32
     load_weight<T, VEC>(w, w_f32, c, H, aligned, v);
   } else {
 #pragma unroll
-    for (int i = 0; i < Slots<T, VEC>::kE; ++i) v[i] = missing;
+    for (int i = 0; i < Slots<T, VEC>::kE; ++i) v[i] = in_row<T, VEC>(c, i, H) ? missing : 0.f;
   }
 }
 
-// A row in registers between its sums and the output, so that it is read once.  The
-// mean first, then the squares of what is left: h^2 - mean^2 would lose the variance
-// of rows whose mean is large.  The second sum goes over h - mean too, which gives
-// what the first one's rounding left of the mean.
-template <class T, bool FP8, bool VEC, int P>
+// A row in registers between its sums and the output, so that it is read once.
+//
+// Mean and variance in one meeting of the row's warps.  Each warp has its own mean m_w,
+// and over its n_w values the sums d_w of what is left of them, h - m_w (m_w's
+// rounding), and q_w of its squares; with m_0 the first warp's mean,
+//     mean = m_0 + sum_w (n_w (m_w - m_0) + d_w) / H = m_0 + m_1
+//     H variance = sum_w q_w + 2 (m_w - mean) d_w + n_w (m_w - mean)^2
+// Nothing is lost where the mean is large: only differences are squared or added (h^2 -
+// mean^2 would lose the variance of such rows), and h - mean is (h - m_w) + (m_w - mean).
+//
+// PLAIN: weight and bias there and of x's type, and with VEC 16-byte aligned rows.
+template <class T, bool FP8, bool VEC, int P, bool PLAIN>
 __global__ void __launch_bounds__(1024)
     ln_fwd_held_kernel(const T* x, int64_t ldx, const T* residual, int64_t ldr,
                        const void* __restrict__ weight, const void* __restrict__ bias, int w_f32,
-                       bool aligned, int64_t N, int H, float eps, T* y, uint8_t* q, float* scale,
-                       T* h_out, float* mean, float* rstd) {
+                       bool al, int64_t N, int H, float inv_h, float eps, T* y, uint8_t* q,
+                       float* scale, T* h_out, float* mean, float* rstd) {
   using S = Slots<T, VEC>;
-  __shared__ float part[64];
-  __shared__ float2 part2[32];
+  constexpr int kE = S::kE;
+  __shared__ float4 part[32];
   griddep_launch_dependents();
   griddep_wait();
   const int64_t row = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
   if (row >= N) return;  // a whole warp (rows share a block only as warps)
-  float h[P][S::kE];
+  const bool aligned = PLAIN || al;
+  const int lane = threadIdx.x & 31;
+  float h[P][kE];
 #pragma unroll
   for (int s = 0; s < P; ++s) load_slot<T, VEC>(x + row * ldx, S::first(s), H, aligned, h[s]);
   if (residual) {
 #pragma unroll
     for (int s = 0; s < P; ++s) {
-      float r[S::kE];
+      float r[kE];
       load_slot<T, VEC>(residual + row * ldr, S::first(s), H, aligned, r);
 #pragma unroll
-      for (int i = 0; i < S::kE; ++i) h[s][i] += r[i];
+      for (int i = 0; i < kE; ++i) h[s][i] += r[i];
     }
   }
+  // columns from the warp's first one in a slot to the row's end
+  const auto left = [&](int s) { return H - (S::first(s) - lane * (VEC ? kE : 1)); };
   float sum = 0.f;
+  int count = 0;  // the warp's values
 #pragma unroll
-  for (int s = 0; s < P; ++s)
+  for (int s = 0; s < P; ++s) {
 #pragma unroll
-    for (int i = 0; i < S::kE; ++i) sum += h[s][i];
+    for (int i = 0; i < kE; ++i) sum += h[s][i];
+    count += min(max(left(s), 0), 32 * kE);
+  }
   if (h_out) {
 #pragma unroll
     for (int s = 0; s < P; ++s) store_slot<T, VEC>(h_out + row * H, S::first(s), H, aligned, h[s]);
   }
-  const float n = static_cast<float>(H);
-  const float m0 = row_sum(sum, part, 0) / n;
-  float2 left = make_float2(0.f, 0.f);
+  float4 own;  // n_w, m_w, d_w, q_w
+  own.x = static_cast<float>(count);
+  own.y = count ? __fdividef(warp_sum(sum), own.x) : 0.f;  // (d_w takes up what is lost here)
+  own.z = own.w = 0.f;
 #pragma unroll
-  for (int s = 0; s < P; ++s)
+  for (int s = 0; s < P; ++s) {  // h is h - m_w from here on (0 past the row)
+    const float m = S::first(s) < H ? own.y : 0.f;
 #pragma unroll
-    for (int i = 0; i < S::kE; ++i) {
-      h[s][i] = in_row<T, VEC>(S::first(s), i, H) ? h[s][i] - m0 : 0.f;
-      left.x += h[s][i];
-      left.y = fmaf(h[s][i], h[s][i], left.y);
+    for (int i = 0; i < kE; ++i) h[s][i] -= m;
+    if (!VEC && left(s) < 32 * kE) {
+#pragma unroll
+      for (int i = 0; i < kE; ++i)
+        if (!in_row<T, VEC>(S::first(s), i, H)) h[s][i] = 0.f;
     }
-  left = row_sum2(left, part2, 0);
-  const float m1 = left.x / n;
-  const float r = rsqrtf(fmaxf(left.y / n - m1 * m1, 0.f) + eps);
+#pragma unroll
+    for (int i = 0; i < kE; ++i) {
+      own.z += h[s][i];
+      own.w = fmaf(h[s][i], h[s][i], own.w);
+    }
+  }
+  const float sums = warp_sum_halves(own.z, own.w);  // d_w or q_w
+  const float mine = own.y;
+  float m0 = own.y, m1, squares;
+  if (blockDim.x == 32) {
+    m1 = __shfl_sync(0xffffffffu, sums, 0) * inv_h;
+    squares = __shfl_sync(0xffffffffu, sums, 16) - static_cast<float>(H) * m1 * m1;
+  } else {
+    auto* p = reinterpret_cast<float*>(&part[threadIdx.x >> 5]);
+    if (lane == 0) p[0] = own.x, p[1] = own.y;
+    if ((lane & 15) == 0) p[2 + (lane >> 4)] = sums;
+    __syncthreads();
+    m0 = part[0].y;
+    own = lane < static_cast<int>(blockDim.x >> 5) ? part[lane] : make_float4(0.f, m0, 0.f, 0.f);
+    const float apart = own.y - m0;
+    m1 = warp_sum(fmaf(own.x, apart, own.z)) * inv_h;
+    const float off = apart - m1;
+    squares = warp_sum(fmaf(off, fmaf(own.x, off, 2.f * own.z), own.w));
+  }
+  const float r = rsqrtf(fmaf(fmaxf(squares, 0.f), inv_h, eps));
   if (rstd && threadIdx.x == 0) {
     mean[row] = m0 + m1;
     rstd[row] = r;
   }
+  const float back = (mine - m0) - m1;  // h - mean = (h - m_w) + back
   const int groups = (H + kScaleGroup - 1) / kScaleGroup;
 #pragma unroll
   for (int s = 0; s < P; ++s) {
     const int c = S::first(s);
-    float w[S::kE], b[S::kE];
-    load_param<T, VEC>(weight, w_f32, 1.f, c, H, aligned, w);
-    load_param<T, VEC>(bias, w_f32, 0.f, c, H, aligned, b);
+    float w[kE], b[kE];
+    if constexpr (PLAIN) {
+      load_slot<T, VEC>(static_cast<const T*>(weight), c, H, true, w);
+      load_slot<T, VEC>(static_cast<const T*>(bias), c, H, true, b);
+    } else {
+      load_param<T, VEC>(weight, w_f32, 1.f, c, H, aligned, w);
+      load_param<T, VEC>(bias, w_f32, 0.f, c, H, aligned, b);
+    }
 #pragma unroll
-    for (int i = 0; i < S::kE; ++i)
-      h[s][i] = in_row<T, VEC>(c, i, H) ? fmaf((h[s][i] - m1) * r, w[i], b[i]) : 0.f;
+    for (int i = 0; i < kE; ++i) h[s][i] = fmaf((h[s][i] + back) * r, w[i], b[i]);
     if constexpr (!FP8) store_slot<T, VEC>(y + row * H, c, H, aligned, h[s]);
     else store_quantized<T, VEC>(h[s], c, H, aligned, q + row * H, scale + row * groups, groups);
   }
@@ -123,11 +237,17 @@ __global__ void __launch_bounds__(1024)
 //
 // h is the sum as the forward stored it, in T (in bf16 rounded by up to 2^-8 of h),
 // where mean and rstd are those of the sum before it was rounded.
+//
+// Threads hold 16 values where the row has them (two slots of bf16, four of float32) and
+// 128 registers, 512 of them an SM: what a row costs besides its values, two sums and a
+// barrier, is a warp's, so few warps do it fastest.  8192 x 3584 bf16 with dh, dx alone:
+// 43 us (5.4 TB/s; a copy of that size 43), with 8 values in 448 threads a row 62, 28 of
+// whose warps an SM have more rows ahead; three or four rows ahead 45.
 constexpr int kLnAhead = 2;
-// Blocks of up to `threads` threads that share an SM, whose registers hold three values
-// a column of a slot.
+constexpr int kLnRing = 200 * 1024;  // of an SM's shared memory
+// Blocks on an SM: up to 512 threads, or 1024 where a row takes more.
 __host__ __device__ constexpr int ln_blocks(int slots, int threads) {
-  return threads >= 1024 ? 1 : (slots == 1 ? 1024 : 512) / threads;
+  return threads <= 512 && slots == 1 ? 2 : 1;
 }
 template <class T, bool VEC, int P, int THREADS, bool AHEAD>
 __global__ void __launch_bounds__(THREADS, ln_blocks(P, THREADS))
@@ -137,16 +257,19 @@ __global__ void __launch_bounds__(THREADS, ln_blocks(P, THREADS))
                        const float* __restrict__ rstd, int64_t N, int H, T* __restrict__ dx,
                        float* __restrict__ sums) {
   using S = Slots<T, VEC>;
-  __shared__ float2 part[64];
+  __shared__ __align__(8) float part[THREADS <= 512 ? 8 : 1][2][32][2];
   extern __shared__ __align__(16) uint4 ring[];  // [kLnAhead][3][P][threads of the block]
   const int64_t first = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
   const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.y;
-  float w[P][S::kE], dw[P][S::kE], db[P][S::kE];
+  constexpr int kE = S::kE, kP = kE / 2;
+  F2 w[P][kP], dw[P][kP], db[P][kP];
 #pragma unroll
   for (int s = 0; s < P; ++s) {
-    load_param<T, VEC>(weight, w_f32, 1.f, S::first(s), H, aligned, w[s]);
+    float v[kE];
+    load_param<T, VEC>(weight, w_f32, 1.f, S::first(s), H, aligned, v);
+    to_pairs<kE>(v, w[s]);
 #pragma unroll
-    for (int i = 0; i < S::kE; ++i) dw[s][i] = db[s][i] = 0.f;
+    for (int i = 0; i < kP; ++i) dw[s][i] = db[s][i] = 0;
   }
   const float inv_h = 1.f / static_cast<float>(H);
   const bool with_dh = dh && dx;
@@ -176,65 +299,70 @@ __global__ void __launch_bounds__(THREADS, ln_blocks(P, THREADS))
   float next_r = first < N ? rstd[first] : 0.f, next_m = first < N ? mean[first] : 0.f;
   int stage = 0, phase = 0;
   for (int64_t row = first; row < N; row += step, phase ^= 1) {
-    const float r = next_r, shift = -next_m * next_r;
+    const F2 r = both(next_r), shift = both(-next_m * next_r);
+    const float minus_r = -next_r;
     if (row + step < N) {
       next_r = rstd[row + step];
       next_m = mean[row + step];
     }
-    Piece<T, VEC> pd[P], ph[P];
+    Piece<T, VEC> held[2][P];  // without AHEAD
+    const auto pairs = [&](int array, int s, F2 (&p)[kP]) {
+      Piece<T, VEC> piece;
+      if constexpr (AHEAD) piece.set(*slot(stage, array, s));
+      else if (array < 2) piece = held[array][s];
+      else piece.load(dh + row * H, S::first(s), H, aligned);
+      float v[kE];
+      piece.floats(v);
+      to_pairs<kE>(v, p);
+    };
     if constexpr (AHEAD) {
       asm volatile("cp.async.wait_group %0;" ::"n"(kLnAhead - 1) : "memory");
-#pragma unroll
-      for (int s = 0; s < P; ++s) {
-        pd[s].set(*slot(stage, 0, s));
-        ph[s].set(*slot(stage, 1, s));
-      }
     } else {
 #pragma unroll
       for (int s = 0; s < P; ++s) {
         const int c = S::first(s);
-        pd[s].load(dy + row * H, c, H, aligned);
-        ph[s].load(h + row * ldh, c, H, aligned);
+        held[0][s].load(dy + row * H, c, H, aligned);
+        held[1][s].load(h + row * ldh, c, H, aligned);
       }
     }
-    float2 dot = make_float2(0.f, 0.f);
+    F2 dot1 = 0, dot2 = 0;
 #pragma unroll
     for (int s = 0; s < P; ++s) {
-      float d[S::kE], v[S::kE];
-      pd[s].floats(d);
-      ph[s].floats(v);
+      F2 d[kP], v[kP];
+      pairs(0, s, d);
+      pairs(1, s, v);
 #pragma unroll
-      for (int i = 0; i < S::kE; ++i) {
+      for (int i = 0; i < kP; ++i) {
         // past the row d is 0, and with it every sum
-        const float n = fmaf(v[i], r, shift), g = d[i] * w[s][i];
-        dw[s][i] = fmaf(d[i], n, dw[s][i]);
-        db[s][i] += d[i];
-        dot.x += g;
-        dot.y = fmaf(g, n, dot.y);
+        const F2 n = fma2(v[i], r, shift), g = mul2(d[i], w[s][i]);
+        dw[s][i] = fma2(d[i], n, dw[s][i]);
+        db[s][i] = add2(db[s][i], d[i]);
+        dot1 = add2(dot1, g);
+        dot2 = fma2(g, n, dot2);
       }
     }
     if (dx) {
-      dot = row_sum2(dot, part, phase);
-      const float k1 = -r * (dot.x * inv_h), k2 = -r * (dot.y * inv_h);
+      const float2 dot =
+          row_sum2(make_float2(sum2(dot1), sum2(dot2)), part[threadIdx.y & 7], phase);
+      const F2 k1 = both(minus_r * (dot.x * inv_h)), k2 = both(minus_r * (dot.y * inv_h));
 #pragma unroll
       for (int s = 0; s < P; ++s) {
-        float d[S::kE], v[S::kE];
-        pd[s].floats(d);
-        ph[s].floats(v);
+        F2 d[kP], v[kP];
+        pairs(0, s, d);
+        pairs(1, s, v);
 #pragma unroll
-        for (int i = 0; i < S::kE; ++i) {
-          const float n = fmaf(v[i], r, shift), g = d[i] * w[s][i];
-          d[i] = fmaf(g, r, fmaf(n, k2, k1));
+        for (int i = 0; i < kP; ++i) {
+          const F2 n = fma2(v[i], r, shift), g = mul2(d[i], w[s][i]);
+          d[i] = fma2(g, r, fma2(n, k2, k1));
         }
         if (with_dh) {
-          Piece<T, VEC> pe;
-          if constexpr (AHEAD) pe.set(*slot(stage, 2, s));
-          else pe.load(dh + row * H, S::first(s), H, aligned);
-          pe.floats(v);
+          pairs(2, s, v);
 #pragma unroll
-          for (int i = 0; i < S::kE; ++i) d[i] += v[i];
+          for (int i = 0; i < kP; ++i) d[i] = add2(d[i], v[i]);
         }
-        store_slot<T, VEC>(dx + row * H, S::first(s), H, aligned, d);
+        float out[kE];
+        from_pairs<kE>(d, out);
+        store_slot<T, VEC>(dx + row * H, S::first(s), H, aligned, out);
       }
     }
     if constexpr (AHEAD) {
@@ -244,27 +372,69 @@ __global__ void __launch_bounds__(THREADS, ln_blocks(P, THREADS))
   }
   if constexpr (AHEAD) asm volatile("cp.async.wait_group 0;" ::: "memory");
   if (!sums) return;
+  griddep_launch_dependents();  // the sum's blocks take the places that become free
+  if (blockDim.y > 1) {
+    // the block's rows one after another into the first one's registers (every copy
+    // into the ring has been read)
+    F2* all = reinterpret_cast<F2*>(ring) + threadIdx.x;  // [P][kE][threads of a row]
+    for (int k = 1; k < static_cast<int>(blockDim.y); ++k) {
+      __syncthreads();
+      if (static_cast<int>(threadIdx.y) == k) {
+#pragma unroll
+        for (int s = 0; s < P; ++s)
+#pragma unroll
+          for (int i = 0; i < kP; ++i) {
+            all[(s * kE + i) * blockDim.x] = dw[s][i];
+            all[(s * kE + kP + i) * blockDim.x] = db[s][i];
+          }
+      }
+      __syncthreads();
+      if (threadIdx.y == 0) {
+#pragma unroll
+        for (int s = 0; s < P; ++s)
+#pragma unroll
+          for (int i = 0; i < kP; ++i) {
+            dw[s][i] = add2(dw[s][i], all[(s * kE + i) * blockDim.x]);
+            db[s][i] = add2(db[s][i], all[(s * kE + kP + i) * blockDim.x]);
+          }
+      }
+    }
+    if (threadIdx.y > 0) return;
+  }
 #pragma unroll
   for (int s = 0; s < P; ++s) {
     const int c = S::first(s);
-    float* p = sums + first * 2 * H;
+    float* p = sums + static_cast<int64_t>(blockIdx.x) * 2 * H;
+    float vw[kE], vb[kE];
+    from_pairs<kE>(dw[s], vw);
+    from_pairs<kE>(db[s], vb);
+    if constexpr (VEC) {  // (H is a multiple of 4, and so is c)
+      if (c >= H) continue;
 #pragma unroll
-    for (int i = 0; i < S::kE; ++i)
-      if (c + i * S::kStep < H) {
-        p[c + i * S::kStep] = dw[s][i];
-        p[H + c + i * S::kStep] = db[s][i];
+      for (int i = 0; i < kE; i += 4) {
+        *reinterpret_cast<float4*>(p + c + i) = make_float4(vw[i], vw[i + 1], vw[i + 2], vw[i + 3]);
+        *reinterpret_cast<float4*>(p + H + c + i) =
+            make_float4(vb[i], vb[i + 1], vb[i + 2], vb[i + 3]);
       }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kE; ++i)
+        if (c + i * S::kStep < H) {
+          p[c + i * S::kStep] = vw[i];
+          p[H + c + i * S::kStep] = vb[i];
+        }
+    }
   }
 }
 
-// dweight and dbias (blockIdx.y) = their partial sums, added in order: 32 columns a
-// block, each of its 32 warps taking every 32nd partial, then the warps in order.
+// dweight and dbias (blockIdx.y) = their partial sums, added in a fixed order: 32
+// columns a block, each of its 32 warps taking every 32nd partial, then a warp a column.
 constexpr int kLnSumWarps = 32;
 template <class W>
 __global__ void __launch_bounds__(32 * kLnSumWarps)
     ln_sum_kernel(const float* __restrict__ part, int64_t parts, int H, W* __restrict__ dweight,
                   W* __restrict__ dbias) {
-  __shared__ float sums[kLnSumWarps][32];
+  __shared__ float sums[kLnSumWarps][33];
   griddep_launch_dependents();
   griddep_wait();
   W* out = blockIdx.y == 0 ? dweight : dbias;
@@ -279,9 +449,8 @@ __global__ void __launch_bounds__(32 * kLnSumWarps)
   }
   sums[warp][lane] = s;
   __syncthreads();
-  if (warp != 0 || c >= H) return;
-  for (int k = 1; k < kLnSumWarps; ++k) s += sums[k][lane];
-  out[c] = from_f<W>(s);
+  s = warp_sum(sums[lane][warp]);
+  if (lane == 0 && blockIdx.x * 32 + warp < H) out[blockIdx.x * 32 + warp] = from_f<W>(s);
 }
 
 // ----------------------------------------------------- small backwards
@@ -484,27 +653,28 @@ __global__ void __launch_bounds__(kNormThreads)
 }
 
 // ------------------------------------------------------------- launching
-// The backward's threads a row: one slot a thread up to 512 threads, for the sums of
-// its columns take twice the registers of a slot; then more slots, and more threads
-// only where a thread holds as many slots as it may.
+// The backward's threads a row: 16 values each as far as the row has a warp of them.
+// Rows share a block of up to 512 threads, whose sums are one partial sum: sixteen of a
+// warp each, else up to eight (a barrier each).  8192 x 3584 bf16 with the sums, two
+// rows a block 51 us, one 55.
 RowPlan plan_ln_bwd(int64_t H, int elems, bool vec) {
   const int64_t units = vec ? (H + elems - 1) / elems
                             : (H + kScaleGroup - 1) / kScaleGroup * 32;
   const int most = 16 / elems;
   int slots = 1;
-  while (slots < most && units > 512 * slots) slots *= 2;
+  while (slots < most && units > 32 * slots) slots *= 2;
   int64_t threads = (units + slots - 1) / slots;
   threads = std::max<int64_t>((threads + 31) / 32 * 32, 32);
-  return {static_cast<int>(threads), slots, threads == 32 ? 8 : 1};
+  const int64_t rows = threads == 32 ? 16 : std::clamp<int64_t>(512 / threads, 1, 8);
+  return {static_cast<int>(threads), slots, static_cast<int>(rows)};
 }
 
-// Partial sums of dweight and dbias: a block's rows at a time.  A fixed number, so
-// that the order of additions depends on the sizes and the type alone: the blocks
-// that 152 SMs hold at once.
+// Partial sums of dweight and dbias, one of each a block.  A fixed number, so that the
+// order of additions depends on the sizes and the type alone: the blocks that 152 SMs
+// hold at once.
 int64_t ln_held_parts(int64_t N, const RowPlan& p) {
-  const int threads = p.threads * p.rows;
-  const int per_sm = ln_blocks(p.slots, threads <= 256 ? 256 : threads <= 512 ? 512 : 1024);
-  return std::min<int64_t>((N + p.rows - 1) / p.rows, 152 * per_sm) * p.rows;
+  const int per_sm = ln_blocks(p.slots, p.threads * p.rows);
+  return std::min<int64_t>((N + p.rows - 1) / p.rows, 152 * per_sm);
 }
 int64_t ln_parts(int64_t N, int64_t H) {
   if (H > kMaxHeld) return (N + kLnDwRows - 1) / kLnDwRows;
@@ -533,14 +703,14 @@ struct LnFwdArgs {
   float* rstd;
 };
 
-template <class T, bool FP8, bool VEC, int P>
+template <class T, bool FP8, bool VEC, int P, bool PLAIN>
 cudaError_t launch_ln_fwd(const RowPlan& p, bool aligned, const LnFwdArgs& a, cudaStream_t s) {
   const unsigned blocks = static_cast<unsigned>((a.N + p.rows - 1) / p.rows);
   return launch_overlapped(
-      ln_fwd_held_kernel<T, FP8, VEC, P>, dim3(blocks), dim3(p.threads, p.rows), 0, s, 1,
+      ln_fwd_held_kernel<T, FP8, VEC, P, PLAIN>, dim3(blocks), dim3(p.threads, p.rows), 0, s, 1,
       static_cast<const T*>(a.x), a.ldx, static_cast<const T*>(a.residual), a.ldr, a.weight, a.bias,
-      a.w_f32, aligned, a.N, a.H, a.eps, static_cast<T*>(a.y), static_cast<uint8_t*>(a.q), a.scale,
-      static_cast<T*>(a.h_out), a.mean, a.rstd);
+      a.w_f32, aligned, a.N, a.H, static_cast<float>(1.0 / a.H), a.eps, static_cast<T*>(a.y),
+      static_cast<uint8_t*>(a.q), a.scale, static_cast<T*>(a.h_out), a.mean, a.rstd);
 }
 
 // Whether every row's pieces are 16-byte aligned.
@@ -555,6 +725,7 @@ bool ln_fwd_aligned(const LnFwdArgs& a) {
 template <class T, bool FP8>
 cudaError_t run_ln_fwd(const LnFwdArgs& a, cudaStream_t s) {
   cudaError_t e = cudaSuccess;
+  const bool plain = a.weight && a.bias && a.w_f32 == (sizeof(T) == 4);
   if (a.H > kMaxHeld) {
     ln_fwd_kernel<T, FP8><<<static_cast<unsigned>(a.N), kNormThreads, 0, s>>>(
         static_cast<const T*>(a.x), a.ldx, static_cast<const T*>(a.residual), a.ldr, a.weight,
@@ -564,14 +735,23 @@ cudaError_t run_ln_fwd(const LnFwdArgs& a, cudaStream_t s) {
     constexpr int kE = Slots<T, true>::kE;
     const bool al = ln_fwd_aligned<T>(a);
     const RowPlan p = plan_rows(a.N, a.H, kE, true);
-    if (p.slots == 1) e = launch_ln_fwd<T, FP8, true, 1>(p, al, a, s);
-    else if (p.slots == 2) e = launch_ln_fwd<T, FP8, true, 2>(p, al, a, s);
-    else if constexpr (kE == 4) e = launch_ln_fwd<T, FP8, true, 4>(p, al, a, s);
+    const auto launch = [&](auto plain) {
+      constexpr bool kPlain = decltype(plain)::value;
+      if (p.slots == 1) return launch_ln_fwd<T, FP8, true, 1, kPlain>(p, al, a, s);
+      if constexpr (kE == 4)
+        if (p.slots == 4) return launch_ln_fwd<T, FP8, true, 4, kPlain>(p, al, a, s);
+      return launch_ln_fwd<T, FP8, true, 2, kPlain>(p, al, a, s);
+    };
+    e = al && plain ? launch(std::true_type{}) : launch(std::false_type{});
   } else {
     const RowPlan p = plan_rows(a.N, a.H, 4, false);
-    if (p.slots == 1) e = launch_ln_fwd<T, FP8, false, 1>(p, false, a, s);
-    else if (p.slots == 2) e = launch_ln_fwd<T, FP8, false, 2>(p, false, a, s);
-    else e = launch_ln_fwd<T, FP8, false, 4>(p, false, a, s);
+    const auto launch = [&](auto plain) {
+      constexpr bool kPlain = decltype(plain)::value;
+      if (p.slots == 1) return launch_ln_fwd<T, FP8, false, 1, kPlain>(p, false, a, s);
+      if (p.slots == 2) return launch_ln_fwd<T, FP8, false, 2, kPlain>(p, false, a, s);
+      return launch_ln_fwd<T, FP8, false, 4, kPlain>(p, false, a, s);
+    };
+    e = plain ? launch(std::true_type{}) : launch(std::false_type{});
   }
   note_launch();
   return e != cudaSuccess ? e : cudaGetLastError();
@@ -597,30 +777,32 @@ struct LnBwdArgs {
 template <class T, bool VEC, int P>
 cudaError_t launch_ln_bwd(const RowPlan& p, bool aligned, int64_t parts, const LnBwdArgs& a,
                           cudaStream_t s) {
-  constexpr int kMost = 200 * 1024;
-  const int threads = p.threads * p.rows, ring = kLnAhead * 3 * P * threads * 16;
+  const int threads = p.threads * p.rows, stage = 3 * P * threads * 16;
   const auto launch = [&](auto* k, int smem) {
+    // the block's sums, where rows share it
+    smem = std::max(smem, p.rows > 1 ? P * Slots<T, VEC>::kE * p.threads * 8 : 0);
     // a plain launch, as the RMS norm's: blocks that wait here would take shared
     // memory from the kernel before them
-    k<<<dim3(static_cast<unsigned>(parts / p.rows)), dim3(p.threads, p.rows), smem, s>>>(
+    k<<<dim3(static_cast<unsigned>(parts)), dim3(p.threads, p.rows), smem, s>>>(
         static_cast<const T*>(a.dy), static_cast<const T*>(a.dh), static_cast<const T*>(a.h),
         a.ldh, a.weight, a.w_f32, aligned, a.mean, a.rstd, a.N, a.H, static_cast<T*>(a.dx),
         a.dweight || a.dbias ? a.part : static_cast<float*>(nullptr));
     return cudaGetLastError();
   };
+  // a row that takes more than 512 threads has 16 values in each
+  constexpr int kMost = P * Slots<T, VEC>::kE == 16 ? 1024 : 512;
   if constexpr (VEC) {
-    if (aligned && ring <= kMost) {
-      auto* k = threads <= 256   ? ln_bwd_held_kernel<T, VEC, P, 256, true>
-                : threads <= 512 ? ln_bwd_held_kernel<T, VEC, P, 512, true>
-                                 : ln_bwd_held_kernel<T, VEC, P, 1024, true>;
-      static SmemLimit limits[3];  // one for each of them
-      const cudaError_t e = allow_smem(reinterpret_cast<const void*>(k), kMost,
-                                       &limits[threads <= 256 ? 0 : threads <= 512 ? 1 : 2]);
-      return e != cudaSuccess ? e : launch(k, ring);
+    if (aligned && kLnAhead * stage * ln_blocks(P, threads) <= kLnRing) {
+      auto* k = threads <= 512 ? ln_bwd_held_kernel<T, VEC, P, 512, true>
+                               : ln_bwd_held_kernel<T, VEC, P, kMost, true>;
+      static SmemLimit limits[2];  // one for each of them
+      const cudaError_t e = allow_smem(reinterpret_cast<const void*>(k), kLnRing,
+                                       &limits[threads <= 512 ? 0 : 1]);
+      return e != cudaSuccess ? e : launch(k, kLnAhead * stage);
     }
   }
   return threads <= 512 ? launch(ln_bwd_held_kernel<T, VEC, P, 512, false>, 0)
-                        : launch(ln_bwd_held_kernel<T, VEC, P, 1024, false>, 0);
+                        : launch(ln_bwd_held_kernel<T, VEC, P, kMost, false>, 0);
 }
 
 // What ln_bwd_small_kernel takes: a column's block adds at most 64 rows a warp, and
