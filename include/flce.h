@@ -585,6 +585,34 @@ flce_status flce_process_logits(const void* logits, int64_t ld_logits, flce_dtyp
                                 void* out, int64_t ld_out, flce_dtype out_dtype,
                                 flce_stream_t stream);
 
+/*
+ * A token a row from logits, by a given random number.  Per row b, with T its
+ * temperature, the tokens are weighed w = exp((l - max l) / T) and put in order, larger
+ * logits first, equal ones by id.  Kept are, one limit after another,
+ *
+ *     top_k   the first top_k[b] tokens                 (0 or less, or V or more: all)
+ *     top_p   of these, those before which the mass, the sum of w, is less than top_p[b]
+ *             times that of all of them; the first one always    (1 or more: all)
+ *     min_p   of these, those with w >= min_p[b]; the first one always   (0 or less: all)
+ *
+ * and out[b] is the first token, by id, at which the mass of the kept ones up to it
+ * exceeds u[b] times the mass of all kept ones.
+ *
+ *   logits   device [B][V] of `dtype`, rows ld_logits apart.  -infinity and NaN are no
+ *            tokens; where there are +infinities, those alone weigh (1 each).
+ *   u        device float [B], in [0, 1) (else clamped to it; NaN is 0).
+ *   temperature, top_p, min_p   device float [B], top_k device int32 [B]; each may be
+ *            NULL (1, 1, 0, 0).  A temperature below 2^-64, or NaN, takes the largest logit
+ *            (the lowest id of equals), whatever the limits and u.  A NaN limit is no limit.
+ *   out      device int64 [B]; -1 where the row has no token.
+ * Weights are right to 2^-31 of them (2^-43 of the largest) and are added as integers, so
+ * that the result does not depend on how a row is split.  B <= 65535, V <= 2^21.
+ */
+flce_status flce_sample_logits(const void* logits, int64_t ld_logits, flce_dtype dtype, int64_t B,
+                               int64_t V, const float* u, const float* temperature,
+                               const int32_t* top_k, const float* top_p, const float* min_p,
+                               int64_t* out, flce_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -30,7 +30,7 @@ __all__ = [
     "linear_cross_entropy", "STATUS",
     "flce_rms_norm", "flce_rms_norm_backward", "rms_norm", "rms_norm_fp8", "flce_layer_norm",
     "flce_layer_norm_backward", "layer_norm", "layer_norm_fp8", "quantize_fp8", "matmul_fp8",
-    "process_logits",
+    "process_logits", "sample_logits",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -458,4 +458,5 @@ def linear_cross_entropy(hidden, weight, labels, ignore_index=-100, shift=False,
 
 from .head_ops import (flce_layer_norm, flce_layer_norm_backward,  # noqa: E402
                        flce_rms_norm, flce_rms_norm_backward, layer_norm, layer_norm_fp8,
-                       matmul_fp8, process_logits, quantize_fp8, rms_norm, rms_norm_fp8)
+                       matmul_fp8, process_logits, quantize_fp8, rms_norm, rms_norm_fp8,
+                       sample_logits)

@@ -22,7 +22,8 @@ OUT_DIR = os.path.join(PKG, "_lib")
 LIB = os.path.join(OUT_DIR, "libflce.so")
 MODULE = os.path.join(OUT_DIR, "_flce_torch.so")
 SOURCES = ["flce_api.cu", "flce_simt.cu", "flce_gemm.cu", "flce_noalloc.cu",
-           "flce_ops.cu", "flce_norm.cu", "flce_layer_norm.cu", "flce_fp8.cu", "flce_process.cu"]
+           "flce_ops.cu", "flce_norm.cu", "flce_layer_norm.cu", "flce_fp8.cu", "flce_process.cu",
+           "flce_sample.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
          "--expt-relaxed-constexpr"]

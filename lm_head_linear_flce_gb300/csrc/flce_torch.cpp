@@ -511,13 +511,47 @@ PyObject* process_logits(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
+// (logits, u, temperature, top_k, top_p, min_p) -> (tokens,)
+PyObject* sample_logits(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  check_count(n, 6);
+  const Tensor z = arg(a[0], "logits");
+  check_cuda(z, "logits");
+  const flce_dtype type = check_float(z, "logits");
+  TORCH_CHECK_VALUE(z.dim() == 2 && z.size(1) > 0, "expected logits [B, V]");
+  const int64_t B = z.size(0), V = z.size(1), dev = z.get_device();
+  OnDevice on(z);
+  const auto per_row = [&](int i, const char* name, at::ScalarType t) {
+    Tensor v = arg(a[i], name);
+    if (!v.defined()) return v;
+    check_cuda(v, name, dev);
+    check_type(v, name, t, t);
+    TORCH_CHECK_VALUE(v.dim() == 1 && v.size(0) == B, name, " must be [B]");
+    return v.is_contiguous() ? v : v.contiguous();
+  };
+  const Tensor u = per_row(1, "u", at::kFloat);
+  TORCH_CHECK_VALUE(u.defined(), "u must be a tensor");
+  const Tensor temperature = per_row(2, "temperature", at::kFloat),
+               top_k = per_row(3, "top_k", at::kInt), top_p = per_row(4, "top_p", at::kFloat),
+               min_p = per_row(5, "min_p", at::kFloat);
+  const Rows r = rows(z, V);
+  Tensor out = empty({B}, z, at::kLong);
+  const flce_status st = flce_sample_logits(
+      r.p, r.ld, type, B, V, static_cast<const float*>(ptr(u)),
+      static_cast<const float*>(ptr(temperature)), static_cast<const int32_t*>(ptr(top_k)),
+      static_cast<const float*>(ptr(top_p)), static_cast<const float*>(ptr(min_p)),
+      static_cast<int64_t*>(ptr(out)), on.stream);
+  return answer(st, std::move(out));
+  END_HANDLE_TH_ERRORS
+}
+
 #define FLCE_METHOD(f) \
   { #f, reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(f)), METH_FASTCALL, nullptr }
 PyMethodDef kMethods[] = {FLCE_METHOD(rms_norm_forward), FLCE_METHOD(rms_norm_fp8),
                           FLCE_METHOD(rms_norm_backward), FLCE_METHOD(layer_norm_forward),
                           FLCE_METHOD(layer_norm_fp8), FLCE_METHOD(layer_norm_backward),
                           FLCE_METHOD(quantize_fp8), FLCE_METHOD(matmul_fp8),
-                          FLCE_METHOD(process_logits),
+                          FLCE_METHOD(process_logits), FLCE_METHOD(sample_logits),
                           {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_flce_torch", nullptr, -1, kMethods,
                        nullptr, nullptr, nullptr, nullptr};

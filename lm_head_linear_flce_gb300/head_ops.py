@@ -27,7 +27,7 @@ from . import _I64, _INT, _P, _SZ, FlceError, library
 
 __all__ = ["flce_rms_norm", "flce_rms_norm_backward", "rms_norm", "rms_norm_fp8",
            "flce_layer_norm", "flce_layer_norm_backward", "layer_norm", "layer_norm_fp8",
-           "quantize_fp8", "matmul_fp8", "process_logits"]
+           "quantize_fp8", "matmul_fp8", "process_logits", "sample_logits"]
 
 _F32 = ctypes.c_float
 _DTYPE = {torch.bfloat16: 0, torch.float32: 1}
@@ -52,6 +52,7 @@ _ARGS = {
                                          _P, _I64, _INT, _P],
     "flce_process_logits": [_P, _I64, _INT, _I64, _I64, _P, _I64, _INT, _I64, _P, _P, _P, _P, _P,
                             _P, _INT, _P, _I64, _P, _I64, _P, _I64, _INT, _P],
+    "flce_sample_logits": [_P, _I64, _INT, _I64, _I64, _P, _P, _P, _P, _P, _P, _P],
 }
 _fns: dict = {}
 _bound = None
@@ -313,3 +314,18 @@ def process_logits(logits, *, tokens=None, lengths=None, prompt_lengths=None,
     return _ok(_native().process_logits(
         logits, tokens, lengths, prompt_lengths, repetition_penalty, frequency_penalty,
         presence_penalty, bias_ids, bias_values, allowed, out, code), "flce_process_logits")[0]
+
+
+def sample_logits(logits, u, *, temperature=None, top_k=None, top_p=None, min_p=None):
+    """A token a row: int64 [B] of ids, -1 where a row of logits [B, V] (bf16 or float32)
+    has nothing above -inf.
+
+    u: float32 [B], random numbers in [0, 1).  Tokens are weighed exp(l / temperature[b])
+    and put in order, larger logits first, equal ones by id.  Kept are the first top_k[b]
+    (int32; 0: all), of these the ones before which less than top_p[b] of their mass lies
+    (the first always; 1: all), of these the ones that weigh at least min_p[b] of what the
+    first does (0: all).  The result is the first token by id at which the kept ones' mass
+    exceeds u[b] of its total.  temperature, top_p and min_p: float32 [B]; any of them may
+    be left out.  A temperature of 0 (below 2^-64) takes the largest logit.  No gradient."""
+    return _ok(_native().sample_logits(logits, u, temperature, top_k, top_p, min_p),
+               "flce_sample_logits")[0]
