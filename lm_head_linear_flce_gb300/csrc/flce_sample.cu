@@ -72,16 +72,21 @@ constexpr float kMagicA = 0x1.8p2f;   // the same for units of 2^-21 and of 2^-4
 constexpr float kMagicB = 0x1.8p-19f; // which a weight is a + b
 constexpr uint32_t kBitsA = 0x40c00000u, kBitsB = 0x36400000u;
 
-__device__ __forceinline__ Scale make_scale(float top, float T) {
+// c of a temperature, in two floats.
+__device__ __forceinline__ float2 inverse_of(float T) {
   constexpr float kHi = 0x1.715476p0f, kLo = 0x1.4ae0cp-26f;  // 1 / ln 2
+  const float hi = __fdiv_rn(kHi, T);
+  return make_float2(hi, __fdividef(fmaf(-hi, T, kHi) + kLo, T));
+}
+__device__ __forceinline__ Scale make_scale(float top, float2 c) {
+  if (!(c.x > 0.f) || top == INFINITY) c = make_float2(0.f, 0.f);  // every token alike
   Scale s;
-  s.c_hi = __fdiv_rn(kHi, T);
-  s.c_lo = __fdividef(fmaf(-s.c_hi, T, kHi) + kLo, T);
-  if (!(s.c_hi > 0.f) || top == INFINITY) s.c_hi = s.c_lo = 0.f;  // every token alike
+  s.c_hi = c.x;
+  s.c_lo = c.y;
   const float x = top * s.c_hi;
-  const bool large = fabsf(x) > 64.f;  // (an infinite top too: least is 0 then)
-  s.base = large || top == INFINITY ? top : 0.f;
-  const float shift = s.base == 0.f ? ceilf(x) : 0.f;
+  const bool from_top = fabsf(x) > 64.f || top == INFINITY;
+  const float shift = from_top ? 0.f : ceilf(x);
+  s.base = from_top ? top : 0.f;
   // below it a weight is less than 2^-59
   s.least = top == INFINITY ? 0.f : s.c_hi > 0.f ? fmaxf(__fdividef(shift - 60.f, s.c_hi), -FLT_MAX)
                                                  : -FLT_MAX;
@@ -130,8 +135,9 @@ __device__ __forceinline__ uint64_t weight(float l, const Scale& s, const float2
 }
 
 // ------------------------------------------------------------ a row's logits
-// A row in units of 16 bytes, the first starting `shift` elements before it; 32 units
-// are a slot, and a warp has consecutive slots.  Elements outside the row are -infinity.
+// A row in units of 16 bytes, the first starting `shift` elements before it.  32 units
+// are a slot; a warp has consecutive slots, and a lane as many consecutive units of them
+// as there are slots.  Elements outside the row are -infinity.
 template <class T>
 struct Row {
   static constexpr int kPer = 16 / static_cast<int>(sizeof(T));
@@ -144,21 +150,22 @@ struct Row {
     units = (V + shift + kPer - 1) / kPer;
   }
   __device__ int first(int u) const { return u * kPer - shift; }  // column of a unit's first element
+  __device__ bool whole(int u) const { return first(u) >= 0 && first(u) + kPer <= V; }
+  __device__ float at(int c) const {
+    if (c < 0 || c >= V) return -INFINITY;
+    if constexpr (sizeof(T) == 4) return p[c];
+    else return __bfloat162float(p[c]);
+  }
   __device__ __forceinline__ uint4 load(int u) const {
+    if (whole(u)) return *reinterpret_cast<const uint4*>(p + first(u));
     const int c = first(u);
-    if (c >= 0 && c + kPer <= V) return *reinterpret_cast<const uint4*>(p + c);
-    constexpr uint32_t kNone = 0xff800000u;  // -infinity
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      if constexpr (sizeof(T) == 4) {
-        w[i] = c + i >= 0 && c + i < V ? __float_as_uint(p[c + i]) : kNone;
-      } else {
-        const int k = c + 2 * i;
-        const uint32_t lo = k >= 0 && k < V ? __bfloat16_as_ushort(p[k]) : kNone >> 16;
-        const uint32_t hi = k + 1 >= 0 && k + 1 < V ? __bfloat16_as_ushort(p[k + 1]) : kNone >> 16;
-        w[i] = lo | hi << 16;
-      }
+      if constexpr (sizeof(T) == 4)
+        w[i] = __float_as_uint(at(c + i));
+      else  // (bf16 values: their lower halves are 0)
+        w[i] = __float_as_uint(at(c + 2 * i)) >> 16 | __float_as_uint(at(c + 2 * i + 1));
     }
     return make_uint4(w[0], w[1], w[2], w[3]);
   }
@@ -192,22 +199,69 @@ __device__ __forceinline__ uint64_t warp_sum_u64(uint64_t v) {
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
+template <class I>
+__device__ __forceinline__ I warp_scan(I v) {  // of this lane and those before
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const I x = __shfl_up_sync(0xffffffffu, v, o);
+    if ((threadIdx.x & 31) >= o) v += x;
+  }
+  return v;
+}
 __device__ __forceinline__ void st_cluster_u64(uint32_t addr, uint64_t v) {
   asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(addr), "l"(v) : "memory");
 }
+__device__ __forceinline__ uint64_t ld_cluster_u64(uint32_t addr) {
+  uint64_t v;
+  asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ void cluster_arrive() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  __syncwarp();
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
 
-// One entry of every warp of the row, in every CTA of its cluster.
-struct Exchange {
+constexpr int kList = 1024;   // tokens of a list
+constexpr int kBins = 2048;   // of a histogram of masses, 1/64 of an octave each
+constexpr int kGroups = 32;   // of bins, whose sums the CTAs exchange
+
+// What the CTAs of a cluster read of one another, and what a CTA works in.
+struct Shared {
+  // one entry of every warp of the row, in every CTA; two sets, used in turn (who writes
+  // one again has passed a barrier since its last readers did)
   uint64_t mass[2][kMaxWarps];
   uint32_t count[2][kMaxWarps];
+  uint64_t group[kMaxCluster][kGroups];
+  uint64_t list[kList];  // this CTA's tokens near a border: key << 32 | ~id
+  union {
+    uint32_t bins[kBins];
+    uint64_t work[kList];  // every CTA's list, in order
+  };
+  uint64_t part[kWarps];
+  float2 table[32];
+  float2 inverse;    // c of the temperature
+  float2 log_min_p;  // T ln(min_p)
+  uint32_t listed;
+  int found;
+  float cut;
 };
+
 struct Sum {
   uint64_t mass;
   uint32_t count;
 };
 
 struct Cluster {
-  Exchange* x;
+  Shared& sh;
   int rank, ctas, phase;
 
   // Gives every CTA this warp's entry, and waits for all of them.
@@ -215,113 +269,204 @@ struct Cluster {
     const int lane = threadIdx.x & 31, me = rank * kWarps + (threadIdx.x >> 5);
     phase ^= 1;
     if (lane < ctas) {
-      st_cluster_u64(mapa_shared(smem_u32(&x->mass[phase][me]), lane), mass);
-      st_shared_cluster_u32(mapa_shared(smem_u32(&x->count[phase][me]), lane), count);
+      st_cluster_u64(mapa_shared(smem_u32(&sh.mass[phase][me]), lane), mass);
+      st_shared_cluster_u32(mapa_shared(smem_u32(&sh.count[phase][me]), lane), count);
     }
-    __syncwarp();
-    cluster_sync_all();
+    cluster_arrive();
+    cluster_wait();
   }
-  // The sum over all warps.  (The other buffer's last readers are past this barrier's
-  // predecessor, so two suffice.)
-  __device__ __forceinline__ Sum total(uint64_t mass, uint32_t count) {
-    share(mass, count);
+  // The sum over the warps first .. last - 1.
+  __device__ __forceinline__ Sum sum(int first, int last) const {
     uint64_t m = 0;
     uint32_t n = 0;
-    for (int i = threadIdx.x & 31; i < ctas * kWarps; i += 32) {
-      m += x->mass[phase][i];
-      n += x->count[phase][i];
+    for (int i = first + (threadIdx.x & 31); i < last; i += 32) {
+      m += sh.mass[phase][i];
+      n += sh.count[phase][i];
     }
     return {warp_sum_u64(m), __reduce_add_sync(0xffffffffu, n)};
   }
+  __device__ __forceinline__ Sum total(uint64_t mass, uint32_t count) {
+    share(mass, count);
+    return sum(0, ctas * kWarps);
+  }
 };
+
+// ------------------------------------------------------- lists in shared memory
+// Sorts the first n (a power of two, 64 to kList) of v, the larger first, with the
+// block's first n / 64 warps, which alone call it.
+__device__ void sort_list(uint64_t* v, int n) {
+  const int threads = n / 2;
+  for (int size = 2; size <= n; size <<= 1) {
+    for (int stride = size / 2; stride > 0; stride >>= 1) {
+      const int t = threadIdx.x;
+      const int i = 2 * t - (t & (stride - 1)), k = i + stride;
+      const uint64_t a = v[i], b = v[k];
+      if ((a < b) == ((i & size) == 0)) {
+        v[i] = b;
+        v[k] = a;
+      }
+      // a warp's 32 pairs lie in 64 neighbours, and stay there while strides do
+      if (stride > 32 || (stride == 1 && size >= 64))
+        asm volatile("bar.sync 1, %0;" ::"r"(threads) : "memory");
+      else __syncwarp();
+    }
+  }
+}
+
+// Sums of w[0 .. n) up to and including each, in place, by `threads` threads (a multiple
+// of 32, which alone call it); returns the total.
+__device__ uint64_t scan_list(uint64_t* w, int n, int threads, uint64_t* part) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  uint64_t carry = 0;
+  for (int i0 = 0; i0 < n; i0 += threads) {
+    const int i = i0 + threadIdx.x;
+    const uint64_t x = warp_scan(i < n ? w[i] : uint64_t{0});
+    if (lane == 31) part[warp] = x;
+    asm volatile("bar.sync 1, %0;" ::"r"(threads) : "memory");
+    const int warps = threads / 32;
+    const uint64_t p = lane < warps ? part[lane] : 0;
+    const uint64_t upto = warp_scan(p);
+    const uint64_t before = __shfl_sync(0xffffffffu, upto - p, warp);
+    if (i < n) w[i] = carry + before + x;
+    carry += __shfl_sync(0xffffffffu, upto, warps - 1);
+    asm volatile("bar.sync 1, %0;" ::"r"(threads) : "memory");
+  }
+  return carry;
+}
+
+__device__ __forceinline__ int list_size(uint32_t n) {  // a power of two, 64 at least
+  return n <= 64 ? 64 : 2 << (31 - __clz(static_cast<int>(n) - 1));
+}
 
 // ------------------------------------------------------------ the kernel
 template <class T, bool HELD>
-__global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a) {
+__global__ void __launch_bounds__(kThreads, 2)
+    sample_kernel(const SampleArgs a, const int stride) {
   using R = Row<T>;
   constexpr int kPer = R::kPer;
-  extern __shared__ __align__(16) uint4 held[];  // HELD: this CTA's slots
-  __shared__ Exchange exchange;
-  __shared__ float2 table[32];
-  __shared__ double log_min_p;
-  // every CTA of the cluster runs before another writes to its shared memory
-  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
-  griddep_launch_dependents();
-  griddep_wait();
+  // kList * 8 bytes at least; HELD: this CTA's part of the row, `stride` units a lane (an
+  // odd number, so that lanes read their units without bank conflicts)
+  extern __shared__ __align__(16) uint4 held[];
+  __shared__ Shared sh;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  Cluster cl{&exchange, 0, 1, 0};
+  Cluster cl{sh, 0, 1, 0};
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(cl.rank));
   asm volatile("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(cl.ctas));
+  // every CTA of the cluster runs before another writes to its shared memory
+  cluster_arrive();
+  griddep_launch_dependents();
+  griddep_wait();
   const int64_t b = blockIdx.x / cl.ctas;
   const R row(a, b);
-  // this warp's slots, and the CTA's first
   const int slots = (row.units + 31) / 32, warps = cl.ctas * kWarps;
-  const auto bound = [&](int w) {
-    return static_cast<int>(static_cast<int64_t>(slots) * w / warps);
+  const int me = cl.rank * kWarps + warp;
+  const auto first_slot = [&](int w) {  // (V <= 2^21: below 2^31)
+    return static_cast<int>(static_cast<uint32_t>(slots * w) / static_cast<uint32_t>(warps));
   };
-  const int me = cl.rank * kWarps + warp, s0 = bound(me), s1 = bound(me + 1);
-  const int cta0 = bound(cl.rank * kWarps);
-  const auto fetch = [&](int s) {
-    uint4 r = make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u);
-    if (sizeof(T) == 4) r = make_uint4(0xff800000u, 0xff800000u, 0xff800000u, 0xff800000u);
-    const int u = s * 32 + lane;
-    if (u < row.units) r = row.load(u);
-    return r;
-  };
-  const auto get = [&](int s, float (&v)[kPer]) {
-    R::floats(HELD ? held[(s - cta0) * 32 + lane] : fetch(s), v);
+  const int s0 = first_slot(me), each = first_slot(me + 1) - s0;
+  const int u0 = s0 * 32;  // the warp's first unit; lane l has each of them from u0 + l * each
+  uint4* mine = held + (warp * 32 + lane) * stride;
+  const auto get = [&](int i, float (&v)[kPer]) {
+    if constexpr (HELD) {
+      R::floats(mine[i], v);
+    } else {
+      R::floats(row.load(u0 + lane * each + i), v);
+    }
   };
 
+  if constexpr (HELD) {
+    // in the order of memory, all of it on its way at once
+    int to = lane / max(each, 1), at = lane - to * each;
+    const int step = 32 / max(each, 1), rest = 32 - step * each;
+    for (int s = 0; s < each; ++s) {
+      const int u = u0 + s * 32 + lane;
+      uint4* dst = held + (warp * 32 + to) * stride + at;
+      if (row.whole(u))
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)),
+                     "l"(row.p + row.first(u))
+                     : "memory");
+      else *dst = row.load(u);
+      to += step;
+      at += rest;
+      if (at >= each) at -= each, ++to;
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  }
   const float T0 = a.temperature ? a.temperature[b] : 1.f;
   const int k = a.top_k ? a.top_k[b] : 0;
   const float p = a.top_p ? a.top_p[b] : 1.f;
   const float min_p = a.min_p ? a.min_p[b] : 0.f;
   const float u = a.u[b];
+  const bool greedy = !(T0 >= kGreedyBelow);
   if (warp == 0) {
-    table[lane] = kPow2[lane];
-    // one lane: 64-bit logarithms are slow
-    if (lane == 0 && min_p > 0.f) log_min_p = log(static_cast<double>(fminf(min_p, 1.f)));
-  }
-
-  // The row, and its largest logit (NaN is passed over).
-  float top = -INFINITY;
-  constexpr int kAtOnce = 4;
-  for (int s = s0; s < s1; s += kAtOnce) {
-    uint4 r[kAtOnce];
-#pragma unroll
-    for (int i = 0; i < kAtOnce; ++i)
-      if (s + i < s1) r[i] = fetch(s + i);
-#pragma unroll
-    for (int i = 0; i < kAtOnce; ++i) {
-      if (s + i >= s1) break;
-      if (HELD) held[(s + i - cta0) * 32 + lane] = r[i];
-      float v[kPer];
-      R::floats(r[i], v);
-#pragma unroll
-      for (int j = 0; j < kPer; ++j) top = fmaxf(top, v[j]);
+    sh.table[lane] = kPow2[lane];
+    if (lane == 0) {
+      sh.listed = 0;
+      sh.cut = -FLT_MAX;
+      sh.inverse = inverse_of(greedy ? 1.f : T0);
+      // one lane: 64-bit operations are slow
+      if (min_p > 0.f) {
+        const double d = static_cast<double>(T0) * log(static_cast<double>(fminf(min_p, 1.f)));
+        sh.log_min_p.x = static_cast<float>(d);
+        sh.log_min_p.y = static_cast<float>(d - static_cast<double>(sh.log_min_p.x));
+      }
     }
   }
+  for (int i = threadIdx.x; i < kBins; i += kThreads) sh.bins[i] = 0;
+  if constexpr (HELD) {
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    __syncwarp();
+  }
+
+  // The largest logit (NaN is passed over): the lane's, the warps', the row's.
+  float lane_top = -INFINITY;
+  for (int i = 0; i < each; ++i) {
+    float v[kPer];
+    get(i, v);
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    for (int j = 0; j < kPer; ++j) lane_top = fmaxf(lane_top, v[j]);
+  }
+  const auto warp_max = [](float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
+  };
+  float top = warp_max(lane_top);
+  cluster_wait();
   cl.share(0, __float_as_uint(top));
-  for (int i = lane; i < warps; i += 32)
-    top = fmaxf(top, __uint_as_float(exchange.count[cl.phase][i]));
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  const uint32_t* warp_tops = sh.count[cl.phase];
+  for (int i = lane; i < warps; i += 32) top = fmaxf(top, __uint_as_float(warp_tops[i]));
+  top = warp_max(top);
   if (top == -INFINITY) {  // nothing to pick from
     if (me == 0 && lane == 0) a.out[b] = -1;
     return;
   }
-  const bool greedy = !(T0 >= kGreedyBelow);
-  const Scale scale = make_scale(top, greedy ? 1.f : T0);
+  const Scale scale = make_scale(top, sh.inverse);
+  // what min_p keeps: w >= min_p w_max, l >= max + T ln(min_p), rounded up
+  float least = -FLT_MAX;
+  if (!greedy && min_p > 0.f) {
+    const float2 d = sh.log_min_p;
+    const float sum = __fadd_rn(top, d.x), back = __fsub_rn(sum, top);
+    const float rest = __fadd_rn(
+        __fadd_rn(__fsub_rn(top, __fsub_rn(sum, back)), __fsub_rn(d.x, back)), d.y);
+    least = rest > 0.f ? nextafterf(sum, INFINITY) : sum;
+    if (!(least > -FLT_MAX)) least = -FLT_MAX;
+    if (top == INFINITY) least = top;
+  }
+  const bool by_k = !greedy && k > 0 && k < a.V, by_p = !greedy && p < 1.f;
+  const uint64_t part_p = __float2ull_rz(fmaxf(fminf(p, 0x1.fffffep-1f), 0.f) * 0x1p64f);
+  // the mass before a token that is kept is less than this
+  const auto target_p = [&](uint64_t all) {  // p * all, rounded up; the first token always
+    return max(static_cast<uint64_t>(__umul64hi(part_p, all)) + (part_p * all != 0), uint64_t{1});
+  };
+  const uint64_t part_u = __float2ull_rz(fminf(fmaxf(u, 0.f), 0x1.fffffep-1f) * 0x1p64f);
 
-  // The tokens at or above x: how many, and (MASS) their mass.
+  // The tokens at or above x: how many, and (with `mass`) their mass.
   const auto at_least = [&](float x, bool mass) {
     uint32_t n = 0, wa = 0, wb = 0;
-    for (int s = s0; s < s1; ++s) {
+    for (int i = 0; i < each; ++i) {
       float v[kPer];
-      get(s, v);
+      get(i, v);
       bool some = false;
 #pragma unroll
       for (int j = 0; j < kPer; ++j) some = some || v[j] >= x;
@@ -331,7 +476,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
         const bool in = v[j] >= x;
         if (mass) {
           uint32_t ka, kb;
-          weigh(v[j], scale, table, ka, kb);
+          weigh(v[j], scale, sh.table, ka, kb);
           wa += in ? ka : 0u;
           wb += in ? kb : 0u;
         }
@@ -340,11 +485,12 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     }
     return cl.total(warp_sum_u64(mass ? mass_of(wa, wb, n) : 0), __reduce_add_sync(0xffffffffu, n));
   };
-  // The least x above which fewer than `target` (tokens, or mass) lie, from `low` on: the
-  // row's tokens above it and so many of those equal to it make the target.
   float t = -FLT_MAX;
   uint32_t ties = UINT_MAX;
-  const auto prefix = [&](uint64_t target, bool mass) {
+  // Narrows t and ties to the prefix that makes `target` (tokens, or mass): halves the
+  // range of logits from t on, a pass over the row and a barrier each.  For any row; the
+  // lists below are faster where they are long enough.
+  const auto halve = [&](uint64_t target, bool mass) {
     int lo = key_of<T>(t), hi = key_of<T>(top);
     uint64_t above = 0;
     while (lo < hi) {
@@ -361,7 +507,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     const float x = value_of<T>(lo);
     uint64_t r = target - above;
     if (mass) {
-      const uint64_t w = max(weight(x, scale, table), uint64_t{1});
+      const uint64_t w = max(weight(x, scale, sh.table), uint64_t{1});
       r = (r + w - 1) / w;
     }
     r = min(r, static_cast<uint64_t>(UINT_MAX));
@@ -370,168 +516,276 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
       ties = static_cast<uint32_t>(r);
     }
   };
-  // The mass of what t and ties keep, warp by warp, and those of the warps before.
-  uint64_t before, mine, total;
-  uint32_t ties_before, own_ties;
-  const auto kept = [&]() {
-    uint32_t n = 0, wa = 0, wb = 0, eq = 0;
-    for (int s = s0; s < s1; ++s) {
+
+  // Puts the tokens with in(l) on the CTA's list, one that is full counts on; returns
+  // the warp's number of them.
+  const auto list_tokens = [&](const auto& in) {
+    uint32_t n = 0;
+    for (int i = 0; i < each; ++i) {
       float v[kPer];
-      get(s, v);
+      get(i, v);
+      uint32_t which = 0;
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) which |= in(v[j]) ? 1u << j : 0u;
+      if (!__any_sync(0xffffffffu, which != 0)) continue;
+      const uint32_t c = __popc(which), upto = warp_scan(c);
+      const uint32_t all = __shfl_sync(0xffffffffu, upto, 31);
+      uint32_t at = 0;
+      if (lane == 31) at = atomicAdd(&sh.listed, all);
+      at = __shfl_sync(0xffffffffu, at, 31) + upto - c;
+      n += all;
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) {
+        if (!(which >> j & 1)) continue;
+        const uint32_t id = static_cast<uint32_t>(row.first(u0 + lane * each + i) + j);
+        const uint32_t key = static_cast<uint32_t>(key_of<float>(v[j] + 0.f)) ^ 0x80000000u;
+        if (at < kList) sh.list[at] = static_cast<uint64_t>(key) << 32 | (id ^ 0xffffffffu);
+        ++at;
+      }
+    }
+    return n;
+  };
+  const auto listed_value = [](uint64_t e) {
+    return value_of<float>(static_cast<int>(static_cast<uint32_t>(e >> 32) ^ 0x80000000u));
+  };
+  // Every CTA's list into `work`, n tokens in all, padded to list_size(n).
+  const auto pull_lists = [&](uint32_t n) {
+    uint32_t at = 0;
+    for (int r = 0; r < cl.ctas; ++r) {
+      const uint32_t c = cl.sum(r * kWarps, (r + 1) * kWarps).count;
+      for (uint32_t i = threadIdx.x; i < c; i += kThreads)
+        sh.work[at + i] = ld_cluster_u64(mapa_shared(smem_u32(&sh.list[i]), r));
+      at += c;
+    }
+    for (uint32_t i = n + threadIdx.x; i < static_cast<uint32_t>(list_size(n)); i += kThreads)
+      sh.work[i] = 0;
+  };
+
+  // --- top-k of few: a list of everything that can be among the first k, which the
+  // cluster's first CTA then has to itself.
+  constexpr int kFew = kMaxWarps * 7 / 8;
+  if (by_k && k <= kFew && k <= warps * 7 / 8) {
+    // the k-th largest of the warps' largest: k tokens are at or above it
+    const int v = threadIdx.x >> 2;
+    uint32_t larger = 0;
+    if (v < warps) {
+      const float x = __uint_as_float(warp_tops[v]);
+      for (int i = threadIdx.x & 3; i < warps; i += 4) {
+        const float y = __uint_as_float(warp_tops[i]);
+        larger += y > x || (y == x && i < v);
+      }
+    }
+    larger += __shfl_xor_sync(0xffffffffu, larger, 1);
+    larger += __shfl_xor_sync(0xffffffffu, larger, 2);
+    if (v < warps && larger == static_cast<uint32_t>(k - 1) && (threadIdx.x & 3) == 0)
+      sh.cut = fmaxf(__uint_as_float(warp_tops[v]), -FLT_MAX);
+    __syncthreads();
+    const float cut = sh.cut;
+    const uint32_t n = list_tokens([&](float l) { return l >= cut; });
+    const uint32_t N = cl.total(0, n).count;
+    if (N <= kList) {
+      if (cl.rank == 0) pull_lists(N);
+      cluster_arrive();  // the lists have been read
+      if (cl.rank != 0) {
+        cluster_wait();
+        return;
+      }
+      __syncthreads();
+      const int size = list_size(N), threads = size / 2;
+      auto* weights = reinterpret_cast<uint64_t*>(held);  // (the row is not needed any more)
+      if (threadIdx.x < threads) {
+        sort_list(sh.work, size);
+        uint32_t keep = min(N, static_cast<uint32_t>(k));
+        for (uint32_t i = threadIdx.x; i < keep; i += threads)
+          weights[i] = weight(listed_value(sh.work[i]), scale, sh.table);
+        asm volatile("bar.sync 1, %0;" ::"r"(threads) : "memory");
+        const uint64_t all = scan_list(weights, keep, threads, sh.part);
+        // p and min_p keep a prefix of these
+        const uint64_t target = by_p ? target_p(all) : UINT64_MAX;
+        uint32_t in = 0;
+        for (uint32_t i = threadIdx.x; i < keep; i += threads)
+          in += i == 0 || (weights[i - 1] < target && listed_value(sh.work[i]) >= least);
+        in = __reduce_add_sync(0xffffffffu, in);
+        if (lane == 0) sh.part[warp] = in;
+        asm volatile("bar.sync 1, %0;" ::"r"(threads) : "memory");
+        keep = 0;
+        for (int w = 0; w < threads / 32; ++w) keep += static_cast<uint32_t>(sh.part[w]);
+        const uint64_t kept = weights[keep - 1];
+        asm volatile("bar.sync 1, %0;" ::"r"(threads) : "memory");
+        // by id: ~id << 32 | place, the larger first
+        const int size2 = list_size(keep);
+        for (int i = threadIdx.x; i < size2; i += threads) {
+          const uint64_t e = i < static_cast<int>(keep) ? sh.work[i] << 32 | i : 0;
+          sh.list[i] = e;
+        }
+        asm volatile("bar.sync 1, %0;" ::"r"(threads) : "memory");
+        if (threadIdx.x < size2 / 2) {
+          const int threads2 = size2 / 2;
+          sort_list(sh.list, size2);
+          uint64_t* by_id = sh.work;
+          for (uint32_t i = threadIdx.x; i < keep; i += threads2) {
+            const uint32_t at = static_cast<uint32_t>(sh.list[i]);
+            by_id[i] = weights[at] - (at ? weights[at - 1] : 0);
+          }
+          asm volatile("bar.sync 1, %0;" ::"r"(threads2) : "memory");
+          scan_list(by_id, keep, threads2, sh.part);
+          const uint64_t pick = __umul64hi(part_u, kept);
+          for (uint32_t i = threadIdx.x; i < keep; i += threads2)
+            if (by_id[i] > pick && (i == 0 || by_id[i - 1] <= pick))
+              a.out[b] = static_cast<int64_t>(~static_cast<uint32_t>(sh.list[i] >> 32));
+        }
+      }
+      __syncwarp();
+      cluster_wait();
+      return;
+    }
+  }
+  if (greedy) {
+    t = top;
+    ties = 1;
+  }
+
+  // What t and ties keep: the lane's mass above t (with `ties` all ones: from t on) and its
+  // tokens equal to t, to every CTA by warps.
+  uint64_t lane_mass = 0;
+  uint32_t lane_ties = 0;
+  const auto weigh_kept = [&]() {
+    uint32_t n = 0, wa = 0, wb = 0;
+    lane_ties = 0;
+    const bool some_ties = ties != UINT_MAX;
+    for (int i = 0; i < each; ++i) {
+      float v[kPer];
+      get(i, v);
       bool some = false;
 #pragma unroll
       for (int j = 0; j < kPer; ++j) some = some || v[j] >= t;
       if (!__any_sync(0xffffffffu, some)) continue;
 #pragma unroll
       for (int j = 0; j < kPer; ++j) {
-        const bool in = v[j] > t;
+        const bool tie = some_ties && v[j] == t, in = v[j] >= t && !tie;
         uint32_t ka, kb;
-        weigh(v[j], scale, table, ka, kb);
+        weigh(v[j], scale, sh.table, ka, kb);
         wa += in ? ka : 0u;
         wb += in ? kb : 0u;
         n += in;
-        eq += v[j] == t;
+        lane_ties += tie;
       }
     }
-    cl.share(warp_sum_u64(mass_of(wa, wb, n)), __reduce_add_sync(0xffffffffu, eq));
-    // every warp goes over all entries: four consecutive ones a lane
-    const uint64_t wt = weight(t, scale, table);
-    constexpr int kEach = kMaxWarps / 32;
-    uint64_t m[kEach];
-    uint32_t e[kEach], sum = 0;
-#pragma unroll
-    for (int i = 0; i < kEach; ++i) {
-      const int w = lane * kEach + i;
-      m[i] = w < warps ? exchange.mass[cl.phase][w] : 0;
-      e[i] = w < warps ? exchange.count[cl.phase][w] : 0;
-      sum += e[i];
-    }
-    uint32_t ahead = sum;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t x = __shfl_up_sync(0xffffffffu, ahead, o);
-      if (lane >= o) ahead += x;
-    }
-    ahead -= sum;
-    uint64_t lane_mass = 0;
-    uint32_t e_at[kEach];
-#pragma unroll
-    for (int i = 0; i < kEach; ++i) {
-      e_at[i] = ahead;
-      const uint32_t room = ties > ahead ? ties - ahead : 0;
-      m[i] += wt * min(e[i], room);
-      lane_mass += m[i];
-      ahead += e[i];
-    }
-    uint64_t upto = lane_mass;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint64_t x = __shfl_up_sync(0xffffffffu, upto, o);
-      if (lane >= o) upto += x;
-    }
-    total = __shfl_sync(0xffffffffu, upto, 31);
-    upto -= lane_mass;
-    // this warp's own entry
-    before = mine = 0;
-    ties_before = own_ties = 0;
-#pragma unroll
-    for (int i = 0; i < kEach; ++i) {
-      const uint64_t ub = __shfl_sync(0xffffffffu, upto, me / kEach);
-      const uint64_t mb = __shfl_sync(0xffffffffu, m[i], me / kEach);
-      const uint32_t tb = __shfl_sync(0xffffffffu, e_at[i], me / kEach);
-      if (i == me % kEach) before = ub, mine = mb, ties_before = tb;
-      upto += m[i];
-    }
+    lane_mass = mass_of(wa, wb, n);
   };
 
-  if (greedy) {
-    t = top;
-    ties = 1;
-  } else {
-    if (k > 0 && k < a.V) prefix(static_cast<uint64_t>(k), false);
-    if (p < 1.f) {
-      kept();
-      const uint64_t part = __float2ull_rz(fmaxf(p, 0.f) * 0x1p64f);  // p in units of 2^-64
-      uint64_t target = __umul64hi(part, total) + (part * total != 0);
-      prefix(max(target, uint64_t{1}), true);
-    }
-    if (min_p > 0.f) {
-      // w >= min_p w_max: l >= max + T ln(min_p), in 64 bits
-      const double least = static_cast<double>(top) + static_cast<double>(T0) * log_min_p;
-      const float x = top == INFINITY ? top : __double2float_ru(least);
-      if (x > t) {
-        t = x;
-        ties = UINT_MAX;
-      }
+  if (by_k) halve(static_cast<uint64_t>(k), false);
+  if (by_p) {
+    weigh_kept();
+    const Sum s = cl.total(warp_sum_u64(lane_mass), __reduce_add_sync(0xffffffffu, lane_ties));
+    const uint64_t wt = weight(t, scale, sh.table);
+    halve(target_p(s.mass + wt * min(s.count, ties)), true);
+  }
+  if (least > t) {
+    t = least;
+    ties = UINT_MAX;
+  }
+  weigh_kept();
+  // The lanes' parts for the warp below; the warps' to every CTA.
+  uint64_t* lane_masses = sh.work;
+  uint32_t* lane_tie_counts = reinterpret_cast<uint32_t*>(sh.work + kThreads);
+  lane_masses[threadIdx.x] = lane_mass;
+  lane_tie_counts[threadIdx.x] = lane_ties;
+  cl.share(warp_sum_u64(lane_mass), __reduce_add_sync(0xffffffffu, lane_ties));
+  // One warp of each CTA goes on: first, which warp has the token; four consecutive
+  // entries a lane.
+  if (warp != 0) return;
+  const uint64_t wt = weight(t, scale, sh.table);
+  constexpr int kEach = kMaxWarps / 32;
+  uint64_t m[kEach], upto = 0;
+  uint32_t e_at[kEach], ahead = 0;
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    const int w = lane * kEach + i;
+    m[i] = w < warps ? sh.mass[cl.phase][w] : 0;
+    e_at[i] = w < warps ? sh.count[cl.phase][w] : 0;
+    ahead += e_at[i];
+  }
+  ahead = warp_scan(ahead) - ahead;  // ties of the lanes before
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    const uint32_t e = e_at[i];
+    e_at[i] = ahead;
+    m[i] += wt * min(e, ties > ahead ? ties - ahead : 0u);
+    upto += m[i];
+    ahead += e;
+  }
+  const uint64_t lane_sum = upto;
+  upto = warp_scan(upto);
+  const uint64_t pick = __umul64hi(part_u, __shfl_sync(0xffffffffu, upto, 31));
+  const int owner = __ffs(__ballot_sync(0xffffffffu, upto > pick)) - 1;
+  upto -= lane_sum;
+  int which = 0;
+  uint64_t before = upto;
+  uint32_t rank = e_at[0];
+#pragma unroll
+  for (int i = 0; i + 1 < kEach; ++i) {
+    if (which == i && before + m[i] <= pick) {
+      before += m[i];
+      which = i + 1;
+      rank = e_at[i + 1];
     }
   }
-  kept();
-  const float uc = fminf(fmaxf(u, 0.f), 0x1.fffffep-1f);
-  const uint64_t target = __umul64hi(__float2ull_rz(uc * 0x1p64f), total);
-  if (target < before || target - before >= mine) return;  // another warp's
-  // this warp's tokens in order
-  const uint64_t wt = weight(t, scale, table);
-  for (int s = s0; s < s1; ++s) {
-    float v[kPer];
-    get(s, v);
-    uint32_t eq = 0;
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) eq += v[j] == t;
-    uint32_t rank = eq;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t x = __shfl_up_sync(0xffffffffu, rank, o);
-      if (lane >= o) rank += x;
+  before = __shfl_sync(0xffffffffu, before, owner);
+  rank = __shfl_sync(0xffffffffu, rank, owner);
+  const int w = owner * kEach + __shfl_sync(0xffffffffu, which, owner) - cl.rank * kWarps;
+  if (w < 0 || w >= kWarps) return;  // another CTA's
+  // The lane that has it, then its tokens, which are consecutive, 32 at a time.
+  lane_mass = lane_masses[w * 32 + lane];
+  lane_ties = lane_tie_counts[w * 32 + lane];
+  rank += warp_scan(lane_ties) - lane_ties;
+  lane_mass += wt * min(lane_ties, ties > rank ? ties - rank : 0u);
+  upto = before + warp_scan(lane_mass);
+  const int who = __ffs(__ballot_sync(0xffffffffu, upto > pick)) - 1;
+  before = __shfl_sync(0xffffffffu, upto - lane_mass, who);
+  rank = __shfl_sync(0xffffffffu, rank, who);
+  const int first = first_slot(cl.rank * kWarps + w);
+  const int count = (first_slot(cl.rank * kWarps + w + 1) - first) * kPer;
+  const int c0 = row.first(first * 32) + who * count;
+  const T* tokens = reinterpret_cast<const T*>(held + (w * 32 + who) * stride);
+  for (int j0 = 0; j0 < count; j0 += 32) {
+    const int j = j0 + lane;
+    float l = -INFINITY;
+    if (j < count) {
+      if constexpr (!HELD) l = row.at(c0 + j);
+      else if constexpr (sizeof(T) == 4) l = tokens[j];
+      else l = __bfloat162float(tokens[j]);
     }
-    const uint32_t eq_all = __shfl_sync(0xffffffffu, rank, 31);
-    rank += ties_before - eq;
-    uint64_t w[kPer], sum = 0;
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-      const bool tie = v[j] == t;
-      w[j] = v[j] > t ? weight(v[j], scale, table) : tie && rank < ties ? wt : 0;
-      rank += tie;
-      sum += w[j];
-    }
-    uint64_t upto = sum;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint64_t x = __shfl_up_sync(0xffffffffu, upto, o);
-      if (lane >= o) upto += x;
-    }
-    const uint64_t all = __shfl_sync(0xffffffffu, upto, 31);
-    if (target - before < all) {
-      // the first token with before + masses up to it > target
-      uint64_t at = before + upto - sum;
-      if (at <= target && target < at + sum) {
-        int found = -1;
-#pragma unroll
-        for (int j = 0; j < kPer; ++j) {
-          at += w[j];
-          if (found < 0 && at > target) found = j;
-        }
-        a.out[b] = row.first(s * 32 + lane) + found;
-      }
+    const uint32_t equal = __ballot_sync(0xffffffffu, l == t);
+    const uint32_t nth = rank + __popc(equal & ((1u << lane) - 1));
+    const uint64_t x = l > t || (l == t && nth < ties) ? weight(l, scale, sh.table) : 0;
+    const uint64_t sum = warp_scan(x);
+    const uint32_t past = __ballot_sync(0xffffffffu, before + sum > pick);
+    if (past) {
+      if (lane == __ffs(past) - 1) a.out[b] = c0 + j;
       return;
     }
-    before += all;
-    ties_before += eq_all;
+    before += __shfl_sync(0xffffffffu, sum, 31);
+    rank += __popc(equal);
   }
 }
 
 // ------------------------------------------------------------- launching
-constexpr int kHeldMost = 96 * 1024;  // of a row in a CTA's shared memory: two CTAs an SM
+// Of a row in a CTA's shared memory: two CTAs an SM.
+static_assert(kThreads * 16 >= kList * 8);
+constexpr int kHeldMost = 112 * 1024 - static_cast<int>(sizeof(Shared));
 
 template <class T, bool HELD>
-cudaError_t launch_sample(const SampleArgs& a, int64_t B, int ctas, int smem, cudaStream_t s) {
+cudaError_t launch_sample(const SampleArgs& a, int64_t B, int ctas, int stride, cudaStream_t s) {
   auto* k = sample_kernel<T, HELD>;
   if (HELD) {
     static SmemLimit limit;
     const cudaError_t e = allow_smem(reinterpret_cast<const void*>(k), kHeldMost, &limit);
     if (e != cudaSuccess) return e;
   }
-  const cudaError_t e = launch_overlapped(k, dim3(static_cast<unsigned>(B * ctas)), dim3(kThreads),
-                                          smem, s, ctas, a);
+  const cudaError_t e =
+      launch_overlapped(k, dim3(static_cast<unsigned>(B * ctas)), dim3(kThreads),
+                        HELD ? kThreads * stride * 16 : kList * 8, s, ctas, a, stride);
   note_launch();
   return e != cudaSuccess ? e : cudaGetLastError();
 }
@@ -541,9 +795,10 @@ cudaError_t run_sample(const SampleArgs& a, int64_t B, cudaStream_t s) {
   constexpr int kPer = 16 / static_cast<int>(sizeof(T));
   const int64_t slots = ((a.V + 2 * kPer - 2) / kPer + 31) / 32;  // whatever the row's shift
   const int ctas = kMaxCluster;
-  const int64_t smem = (slots / ctas + 2) * 512;
-  return smem <= kHeldMost ? launch_sample<T, true>(a, B, ctas, static_cast<int>(smem), s)
-                           : launch_sample<T, false>(a, B, ctas, 0, s);
+  const int each = static_cast<int>((slots + ctas * kWarps - 1) / (ctas * kWarps));
+  const int stride = each | 1;
+  return kThreads * stride * 16 <= kHeldMost ? launch_sample<T, true>(a, B, ctas, stride, s)
+                                             : launch_sample<T, false>(a, B, ctas, stride, s);
 }
 
 }  // namespace
