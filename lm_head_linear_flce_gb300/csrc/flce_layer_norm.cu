@@ -3,45 +3,13 @@
 
 #include "flce_internal.h"
 #include "flce_norm_device.cuh"
+#include "flce_pairs.cuh"
 
 namespace flce {
 namespace {
 
 constexpr int kLnDwRows = 64;  // rows per partial sum of dweight and dbias past kMaxHeld
 
-// Two FP32 values in one 64-bit register: one instruction works on both, and these
-// kernels are short of issue slots in bf16.
-using F2 = uint64_t;
-__device__ __forceinline__ F2 pack2(float lo, float hi) {
-  F2 d;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
-  return d;
-}
-__device__ __forceinline__ float2 unpack2(F2 v) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-  return r;
-}
-__device__ __forceinline__ F2 both(float v) { return pack2(v, v); }
-__device__ __forceinline__ F2 add2(F2 a, F2 b) {
-  F2 d;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
-  F2 d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
-  F2 d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
-}
-__device__ __forceinline__ float sum2(F2 v) {
-  const float2 p = unpack2(v);
-  return p.x + p.y;
-}
 template <int E>
 __device__ __forceinline__ void to_pairs(const float (&v)[E], F2 (&p)[E / 2]) {
 #pragma unroll

@@ -1,11 +1,13 @@
 // A token a row by temperature, top-k, top-p and min-p from a given random number
 // (flce_sample_logits).
 //
-// A cluster of CTAs takes a row: each holds a part of it in shared memory, so that the
-// row is read once however often its tokens are gone over.  What a row keeps is a prefix
-// of its tokens in descending order (equal logits by id), which a logit t and a number r
-// say: all tokens above t, and the first r of those equal to t.  The token is then the
-// first, by id, whose cumulative mass among the kept ones exceeds u times their total.
+// One CTA takes a row, or a cluster of up to eight where rows are few.  It streams the row
+// once for the largest logit of the row and of each lane's tokens; what follows reads
+// again, from L2, as little as the limits leave: a list of candidates for top-k, all of it
+// where every token's mass counts.  What a row keeps is a prefix of its tokens in
+// descending order (equal logits by id), which a logit t and a number r say: all tokens
+// above t, and the first r of those equal to t.  The token is then the first, by id, whose
+// cumulative mass among the kept ones exceeds u times their total.
 //
 // Masses are integers.  A token weighs 2^((l - max) / (T ln 2)) in units of 2^-42, off by
 // 2^-31.6 of it (rms), and sums of integers do not depend on their order: however the
@@ -18,18 +20,35 @@
 #include <algorithm>
 #include <cfloat>
 #include <climits>
+#include <type_traits>
 
 #include "flce_device.cuh"
 #include "flce_internal.h"
 #include "flce_ops.h"
 
+#ifndef AHEAD1
+#define AHEAD1 8
+#endif
+#ifndef AHEAD2
+#define AHEAD2 4
+#endif
+#ifndef MINB
+#define MINB 2
+#endif
+#ifndef KT
+#define KT 512
+#endif
+#ifndef SM_FILL
+#define SM_FILL 1
+#endif
 namespace flce {
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = KT;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
 constexpr int kMaxWarps = kWarps * kMaxCluster;  // of a row
+constexpr int kMaxSlots = 1024;  // of a warp: 2^21 float32 logits in one CTA, with one to spare
 constexpr float kGreedyBelow = 0x1p-64f;         // temperatures that take the largest logit
 
 struct SampleArgs {
@@ -97,35 +116,33 @@ __device__ __forceinline__ Scale make_scale(float top, float2 c) {
 // A token's weight as a * 2^-21 + b * 2^-42, each as the float that holds its bits above
 // kBitsA and kBitsB.  With x = c (l - base) = k / 32 + f, |f| <= 1/64: 2^x by the table
 // (Tang 1989) times 2^f by its series; f carries the rounding errors of x and of the
-// table's entry.  Written with intrinsics so that every use rounds alike.
+// table's entry.  -infinity and NaN weigh nothing.  Written with intrinsics so that every
+// use rounds alike.  (Two values an instruction cost more registers than they save time.)
 __device__ __forceinline__ void weigh(float l, const Scale& s, const float2* table, uint32_t& a,
-                                      uint32_t& b) {
+                                       uint32_t& b) {
   const float d = fmaxf(__fsub_rn(l, s.base), s.least);
-  const float nq = __fmul_rn(d, -s.c_hi);
-  const float e = __fmaf_rn(d, s.c_lo, __fmaf_rn(d, s.c_hi, nq));
-  const float z = __fsub_rn(s.magic, nq);
-  const float g = __fadd_rn(nq, __fsub_rn(z, s.magic));
+  const float q = __fmul_rn(d, s.c_hi);
+  const float e = __fmaf_rn(d, s.c_lo, __fmaf_rn(d, s.c_hi, -q));
+  const float z = __fadd_rn(q, s.magic);
   const uint32_t k = __float_as_uint(z);
   const float2 t = table[k & 31];
-  const float f = __fsub_rn(__fadd_rn(e, t.y), g);
+  const float f = __fadd_rn(__fsub_rn(q, __fsub_rn(z, s.magic)), __fadd_rn(e, t.y));
   constexpr float kLn2 = 0.69314718055994531f;
   float p = __fmaf_rn(f, kLn2 * kLn2 * kLn2 * kLn2 / 24, kLn2 * kLn2 * kLn2 / 6);
   p = __fmaf_rn(f, p, kLn2 * kLn2 / 2);
   p = __fmul_rn(f, __fmaf_rn(f, p, kLn2));
   // (k's bits above the table's are the exponent; the constant's fall off the top)
   const float th = __uint_as_float(__float_as_uint(t.x) + ((k & ~31u) << 18));
-  const float y = __fmul_rn(th, p);
-  const float v = __fadd_rn(th, y);
-  const float rest = __fsub_rn(y, __fsub_rn(v, th));
+  const float v = __fmaf_rn(th, p, th);  // v + rest = th (1 + p)
+  const float rest = __fmaf_rn(th, p, __fsub_rn(th, v));
   const float fa = __fadd_rn(v, kMagicA);
-  const float fb =
-      __fadd_rn(__fadd_rn(__fsub_rn(v, __fsub_rn(fa, kMagicA)), rest), kMagicB);
+  const float fb = __fadd_rn(__fadd_rn(__fsub_rn(v, __fsub_rn(fa, kMagicA)), rest), kMagicB);
   a = __float_as_uint(fa);
   b = __float_as_uint(fb);
 }
-// The sum of n weights, from the sums of their a and b modulo 2^32.
+// The mass of n weights, from the sums of their a and b modulo 2^32 (n <= 1024).
 __device__ __forceinline__ uint64_t mass_of(uint32_t a, uint32_t b, uint32_t n) {
-  const int64_t ia = static_cast<int32_t>(a - n * kBitsA), ib = static_cast<int32_t>(b - n * kBitsB);
+  const int64_t ia = a - n * kBitsA, ib = static_cast<int32_t>(b - n * kBitsB);
   return static_cast<uint64_t>(ia * (int64_t{1} << 21) + ib);
 }
 __device__ __forceinline__ uint64_t weight(float l, const Scale& s, const float2* table) {
@@ -136,18 +153,20 @@ __device__ __forceinline__ uint64_t weight(float l, const Scale& s, const float2
 
 // ------------------------------------------------------------ a row's logits
 // A row in units of 16 bytes, the first starting `shift` elements before it.  32 units
-// are a slot; a warp has consecutive slots, and a lane as many consecutive units of them
-// as there are slots.  Elements outside the row are -infinity.
+// are a slot, a lane of a warp each; a warp has consecutive slots.  Elements outside the
+// row are -infinity.
 template <class T>
 struct Row {
   static constexpr int kPer = 16 / static_cast<int>(sizeof(T));
   const T* p;
+  const uint4* aligned;
   int V, shift, units;
 
   __device__ Row(const SampleArgs& a, int64_t b)
       : p(static_cast<const T*>(a.logits) + b * a.ld), V(a.V) {
     shift = static_cast<int>(reinterpret_cast<uintptr_t>(p) % 16 / sizeof(T));
     units = (V + shift + kPer - 1) / kPer;
+    aligned = reinterpret_cast<const uint4*>(reinterpret_cast<uintptr_t>(p) & ~uintptr_t{15});
   }
   __device__ int first(int u) const { return u * kPer - shift; }  // column of a unit's first element
   __device__ bool whole(int u) const { return first(u) >= 0 && first(u) + kPer <= V; }
@@ -156,8 +175,7 @@ struct Row {
     if constexpr (sizeof(T) == 4) return p[c];
     else return __bfloat162float(p[c]);
   }
-  __device__ __forceinline__ uint4 load(int u) const {
-    if (whole(u)) return *reinterpret_cast<const uint4*>(p + first(u));
+  __device__ __noinline__ uint4 load_edge(int u) const {
     const int c = first(u);
     uint32_t w[4];
 #pragma unroll
@@ -168,6 +186,9 @@ struct Row {
         w[i] = __float_as_uint(at(c + 2 * i)) >> 16 | __float_as_uint(at(c + 2 * i + 1));
     }
     return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  __device__ __forceinline__ uint4 load(int u) const {
+    return whole(u) ? aligned[u] : load_edge(u);
   }
   __device__ static __forceinline__ void floats(const uint4& r, float (&v)[kPer]) {
     const uint32_t w[4] = {r.x, r.y, r.z, r.w};
@@ -216,11 +237,6 @@ __device__ __forceinline__ uint64_t ld_cluster_u64(uint32_t addr) {
   asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(addr) : "memory");
   return v;
 }
-__device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
-  uint32_t v;
-  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
-  return v;
-}
 __device__ __forceinline__ void cluster_arrive() {
   __syncwarp();
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
@@ -230,9 +246,10 @@ __device__ __forceinline__ void cluster_wait() {
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-constexpr int kList = 1024;   // tokens of a list
-constexpr int kBins = 2048;   // of a histogram of masses, 1/64 of an octave each
-constexpr int kGroups = 32;   // of bins, whose sums the CTAs exchange
+constexpr int kList = 2048;        // tokens of a list
+constexpr int kBins = 2048;        // of a histogram
+constexpr int kGroups = 32;        // of bins, whose sums the CTAs exchange
+constexpr int kGroupBins = kBins / kGroups;
 
 // What the CTAs of a cluster read of one another, and what a CTA works in.
 struct Shared {
@@ -245,13 +262,19 @@ struct Shared {
   union {
     uint32_t bins[kBins];
     uint64_t work[kList];  // every CTA's list, in order
+    struct {
+      uint64_t mass[kMaxSlots];
+      uint32_t ties[kMaxSlots];
+    } slot;  // of the warp that has the token
   };
+  uint64_t weights[kList / 2];
   uint64_t part[kWarps];
   float2 table[32];
   float2 inverse;    // c of the temperature
   float2 log_min_p;  // T ln(min_p)
-  uint32_t listed;
-  int found;
+  uint64_t before;
+  uint32_t listed, rank;
+  int found[2];
   float cut;
 };
 
@@ -292,18 +315,18 @@ struct Cluster {
 };
 
 // ------------------------------------------------------- lists in shared memory
-// Sorts the first n (a power of two, 64 to kList) of v, the larger first, with the
-// block's first n / 64 warps, which alone call it.
-__device__ void sort_list(uint64_t* v, int n) {
-  const int threads = n / 2;
+// Sorts the first n (a power of two, 64 at least) of v, the larger first, with the block's
+// first `threads` = min(n / 2, kThreads) threads, which alone call it.
+__device__ void sort_list(uint64_t* v, int n, int threads) {
   for (int size = 2; size <= n; size <<= 1) {
     for (int stride = size / 2; stride > 0; stride >>= 1) {
-      const int t = threadIdx.x;
-      const int i = 2 * t - (t & (stride - 1)), k = i + stride;
-      const uint64_t a = v[i], b = v[k];
-      if ((a < b) == ((i & size) == 0)) {
-        v[i] = b;
-        v[k] = a;
+      for (int t = threadIdx.x; t < n / 2; t += threads) {
+        const int i = 2 * t - (t & (stride - 1)), k = i + stride;
+        const uint64_t a = v[i], b = v[k];
+        if ((a < b) == ((i & size) == 0)) {
+          v[i] = b;
+          v[k] = a;
+        }
       }
       // a warp's 32 pairs lie in 64 neighbours, and stay there while strides do
       if (stride > 32 || (stride == 1 && size >= 64))
@@ -339,14 +362,46 @@ __device__ __forceinline__ int list_size(uint32_t n) {  // a power of two, 64 at
 }
 
 // ------------------------------------------------------------ the kernel
-template <class T, bool HELD>
-__global__ void __launch_bounds__(kThreads, 2)
-    sample_kernel(const SampleArgs a, const int stride) {
+// Bins of a token: of its distance from the largest logit, 1/64 of its octave each from
+// 2^-12 on, for counts (a distance of any size lies in one of them); of its weight, 1/64
+// of an octave each, for masses.  The last one takes what lies beyond.
+constexpr int kFirstBin = (127 - 12) << 6, kBinShift = 17;
+__device__ __forceinline__ int distance_bin(float l, float top) {
+  const float d = l == top ? 0.f : top - l;
+  const int k = static_cast<int>(__float_as_uint(d) >> kBinShift) - kFirstBin;
+  return min(max(k, 0), kBins - 1);
+}
+// The least logit that may be in bin `last` or one before (or a little less).
+__device__ __forceinline__ float distance_cut(int last, float top) {
+  if (last == kBins - 1 || top == INFINITY) return top == INFINITY ? top : -FLT_MAX;
+  const float d = __uint_as_float(static_cast<uint32_t>(last + 1 + kFirstBin) << kBinShift);
+  return fmaxf(nextafterf(top - d, -INFINITY), -FLT_MAX);
+}
+constexpr float kRound = 0x1.8p23f;  // + x: its last bits are x's nearest integer
+// The logit of `step` 64ths of an octave, rounded towards `to`.
+__device__ __forceinline__ float step_value(float step, float to, const Scale& s) {
+  if (!(s.c_hi > 0.f)) return to;
+  const float d = __fdiv_rn((kMagic - s.magic) - step * (1.f / 64), s.c_hi);
+  return nextafterf(__fadd_rn(s.base, nextafterf(d, to)), to);
+}
+// A bin's mass is kept as what its tokens weigh beside the bin's middle, in 1 / kPerToken:
+// the weight there is 1 within 0.55%, and rounded to that, so sums are right to half of it.
+constexpr int kPerToken = 1024;  // (2^21 tokens: below 2^32)
+__device__ __forceinline__ uint32_t beside_middle(float l, const Scale& s, int& bin) {
+  const float d = fmaxf(__fsub_rn(l, s.base), s.least);
+  // -64 log2 of the weight
+  const float x = __fmul_rn(64.f, __fmaf_rn(d, -s.c_hi, kMagic - s.magic));
+  const float k = __fadd_rn(x, kRound);
+  bin = min(max(__float_as_int(k) - __float_as_int(kRound), 0), kBins - 1);
+  const float n = __fmaf_rn(__fsub_rn(x, __fsub_rn(k, kRound)), -kPerToken * 0.010830424696f,
+                            kRound + kPerToken);
+  return static_cast<uint32_t>(__float_as_int(n) - __float_as_int(kRound));
+}
+
+template <class T>
+__global__ void __launch_bounds__(kThreads, MINB) sample_kernel(const SampleArgs a) {
   using R = Row<T>;
   constexpr int kPer = R::kPer;
-  // kList * 8 bytes at least; HELD: this CTA's part of the row, `stride` units a lane (an
-  // odd number, so that lanes read their units without bank conflicts)
-  extern __shared__ __align__(16) uint4 held[];
   __shared__ Shared sh;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   Cluster cl{sh, 0, 1, 0};
@@ -364,34 +419,36 @@ __global__ void __launch_bounds__(kThreads, 2)
     return static_cast<int>(static_cast<uint32_t>(slots * w) / static_cast<uint32_t>(warps));
   };
   const int s0 = first_slot(me), each = first_slot(me + 1) - s0;
-  const int u0 = s0 * 32;  // the warp's first unit; lane l has each of them from u0 + l * each
-  uint4* mine = held + (warp * 32 + lane) * stride;
-  const auto get = [&](int i, float (&v)[kPer]) {
-    if constexpr (HELD) {
-      R::floats(mine[i], v);
-    } else {
-      R::floats(row.load(u0 + lane * each + i), v);
+  const int u0 = s0 * 32 + lane;  // the lane's first unit; one in each slot
+  const bool inner = row.whole(s0 * 32) && row.whole((s0 + each) * 32 - 1);
+
+  // f(number in the batch, the unit's column, its logits) for the lane's units, a batch of
+  // them loaded at once.
+  const auto stream = [&](auto ahead, const auto& f) {
+    constexpr int kAhead = decltype(ahead)::value;
+    for (int s = 0; s < each; s += kAhead) {
+      uint4 r[kAhead];
+      const int u = u0 + s * 32;
+      if (inner && s + kAhead <= each) {
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) r[i] = row.aligned[u + i * 32];
+      } else {
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i)
+          if (s + i < each) r[i] = row.load(u + i * 32);
+      }
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        if (s + i >= each) break;
+        float v[kPer];
+        R::floats(r[i], v);
+        f(i, row.first(u + i * 32), v);
+      }
     }
   };
+  using Wide = std::integral_constant<int, AHEAD1>;  // where registers allow it
+  using Few = std::integral_constant<int, AHEAD2>;
 
-  if constexpr (HELD) {
-    // in the order of memory, all of it on its way at once
-    int to = lane / max(each, 1), at = lane - to * each;
-    const int step = 32 / max(each, 1), rest = 32 - step * each;
-    for (int s = 0; s < each; ++s) {
-      const int u = u0 + s * 32 + lane;
-      uint4* dst = held + (warp * 32 + to) * stride + at;
-      if (row.whole(u))
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)),
-                     "l"(row.p + row.first(u))
-                     : "memory");
-      else *dst = row.load(u);
-      to += step;
-      at += rest;
-      if (at >= each) at -= each, ++to;
-    }
-    asm volatile("cp.async.commit_group;" ::: "memory");
-  }
   const float T0 = a.temperature ? a.temperature[b] : 1.f;
   const int k = a.top_k ? a.top_k[b] : 0;
   const float p = a.top_p ? a.top_p[b] : 1.f;
@@ -402,30 +459,33 @@ __global__ void __launch_bounds__(kThreads, 2)
     sh.table[lane] = kPow2[lane];
     if (lane == 0) {
       sh.listed = 0;
-      sh.cut = -FLT_MAX;
       sh.inverse = inverse_of(greedy ? 1.f : T0);
-      // one lane: 64-bit operations are slow
-      if (min_p > 0.f) {
-        const double d = static_cast<double>(T0) * log(static_cast<double>(fminf(min_p, 1.f)));
-        sh.log_min_p.x = static_cast<float>(d);
-        sh.log_min_p.y = static_cast<float>(d - static_cast<double>(sh.log_min_p.x));
+    }
+    __syncwarp();
+    if (min_p > 0.f) {
+      // T ln(min_p) in two floats: FP32's logarithm, corrected by what its exponential
+      // leaves of min_p
+      const float m = fminf(min_p, 1.f), y = logf(m);
+      float rest = 0.f;
+      if (m > 0x1p-30f) {
+        const uint64_t w = weight(y, make_scale(0.f, inverse_of(1.f)), sh.table);
+        rest = static_cast<float>(static_cast<int64_t>(__float2ull_rn(m * 0x1p42f) - w)) /
+               static_cast<float>(w);
       }
+      const float hi = T0 * y;
+      if (lane == 0) sh.log_min_p = make_float2(hi, fmaf(T0, y, -hi) + T0 * rest);
     }
   }
   for (int i = threadIdx.x; i < kBins; i += kThreads) sh.bins[i] = 0;
-  if constexpr (HELD) {
-    asm volatile("cp.async.wait_group 0;" ::: "memory");
-    __syncwarp();
-  }
 
-  // The largest logit (NaN is passed over): the lane's, the warps', the row's.
-  float lane_top = -INFINITY;
-  for (int i = 0; i < each; ++i) {
-    float v[kPer];
-    get(i, v);
+  // The largest logit (NaN is passed over): of every fourth of the lane's units, the
+  // lane's, the warp's, the row's.
+  float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+  stream(Wide{}, [&](int i, int, const float (&v)[kPer]) {
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) lane_top = fmaxf(lane_top, v[j]);
-  }
+    for (int j = 0; j < kPer; ++j) tops[i % 4] = fmaxf(tops[i % 4], v[j]);
+  });
+  const float lane_top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
   const auto warp_max = [](float v) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
@@ -434,8 +494,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   float top = warp_max(lane_top);
   cluster_wait();
   cl.share(0, __float_as_uint(top));
-  const uint32_t* warp_tops = sh.count[cl.phase];
-  for (int i = lane; i < warps; i += 32) top = fmaxf(top, __uint_as_float(warp_tops[i]));
+  for (int i = lane; i < warps; i += 32) top = fmaxf(top, __uint_as_float(sh.count[cl.phase][i]));
   top = warp_max(top);
   if (top == -INFINITY) {  // nothing to pick from
     if (me == 0 && lane == 0) a.out[b] = -1;
@@ -461,32 +520,64 @@ __global__ void __launch_bounds__(kThreads, 2)
   };
   const uint64_t part_u = __float2ull_rz(fminf(fmaxf(u, 0.f), 0x1.fffffep-1f) * 0x1p64f);
 
-  // The tokens at or above x: how many, and (with `mass`) their mass.
-  const auto at_least = [&](float x, bool mass) {
-    uint32_t n = 0, wa = 0, wb = 0;
-    for (int i = 0; i < each; ++i) {
-      float v[kPer];
-      get(i, v);
-      bool some = false;
-#pragma unroll
-      for (int j = 0; j < kPer; ++j) some = some || v[j] >= x;
-      if (!__any_sync(0xffffffffu, some)) continue;
-#pragma unroll
-      for (int j = 0; j < kPer; ++j) {
-        const bool in = v[j] >= x;
-        if (mass) {
-          uint32_t ka, kb;
-          weigh(v[j], scale, sh.table, ka, kb);
-          wa += in ? ka : 0u;
-          wb += in ? kb : 0u;
-        }
-        n += in;
-      }
-    }
-    return cl.total(warp_sum_u64(mass ? mass_of(wa, wb, n) : 0), __reduce_add_sync(0xffffffffu, n));
-  };
   float t = -FLT_MAX;
   uint32_t ties = UINT_MAX;
+
+  // The mass of the lane's tokens from x on.
+  const auto weigh_from = [&](float x) {
+    uint64_t mass = 0;
+    uint32_t wa = 0, wb = 0, n = 0;
+    const auto add = [&](const float (&v)[kPer]) {
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) {
+        uint32_t ka, kb;
+        weigh(v[j], scale, sh.table, ka, kb);
+        wa += ka;
+        wb += kb;
+      }
+      n += kPer;
+      if (n >= 512) {  // the sums of so many fit into 32 bits
+        mass += mass_of(wa, wb, n);
+        wa = wb = n = 0;
+      }
+    };
+    if (x == -FLT_MAX) {
+      stream(Few{}, [&](int, int, const float (&v)[kPer]) { add(v); });
+    } else if (__any_sync(0xffffffffu, lane_top >= x)) {
+      stream(Few{}, [&](int, int, const float (&v)[kPer]) {
+        float w[kPer];
+        bool some = false;
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) {
+          some = some || v[j] >= x;
+          w[j] = v[j] >= x ? v[j] : -INFINITY;
+        }
+        if (__any_sync(0xffffffffu, some)) add(w);
+      });
+    }
+    return mass + mass_of(wa, wb, n);
+  };
+  // The mass above t, or with all ties from it on, and the number of those; to every CTA.
+  const auto share_kept = [&]() {
+    const bool all_ties = ties == UINT_MAX;
+    const uint64_t mass = weigh_from(all_ties ? t : nextafterf(t, INFINITY));
+    uint32_t n = 0;
+    if (!all_ties && __any_sync(0xffffffffu, lane_top >= t))
+      stream(Wide{}, [&](int, int, const float (&v)[kPer]) {
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) n += v[j] == t;
+      });
+    cl.share(warp_sum_u64(mass), __reduce_add_sync(0xffffffffu, n));
+  };
+  const auto count_from = [&](float x) {
+    uint32_t n = 0;
+    if (__any_sync(0xffffffffu, lane_top >= x))
+      stream(Wide{}, [&](int, int, const float (&v)[kPer]) {
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) n += v[j] >= x;
+      });
+    return n;
+  };
   // Narrows t and ties to the prefix that makes `target` (tokens, or mass): halves the
   // range of logits from t on, a pass over the row and a barrier each.  For any row; the
   // lists below are faster where they are long enough.
@@ -495,7 +586,10 @@ __global__ void __launch_bounds__(kThreads, 2)
     uint64_t above = 0;
     while (lo < hi) {
       const int mid = static_cast<int>(lo + (static_cast<int64_t>(hi) - lo + 1) / 2);
-      const Sum s = at_least(value_of<T>(mid), mass);
+      const float x = value_of<T>(mid);
+      const uint64_t m = mass ? weigh_from(x) : 0;
+      const uint32_t n = mass ? 0 : count_from(x);
+      const Sum s = cl.total(warp_sum_u64(m), __reduce_add_sync(0xffffffffu, n));
       const uint64_t have = mass ? s.mass : s.count;
       if (have >= target) {
         lo = mid;
@@ -517,42 +611,91 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
   };
 
-  // Puts the tokens with in(l) on the CTA's list, one that is full counts on; returns
-  // the warp's number of them.
-  const auto list_tokens = [&](const auto& in) {
-    uint32_t n = 0;
-    for (int i = 0; i < each; ++i) {
-      float v[kPer];
-      get(i, v);
-      uint32_t which = 0;
-#pragma unroll
-      for (int j = 0; j < kPer; ++j) which |= in(v[j]) ? 1u << j : 0u;
-      if (!__any_sync(0xffffffffu, which != 0)) continue;
-      const uint32_t c = __popc(which), upto = warp_scan(c);
-      const uint32_t all = __shfl_sync(0xffffffffu, upto, 31);
-      uint32_t at = 0;
-      if (lane == 31) at = atomicAdd(&sh.listed, all);
-      at = __shfl_sync(0xffffffffu, at, 31) + upto - c;
-      n += all;
-#pragma unroll
-      for (int j = 0; j < kPer; ++j) {
-        if (!(which >> j & 1)) continue;
-        const uint32_t id = static_cast<uint32_t>(row.first(u0 + lane * each + i) + j);
-        const uint32_t key = static_cast<uint32_t>(key_of<float>(v[j] + 0.f)) ^ 0x80000000u;
-        if (at < kList) sh.list[at] = static_cast<uint64_t>(key) << 32 | (id ^ 0xffffffffu);
-        ++at;
+  // The sums of this CTA's bins by groups, to every CTA (before a barrier).
+  const auto bin_amount = [&](int i, uint32_t n, bool mass) {
+    return mass ? static_cast<uint64_t>(static_cast<float>(n) *
+                                        exp2f(42.f - i * (1.f / 64) - __log2f(kPerToken)))
+                : static_cast<uint64_t>(n);
+  };
+  const auto share_groups = [&](bool mass) {
+    __syncthreads();
+    for (int g = warp; g < kGroups; g += kWarps) {
+      uint64_t m = 0;
+      for (int i = lane; i < kGroupBins; i += 32) {
+        const uint32_t n = sh.bins[g * kGroupBins + i];
+        if (n) m += bin_amount(g * kGroupBins + i, n, mass);
       }
+      m = warp_sum_u64(m);
+      if (lane < cl.ctas) st_cluster_u64(mapa_shared(smem_u32(&sh.group[cl.rank][g]), lane), m);
     }
-    return n;
+  };
+  // The bins at which the row's sum reaches `lower` and `target` (after that barrier; the
+  // last one if none).  Bins keep until the next barrier.
+  const auto find_bins = [&](uint64_t lower, uint64_t target, bool mass) {
+    if (warp < 2) {
+      const uint64_t to = warp == 0 ? lower : target;
+      uint64_t m = 0;
+      for (int r = 0; r < cl.ctas; ++r) m += sh.group[r][lane];
+      uint64_t upto = warp_scan(m);
+      uint32_t past = __ballot_sync(0xffffffffu, upto >= to);
+      int found = kBins - 1;
+      if (past) {
+        const int g = __ffs(past) - 1;
+        const uint64_t before = __shfl_sync(0xffffffffu, upto - m, g);
+        // two neighbouring bins a lane, every CTA's at once
+        const int i = g * kGroupBins + 2 * lane;
+        uint64_t n[kMaxCluster];
+#pragma unroll
+        for (int r = 0; r < kMaxCluster; ++r)
+          n[r] = r < cl.ctas ? ld_cluster_u64(mapa_shared(smem_u32(&sh.bins[i]), r)) : 0;
+        uint64_t m0 = 0, m1 = 0;
+#pragma unroll
+        for (int r = 0; r < kMaxCluster; ++r) {
+          m0 += bin_amount(i, static_cast<uint32_t>(n[r]), mass);
+          m1 += bin_amount(i + 1, static_cast<uint32_t>(n[r] >> 32), mass);
+        }
+        upto = before + warp_scan(m0 + m1);
+        past = __ballot_sync(0xffffffffu, upto >= to);
+        const int who = past ? __ffs(past) - 1 : 31;
+        found = g * kGroupBins + 2 * who +
+                (__shfl_sync(0xffffffffu, static_cast<int>(upto - m1 >= to), who) ? 0 : 1);
+      }
+      if (lane == 0) sh.found[warp] = found;
+    }
+    __syncthreads();
+    return make_int2(sh.found[0], sh.found[1]);
+  };
+
+  // Puts the unit's tokens that are in `which` on the CTA's list; one that is full counts
+  // on.  All lanes of a warp call it.
+  const auto list_unit = [&](int c, const float (&v)[kPer], uint32_t which) {
+    if (!__any_sync(0xffffffffu, which != 0)) return;
+    const uint32_t n = __popc(which), upto = warp_scan(n);
+    uint32_t at = 0;
+    if (lane == 31) at = atomicAdd(&sh.listed, upto);
+    at = __shfl_sync(0xffffffffu, at, 31) + upto - n;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      if (!(which >> j & 1)) continue;
+      const uint32_t key = static_cast<uint32_t>(key_of<float>(v[j] + 0.f)) ^ 0x80000000u;
+      if (at < kList)
+        sh.list[at] = static_cast<uint64_t>(key) << 32 | (static_cast<uint32_t>(c + j) ^ 0xffffffffu);
+      ++at;
+    }
   };
   const auto listed_value = [](uint64_t e) {
     return value_of<float>(static_cast<int>(static_cast<uint32_t>(e >> 32) ^ 0x80000000u));
+  };
+  // Shares the length of this CTA's list (and a warp's mass); the row's.
+  const auto share_list = [&](uint64_t mass) {
+    __syncthreads();
+    return cl.total(mass, warp == 0 ? sh.listed : 0);
   };
   // Every CTA's list into `work`, n tokens in all, padded to list_size(n).
   const auto pull_lists = [&](uint32_t n) {
     uint32_t at = 0;
     for (int r = 0; r < cl.ctas; ++r) {
-      const uint32_t c = cl.sum(r * kWarps, (r + 1) * kWarps).count;
+      const uint32_t c = sh.count[cl.phase][r * kWarps];
       for (uint32_t i = threadIdx.x; i < c; i += kThreads)
         sh.work[at + i] = ld_cluster_u64(mapa_shared(smem_u32(&sh.list[i]), r));
       at += c;
@@ -561,28 +704,44 @@ __global__ void __launch_bounds__(kThreads, 2)
       sh.work[i] = 0;
   };
 
-  // --- top-k of few: a list of everything that can be among the first k, which the
-  // cluster's first CTA then has to itself.
-  constexpr int kFew = kMaxWarps * 7 / 8;
-  if (by_k && k <= kFew && k <= warps * 7 / 8) {
-    // the k-th largest of the warps' largest: k tokens are at or above it
-    const int v = threadIdx.x >> 2;
-    uint32_t larger = 0;
-    if (v < warps) {
-      const float x = __uint_as_float(warp_tops[v]);
-      for (int i = threadIdx.x & 3; i < warps; i += 4) {
-        const float y = __uint_as_float(warp_tops[i]);
-        larger += y > x || (y == x && i < v);
+  // --- top-k: a list of everything that can be among the first k, which the cluster's
+  // first CTA then has to itself.  k of the largest logits of quarters of lanes are in the
+  // bins up to the one that holds the k-th, so are k tokens; other quarters have none there.
+  constexpr int kFewLanes = 3;
+  if (by_k && k <= kList / 2) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (tops[i] > -INFINITY) atomicAdd(&sh.bins[distance_bin(tops[i], top)], 1);
+    share_groups(false);
+    cluster_arrive();
+    cluster_wait();
+    const float cut = distance_cut(find_bins(k, k, false).y, top);
+    const uint32_t flagged = __ballot_sync(0xffffffffu, lane_top >= cut);
+    const auto in = [&](const float (&v)[kPer]) {
+      uint32_t which = 0;
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) which |= v[j] >= cut ? 1u << j : 0u;
+      return which;
+    };
+    if (__popc(flagged) > kFewLanes) {
+      stream(Wide{}, [&](int, int c, const float (&v)[kPer]) { list_unit(c, v, in(v)); });
+    } else {
+      for (uint32_t some = flagged; some; some &= some - 1) {
+        // one of those lanes' units, a lane each
+        const int who = __ffs(some) - 1;
+        for (int s = 0; s < each; s += 32) {
+          const int un = u0 - lane + who + (s + lane) * 32;
+          float v[kPer];
+          uint32_t which = 0;
+          if (s + lane < each) {
+            R::floats(row.load(un), v);
+            which = in(v);
+          }
+          list_unit(row.first(un), v, which);
+        }
       }
     }
-    larger += __shfl_xor_sync(0xffffffffu, larger, 1);
-    larger += __shfl_xor_sync(0xffffffffu, larger, 2);
-    if (v < warps && larger == static_cast<uint32_t>(k - 1) && (threadIdx.x & 3) == 0)
-      sh.cut = fmaxf(__uint_as_float(warp_tops[v]), -FLT_MAX);
-    __syncthreads();
-    const float cut = sh.cut;
-    const uint32_t n = list_tokens([&](float l) { return l >= cut; });
-    const uint32_t N = cl.total(0, n).count;
+    const uint32_t N = share_list(0).count;
     if (N <= kList) {
       if (cl.rank == 0) pull_lists(N);
       cluster_arrive();  // the lists have been read
@@ -591,41 +750,37 @@ __global__ void __launch_bounds__(kThreads, 2)
         return;
       }
       __syncthreads();
-      const int size = list_size(N), threads = size / 2;
-      auto* weights = reinterpret_cast<uint64_t*>(held);  // (the row is not needed any more)
+      const int size = list_size(N), threads = min(size / 2, kThreads);
       if (threadIdx.x < threads) {
-        sort_list(sh.work, size);
+        sort_list(sh.work, size, threads);
         uint32_t keep = min(N, static_cast<uint32_t>(k));
         for (uint32_t i = threadIdx.x; i < keep; i += threads)
-          weights[i] = weight(listed_value(sh.work[i]), scale, sh.table);
+          sh.weights[i] = weight(listed_value(sh.work[i]), scale, sh.table);
         asm volatile("bar.sync 1, %0;" ::"r"(threads) : "memory");
-        const uint64_t all = scan_list(weights, keep, threads, sh.part);
+        const uint64_t all = scan_list(sh.weights, keep, threads, sh.part);
         // p and min_p keep a prefix of these
         const uint64_t target = by_p ? target_p(all) : UINT64_MAX;
-        uint32_t in = 0;
+        uint32_t in_all = 0;
         for (uint32_t i = threadIdx.x; i < keep; i += threads)
-          in += i == 0 || (weights[i - 1] < target && listed_value(sh.work[i]) >= least);
-        in = __reduce_add_sync(0xffffffffu, in);
-        if (lane == 0) sh.part[warp] = in;
+          in_all += i == 0 || (sh.weights[i - 1] < target && listed_value(sh.work[i]) >= least);
+        in_all = __reduce_add_sync(0xffffffffu, in_all);
+        if (lane == 0) sh.part[warp] = in_all;
         asm volatile("bar.sync 1, %0;" ::"r"(threads) : "memory");
         keep = 0;
         for (int w = 0; w < threads / 32; ++w) keep += static_cast<uint32_t>(sh.part[w]);
-        const uint64_t kept = weights[keep - 1];
+        const uint64_t kept = sh.weights[keep - 1];
         asm volatile("bar.sync 1, %0;" ::"r"(threads) : "memory");
         // by id: ~id << 32 | place, the larger first
-        const int size2 = list_size(keep);
-        for (int i = threadIdx.x; i < size2; i += threads) {
-          const uint64_t e = i < static_cast<int>(keep) ? sh.work[i] << 32 | i : 0;
-          sh.list[i] = e;
-        }
+        const int size2 = list_size(keep), threads2 = min(size2 / 2, kThreads);
+        for (int i = threadIdx.x; i < size2; i += threads)
+          sh.list[i] = i < static_cast<int>(keep) ? sh.work[i] << 32 | i : 0;
         asm volatile("bar.sync 1, %0;" ::"r"(threads) : "memory");
-        if (threadIdx.x < size2 / 2) {
-          const int threads2 = size2 / 2;
-          sort_list(sh.list, size2);
+        if (threadIdx.x < threads2) {
+          sort_list(sh.list, size2, threads2);
           uint64_t* by_id = sh.work;
           for (uint32_t i = threadIdx.x; i < keep; i += threads2) {
             const uint32_t at = static_cast<uint32_t>(sh.list[i]);
-            by_id[i] = weights[at] - (at ? weights[at - 1] : 0);
+            by_id[i] = sh.weights[at] - (at ? sh.weights[at - 1] : 0);
           }
           asm volatile("bar.sync 1, %0;" ::"r"(threads2) : "memory");
           scan_list(by_id, keep, threads2, sh.part);
@@ -644,161 +799,255 @@ __global__ void __launch_bounds__(kThreads, 2)
     t = top;
     ties = 1;
   }
-
-  // What t and ties keep: the lane's mass above t (with `ties` all ones: from t on) and its
-  // tokens equal to t, to every CTA by warps.
-  uint64_t lane_mass = 0;
-  uint32_t lane_ties = 0;
-  const auto weigh_kept = [&]() {
-    uint32_t n = 0, wa = 0, wb = 0;
-    lane_ties = 0;
-    const bool some_ties = ties != UINT_MAX;
-    for (int i = 0; i < each; ++i) {
-      float v[kPer];
-      get(i, v);
-      bool some = false;
+  if (by_k) halve(static_cast<uint64_t>(k), false);
+  // --- top-p over many tokens: their mass, and a histogram by weight that says near which
+  // one the border lies; a list of that bin's tokens then gives it.
+  bool shared = false;  // every CTA has what t and ties keep, by warps
+  if (by_p) {
+    if (by_k) {  // (the bins have been used)
+      for (int i = threadIdx.x; i < kBins; i += kThreads) sh.bins[i] = 0;
+      if (threadIdx.x == 0) sh.listed = 0;
+      __syncthreads();
+    }
+    if (__any_sync(0xffffffffu, lane_top >= t))
+      stream(Few{}, [&](int, int, const float (&v)[kPer]) {
 #pragma unroll
-      for (int j = 0; j < kPer; ++j) some = some || v[j] >= t;
-      if (!__any_sync(0xffffffffu, some)) continue;
+        for (int j = 0; j < kPer; ++j) {
+          int bin;
+          const uint32_t n = beside_middle(v[j], scale, bin);
+          if (v[j] >= t) atomicAdd(&sh.bins[bin], n);
+        }
+      });
+    share_groups(true);
+    share_kept();
+    const Sum s = cl.sum(0, warps);
+    const uint64_t target = target_p(s.mass + weight(t, scale, sh.table) * min(s.count, ties));
+    // the bins' sums are off by 1 / (2 kPerToken) of them, and FP32's rounding
+    const uint64_t slack = target / (2 * kPerToken - 128) + kBins;
+    const int2 bins = find_bins(target - min(slack, target - 1), target + slack, true);
+    bool done = false;
+    if (bins.y < kBins - 1) {
+      uint64_t mass = 0;
+      // logits at and a little beyond the ends of these bins
+      const float lo = fmaxf(step_value(bins.y + 0.51f, -INFINITY, scale), t);
+      const float hi = bins.x == 0 ? INFINITY : step_value(bins.x - 0.51f, INFINITY, scale);
+      if (__any_sync(0xffffffffu, lane_top >= lo)) {
+        uint32_t wa = 0, wb = 0, n = 0;
+        stream(Few{}, [&](int, int c, const float (&v)[kPer]) {
+          uint32_t at = 0;
+          float w[kPer];
+          bool above = false;
 #pragma unroll
-      for (int j = 0; j < kPer; ++j) {
-        const bool tie = some_ties && v[j] == t, in = v[j] >= t && !tie;
-        uint32_t ka, kb;
-        weigh(v[j], scale, sh.table, ka, kb);
-        wa += in ? ka : 0u;
-        wb += in ? kb : 0u;
-        n += in;
-        lane_ties += tie;
+          for (int j = 0; j < kPer; ++j) {
+            at |= v[j] >= lo && v[j] <= hi ? 1u << j : 0u;
+            w[j] = v[j] > hi ? v[j] : -INFINITY;
+            above = above || v[j] > hi;
+          }
+          list_unit(c, v, at);
+          if (!__any_sync(0xffffffffu, above)) return;
+#pragma unroll
+          for (int j = 0; j < kPer; ++j) {
+            uint32_t ka, kb;
+            weigh(w[j], scale, sh.table, ka, kb);
+            wa += ka;
+            wb += kb;
+          }
+          n += kPer;
+          if (n >= 512) {
+            mass += mass_of(wa, wb, n);
+            wa = wb = n = 0;
+          }
+        });
+        mass += mass_of(wa, wb, n);
+      }
+      const Sum in = share_list(warp_sum_u64(mass));
+      if (in.count <= kList) {
+        pull_lists(in.count);
+        if (threadIdx.x == 0) sh.found[0] = 0;
+        cluster_arrive();
+        cluster_wait();
+        const int size = list_size(in.count), threads = min(size / 2, kThreads);
+        if (threadIdx.x < threads) {
+          sort_list(sh.work, size, threads);
+          uint64_t* upto = sh.list;  // (all have read it)
+          for (int i = threadIdx.x; i < static_cast<int>(in.count); i += threads)
+            upto[i] = weight(listed_value(sh.work[i]), scale, sh.table);
+          asm volatile("bar.sync 1, %0;" ::"r"(threads) : "memory");
+          scan_list(upto, in.count, threads, sh.part);
+          for (int i = threadIdx.x; i < static_cast<int>(in.count); i += threads)
+            if (in.mass + upto[i] >= target &&
+                (i ? in.mass + upto[i - 1] : in.mass) < target) {  // the border: at most one
+              int equal = i;
+              while (equal > 0 && sh.work[equal - 1] >> 32 == sh.work[i] >> 32) --equal;
+              sh.rank = static_cast<uint32_t>(i - equal + 1);
+              sh.cut = listed_value(sh.work[i]);
+              sh.found[0] = 1;
+            }
+        }
+        // every warp's mass above the border's logit and tokens equal to it, as
+        // share_kept would leave them
+        if (threadIdx.x < warps) sh.count[cl.phase][threadIdx.x] = 0;
+        __syncthreads();
+        done = sh.found[0] == 1;
+        if (done) {
+          t = sh.cut;
+          ties = sh.rank;
+          for (uint32_t i = threadIdx.x; i < in.count; i += kThreads) {
+            const float l = listed_value(sh.work[i]);
+            if (!(l >= t)) continue;
+            const int id = static_cast<int>(~static_cast<uint32_t>(sh.work[i]));
+            const int slot = (id + row.shift) / (32 * kPer);
+            const int w = ((slot + 1) * warps - 1) / slots;  // first_slot(w) <= slot
+            if (l > t)
+              atomicAdd(reinterpret_cast<unsigned long long*>(&sh.mass[cl.phase][w]),
+                        static_cast<unsigned long long>(weight(l, scale, sh.table)));
+            else atomicAdd(&sh.count[cl.phase][w], 1);
+          }
+          __syncthreads();
+        }
       }
     }
-    lane_mass = mass_of(wa, wb, n);
-  };
-
-  if (by_k) halve(static_cast<uint64_t>(k), false);
-  if (by_p) {
-    weigh_kept();
-    const Sum s = cl.total(warp_sum_u64(lane_mass), __reduce_add_sync(0xffffffffu, lane_ties));
-    const uint64_t wt = weight(t, scale, sh.table);
-    halve(target_p(s.mass + wt * min(s.count, ties)), true);
+    shared = done;
+    if (!done) halve(target, true);
   }
   if (least > t) {
     t = least;
     ties = UINT_MAX;
+    shared = false;
   }
-  weigh_kept();
-  // The lanes' parts for the warp below; the warps' to every CTA.
-  uint64_t* lane_masses = sh.work;
-  uint32_t* lane_tie_counts = reinterpret_cast<uint32_t*>(sh.work + kThreads);
-  lane_masses[threadIdx.x] = lane_mass;
-  lane_tie_counts[threadIdx.x] = lane_ties;
-  cl.share(warp_sum_u64(lane_mass), __reduce_add_sync(0xffffffffu, lane_ties));
-  // One warp of each CTA goes on: first, which warp has the token; four consecutive
-  // entries a lane.
-  if (warp != 0) return;
+  if (!shared) share_kept();
   const uint64_t wt = weight(t, scale, sh.table);
-  constexpr int kEach = kMaxWarps / 32;
-  uint64_t m[kEach], upto = 0;
-  uint32_t e_at[kEach], ahead = 0;
+  if (warp == 0) {
+    // which warp has the token: four consecutive entries a lane
+    constexpr int kEach = kMaxWarps / 32;
+    uint64_t m[kEach], upto = 0;
+    uint32_t e_at[kEach], ahead = 0;
 #pragma unroll
-  for (int i = 0; i < kEach; ++i) {
-    const int w = lane * kEach + i;
-    m[i] = w < warps ? sh.mass[cl.phase][w] : 0;
-    e_at[i] = w < warps ? sh.count[cl.phase][w] : 0;
-    ahead += e_at[i];
-  }
-  ahead = warp_scan(ahead) - ahead;  // ties of the lanes before
+    for (int i = 0; i < kEach; ++i) {
+      const int w = lane * kEach + i;
+      m[i] = w < warps ? sh.mass[cl.phase][w] : 0;
+      e_at[i] = w < warps ? sh.count[cl.phase][w] : 0;
+      ahead += e_at[i];
+    }
+    ahead = warp_scan(ahead) - ahead;  // ties of the lanes before
 #pragma unroll
-  for (int i = 0; i < kEach; ++i) {
-    const uint32_t e = e_at[i];
-    e_at[i] = ahead;
-    m[i] += wt * min(e, ties > ahead ? ties - ahead : 0u);
-    upto += m[i];
-    ahead += e;
-  }
-  const uint64_t lane_sum = upto;
-  upto = warp_scan(upto);
-  const uint64_t pick = __umul64hi(part_u, __shfl_sync(0xffffffffu, upto, 31));
-  const int owner = __ffs(__ballot_sync(0xffffffffu, upto > pick)) - 1;
-  upto -= lane_sum;
-  int which = 0;
-  uint64_t before = upto;
-  uint32_t rank = e_at[0];
+    for (int i = 0; i < kEach; ++i) {
+      const uint32_t e = e_at[i];
+      e_at[i] = ahead;
+      m[i] += wt * min(e, ties > ahead ? ties - ahead : 0u);
+      upto += m[i];
+      ahead += e;
+    }
+    const uint64_t lane_sum = upto;
+    upto = warp_scan(upto);
+    const uint64_t pick = __umul64hi(part_u, __shfl_sync(0xffffffffu, upto, 31));
+    const int owner = __ffs(__ballot_sync(0xffffffffu, upto > pick)) - 1;
+    uint64_t before = upto - lane_sum;
+    int which = 0;
+    uint32_t rank = e_at[0];
 #pragma unroll
-  for (int i = 0; i + 1 < kEach; ++i) {
-    if (which == i && before + m[i] <= pick) {
-      before += m[i];
-      which = i + 1;
-      rank = e_at[i + 1];
+    for (int i = 0; i + 1 < kEach; ++i) {
+      if (which == i && before + m[i] <= pick) {
+        before += m[i];
+        which = i + 1;
+        rank = e_at[i + 1];
+      }
+    }
+    if (lane == owner) {
+      sh.before = pick - before;  // what is left to pick from there on
+      sh.rank = rank;
+      sh.found[0] = owner * kEach + which - cl.rank * kWarps;
     }
   }
-  before = __shfl_sync(0xffffffffu, before, owner);
-  rank = __shfl_sync(0xffffffffu, rank, owner);
-  const int w = owner * kEach + __shfl_sync(0xffffffffu, which, owner) - cl.rank * kWarps;
+  __syncthreads();
+  const int w = sh.found[0];
   if (w < 0 || w >= kWarps) return;  // another CTA's
-  // The lane that has it, then its tokens, which are consecutive, 32 at a time.
-  lane_mass = lane_masses[w * 32 + lane];
-  lane_ties = lane_tie_counts[w * 32 + lane];
-  rank += warp_scan(lane_ties) - lane_ties;
-  lane_mass += wt * min(lane_ties, ties > rank ? ties - rank : 0u);
-  upto = before + warp_scan(lane_mass);
-  const int who = __ffs(__ballot_sync(0xffffffffu, upto > pick)) - 1;
-  before = __shfl_sync(0xffffffffu, upto - lane_mass, who);
-  rank = __shfl_sync(0xffffffffu, rank, who);
-  const int first = first_slot(cl.rank * kWarps + w);
-  const int count = (first_slot(cl.rank * kWarps + w + 1) - first) * kPer;
-  const int c0 = row.first(first * 32) + who * count;
-  const T* tokens = reinterpret_cast<const T*>(held + (w * 32 + who) * stride);
-  for (int j0 = 0; j0 < count; j0 += 32) {
-    const int j = j0 + lane;
-    float l = -INFINITY;
-    if (j < count) {
-      if constexpr (!HELD) l = row.at(c0 + j);
-      else if constexpr (sizeof(T) == 4) l = tokens[j];
-      else l = __bfloat162float(tokens[j]);
+  // The warp's slots, a warp of this CTA each: their masses above t, and ties.
+  const int first = first_slot(cl.rank * kWarps + w), count = first_slot(cl.rank * kWarps + w + 1) - first;
+  for (int s = warp; s < count; s += kWarps) {
+    float v[kPer];
+    R::floats(row.load((first + s) * 32 + lane), v);
+    uint32_t wa = 0, wb = 0, e = 0;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const bool tie = ties != UINT_MAX && v[j] == t;
+      e += tie;
+      if (!(v[j] >= t) || tie) v[j] = -INFINITY;
     }
-    const uint32_t equal = __ballot_sync(0xffffffffu, l == t);
-    const uint32_t nth = rank + __popc(equal & ((1u << lane) - 1));
-    const uint64_t x = l > t || (l == t && nth < ties) ? weight(l, scale, sh.table) : 0;
-    const uint64_t sum = warp_scan(x);
-    const uint32_t past = __ballot_sync(0xffffffffu, before + sum > pick);
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      uint32_t ka, kb;
+      weigh(v[j], scale, sh.table, ka, kb);
+      wa += ka;
+      wb += kb;
+    }
+    const uint64_t mass = warp_sum_u64(mass_of(wa, wb, kPer));
+    e = __reduce_add_sync(0xffffffffu, e);
+    if (lane == 0) {
+      sh.slot.mass[s] = mass;
+      sh.slot.ties[s] = e;
+    }
+  }
+  __syncthreads();
+  if (warp != 0) return;
+  uint64_t pick = sh.before;
+  uint32_t rank = sh.rank;
+  for (int s = 0; s < count; s += 32) {
+    const uint32_t e = s + lane < count ? sh.slot.ties[s + lane] : 0;
+    const uint32_t ahead = rank + warp_scan(e) - e;
+    const uint64_t m = (s + lane < count ? sh.slot.mass[s + lane] : 0) +
+                       wt * min(e, ties > ahead ? ties - ahead : 0u);
+    const uint64_t upto = warp_scan(m);
+    const uint32_t past = __ballot_sync(0xffffffffu, upto > pick);
     if (past) {
-      if (lane == __ffs(past) - 1) a.out[b] = c0 + j;
+      const int who = __ffs(past) - 1;
+      pick -= __shfl_sync(0xffffffffu, upto - m, who);
+      rank = __shfl_sync(0xffffffffu, ahead, who);
+      s += who;
+      // the slot's tokens, a unit a lane
+      float v[kPer];
+      R::floats(row.load((first + s) * 32 + lane), v);
+      uint32_t equal = 0;
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) equal += ties != UINT_MAX && v[j] == t;
+      rank += warp_scan(equal) - equal;
+      uint64_t x[kPer], sum = 0;
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) {
+        const bool tie = ties != UINT_MAX && v[j] == t;
+        x[j] = tie ? (rank < ties ? wt : 0)
+                   : v[j] >= t ? weight(v[j], scale, sh.table) : 0;
+        rank += tie;
+        sum += x[j];
+      }
+      uint64_t at = warp_scan(sum);
+      const int last = __ffs(__ballot_sync(0xffffffffu, at > pick)) - 1;
+      at -= sum;
+      if (lane == last) {
+        int found = -1;
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) {
+          at += x[j];
+          if (found < 0 && at > pick) found = j;
+        }
+        a.out[b] = row.first((first + s) * 32 + lane) + found;
+      }
       return;
     }
-    before += __shfl_sync(0xffffffffu, sum, 31);
-    rank += __popc(equal);
+    pick -= __shfl_sync(0xffffffffu, upto, 31);
+    rank = __shfl_sync(0xffffffffu, ahead + e, 31);
   }
 }
 
 // ------------------------------------------------------------- launching
-// Of a row in a CTA's shared memory: two CTAs an SM.
-static_assert(kThreads * 16 >= kList * 8);
-constexpr int kHeldMost = 112 * 1024 - static_cast<int>(sizeof(Shared));
-
-template <class T, bool HELD>
-cudaError_t launch_sample(const SampleArgs& a, int64_t B, int ctas, int stride, cudaStream_t s) {
-  auto* k = sample_kernel<T, HELD>;
-  if (HELD) {
-    static SmemLimit limit;
-    const cudaError_t e = allow_smem(reinterpret_cast<const void*>(k), kHeldMost, &limit);
-    if (e != cudaSuccess) return e;
-  }
-  const cudaError_t e =
-      launch_overlapped(k, dim3(static_cast<unsigned>(B * ctas)), dim3(kThreads),
-                        HELD ? kThreads * stride * 16 : kList * 8, s, ctas, a, stride);
+template <class T>
+cudaError_t run_sample(const SampleArgs& a, int64_t B, int sms, cudaStream_t s) {
+  int ctas = 1;
+  while (ctas < kMaxCluster && B * ctas < 2 * sms) ctas *= 2;
+  const cudaError_t e = launch_overlapped(sample_kernel<T>, dim3(static_cast<unsigned>(B * ctas)),
+                                          dim3(kThreads), 0, s, ctas, a);
   note_launch();
   return e != cudaSuccess ? e : cudaGetLastError();
-}
-
-template <class T>
-cudaError_t run_sample(const SampleArgs& a, int64_t B, cudaStream_t s) {
-  constexpr int kPer = 16 / static_cast<int>(sizeof(T));
-  const int64_t slots = ((a.V + 2 * kPer - 2) / kPer + 31) / 32;  // whatever the row's shift
-  const int ctas = kMaxCluster;
-  const int each = static_cast<int>((slots + ctas * kWarps - 1) / (ctas * kWarps));
-  const int stride = each | 1;
-  return kThreads * stride * 16 <= kHeldMost ? launch_sample<T, true>(a, B, ctas, stride, s)
-                                             : launch_sample<T, false>(a, B, ctas, stride, s);
 }
 
 }  // namespace
@@ -844,7 +1093,7 @@ extern "C" flce_status flce_sample_logits(const void* logits, int64_t ld_logits,
   a.min_p = min_p;
   a.out = out;
   const auto s = reinterpret_cast<cudaStream_t>(stream);
-  const cudaError_t err = dtype == FLCE_BF16 ? run_sample<__nv_bfloat16>(a, B, s)
-                                             : run_sample<float>(a, B, s);
+  const cudaError_t err = dtype == FLCE_BF16 ? run_sample<__nv_bfloat16>(a, B, sms, s)
+                                             : run_sample<float>(a, B, sms, s);
   return err == cudaSuccess ? FLCE_OK : FLCE_ERR_CUDA;
 }
