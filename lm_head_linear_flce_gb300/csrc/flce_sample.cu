@@ -20,36 +20,21 @@
 #include <algorithm>
 #include <cfloat>
 #include <climits>
-#include <type_traits>
 
 #include "flce_device.cuh"
 #include "flce_internal.h"
 #include "flce_ops.h"
 
-#ifndef AHEAD1
-#define AHEAD1 8
-#endif
-#ifndef AHEAD2
-#define AHEAD2 4
-#endif
-#ifndef MINB
-#define MINB 2
-#endif
-#ifndef KT
-#define KT 512
-#endif
-#ifndef SM_FILL
-#define SM_FILL 1
-#endif
 namespace flce {
 namespace {
 
-constexpr int kThreads = KT;
+constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
 constexpr int kMaxWarps = kWarps * kMaxCluster;  // of a row
-constexpr int kMaxSlots = 1024;  // of a warp: 2^21 float32 logits in one CTA, with one to spare
-constexpr float kGreedyBelow = 0x1p-64f;         // temperatures that take the largest logit
+constexpr int64_t kMaxVocab = int64_t{1} << 21;
+constexpr int kMaxSlots = 1032;           // of a warp: kMaxVocab float32 logits in one CTA
+constexpr float kGreedyBelow = 0x1p-64f;  // temperatures that take the largest logit
 
 struct SampleArgs {
   const void* logits;
@@ -145,28 +130,60 @@ __device__ __forceinline__ uint64_t mass_of(uint32_t a, uint32_t b, uint32_t n) 
   const int64_t ia = a - n * kBitsA, ib = static_cast<int32_t>(b - n * kBitsB);
   return static_cast<uint64_t>(ia * (int64_t{1} << 21) + ib);
 }
-__device__ __forceinline__ uint64_t weight(float l, const Scale& s, const float2* table) {
+__device__ __forceinline__ uint64_t weight(float l, const Scale s, const float2* table) {
   uint32_t a, b;
   weigh(l, s, table, a, b);
   return mass_of(a, b, 1);
 }
 
+// Weights being added up.
+template <int PER>
+struct Adder {
+  uint64_t mass = 0;
+  uint32_t a = 0, b = 0, n = 0;
+  __device__ __forceinline__ void add(const float (&l)[PER], const Scale& s, const float2* table) {
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+      uint32_t ka, kb;
+      weigh(l[j], s, table, ka, kb);
+      a += ka;
+      b += kb;
+    }
+    n += PER;
+    if (n >= 512) flush();  // the sums of so many fit into 32 bits
+  }
+  __device__ __forceinline__ void flush() {
+    mass += mass_of(a, b, n);
+    a = b = n = 0;
+  }
+};
+
 // ------------------------------------------------------------ a row's logits
 // A row in units of 16 bytes, the first starting `shift` elements before it.  32 units
-// are a slot, a lane of a warp each; a warp has consecutive slots.  Elements outside the
-// row are -infinity.
+// are a slot, a lane of a warp each; a warp has consecutive slots, a lane its unit of each.
+// Elements outside the row are -infinity.
 template <class T>
-struct Row {
+struct Part {
   static constexpr int kPer = 16 / static_cast<int>(sizeof(T));
   const T* p;
   const uint4* aligned;
-  int V, shift, units;
+  int V, shift, slots;
+  int u0, each;  // this lane's first unit, and how many
+  bool inner;    // the warp's units lie in the row
 
-  __device__ Row(const SampleArgs& a, int64_t b)
+  __device__ Part(const SampleArgs& a, int64_t b)
       : p(static_cast<const T*>(a.logits) + b * a.ld), V(a.V) {
     shift = static_cast<int>(reinterpret_cast<uintptr_t>(p) % 16 / sizeof(T));
-    units = (V + shift + kPer - 1) / kPer;
+    slots = ((V + shift + kPer - 1) / kPer + 31) / 32;
     aligned = reinterpret_cast<const uint4*>(reinterpret_cast<uintptr_t>(p) & ~uintptr_t{15});
+  }
+  // The first slot of warp w of `warps` (a product below 2^31).
+  __device__ int first_slot(int w, int warps) const {
+    return static_cast<int>(static_cast<uint32_t>(slots * w) / static_cast<uint32_t>(warps));
+  }
+  __device__ int warp_of(int id, int warps) const {
+    const int slot = (id + shift) / (32 * kPer);  // first_slot(w) <= slot < first_slot(w + 1)
+    return ((slot + 1) * warps - 1) / slots;
   }
   __device__ int first(int u) const { return u * kPer - shift; }  // column of a unit's first element
   __device__ bool whole(int u) const { return first(u) >= 0 && first(u) + kPer <= V; }
@@ -198,7 +215,32 @@ struct Row {
       else v[i] = __uint_as_float(i % 2 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
     }
   }
+  // f(place in the batch, the unit's column, its logits) for the lane's units, a batch of
+  // them loaded at once.
+  template <int BATCH, class F>
+  __device__ __forceinline__ void stream(const F& f) const {
+    for (int s = 0; s < each; s += BATCH) {
+      uint4 r[BATCH];
+      const int u = u0 + s * 32;
+      if (inner && s + BATCH <= each) {
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i) r[i] = aligned[u + i * 32];
+      } else {
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i)
+          if (s + i < each) r[i] = load(u + i * 32);
+      }
+#pragma unroll
+      for (int i = 0; i < BATCH; ++i) {
+        if (s + i >= each) break;
+        float v[kPer];
+        floats(r[i], v);
+        f(i, first(u + i * 32), v);
+      }
+    }
+  }
 };
+constexpr int kWide = 8, kFew = 4;  // batches: of passes that do little, and of those that weigh
 
 // Logits in an order of integers (equal ones, but for the sign of a zero, alike).
 // bf16 logits differ in the upper half alone.
@@ -229,6 +271,11 @@ __device__ __forceinline__ I warp_scan(I v) {  // of this lane and those before
   }
   return v;
 }
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
 __device__ __forceinline__ void st_cluster_u64(uint32_t addr, uint64_t v) {
   asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(addr), "l"(v) : "memory");
 }
@@ -244,6 +291,10 @@ __device__ __forceinline__ void cluster_arrive() {
 __device__ __forceinline__ void cluster_wait() {
   __syncwarp();
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// A barrier of the block's first `threads` threads.
+__device__ __forceinline__ void bar_first(int threads) {
+  asm volatile("bar.sync 1, %0;" ::"r"(threads) : "memory");
 }
 
 constexpr int kList = 2048;        // tokens of a list
@@ -298,28 +349,41 @@ struct Cluster {
     cluster_arrive();
     cluster_wait();
   }
-  // The sum over the warps first .. last - 1.
-  __device__ __forceinline__ Sum sum(int first, int last) const {
+  __device__ __forceinline__ Sum sum() const {
     uint64_t m = 0;
     uint32_t n = 0;
-    for (int i = first + (threadIdx.x & 31); i < last; i += 32) {
+    for (int i = threadIdx.x & 31; i < ctas * kWarps; i += 32) {
       m += sh.mass[phase][i];
       n += sh.count[phase][i];
     }
     return {warp_sum_u64(m), __reduce_add_sync(0xffffffffu, n)};
   }
-  __device__ __forceinline__ Sum total(uint64_t mass, uint32_t count) {
-    share(mass, count);
-    return sum(0, ctas * kWarps);
-  }
 };
 
 // ------------------------------------------------------- lists in shared memory
+__device__ __forceinline__ int list_size(uint32_t n) {  // a power of two, 64 at least
+  return n <= 64 ? 64 : 2 << (31 - __clz(static_cast<int>(n) - 1));
+}
+__device__ __forceinline__ uint64_t list_entry(float l, int id) {
+  const uint32_t key = static_cast<uint32_t>(key_of<float>(l + 0.f)) ^ 0x80000000u;
+  return static_cast<uint64_t>(key) << 32 | (static_cast<uint32_t>(id) ^ 0xffffffffu);
+}
+__device__ __forceinline__ float listed_logit(uint64_t e) {
+  return value_of<float>(static_cast<int>(static_cast<uint32_t>(e >> 32) ^ 0x80000000u));
+}
+__device__ __forceinline__ int listed_id(uint64_t e) {
+  return static_cast<int>(~static_cast<uint32_t>(e));
+}
+
 // Sorts the first n (a power of two, 64 at least) of v, the larger first, with the block's
-// first `threads` = min(n / 2, kThreads) threads, which alone call it.
-__device__ void sort_list(uint64_t* v, int n, int threads) {
-  for (int size = 2; size <= n; size <<= 1) {
-    for (int stride = size / 2; stride > 0; stride >>= 1) {
+// first `threads` = min(n / 2, kThreads) threads, which alone call it.  Bitonic; a warp has
+// 64 neighbours in registers where strides are shorter.
+__device__ __forceinline__ void sort_list(uint64_t* v, int n, int threads) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll 1
+  for (int size = 64; size <= n; size <<= 1) {
+#pragma unroll 1
+    for (int stride = size / 2; stride > 32; stride >>= 1) {
       for (int t = threadIdx.x; t < n / 2; t += threads) {
         const int i = 2 * t - (t & (stride - 1)), k = i + stride;
         const uint64_t a = v[i], b = v[k];
@@ -328,40 +392,60 @@ __device__ void sort_list(uint64_t* v, int n, int threads) {
           v[k] = a;
         }
       }
-      // a warp's 32 pairs lie in 64 neighbours, and stay there while strides do
-      if (stride > 32 || (stride == 1 && size >= 64))
-        asm volatile("bar.sync 1, %0;" ::"r"(threads) : "memory");
-      else __syncwarp();
+      bar_first(threads);
     }
+    for (int i0 = 64 * warp; i0 < n; i0 += 2 * threads) {
+      uint64_t a = v[i0 + lane], b = v[i0 + lane + 32];
+      const auto exchange = [&](int z, int stride) {
+        const uint64_t x = __shfl_xor_sync(0xffffffffu, a, stride),
+                       y = __shfl_xor_sync(0xffffffffu, b, stride);
+        const bool low = (lane & stride) == 0;
+        if ((a < x) == (low == (((i0 + lane) & z) == 0))) a = x;
+        if ((b < y) == (low == (((i0 + lane + 32) & z) == 0))) b = y;
+      };
+      if (size == 64) {  // from single elements on
+#pragma unroll 1
+        for (int z = 2; z < 64; z <<= 1)
+#pragma unroll 1
+          for (int stride = z / 2; stride > 0; stride >>= 1) exchange(z, stride);
+      }
+      if ((a < b) == ((i0 & size) == 0)) {
+        const uint64_t x = a;
+        a = b;
+        b = x;
+      }
+#pragma unroll 1
+      for (int stride = 16; stride > 0; stride >>= 1) exchange(size, stride);
+      v[i0 + lane] = a;
+      v[i0 + lane + 32] = b;
+    }
+    bar_first(threads);
   }
 }
 
-// Sums of w[0 .. n) up to and including each, in place, by `threads` threads (a multiple
-// of 32, which alone call it); returns the total.
-__device__ uint64_t scan_list(uint64_t* w, int n, int threads, uint64_t* part) {
+// Sums of w[0 .. n) up to and including each, in place, by the block's first `threads`
+// threads (a multiple of 32), which alone call it; returns the total.
+__device__ __forceinline__ uint64_t scan_list(uint64_t* w, int n, int threads, uint64_t* part) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   uint64_t carry = 0;
+#pragma unroll 1
   for (int i0 = 0; i0 < n; i0 += threads) {
     const int i = i0 + threadIdx.x;
     const uint64_t x = warp_scan(i < n ? w[i] : uint64_t{0});
     if (lane == 31) part[warp] = x;
-    asm volatile("bar.sync 1, %0;" ::"r"(threads) : "memory");
+    bar_first(threads);
     const int warps = threads / 32;
     const uint64_t p = lane < warps ? part[lane] : 0;
     const uint64_t upto = warp_scan(p);
     const uint64_t before = __shfl_sync(0xffffffffu, upto - p, warp);
     if (i < n) w[i] = carry + before + x;
     carry += __shfl_sync(0xffffffffu, upto, warps - 1);
-    asm volatile("bar.sync 1, %0;" ::"r"(threads) : "memory");
+    bar_first(threads);
   }
   return carry;
 }
 
-__device__ __forceinline__ int list_size(uint32_t n) {  // a power of two, 64 at least
-  return n <= 64 ? 64 : 2 << (31 - __clz(static_cast<int>(n) - 1));
-}
-
-// ------------------------------------------------------------ the kernel
+// ------------------------------------------------------------------- bins
 // Bins of a token: of its distance from the largest logit, 1/64 of its octave each from
 // 2^-12 on, for counts (a distance of any size lies in one of them); of its weight, 1/64
 // of an octave each, for masses.  The last one takes what lies beyond.
@@ -377,31 +461,254 @@ __device__ __forceinline__ float distance_cut(int last, float top) {
   const float d = __uint_as_float(static_cast<uint32_t>(last + 1 + kFirstBin) << kBinShift);
   return fmaxf(nextafterf(top - d, -INFINITY), -FLT_MAX);
 }
-constexpr float kRound = 0x1.8p23f;  // + x: its last bits are x's nearest integer
 // The logit of `step` 64ths of an octave, rounded towards `to`.
 __device__ __forceinline__ float step_value(float step, float to, const Scale& s) {
   if (!(s.c_hi > 0.f)) return to;
   const float d = __fdiv_rn((kMagic - s.magic) - step * (1.f / 64), s.c_hi);
   return nextafterf(__fadd_rn(s.base, nextafterf(d, to)), to);
 }
-// A bin's mass is kept as what its tokens weigh beside the bin's middle, in 1 / kPerToken:
-// the weight there is 1 within 0.55%, and rounded to that, so sums are right to half of it.
-constexpr int kPerToken = 1024;  // (2^21 tokens: below 2^32)
-__device__ __forceinline__ uint32_t beside_middle(float l, const Scale& s, int& bin) {
+// A bin's mass is kept as what its tokens weigh beside the bin's middle, in units of
+// 2^-bits of that: the weight there is 1 within 0.55%, and rounded to a unit, so sums are
+// right to half a unit a token.  A row's tokens in one bin must stay below 2^32.
+__device__ __forceinline__ int unit_bits(int V) { return min(13, __clz(V - 1) - 1); }
+__device__ __forceinline__ uint32_t beside_middle(float l, const Scale& s, float unit, int& bin) {
+  constexpr float kRound = 0x1.8p23f;  // + x: its last bits are x's nearest integer
   const float d = fmaxf(__fsub_rn(l, s.base), s.least);
   // -64 log2 of the weight
   const float x = __fmul_rn(64.f, __fmaf_rn(d, -s.c_hi, kMagic - s.magic));
   const float k = __fadd_rn(x, kRound);
   bin = min(max(__float_as_int(k) - __float_as_int(kRound), 0), kBins - 1);
-  const float n = __fmaf_rn(__fsub_rn(x, __fsub_rn(k, kRound)), -kPerToken * 0.010830424696f,
-                            kRound + kPerToken);
+  const float y = __fsub_rn(x, __fsub_rn(k, kRound)) * -0.010830424696f;  // (ln 2 / 64)
+  const float n = __fmaf_rn(unit, __fmaf_rn(y, __fmaf_rn(y, 0.5f, 1.f), 1.f), kRound);
   return static_cast<uint32_t>(__float_as_int(n) - __float_as_int(kRound));
 }
+// What n in bin i amounts to; bits: of the unit, or -1 where tokens are counted.
+__device__ __forceinline__ uint64_t bin_amount(int i, uint32_t n, int bits) {
+  if (bits < 0 || n == 0) return n;
+  return static_cast<uint64_t>(static_cast<float>(n) *
+                               exp2f(static_cast<float>(42 - bits) - i * (1.f / 64)));
+}
 
+// The sums of this CTA's bins by groups, to every CTA (before a barrier).
+__device__ __forceinline__ void share_groups(const Cluster cl, int bits) {
+  const int lane = threadIdx.x & 31;
+  __syncthreads();
+#pragma unroll 1
+  for (int g = threadIdx.x >> 5; g < kGroups; g += kWarps) {
+    const int i = g * kGroupBins + 2 * lane;
+    const uint2 n = *reinterpret_cast<const uint2*>(&cl.sh.bins[i]);
+    const uint64_t m = warp_sum_u64(bin_amount(i, n.x, bits) + bin_amount(i + 1, n.y, bits));
+    if (lane < cl.ctas) st_cluster_u64(mapa_shared(smem_u32(&cl.sh.group[cl.rank][g]), lane), m);
+  }
+}
+// The bins at which the row's sum reaches the first `n` warps' `to` (after that barrier;
+// the last one if none).  Bins keep until the next barrier.
+__device__ __forceinline__ int2 find_bins(const Cluster cl, int bits, int n_warps, uint64_t to) {
+  static_assert(kGroups == 32 && kGroupBins == 64);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (warp < n_warps) {
+    uint64_t m = 0;
+    for (int r = 0; r < cl.ctas; ++r) m += cl.sh.group[r][lane];
+    uint64_t upto = warp_scan(m);
+    uint32_t past = __ballot_sync(0xffffffffu, upto >= to);
+    int found = kBins - 1;
+    if (past) {
+      const int g = __ffs(past) - 1;
+      const uint64_t before = __shfl_sync(0xffffffffu, upto - m, g);
+      // two neighbouring bins a lane, every CTA's at once
+      const int i = g * kGroupBins + 2 * lane;
+      const uint32_t here = smem_u32(&cl.sh.bins[i]);
+      uint64_t n[kMaxCluster];
+#pragma unroll
+      for (int r = 0; r < kMaxCluster; ++r)  // (its own again, instead of those there are not)
+        n[r] = ld_cluster_u64(mapa_shared(here, r < cl.ctas ? r : cl.rank));
+      uint64_t m0 = 0, m1 = 0;
+#pragma unroll
+      for (int r = 0; r < kMaxCluster; ++r) {
+        if (r >= cl.ctas) break;
+        m0 += bin_amount(i, static_cast<uint32_t>(n[r]), bits);
+        m1 += bin_amount(i + 1, static_cast<uint32_t>(n[r] >> 32), bits);
+      }
+      upto = before + warp_scan(m0 + m1);
+      past = __ballot_sync(0xffffffffu, upto >= to);
+      const int who = past ? __ffs(past) - 1 : 31;
+      found = g * kGroupBins + 2 * who +
+              (__shfl_sync(0xffffffffu, static_cast<int>(upto - m1 >= to), who) ? 0 : 1);
+    }
+    if (lane == 0) cl.sh.found[warp] = found;
+  }
+  __syncthreads();
+  return make_int2(cl.sh.found[0], cl.sh.found[1]);
+}
+
+// ------------------------------------------------- passes over a lane's part
+// The largest logits of every fourth of its units (NaN is passed over).
 template <class T>
-__global__ void __launch_bounds__(kThreads, MINB) sample_kernel(const SampleArgs a) {
-  using R = Row<T>;
-  constexpr int kPer = R::kPer;
+__device__ __forceinline__ float4 largest(const Part<T> part) {
+  float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+  part.template stream<kWide>([&](int i, int, const float (&v)[Part<T>::kPer]) {
+#pragma unroll
+    for (int j = 0; j < Part<T>::kPer; ++j) top[i % 4] = fmaxf(top[i % 4], v[j]);
+  });
+  return make_float4(top[0], top[1], top[2], top[3]);
+}
+// How many are at or above x.
+template <class T>
+__device__ __forceinline__ uint32_t count_from(const Part<T> part, float x) {
+  uint32_t n = 0;
+  part.template stream<kWide>([&](int, int, const float (&v)[Part<T>::kPer]) {
+#pragma unroll
+    for (int j = 0; j < Part<T>::kPer; ++j) n += v[j] >= x;
+  });
+  return n;
+}
+// Their mass.
+template <class T>
+__device__ __forceinline__ uint64_t weigh_all(const Part<T> part, const Scale s, const float2* table) {
+  Adder<Part<T>::kPer> sum;
+  part.template stream<kFew>(
+      [&](int, int, const float (&v)[Part<T>::kPer]) { sum.add(v, s, table); });
+  sum.flush();
+  return sum.mass;
+}
+// The mass of those at or above x.
+template <class T>
+__device__ __forceinline__ uint64_t weigh_from(const Part<T> part, const Scale s, const float2* table,
+                                            float x) {
+  Adder<Part<T>::kPer> sum;
+  part.template stream<kFew>([&](int, int, const float (&v)[Part<T>::kPer]) {
+    float w[Part<T>::kPer];
+    bool some = false;
+#pragma unroll
+    for (int j = 0; j < Part<T>::kPer; ++j) {
+      some = some || v[j] >= x;
+      w[j] = v[j] >= x ? v[j] : -INFINITY;
+    }
+    if (__any_sync(0xffffffffu, some)) sum.add(w, s, table);
+  });
+  sum.flush();
+  return sum.mass;
+}
+// Counts all in the CTA's bins.
+template <class T>
+__device__ __forceinline__ void count_bins(const Part<T> part, float top, uint32_t* bins) {
+  part.template stream<kFew>([&](int, int, const float (&v)[Part<T>::kPer]) {
+#pragma unroll
+    for (int j = 0; j < Part<T>::kPer; ++j)
+      if (v[j] > -INFINITY) atomicAdd(&bins[distance_bin(v[j], top)], 1);
+  });
+}
+// Adds those at or above x to the CTA's bins of masses.
+template <class T>
+__device__ __forceinline__ void fill_bins(const Part<T> part, const Scale s, float x, float unit,
+                                          uint32_t* bins) {
+  part.template stream<kFew>([&](int, int, const float (&v)[Part<T>::kPer]) {
+#pragma unroll
+    for (int j = 0; j < Part<T>::kPer; ++j) {
+      int bin;
+      const uint32_t n = beside_middle(v[j], s, unit, bin);
+      if (v[j] >= x) atomicAdd(&bins[bin], n);
+    }
+  });
+}
+// Puts a unit's tokens from lo to hi on the CTA's list; one that is full counts on.  All
+// lanes of a warp call it.
+template <int PER>
+__device__ __forceinline__ void list_unit(Shared& sh, int c, const float (&v)[PER], float lo,
+                                          float hi) {
+  uint32_t which = 0;
+#pragma unroll
+  for (int j = 0; j < PER; ++j) which |= v[j] >= lo && v[j] <= hi ? 1u << j : 0u;
+  if (!__any_sync(0xffffffffu, which != 0)) return;
+  const int lane = threadIdx.x & 31;
+  const uint32_t n = __popc(which), upto = warp_scan(n);
+  uint32_t at = 0;
+  if (lane == 31) at = atomicAdd(&sh.listed, upto);
+  at = __shfl_sync(0xffffffffu, at, 31) + upto - n;
+#pragma unroll
+  for (int j = 0; j < PER; ++j) {
+    if (!(which >> j & 1)) continue;
+    if (at < kList) sh.list[at] = list_entry(v[j], c + j);
+    ++at;
+  }
+}
+// Lists those at or above x.  `lanes`: which of the warp's lanes have one.
+template <class T>
+__device__ __forceinline__ void list_from(const Part<T> part, Shared& sh, float x, uint32_t lanes) {
+  constexpr int kFewLanes = 3;
+  if (__popc(lanes) > kFewLanes) {
+    part.template stream<kWide>([&](int, int c, const float (&v)[Part<T>::kPer]) {
+      list_unit(sh, c, v, x, INFINITY);
+    });
+    return;
+  }
+  const int lane = threadIdx.x & 31;
+#pragma unroll 1
+  for (; lanes; lanes &= lanes - 1) {  // one lane's units, spread over all
+    const int u0 = part.u0 - lane + __ffs(lanes) - 1;
+#pragma unroll 1
+    for (int s = 0; s < part.each; s += 32) {
+      const int u = u0 + (s + lane) * 32;
+      float v[Part<T>::kPer];
+      Part<T>::floats(s + lane < part.each ? part.load(u) : make_uint4(~0u, ~0u, ~0u, ~0u), v);
+      list_unit(sh, part.first(u), v, x, INFINITY);  // (NaN is on no list)
+    }
+  }
+}
+// Lists those from lo to hi; the mass of those above hi.
+template <class T>
+__device__ __forceinline__ uint64_t list_and_weigh(const Part<T> part, const Scale s, Shared& sh,
+                                                float lo, float hi) {
+  Adder<Part<T>::kPer> sum;
+  part.template stream<kFew>([&](int, int c, const float (&v)[Part<T>::kPer]) {
+    list_unit(sh, c, v, lo, hi);
+    float w[Part<T>::kPer];
+    bool some = false;
+#pragma unroll
+    for (int j = 0; j < Part<T>::kPer; ++j) {
+      some = some || v[j] > hi;
+      w[j] = v[j] > hi ? v[j] : -INFINITY;
+    }
+    if (__any_sync(0xffffffffu, some)) sum.add(w, s, sh.table);
+  });
+  sum.flush();
+  return sum.mass;
+}
+// Shares the length of this CTA's list and a warp's mass.
+__device__ __forceinline__ Sum share_list(Cluster& cl, uint64_t mass) {
+  __syncthreads();
+  cl.share(mass, threadIdx.x < 32 ? cl.sh.listed : 0);
+  return cl.sum();
+}
+// Every CTA's list into `work`, n tokens in all, padded to list_size(n).
+__device__ __forceinline__ void pull_lists(const Cluster cl, uint32_t n) {
+  Shared& sh = cl.sh;
+  uint32_t most = 0;
+  for (int r = 0; r < cl.ctas; ++r) most = max(most, sh.count[cl.phase][r * kWarps]);
+#pragma unroll 1
+  for (uint32_t i = threadIdx.x; i < most; i += kThreads) {
+    const uint32_t here = smem_u32(&sh.list[i]);
+    uint64_t e[kMaxCluster];
+#pragma unroll
+    for (int r = 0; r < kMaxCluster; ++r)  // (entries past a list's end are not used)
+      e[r] = ld_cluster_u64(mapa_shared(here, r < cl.ctas ? r : cl.rank));
+    uint32_t at = 0;
+#pragma unroll
+    for (int r = 0; r < kMaxCluster; ++r) {
+      if (r >= cl.ctas) break;
+      const uint32_t c = sh.count[cl.phase][r * kWarps];
+      if (i < c) sh.work[at + i] = e[r];
+      at += c;
+    }
+  }
+  for (uint32_t i = n + threadIdx.x; i < static_cast<uint32_t>(list_size(n)); i += kThreads)
+    sh.work[i] = 0;
+}
+
+// ------------------------------------------------------------ the kernel
+template <class T>
+__global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a) {
+  constexpr int kPer = Part<T>::kPer;
   __shared__ Shared sh;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   Cluster cl{sh, 0, 1, 0};
@@ -412,42 +719,12 @@ __global__ void __launch_bounds__(kThreads, MINB) sample_kernel(const SampleArgs
   griddep_launch_dependents();
   griddep_wait();
   const int64_t b = blockIdx.x / cl.ctas;
-  const R row(a, b);
-  const int slots = (row.units + 31) / 32, warps = cl.ctas * kWarps;
-  const int me = cl.rank * kWarps + warp;
-  const auto first_slot = [&](int w) {  // (V <= 2^21: below 2^31)
-    return static_cast<int>(static_cast<uint32_t>(slots * w) / static_cast<uint32_t>(warps));
-  };
-  const int s0 = first_slot(me), each = first_slot(me + 1) - s0;
-  const int u0 = s0 * 32 + lane;  // the lane's first unit; one in each slot
-  const bool inner = row.whole(s0 * 32) && row.whole((s0 + each) * 32 - 1);
-
-  // f(number in the batch, the unit's column, its logits) for the lane's units, a batch of
-  // them loaded at once.
-  const auto stream = [&](auto ahead, const auto& f) {
-    constexpr int kAhead = decltype(ahead)::value;
-    for (int s = 0; s < each; s += kAhead) {
-      uint4 r[kAhead];
-      const int u = u0 + s * 32;
-      if (inner && s + kAhead <= each) {
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i) r[i] = row.aligned[u + i * 32];
-      } else {
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i)
-          if (s + i < each) r[i] = row.load(u + i * 32);
-      }
-#pragma unroll
-      for (int i = 0; i < kAhead; ++i) {
-        if (s + i >= each) break;
-        float v[kPer];
-        R::floats(r[i], v);
-        f(i, row.first(u + i * 32), v);
-      }
-    }
-  };
-  using Wide = std::integral_constant<int, AHEAD1>;  // where registers allow it
-  using Few = std::integral_constant<int, AHEAD2>;
+  const int warps = cl.ctas * kWarps, me = cl.rank * kWarps + warp;
+  Part<T> part(a, b);
+  const int s0 = part.first_slot(me, warps);
+  part.each = part.first_slot(me + 1, warps) - s0;
+  part.u0 = s0 * 32 + lane;
+  part.inner = part.whole(s0 * 32) && part.whole((s0 + part.each) * 32 - 1);
 
   const float T0 = a.temperature ? a.temperature[b] : 1.f;
   const int k = a.top_k ? a.top_k[b] : 0;
@@ -455,6 +732,7 @@ __global__ void __launch_bounds__(kThreads, MINB) sample_kernel(const SampleArgs
   const float min_p = a.min_p ? a.min_p[b] : 0.f;
   const float u = a.u[b];
   const bool greedy = !(T0 >= kGreedyBelow);
+  for (int i = threadIdx.x; i < kBins; i += kThreads) sh.bins[i] = 0;
   if (warp == 0) {
     sh.table[lane] = kPow2[lane];
     if (lane == 0) {
@@ -476,21 +754,9 @@ __global__ void __launch_bounds__(kThreads, MINB) sample_kernel(const SampleArgs
       if (lane == 0) sh.log_min_p = make_float2(hi, fmaf(T0, y, -hi) + T0 * rest);
     }
   }
-  for (int i = threadIdx.x; i < kBins; i += kThreads) sh.bins[i] = 0;
 
-  // The largest logit (NaN is passed over): of every fourth of the lane's units, the
-  // lane's, the warp's, the row's.
-  float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-  stream(Wide{}, [&](int i, int, const float (&v)[kPer]) {
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) tops[i % 4] = fmaxf(tops[i % 4], v[j]);
-  });
-  const float lane_top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
-  const auto warp_max = [](float v) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-    return v;
-  };
+  const float4 tops = largest(part);
+  const float lane_top = fmaxf(fmaxf(tops.x, tops.y), fmaxf(tops.z, tops.w));
   float top = warp_max(lane_top);
   cluster_wait();
   cl.share(0, __float_as_uint(top));
@@ -503,14 +769,13 @@ __global__ void __launch_bounds__(kThreads, MINB) sample_kernel(const SampleArgs
   const Scale scale = make_scale(top, sh.inverse);
   // what min_p keeps: w >= min_p w_max, l >= max + T ln(min_p), rounded up
   float least = -FLT_MAX;
-  if (!greedy && min_p > 0.f) {
+  if (!greedy && min_p > 0.f && top < INFINITY) {
     const float2 d = sh.log_min_p;
     const float sum = __fadd_rn(top, d.x), back = __fsub_rn(sum, top);
     const float rest = __fadd_rn(
         __fadd_rn(__fsub_rn(top, __fsub_rn(sum, back)), __fsub_rn(d.x, back)), d.y);
     least = rest > 0.f ? nextafterf(sum, INFINITY) : sum;
     if (!(least > -FLT_MAX)) least = -FLT_MAX;
-    if (top == INFINITY) least = top;
   }
   const bool by_k = !greedy && k > 0 && k < a.V, by_p = !greedy && p < 1.f;
   const uint64_t part_p = __float2ull_rz(fmaxf(fminf(p, 0x1.fffffep-1f), 0.f) * 0x1p64f);
@@ -520,76 +785,107 @@ __global__ void __launch_bounds__(kThreads, MINB) sample_kernel(const SampleArgs
   };
   const uint64_t part_u = __float2ull_rz(fminf(fmaxf(u, 0.f), 0x1.fffffep-1f) * 0x1p64f);
 
-  float t = -FLT_MAX;
-  uint32_t ties = UINT_MAX;
-
-  // The mass of the lane's tokens from x on.
-  const auto weigh_from = [&](float x) {
-    uint64_t mass = 0;
-    uint32_t wa = 0, wb = 0, n = 0;
-    const auto add = [&](const float (&v)[kPer]) {
+  // --- top-k: a list of everything that can be among the first k, which the cluster's
+  // first CTA then has to itself.  k of the largest logits of quarters of lanes are in the
+  // bins up to the one that holds the k-th, so are k tokens; other quarters have none there.
+  // Where quarters are not many more than k, all tokens are counted instead.
+  if (by_k && k <= kList / 2) {
+    if (2 * k > min(4 * warps, part.slots) * 32) {
+      count_bins(part, top, sh.bins);
+    } else {
+      const float quarter[4] = {tops.x, tops.y, tops.z, tops.w};
 #pragma unroll
-      for (int j = 0; j < kPer; ++j) {
-        uint32_t ka, kb;
-        weigh(v[j], scale, sh.table, ka, kb);
-        wa += ka;
-        wb += kb;
-      }
-      n += kPer;
-      if (n >= 512) {  // the sums of so many fit into 32 bits
-        mass += mass_of(wa, wb, n);
-        wa = wb = n = 0;
-      }
-    };
-    if (x == -FLT_MAX) {
-      stream(Few{}, [&](int, int, const float (&v)[kPer]) { add(v); });
-    } else if (__any_sync(0xffffffffu, lane_top >= x)) {
-      stream(Few{}, [&](int, int, const float (&v)[kPer]) {
-        float w[kPer];
-        bool some = false;
-#pragma unroll
-        for (int j = 0; j < kPer; ++j) {
-          some = some || v[j] >= x;
-          w[j] = v[j] >= x ? v[j] : -INFINITY;
-        }
-        if (__any_sync(0xffffffffu, some)) add(w);
-      });
+      for (int i = 0; i < 4; ++i)
+        if (quarter[i] > -INFINITY) atomicAdd(&sh.bins[distance_bin(quarter[i], top)], 1);
     }
-    return mass + mass_of(wa, wb, n);
+    share_groups(cl, -1);
+    cluster_arrive();
+    cluster_wait();
+    const float cut = distance_cut(find_bins(cl, -1, 1, k).x, top);
+    const uint32_t lanes = __ballot_sync(0xffffffffu, lane_top >= cut);
+    if (lanes) list_from(part, sh, cut, lanes);
+    const uint32_t N = share_list(cl, 0).count;
+    if (N <= kList) {
+      if (cl.rank == 0) pull_lists(cl, N);
+      cluster_arrive();  // the lists have been read
+      if (cl.rank != 0) {
+        cluster_wait();
+        return;
+      }
+      __syncthreads();
+      const int size = list_size(N), threads = min(size / 2, kThreads);
+      if (threadIdx.x < threads) {
+        sort_list(sh.work, size, threads);
+        int keep = min(static_cast<int>(N), k);
+        for (int i = threadIdx.x; i < keep; i += threads)
+          sh.weights[i] = weight(listed_logit(sh.work[i]), scale, sh.table);
+        bar_first(threads);
+        const uint64_t all = scan_list(sh.weights, keep, threads, sh.part);
+        // p and min_p keep a prefix of these
+        const uint64_t target = by_p ? target_p(all) : UINT64_MAX;
+        uint32_t in = 0;
+        for (int i = threadIdx.x; i < keep; i += threads)
+          in += i == 0 || (sh.weights[i - 1] < target && listed_logit(sh.work[i]) >= least);
+        in = __reduce_add_sync(0xffffffffu, in);
+        if (lane == 0) sh.part[warp] = in;
+        bar_first(threads);
+        keep = 0;
+        for (int w = 0; w < threads / 32; ++w) keep += static_cast<int>(sh.part[w]);
+        const uint64_t kept = sh.weights[keep - 1];
+        // by id: ~id << 32 | place, the larger first
+        const int size2 = list_size(keep), threads2 = min(size2 / 2, kThreads);
+        for (int i = threadIdx.x; i < size2; i += threads)
+          sh.list[i] = i < keep ? sh.work[i] << 32 | i : 0;
+        bar_first(threads);
+        if (threadIdx.x < threads2) {
+          sort_list(sh.list, size2, threads2);
+          uint64_t* by_id = sh.work;
+          for (int i = threadIdx.x; i < keep; i += threads2) {
+            const uint32_t at = static_cast<uint32_t>(sh.list[i]);
+            by_id[i] = sh.weights[at] - (at ? sh.weights[at - 1] : 0);
+          }
+          bar_first(threads2);
+          scan_list(by_id, keep, threads2, sh.part);
+          const uint64_t pick = __umul64hi(part_u, kept);
+          for (int i = threadIdx.x; i < keep; i += threads2)
+            if (by_id[i] > pick && (i == 0 || by_id[i - 1] <= pick))
+              a.out[b] = static_cast<int64_t>(~static_cast<uint32_t>(sh.list[i] >> 32));
+        }
+      }
+      cluster_wait();
+      return;
+    }
+  }
+
+  // --- otherwise what is kept as t and ties, which the limits narrow one after another.
+  float t = top < INFINITY ? -FLT_MAX : top;
+  uint32_t ties = UINT_MAX;
+  if (greedy) {
+    t = top;
+    ties = 1;
+  }
+  // Of the lane's tokens, as far as its warp has any (x > -infinity).
+  const auto mass_from = [&](float x) {
+    if (!__any_sync(0xffffffffu, lane_top >= x)) return uint64_t{0};
+    return x == -FLT_MAX && scale.least > -FLT_MAX ? weigh_all(part, scale, sh.table)
+                                                   : weigh_from(part, scale, sh.table, x);
   };
-  // The mass above t, or with all ties from it on, and the number of those; to every CTA.
-  const auto share_kept = [&]() {
-    const bool all_ties = ties == UINT_MAX;
-    const uint64_t mass = weigh_from(all_ties ? t : nextafterf(t, INFINITY));
-    uint32_t n = 0;
-    if (!all_ties && __any_sync(0xffffffffu, lane_top >= t))
-      stream(Wide{}, [&](int, int, const float (&v)[kPer]) {
-#pragma unroll
-        for (int j = 0; j < kPer; ++j) n += v[j] == t;
-      });
-    cl.share(warp_sum_u64(mass), __reduce_add_sync(0xffffffffu, n));
-  };
-  const auto count_from = [&](float x) {
-    uint32_t n = 0;
-    if (__any_sync(0xffffffffu, lane_top >= x))
-      stream(Wide{}, [&](int, int, const float (&v)[kPer]) {
-#pragma unroll
-        for (int j = 0; j < kPer; ++j) n += v[j] >= x;
-      });
-    return n;
+  const auto number_from = [&](float x) {
+    return __any_sync(0xffffffffu, lane_top >= x) ? count_from(part, x) : 0u;
   };
   // Narrows t and ties to the prefix that makes `target` (tokens, or mass): halves the
   // range of logits from t on, a pass over the row and a barrier each.  For any row; the
-  // lists below are faster where they are long enough.
+  // lists are faster where they are long enough.
   const auto halve = [&](uint64_t target, bool mass) {
     int lo = key_of<T>(t), hi = key_of<T>(top);
     uint64_t above = 0;
+#pragma unroll 1
     while (lo < hi) {
       const int mid = static_cast<int>(lo + (static_cast<int64_t>(hi) - lo + 1) / 2);
       const float x = value_of<T>(mid);
-      const uint64_t m = mass ? weigh_from(x) : 0;
-      const uint32_t n = mass ? 0 : count_from(x);
-      const Sum s = cl.total(warp_sum_u64(m), __reduce_add_sync(0xffffffffu, n));
+      cl.share(mass ? warp_sum_u64(mass_from(x)) : 0,
+               mass ? 0 : __reduce_add_sync(0xffffffffu, number_from(x)));
+      const Sum s = cl.sum();
       const uint64_t have = mass ? s.mass : s.count;
       if (have >= target) {
         lo = mid;
@@ -610,277 +906,65 @@ __global__ void __launch_bounds__(kThreads, MINB) sample_kernel(const SampleArgs
       ties = static_cast<uint32_t>(r);
     }
   };
-
-  // The sums of this CTA's bins by groups, to every CTA (before a barrier).
-  const auto bin_amount = [&](int i, uint32_t n, bool mass) {
-    return mass ? static_cast<uint64_t>(static_cast<float>(n) *
-                                        exp2f(42.f - i * (1.f / 64) - __log2f(kPerToken)))
-                : static_cast<uint64_t>(n);
-  };
-  const auto share_groups = [&](bool mass) {
-    __syncthreads();
-    for (int g = warp; g < kGroups; g += kWarps) {
-      uint64_t m = 0;
-      for (int i = lane; i < kGroupBins; i += 32) {
-        const uint32_t n = sh.bins[g * kGroupBins + i];
-        if (n) m += bin_amount(g * kGroupBins + i, n, mass);
-      }
-      m = warp_sum_u64(m);
-      if (lane < cl.ctas) st_cluster_u64(mapa_shared(smem_u32(&sh.group[cl.rank][g]), lane), m);
-    }
-  };
-  // The bins at which the row's sum reaches `lower` and `target` (after that barrier; the
-  // last one if none).  Bins keep until the next barrier.
-  const auto find_bins = [&](uint64_t lower, uint64_t target, bool mass) {
-    if (warp < 2) {
-      const uint64_t to = warp == 0 ? lower : target;
-      uint64_t m = 0;
-      for (int r = 0; r < cl.ctas; ++r) m += sh.group[r][lane];
-      uint64_t upto = warp_scan(m);
-      uint32_t past = __ballot_sync(0xffffffffu, upto >= to);
-      int found = kBins - 1;
-      if (past) {
-        const int g = __ffs(past) - 1;
-        const uint64_t before = __shfl_sync(0xffffffffu, upto - m, g);
-        // two neighbouring bins a lane, every CTA's at once
-        const int i = g * kGroupBins + 2 * lane;
-        uint64_t n[kMaxCluster];
-#pragma unroll
-        for (int r = 0; r < kMaxCluster; ++r)
-          n[r] = r < cl.ctas ? ld_cluster_u64(mapa_shared(smem_u32(&sh.bins[i]), r)) : 0;
-        uint64_t m0 = 0, m1 = 0;
-#pragma unroll
-        for (int r = 0; r < kMaxCluster; ++r) {
-          m0 += bin_amount(i, static_cast<uint32_t>(n[r]), mass);
-          m1 += bin_amount(i + 1, static_cast<uint32_t>(n[r] >> 32), mass);
-        }
-        upto = before + warp_scan(m0 + m1);
-        past = __ballot_sync(0xffffffffu, upto >= to);
-        const int who = past ? __ffs(past) - 1 : 31;
-        found = g * kGroupBins + 2 * who +
-                (__shfl_sync(0xffffffffu, static_cast<int>(upto - m1 >= to), who) ? 0 : 1);
-      }
-      if (lane == 0) sh.found[warp] = found;
-    }
-    __syncthreads();
-    return make_int2(sh.found[0], sh.found[1]);
+  // The mass above t, or with all ties from it on, and the number of those; to every CTA.
+  const auto share_kept = [&]() {
+    const float next = ties == UINT_MAX ? t : nextafterf(t, INFINITY);
+    const uint32_t n = ties == UINT_MAX ? 0
+                       : t == INFINITY  ? number_from(t)
+                                        : number_from(t) - number_from(next);
+    const uint64_t m = ties != UINT_MAX && t == INFINITY ? 0 : mass_from(next);
+    cl.share(warp_sum_u64(m), __reduce_add_sync(0xffffffffu, n));
   };
 
-  // Puts the unit's tokens that are in `which` on the CTA's list; one that is full counts
-  // on.  All lanes of a warp call it.
-  const auto list_unit = [&](int c, const float (&v)[kPer], uint32_t which) {
-    if (!__any_sync(0xffffffffu, which != 0)) return;
-    const uint32_t n = __popc(which), upto = warp_scan(n);
-    uint32_t at = 0;
-    if (lane == 31) at = atomicAdd(&sh.listed, upto);
-    at = __shfl_sync(0xffffffffu, at, 31) + upto - n;
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-      if (!(which >> j & 1)) continue;
-      const uint32_t key = static_cast<uint32_t>(key_of<float>(v[j] + 0.f)) ^ 0x80000000u;
-      if (at < kList)
-        sh.list[at] = static_cast<uint64_t>(key) << 32 | (static_cast<uint32_t>(c + j) ^ 0xffffffffu);
-      ++at;
-    }
-  };
-  const auto listed_value = [](uint64_t e) {
-    return value_of<float>(static_cast<int>(static_cast<uint32_t>(e >> 32) ^ 0x80000000u));
-  };
-  // Shares the length of this CTA's list (and a warp's mass); the row's.
-  const auto share_list = [&](uint64_t mass) {
-    __syncthreads();
-    return cl.total(mass, warp == 0 ? sh.listed : 0);
-  };
-  // Every CTA's list into `work`, n tokens in all, padded to list_size(n).
-  const auto pull_lists = [&](uint32_t n) {
-    uint32_t at = 0;
-    for (int r = 0; r < cl.ctas; ++r) {
-      const uint32_t c = sh.count[cl.phase][r * kWarps];
-      for (uint32_t i = threadIdx.x; i < c; i += kThreads)
-        sh.work[at + i] = ld_cluster_u64(mapa_shared(smem_u32(&sh.list[i]), r));
-      at += c;
-    }
-    for (uint32_t i = n + threadIdx.x; i < static_cast<uint32_t>(list_size(n)); i += kThreads)
-      sh.work[i] = 0;
-  };
-
-  // --- top-k: a list of everything that can be among the first k, which the cluster's
-  // first CTA then has to itself.  k of the largest logits of quarters of lanes are in the
-  // bins up to the one that holds the k-th, so are k tokens; other quarters have none there.
-  constexpr int kFewLanes = 3;
-  if (by_k && k <= kList / 2) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (tops[i] > -INFINITY) atomicAdd(&sh.bins[distance_bin(tops[i], top)], 1);
-    share_groups(false);
-    cluster_arrive();
-    cluster_wait();
-    const float cut = distance_cut(find_bins(k, k, false).y, top);
-    const uint32_t flagged = __ballot_sync(0xffffffffu, lane_top >= cut);
-    const auto in = [&](const float (&v)[kPer]) {
-      uint32_t which = 0;
-#pragma unroll
-      for (int j = 0; j < kPer; ++j) which |= v[j] >= cut ? 1u << j : 0u;
-      return which;
-    };
-    if (__popc(flagged) > kFewLanes) {
-      stream(Wide{}, [&](int, int c, const float (&v)[kPer]) { list_unit(c, v, in(v)); });
-    } else {
-      for (uint32_t some = flagged; some; some &= some - 1) {
-        // one of those lanes' units, a lane each
-        const int who = __ffs(some) - 1;
-        for (int s = 0; s < each; s += 32) {
-          const int un = u0 - lane + who + (s + lane) * 32;
-          float v[kPer];
-          uint32_t which = 0;
-          if (s + lane < each) {
-            R::floats(row.load(un), v);
-            which = in(v);
-          }
-          list_unit(row.first(un), v, which);
-        }
-      }
-    }
-    const uint32_t N = share_list(0).count;
-    if (N <= kList) {
-      if (cl.rank == 0) pull_lists(N);
-      cluster_arrive();  // the lists have been read
-      if (cl.rank != 0) {
-        cluster_wait();
-        return;
-      }
-      __syncthreads();
-      const int size = list_size(N), threads = min(size / 2, kThreads);
-      if (threadIdx.x < threads) {
-        sort_list(sh.work, size, threads);
-        uint32_t keep = min(N, static_cast<uint32_t>(k));
-        for (uint32_t i = threadIdx.x; i < keep; i += threads)
-          sh.weights[i] = weight(listed_value(sh.work[i]), scale, sh.table);
-        asm volatile("bar.sync 1, %0;" ::"r"(threads) : "memory");
-        const uint64_t all = scan_list(sh.weights, keep, threads, sh.part);
-        // p and min_p keep a prefix of these
-        const uint64_t target = by_p ? target_p(all) : UINT64_MAX;
-        uint32_t in_all = 0;
-        for (uint32_t i = threadIdx.x; i < keep; i += threads)
-          in_all += i == 0 || (sh.weights[i - 1] < target && listed_value(sh.work[i]) >= least);
-        in_all = __reduce_add_sync(0xffffffffu, in_all);
-        if (lane == 0) sh.part[warp] = in_all;
-        asm volatile("bar.sync 1, %0;" ::"r"(threads) : "memory");
-        keep = 0;
-        for (int w = 0; w < threads / 32; ++w) keep += static_cast<uint32_t>(sh.part[w]);
-        const uint64_t kept = sh.weights[keep - 1];
-        asm volatile("bar.sync 1, %0;" ::"r"(threads) : "memory");
-        // by id: ~id << 32 | place, the larger first
-        const int size2 = list_size(keep), threads2 = min(size2 / 2, kThreads);
-        for (int i = threadIdx.x; i < size2; i += threads)
-          sh.list[i] = i < static_cast<int>(keep) ? sh.work[i] << 32 | i : 0;
-        asm volatile("bar.sync 1, %0;" ::"r"(threads) : "memory");
-        if (threadIdx.x < threads2) {
-          sort_list(sh.list, size2, threads2);
-          uint64_t* by_id = sh.work;
-          for (uint32_t i = threadIdx.x; i < keep; i += threads2) {
-            const uint32_t at = static_cast<uint32_t>(sh.list[i]);
-            by_id[i] = sh.weights[at] - (at ? sh.weights[at - 1] : 0);
-          }
-          asm volatile("bar.sync 1, %0;" ::"r"(threads2) : "memory");
-          scan_list(by_id, keep, threads2, sh.part);
-          const uint64_t pick = __umul64hi(part_u, kept);
-          for (uint32_t i = threadIdx.x; i < keep; i += threads2)
-            if (by_id[i] > pick && (i == 0 || by_id[i - 1] <= pick))
-              a.out[b] = static_cast<int64_t>(~static_cast<uint32_t>(sh.list[i] >> 32));
-        }
-      }
-      __syncwarp();
-      cluster_wait();
-      return;
-    }
-  }
-  if (greedy) {
-    t = top;
-    ties = 1;
-  }
   if (by_k) halve(static_cast<uint64_t>(k), false);
-  // --- top-p over many tokens: their mass, and a histogram by weight that says near which
-  // one the border lies; a list of that bin's tokens then gives it.
   bool shared = false;  // every CTA has what t and ties keep, by warps
+  // --- top-p over many tokens: their mass, and a histogram by weight that says near which
+  // one the border lies; a list of those bins' tokens then gives it.
   if (by_p) {
     if (by_k) {  // (the bins have been used)
       for (int i = threadIdx.x; i < kBins; i += kThreads) sh.bins[i] = 0;
       if (threadIdx.x == 0) sh.listed = 0;
       __syncthreads();
     }
-    if (__any_sync(0xffffffffu, lane_top >= t))
-      stream(Few{}, [&](int, int, const float (&v)[kPer]) {
-#pragma unroll
-        for (int j = 0; j < kPer; ++j) {
-          int bin;
-          const uint32_t n = beside_middle(v[j], scale, bin);
-          if (v[j] >= t) atomicAdd(&sh.bins[bin], n);
-        }
-      });
-    share_groups(true);
+    const int bits = unit_bits(a.V), unit = 1 << bits;
+    if (__any_sync(0xffffffffu, lane_top >= t)) fill_bins(part, scale, t, unit, sh.bins);
+    share_groups(cl, bits);
     share_kept();
-    const Sum s = cl.sum(0, warps);
+    const Sum s = cl.sum();
     const uint64_t target = target_p(s.mass + weight(t, scale, sh.table) * min(s.count, ties));
-    // the bins' sums are off by 1 / (2 kPerToken) of them, and FP32's rounding
-    const uint64_t slack = target / (2 * kPerToken - 128) + kBins;
-    const int2 bins = find_bins(target - min(slack, target - 1), target + slack, true);
-    bool done = false;
+    // the bins' sums are off by half a unit of them, and FP32's rounding
+    const uint64_t slack = target / (2 * unit - unit / 16) + kBins;
+    const int2 bins =
+        find_bins(cl, bits, 2, warp == 0 ? target - min(slack, target - 1) : target + slack);
     if (bins.y < kBins - 1) {
-      uint64_t mass = 0;
       // logits at and a little beyond the ends of these bins
       const float lo = fmaxf(step_value(bins.y + 0.51f, -INFINITY, scale), t);
       const float hi = bins.x == 0 ? INFINITY : step_value(bins.x - 0.51f, INFINITY, scale);
-      if (__any_sync(0xffffffffu, lane_top >= lo)) {
-        uint32_t wa = 0, wb = 0, n = 0;
-        stream(Few{}, [&](int, int c, const float (&v)[kPer]) {
-          uint32_t at = 0;
-          float w[kPer];
-          bool above = false;
-#pragma unroll
-          for (int j = 0; j < kPer; ++j) {
-            at |= v[j] >= lo && v[j] <= hi ? 1u << j : 0u;
-            w[j] = v[j] > hi ? v[j] : -INFINITY;
-            above = above || v[j] > hi;
-          }
-          list_unit(c, v, at);
-          if (!__any_sync(0xffffffffu, above)) return;
-#pragma unroll
-          for (int j = 0; j < kPer; ++j) {
-            uint32_t ka, kb;
-            weigh(w[j], scale, sh.table, ka, kb);
-            wa += ka;
-            wb += kb;
-          }
-          n += kPer;
-          if (n >= 512) {
-            mass += mass_of(wa, wb, n);
-            wa = wb = n = 0;
-          }
-        });
-        mass += mass_of(wa, wb, n);
-      }
-      const Sum in = share_list(warp_sum_u64(mass));
+      const uint64_t mass = __any_sync(0xffffffffu, lane_top >= lo)
+                                ? list_and_weigh(part, scale, sh, lo, hi)
+                                : 0;
+      const Sum in = share_list(cl, warp_sum_u64(mass));
       if (in.count <= kList) {
-        pull_lists(in.count);
+        pull_lists(cl, in.count);
         if (threadIdx.x == 0) sh.found[0] = 0;
         cluster_arrive();
         cluster_wait();
         const int size = list_size(in.count), threads = min(size / 2, kThreads);
+        const int n = static_cast<int>(in.count);
         if (threadIdx.x < threads) {
           sort_list(sh.work, size, threads);
           uint64_t* upto = sh.list;  // (all have read it)
-          for (int i = threadIdx.x; i < static_cast<int>(in.count); i += threads)
-            upto[i] = weight(listed_value(sh.work[i]), scale, sh.table);
-          asm volatile("bar.sync 1, %0;" ::"r"(threads) : "memory");
-          scan_list(upto, in.count, threads, sh.part);
-          for (int i = threadIdx.x; i < static_cast<int>(in.count); i += threads)
+          for (int i = threadIdx.x; i < n; i += threads)
+            upto[i] = weight(listed_logit(sh.work[i]), scale, sh.table);
+          bar_first(threads);
+          scan_list(upto, n, threads, sh.part);
+          for (int i = threadIdx.x; i < n; i += threads)
             if (in.mass + upto[i] >= target &&
                 (i ? in.mass + upto[i - 1] : in.mass) < target) {  // the border: at most one
               int equal = i;
               while (equal > 0 && sh.work[equal - 1] >> 32 == sh.work[i] >> 32) --equal;
               sh.rank = static_cast<uint32_t>(i - equal + 1);
-              sh.cut = listed_value(sh.work[i]);
+              sh.cut = listed_logit(sh.work[i]);
               sh.found[0] = 1;
             }
         }
@@ -888,16 +972,14 @@ __global__ void __launch_bounds__(kThreads, MINB) sample_kernel(const SampleArgs
         // share_kept would leave them
         if (threadIdx.x < warps) sh.count[cl.phase][threadIdx.x] = 0;
         __syncthreads();
-        done = sh.found[0] == 1;
-        if (done) {
+        shared = sh.found[0] == 1;
+        if (shared) {
           t = sh.cut;
           ties = sh.rank;
-          for (uint32_t i = threadIdx.x; i < in.count; i += kThreads) {
-            const float l = listed_value(sh.work[i]);
+          for (int i = threadIdx.x; i < n; i += kThreads) {
+            const float l = listed_logit(sh.work[i]);
             if (!(l >= t)) continue;
-            const int id = static_cast<int>(~static_cast<uint32_t>(sh.work[i]));
-            const int slot = (id + row.shift) / (32 * kPer);
-            const int w = ((slot + 1) * warps - 1) / slots;  // first_slot(w) <= slot
+            const int w = part.warp_of(listed_id(sh.work[i]), warps);
             if (l > t)
               atomicAdd(reinterpret_cast<unsigned long long*>(&sh.mass[cl.phase][w]),
                         static_cast<unsigned long long>(weight(l, scale, sh.table)));
@@ -907,8 +989,7 @@ __global__ void __launch_bounds__(kThreads, MINB) sample_kernel(const SampleArgs
         }
       }
     }
-    shared = done;
-    if (!done) halve(target, true);
+    if (!shared) halve(target, true);
   }
   if (least > t) {
     t = least;
@@ -916,9 +997,11 @@ __global__ void __launch_bounds__(kThreads, MINB) sample_kernel(const SampleArgs
     shared = false;
   }
   if (!shared) share_kept();
+
+  // --- the pick: which warp has it, which of its slots, which token of that.
   const uint64_t wt = weight(t, scale, sh.table);
   if (warp == 0) {
-    // which warp has the token: four consecutive entries a lane
+    // four consecutive entries a lane
     constexpr int kEach = kMaxWarps / 32;
     uint64_t m[kEach], upto = 0;
     uint32_t e_at[kEach], ahead = 0;
@@ -963,28 +1046,32 @@ __global__ void __launch_bounds__(kThreads, MINB) sample_kernel(const SampleArgs
   const int w = sh.found[0];
   if (w < 0 || w >= kWarps) return;  // another CTA's
   // The warp's slots, a warp of this CTA each: their masses above t, and ties.
-  const int first = first_slot(cl.rank * kWarps + w), count = first_slot(cl.rank * kWarps + w + 1) - first;
+  const int first = part.first_slot(cl.rank * kWarps + w, warps);
+  const int count = part.first_slot(cl.rank * kWarps + w + 1, warps) - first;
+#pragma unroll 1
   for (int s = warp; s < count; s += kWarps) {
     float v[kPer];
-    R::floats(row.load((first + s) * 32 + lane), v);
-    uint32_t wa = 0, wb = 0, e = 0;
+    Part<T>::floats(part.load((first + s) * 32 + lane), v);
+    uint32_t e = 0;
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
       const bool tie = ties != UINT_MAX && v[j] == t;
       e += tie;
       if (!(v[j] >= t) || tie) v[j] = -INFINITY;
     }
+    Adder<kPer> sum;
+    if (scale.least > -FLT_MAX) {
+      sum.add(v, scale, sh.table);
+      sum.flush();
+    } else {  // (-infinity weighs as much as any)
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-      uint32_t ka, kb;
-      weigh(v[j], scale, sh.table, ka, kb);
-      wa += ka;
-      wb += kb;
+      for (int j = 0; j < kPer; ++j)
+        if (v[j] > -INFINITY) sum.mass += weight(v[j], scale, sh.table);
     }
-    const uint64_t mass = warp_sum_u64(mass_of(wa, wb, kPer));
+    sum.mass = warp_sum_u64(sum.mass);
     e = __reduce_add_sync(0xffffffffu, e);
     if (lane == 0) {
-      sh.slot.mass[s] = mass;
+      sh.slot.mass[s] = sum.mass;
       sh.slot.ties[s] = e;
     }
   }
@@ -992,6 +1079,7 @@ __global__ void __launch_bounds__(kThreads, MINB) sample_kernel(const SampleArgs
   if (warp != 0) return;
   uint64_t pick = sh.before;
   uint32_t rank = sh.rank;
+#pragma unroll 1
   for (int s = 0; s < count; s += 32) {
     const uint32_t e = s + lane < count ? sh.slot.ties[s + lane] : 0;
     const uint32_t ahead = rank + warp_scan(e) - e;
@@ -999,51 +1087,56 @@ __global__ void __launch_bounds__(kThreads, MINB) sample_kernel(const SampleArgs
                        wt * min(e, ties > ahead ? ties - ahead : 0u);
     const uint64_t upto = warp_scan(m);
     const uint32_t past = __ballot_sync(0xffffffffu, upto > pick);
-    if (past) {
-      const int who = __ffs(past) - 1;
-      pick -= __shfl_sync(0xffffffffu, upto - m, who);
-      rank = __shfl_sync(0xffffffffu, ahead, who);
-      s += who;
-      // the slot's tokens, a unit a lane
-      float v[kPer];
-      R::floats(row.load((first + s) * 32 + lane), v);
-      uint32_t equal = 0;
+    if (!past) {
+      pick -= __shfl_sync(0xffffffffu, upto, 31);
+      rank = __shfl_sync(0xffffffffu, ahead + e, 31);
+      continue;
+    }
+    const int who = __ffs(past) - 1;
+    pick -= __shfl_sync(0xffffffffu, upto - m, who);
+    rank = __shfl_sync(0xffffffffu, ahead, who);
+    // the slot's tokens, a unit a lane
+    const int unit = (first + s + who) * 32 + lane;
+    float v[kPer];
+    Part<T>::floats(part.load(unit), v);
+    uint32_t equal = 0;
 #pragma unroll
-      for (int j = 0; j < kPer; ++j) equal += ties != UINT_MAX && v[j] == t;
-      rank += warp_scan(equal) - equal;
-      uint64_t x[kPer], sum = 0;
+    for (int j = 0; j < kPer; ++j) equal += ties != UINT_MAX && v[j] == t;
+    rank += warp_scan(equal) - equal;
+    uint64_t x[kPer], sum = 0;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const bool tie = ties != UINT_MAX && v[j] == t;
+      x[j] = tie ? (rank < ties ? wt : 0) : v[j] >= t ? weight(v[j], scale, sh.table) : 0;
+      rank += tie;
+      sum += x[j];
+    }
+    uint64_t at = warp_scan(sum);
+    const int last = __ffs(__ballot_sync(0xffffffffu, at > pick)) - 1;
+    at -= sum;
+    if (lane == last) {
+      int found = -1;
 #pragma unroll
       for (int j = 0; j < kPer; ++j) {
-        const bool tie = ties != UINT_MAX && v[j] == t;
-        x[j] = tie ? (rank < ties ? wt : 0)
-                   : v[j] >= t ? weight(v[j], scale, sh.table) : 0;
-        rank += tie;
-        sum += x[j];
+        at += x[j];
+        if (found < 0 && at > pick) found = j;
       }
-      uint64_t at = warp_scan(sum);
-      const int last = __ffs(__ballot_sync(0xffffffffu, at > pick)) - 1;
-      at -= sum;
-      if (lane == last) {
-        int found = -1;
-#pragma unroll
-        for (int j = 0; j < kPer; ++j) {
-          at += x[j];
-          if (found < 0 && at > pick) found = j;
-        }
-        a.out[b] = row.first((first + s) * 32 + lane) + found;
-      }
-      return;
+      a.out[b] = part.first(unit) + found;
     }
-    pick -= __shfl_sync(0xffffffffu, upto, 31);
-    rank = __shfl_sync(0xffffffffu, ahead + e, 31);
+    return;
   }
 }
 
 // ------------------------------------------------------------- launching
+// CTAs a row: as many as one wave of two an SM has for it, two at least; fewer where a
+// warp would have less than three slots of it.
 template <class T>
 cudaError_t run_sample(const SampleArgs& a, int64_t B, int sms, cudaStream_t s) {
+  const int64_t slots = a.V / (32 * Part<T>::kPer);
   int ctas = 1;
-  while (ctas < kMaxCluster && B * ctas < 2 * sms) ctas *= 2;
+  while (ctas < kMaxCluster && (ctas == 1 || 2 * B * ctas <= 2 * sms) &&
+         slots >= 2 * ctas * kWarps * 3)
+    ctas *= 2;
   const cudaError_t e = launch_overlapped(sample_kernel<T>, dim3(static_cast<unsigned>(B * ctas)),
                                           dim3(kThreads), 0, s, ctas, a);
   note_launch();
@@ -1062,7 +1155,7 @@ extern "C" flce_status flce_sample_logits(const void* logits, int64_t ld_logits,
                                           flce_stream_t stream) {
   OpRange range("flce_sample_logits");
   if (B < 0 || V <= 0 || !valid_dtype(dtype)) return FLCE_ERR_INVALID_ARG;
-  if (B > 65535 || V > (int64_t{1} << 21)) return FLCE_ERR_UNSUPPORTED_SHAPE;
+  if (B > 65535 || V > kMaxVocab) return FLCE_ERR_UNSUPPORTED_SHAPE;
   if (B == 0) return FLCE_OK;
   if (!logits || !u || !out || ld_logits < V) return FLCE_ERR_INVALID_ARG;
   const size_t e = dtype_bytes(dtype), nb = static_cast<size_t>(B) * 4;
