@@ -2,18 +2,17 @@
 // (flce_sample_logits).
 //
 // One CTA takes a row, or a cluster of up to eight where rows are few.  It streams the row
-// once for the largest logit of the row and of each lane's tokens; what follows reads
-// again, from L2, as little as the limits leave: a list of candidates for top-k, all of it
-// where every token's mass counts.  What a row keeps is a prefix of its tokens in
-// descending order (equal logits by id), which a logit t and a number r say: all tokens
-// above t, and the first r of those equal to t.  The token is then the first, by id, whose
-// cumulative mass among the kept ones exceeds u times their total.
+// once, for the largest logit and, where every token counts, for their mass; what follows
+// reads again, from L2, as little as the limits leave: a list of candidates for top-k, the
+// tokens near the border for top-p.  What a row keeps is a prefix of its tokens in
+// descending order (equal logits by id), which a logit t and a number say: all tokens
+// above t, and the first so many of those equal to t.  The token is then the first, by id,
+// whose cumulative mass among the kept ones exceeds u times their total.
 //
 // Masses are integers.  A token weighs 2^((l - max) / (T ln 2)) in units of 2^-42, off by
-// 2^-31.6 of it (rms), and sums of integers do not depend on their order: however the
-// row is split, the same tokens are kept and the same one is picked, and next to a
-// border the cumulative mass is right to some 1e-12 where FP32 sums would be off by
-// 1e-7, on a vocabulary with a border every 1e-5.
+// 2^-31.8 of it (rms, without bias), so that next to a border the cumulative mass is right
+// to some 1e-12, where FP32 sums would be off by 1e-7 on a vocabulary with a border every
+// 1e-5; and sums of integers do not depend on their order.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -65,9 +64,10 @@ __constant__ float2 kPow2[32] = {
     {0x1.ea4afap0f, 0x1.fda57cp-28f}, {0x1.f50766p0f, -0x1.af2102p-27f}};
 
 // What turns a row's logits into weights.  With c = 1 / (T ln 2) a weight is
-// 2^(c (l - base) - shift): base is the largest logit where |c max| is large (l - base is
-// then exact for every l that weighs anything), else 0 with shift = ceil(c max), so that
+// 2^(c (l - base) - shift): base is the largest logit where |c max| is very large (l - base
+// is then exact for every l that weighs anything), else 0 with shift = ceil(c max), so that
 // l is used as it is.  c in two floats.
+constexpr float kLargestShift = 4096.f;
 struct Scale {
   float base, least, c_hi, c_lo, magic;
 };
@@ -88,7 +88,7 @@ __device__ __forceinline__ Scale make_scale(float top, float2 c) {
   s.c_hi = c.x;
   s.c_lo = c.y;
   const float x = top * s.c_hi;
-  const bool from_top = fabsf(x) > 64.f || top == INFINITY;
+  const bool from_top = !(fabsf(x) <= kLargestShift);
   const float shift = from_top ? 0.f : ceilf(x);
   s.base = from_top ? top : 0.f;
   // below it a weight is less than 2^-59
@@ -103,9 +103,10 @@ __device__ __forceinline__ Scale make_scale(float top, float2 c) {
 // (Tang 1989) times 2^f by its series; f carries the rounding errors of x and of the
 // table's entry.  -infinity and NaN weigh nothing.  Written with intrinsics so that every
 // use rounds alike.  (Two values an instruction cost more registers than they save time.)
+template <bool BASE = true>
 __device__ __forceinline__ void weigh(float l, const Scale& s, const float2* table, uint32_t& a,
-                                       uint32_t& b) {
-  const float d = fmaxf(__fsub_rn(l, s.base), s.least);
+                                      uint32_t& b) {
+  const float d = fmaxf(BASE ? __fsub_rn(l, s.base) : l, s.least);
   const float q = __fmul_rn(d, s.c_hi);
   const float e = __fmaf_rn(d, s.c_lo, __fmaf_rn(d, s.c_hi, -q));
   const float z = __fadd_rn(q, s.magic);
@@ -141,11 +142,12 @@ template <int PER>
 struct Adder {
   uint64_t mass = 0;
   uint32_t a = 0, b = 0, n = 0;
+  template <bool BASE = true>
   __device__ __forceinline__ void add(const float (&l)[PER], const Scale& s, const float2* table) {
 #pragma unroll
     for (int j = 0; j < PER; ++j) {
       uint32_t ka, kb;
-      weigh(l[j], s, table, ka, kb);
+      weigh<BASE>(l[j], s, table, ka, kb);
       a += ka;
       b += kb;
     }
@@ -219,24 +221,36 @@ struct Part {
   // them loaded at once.
   template <int BATCH, class F>
   __device__ __forceinline__ void stream(const F& f) const {
-    for (int s = 0; s < each; s += BATCH) {
+    int s = 0;
+    for (; s + BATCH <= each; s += BATCH) {
       uint4 r[BATCH];
       const int u = u0 + s * 32;
-      if (inner && s + BATCH <= each) {
+      if (inner) {
 #pragma unroll
         for (int i = 0; i < BATCH; ++i) r[i] = aligned[u + i * 32];
       } else {
 #pragma unroll
-        for (int i = 0; i < BATCH; ++i)
-          if (s + i < each) r[i] = load(u + i * 32);
+        for (int i = 0; i < BATCH; ++i) r[i] = load(u + i * 32);
       }
 #pragma unroll
       for (int i = 0; i < BATCH; ++i) {
-        if (s + i >= each) break;
         float v[kPer];
         floats(r[i], v);
         f(i, first(u + i * 32), v);
       }
+    }
+    if (s == each) return;
+    uint4 r[BATCH];
+    const int u = u0 + s * 32;
+#pragma unroll
+    for (int i = 0; i + 1 < BATCH; ++i)
+      if (s + i < each) r[i] = load(u + i * 32);
+#pragma unroll
+    for (int i = 0; i + 1 < BATCH; ++i) {
+      if (s + i >= each) break;
+      float v[kPer];
+      floats(r[i], v);
+      f(i, first(u + i * 32), v);
     }
   }
 };
@@ -552,6 +566,49 @@ __device__ __forceinline__ float4 largest(const Part<T> part) {
   });
   return make_float4(top[0], top[1], top[2], top[3]);
 }
+// Its largest logit and its mass, in one pass: weights are relative to 2^shift, which
+// goes up with the warp's largest logit so far, and the mass with it.  For |c l| up to
+// kLargestShift where anything weighs.
+struct Mass {
+  float top;
+  uint64_t mass;
+};
+__device__ __forceinline__ uint64_t shifted(uint64_t mass, float by) {  // rounded
+  if (!(by > 0.f)) return mass;
+  if (by > 63.f) return 0;
+  const int n = static_cast<int>(by);
+  return (mass >> n) + (mass >> (n - 1) & 1);
+}
+template <class T>
+__device__ __forceinline__ Mass largest_and_mass(const Part<T> part, float2 c,
+                                                 const float2* table) {
+  constexpr int kPer = Part<T>::kPer;
+  Mass all = {-INFINITY, 0};
+  Scale s = {0.f, 0.f, c.x, c.y, 0.f};
+  Adder<kPer> sum;
+  float shift = -2.f * kLargestShift, next;  // next: the logit that weighs 1
+  const auto raise = [&] {
+    sum.flush();
+    const float to = fmaxf(shift, fminf(ceilf(warp_max(all.top) * c.x), 2.f * kLargestShift));
+    sum.mass = shifted(sum.mass, to - shift);
+    shift = to;
+    s.magic = kMagic - to;
+    s.least = __fdividef(to - 60.f, c.x);
+    next = __fdividef(to, c.x);
+  };
+  raise();
+  part.template stream<kFew>([&](int, int, const float (&v)[kPer]) {
+    float m = v[0];
+#pragma unroll
+    for (int j = 1; j < kPer; ++j) m = fmaxf(m, v[j]);
+    all.top = fmaxf(all.top, m);
+    if (__any_sync(0xffffffffu, m > next)) raise();
+    sum.template add<false>(v, s, table);
+  });
+  raise();  // (`next` is rounded)
+  all.mass = sum.mass;
+  return all;
+}
 // How many are at or above x.
 template <class T>
 __device__ __forceinline__ uint32_t count_from(const Part<T> part, float x) {
@@ -755,11 +812,26 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     }
   }
 
-  const float4 tops = largest(part);
-  const float lane_top = fmaxf(fmaxf(tops.x, tops.y), fmaxf(tops.z, tops.w));
-  float top = warp_max(lane_top);
+  // The largest logit, and, where all tokens' mass will be asked for, that too.
+  const bool by_k = !greedy && k > 0 && k < a.V, by_p = !greedy && p < 1.f;
+  bool weighed = !greedy && !by_k && (by_p || !(min_p > 0.f)) && T0 < 0x1p64f;
+  float4 tops;
+  float lane_top, top;
+  uint64_t mass = 0;
+  if (weighed) {
+    __syncthreads();  // (the table)
+    const Mass m = largest_and_mass(part, sh.inverse, sh.table);
+    lane_top = m.top;
+    tops = make_float4(m.top, m.top, m.top, m.top);  // (not used)
+    top = warp_max(lane_top);
+    mass = warp_sum_u64(m.mass);
+  } else {
+    tops = largest(part);
+    lane_top = fmaxf(fmaxf(tops.x, tops.y), fmaxf(tops.z, tops.w));
+    top = warp_max(lane_top);
+  }
   cluster_wait();
-  cl.share(0, __float_as_uint(top));
+  cl.share(mass, __float_as_uint(top));
   for (int i = lane; i < warps; i += 32) top = fmaxf(top, __uint_as_float(sh.count[cl.phase][i]));
   top = warp_max(top);
   if (top == -INFINITY) {  // nothing to pick from
@@ -767,6 +839,19 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     return;
   }
   const Scale scale = make_scale(top, sh.inverse);
+  weighed = weighed && scale.base == 0.f && top < INFINITY;
+  if (weighed) {  // every warp's mass relative to the row's largest logit, as share_kept leaves it
+    __syncthreads();
+    if (threadIdx.x < warps) {
+      const float warp_top = __uint_as_float(sh.count[cl.phase][threadIdx.x]);
+      uint64_t& m = sh.mass[cl.phase][threadIdx.x];
+      m = warp_top > -INFINITY
+              ? shifted(m, (kMagic - scale.magic) - ceilf(warp_top * scale.c_hi))
+              : 0;
+      sh.count[cl.phase][threadIdx.x] = 0;
+    }
+    __syncthreads();
+  }
   // what min_p keeps: w >= min_p w_max, l >= max + T ln(min_p), rounded up
   float least = -FLT_MAX;
   if (!greedy && min_p > 0.f && top < INFINITY) {
@@ -777,7 +862,6 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     least = rest > 0.f ? nextafterf(sum, INFINITY) : sum;
     if (!(least > -FLT_MAX)) least = -FLT_MAX;
   }
-  const bool by_k = !greedy && k > 0 && k < a.V, by_p = !greedy && p < 1.f;
   const uint64_t part_p = __float2ull_rz(fmaxf(fminf(p, 0x1.fffffep-1f), 0.f) * 0x1p64f);
   // the mass before a token that is kept is less than this
   const auto target_p = [&](uint64_t all) {  // p * all, rounded up; the first token always
@@ -917,7 +1001,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
   };
 
   if (by_k) halve(static_cast<uint64_t>(k), false);
-  bool shared = false;  // every CTA has what t and ties keep, by warps
+  bool shared = weighed;  // every CTA has what t and ties keep, by warps
   // --- top-p over many tokens: their mass, and a histogram by weight that says near which
   // one the border lies; a list of those bins' tokens then gives it.
   if (by_p) {
@@ -929,17 +1013,24 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     const int bits = unit_bits(a.V), unit = 1 << bits;
     if (__any_sync(0xffffffffu, lane_top >= t)) fill_bins(part, scale, t, unit, sh.bins);
     share_groups(cl, bits);
-    share_kept();
+    if (weighed) {
+      cluster_arrive();
+      cluster_wait();
+    } else {
+      share_kept();
+    }
     const Sum s = cl.sum();
     const uint64_t target = target_p(s.mass + weight(t, scale, sh.table) * min(s.count, ties));
     // the bins' sums are off by half a unit of them, and FP32's rounding
     const uint64_t slack = target / (2 * unit - unit / 16) + kBins;
     const int2 bins =
         find_bins(cl, bits, 2, warp == 0 ? target - min(slack, target - 1) : target + slack);
+    shared = false;
     if (bins.y < kBins - 1) {
-      // logits at and a little beyond the ends of these bins
-      const float lo = fmaxf(step_value(bins.y + 0.51f, -INFINITY, scale), t);
-      const float hi = bins.x == 0 ? INFINITY : step_value(bins.x - 0.51f, INFINITY, scale);
+      // logits a little beyond the ends of these bins (|c l| up to kLargestShift, in FP32:
+      // a token's step is right to 0.02)
+      const float lo = fmaxf(step_value(bins.y + 0.55f, -INFINITY, scale), t);
+      const float hi = bins.x == 0 ? INFINITY : step_value(bins.x - 0.55f, INFINITY, scale);
       const uint64_t mass = __any_sync(0xffffffffu, lane_top >= lo)
                                 ? list_and_weigh(part, scale, sh, lo, hi)
                                 : 0;
@@ -1079,6 +1170,31 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
   if (warp != 0) return;
   uint64_t pick = sh.before;
   uint32_t rank = sh.rank;
+  if (weighed && !by_p && t == -FLT_MAX) {
+    // The pass that weighed all rounded each lane's mass: should these sum to a unit less,
+    // the last token is taken, and if all of them weigh nothing, the first one.
+    uint64_t all = 0;
+    for (int s = lane; s < count; s += 32) all += sh.slot.mass[s];
+    all = warp_sum_u64(all);
+    if (all > 0) {
+      pick = min(pick, all - 1);
+    } else {
+#pragma unroll 1
+      for (int s = 0; s < count; ++s) {
+        const int unit = (first + s) * 32 + lane;
+        float v[kPer];
+        Part<T>::floats(part.load(unit), v);
+        int found = -1;
+#pragma unroll
+        for (int j = kPer - 1; j >= 0; --j)
+          if (v[j] >= t) found = j;
+        const uint32_t some = __ballot_sync(0xffffffffu, found >= 0);
+        if (!some) continue;
+        if (lane == __ffs(some) - 1) a.out[b] = part.first(unit) + found;
+        return;
+      }
+    }
+  }
 #pragma unroll 1
   for (int s = 0; s < count; s += 32) {
     const uint32_t e = s + lane < count ? sh.slot.ties[s + lane] : 0;
