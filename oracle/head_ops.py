@@ -101,3 +101,61 @@ def process_logits(logits, tokens=None, lengths=None, prompt_lengths=None, repet
                 if not (int(words[v // 32]) >> (v % 32)) & 1:
                     out[b, v] = -np.inf
     return out
+
+
+def layer_norm(x, weight, bias, eps, residual=None):
+    """(y, h, mean, rstd) in float64; weight and bias may be None."""
+    h = np.asarray(x, np.float64)
+    if residual is not None:
+        h = h + np.asarray(residual, np.float64)
+    mean = h.mean(-1)
+    d = h - mean[:, None]
+    rstd = 1.0 / np.sqrt((d * d).mean(-1) + eps)
+    y = d * rstd[:, None]
+    if weight is not None:
+        y = y * np.asarray(weight, np.float64)
+    if bias is not None:
+        y = y + np.asarray(bias, np.float64)
+    return y, h, mean, rstd
+
+
+def layer_norm_backward(dy, h, weight, eps, dh=None):
+    """(dx, dweight, dbias) for y = n(h) * weight + bias, plus dh on dx."""
+    dy, h = np.asarray(dy, np.float64), np.asarray(h, np.float64)
+    n, _, _, rstd = layer_norm(h, None, None, eps)
+    g = dy if weight is None else dy * np.asarray(weight, np.float64)
+    dx = g - g.mean(-1, keepdims=True) - n * (g * n).mean(-1, keepdims=True)
+    dx = rstd[:, None] * dx
+    if dh is not None:
+        dx = dx + np.asarray(dh, np.float64)
+    return dx, (dy * n).sum(0), dy.sum(0)
+
+
+def sample(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0):
+    """The token of one row, as include/flce.h defines it."""
+    l = np.asarray(logits, np.float64)
+    ids = [v for v in range(l.size) if l[v] > -np.inf]  # (NaN is no token)
+    if not ids:
+        return -1
+    ids.sort(key=lambda v: (-l[v], v))
+    if not temperature >= 2.0 ** -64:
+        return ids[0]
+    top = l[ids[0]]
+    if top == np.inf:
+        ids = [v for v in ids if l[v] == np.inf]
+        w = np.ones(len(ids))
+    else:
+        w = np.exp((l[ids] - top) / temperature)
+    n = len(ids)
+    if 0 < top_k < l.size:
+        n = min(n, top_k)
+    if top_p < 1:
+        target = top_p * w[:n].sum()
+        before = np.concatenate([[0.0], np.cumsum(w[:n])[:-1]])
+        n = max(1, int((before < target).sum()))
+    if min_p > 0:
+        n = max(1, int((w[:n] >= min(min_p, 1.0)).sum()))
+    kept = sorted(zip(ids[:n], w[:n]))
+    mass = np.cumsum([x for _, x in kept])
+    u = min(max(0.0 if np.isnan(u) else u, 0.0), 1 - 2.0 ** -24)
+    return kept[int(np.searchsorted(mass, u * mass[-1], side="right"))][0]
