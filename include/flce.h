@@ -593,7 +593,8 @@ flce_status flce_process_logits(const void* logits, int64_t ld_logits, flce_dtyp
  *     top_k   the first top_k[b] tokens                 (0 or less, or V or more: all)
  *     top_p   of these, those before which the mass, the sum of w, is less than top_p[b]
  *             times that of all of them; the first one always    (1 or more: all)
- *     min_p   of these, those with w >= min_p[b]; the first one always   (0 or less: all)
+ *     min_p   of these, those with w >= min_p[b]; the first one always   (0 or less: all;
+ *             more than 1 is 1)
  *
  * and out[b] is the first token, by id, at which the mass of the kept ones up to it
  * exceeds u[b] times the mass of all kept ones.
@@ -603,10 +604,12 @@ flce_status flce_process_logits(const void* logits, int64_t ld_logits, flce_dtyp
  *   u        device float [B], in [0, 1) (else clamped to it; NaN is 0).
  *   temperature, top_p, min_p   device float [B], top_k device int32 [B]; each may be
  *            NULL (1, 1, 0, 0).  A temperature below 2^-64, or NaN, takes the largest logit
- *            (the lowest id of equals), whatever the limits and u.  A NaN limit is no limit.
+ *            (the lowest id of equals), whatever the limits and u; one above 2^100
+ *            is 2^100.  A NaN limit is no limit.
  *   out      device int64 [B]; -1 where the row has no token.
- * Weights are right to 2^-31 of them (2^-43 of the largest) and are added as integers, so
- * that the result does not depend on how a row is split.  B <= 65535, V <= 2^21.
+ * Weights are right to 2^-29 of them (a root mean square of 2^-31.8) and 2^-43 of the
+ * largest, and are added as integers: a call that is repeated gives the same tokens.
+ * B <= 65535, V <= 2^21.
  */
 flce_status flce_sample_logits(const void* logits, int64_t ld_logits, flce_dtype dtype, int64_t B,
                                int64_t V, const float* u, const float* temperature,

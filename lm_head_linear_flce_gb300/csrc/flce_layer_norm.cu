@@ -168,7 +168,8 @@ __global__ void __launch_bounds__(1024)
     const float off = apart - m1;
     squares = warp_sum(fmaf(off, fmaf(own.x, off, 2.f * own.z), own.w));
   }
-  const float r = rsqrtf(fmaf(fmaxf(squares, 0.f), inv_h, eps));
+  // (a row with NaN or an infinity has a variance of NaN, and keeps it)
+  const float r = rsqrtf(fmaf(squares < 0.f ? 0.f : squares, inv_h, eps));
   if (rstd && threadIdx.x == 0) {
     mean[row] = m0 + m1;
     rstd[row] = r;
@@ -540,7 +541,8 @@ __global__ void __launch_bounds__(kNormThreads)
     squares = fmaf(d, d, squares);
   }
   const float m1 = block_sum(rest) / n;
-  const float r = rsqrtf(fmaxf(block_sum(squares) / n - m1 * m1, 0.f) + eps);
+  const float variance = block_sum(squares) / n - m1 * m1;
+  const float r = rsqrtf((variance < 0.f ? 0.f : variance) + eps);  // (NaN stays NaN)
   if (rstd && threadIdx.x == 0) {
     mean[row] = m0 + m1;
     rstd[row] = r;

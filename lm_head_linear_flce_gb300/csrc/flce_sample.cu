@@ -34,6 +34,9 @@ constexpr int kMaxWarps = kWarps * kMaxCluster;  // of a row
 constexpr int64_t kMaxVocab = int64_t{1} << 21;
 constexpr int kMaxSlots = 1032;           // of a warp: kMaxVocab float32 logits in one CTA
 constexpr float kGreedyBelow = 0x1p-64f;  // temperatures that take the largest logit
+// The largest temperature (all logits up to 2^50 weigh the same there): 1 / T in two floats
+// is as precise as weights need it up to about 2^117.
+constexpr float kHottest = 0x1p100f;
 
 struct SampleArgs {
   const void* logits;
@@ -83,7 +86,7 @@ __device__ __forceinline__ float2 inverse_of(float T) {
   return make_float2(hi, __fdividef(fmaf(-hi, T, kHi) + kLo, T));
 }
 __device__ __forceinline__ Scale make_scale(float top, float2 c) {
-  if (!(c.x > 0.f) || top == INFINITY) c = make_float2(0.f, 0.f);  // every token alike
+  if (top == INFINITY) return {top, 0.f, 0.f, 0.f, kMagic};  // (only +infinities are weighed)
   Scale s;
   s.c_hi = c.x;
   s.c_lo = c.y;
@@ -91,9 +94,7 @@ __device__ __forceinline__ Scale make_scale(float top, float2 c) {
   const bool from_top = !(fabsf(x) <= kLargestShift);
   const float shift = from_top ? 0.f : ceilf(x);
   s.base = from_top ? top : 0.f;
-  // below it a weight is less than 2^-59
-  s.least = top == INFINITY ? 0.f : s.c_hi > 0.f ? fmaxf(__fdividef(shift - 60.f, s.c_hi), -FLT_MAX)
-                                                 : -FLT_MAX;
+  s.least = __fdividef(shift - 60.f, s.c_hi);  // below it a weight is less than 2^-59
   s.magic = kMagic - shift;
   return s;
 }
@@ -477,7 +478,6 @@ __device__ __forceinline__ float distance_cut(int last, float top) {
 }
 // The logit of `step` 64ths of an octave, rounded towards `to`.
 __device__ __forceinline__ float step_value(float step, float to, const Scale& s) {
-  if (!(s.c_hi > 0.f)) return to;
   const float d = __fdiv_rn((kMagic - s.magic) - step * (1.f / 64), s.c_hi);
   return nextafterf(__fadd_rn(s.base, nextafterf(d, to)), to);
 }
@@ -783,7 +783,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
   part.u0 = s0 * 32 + lane;
   part.inner = part.whole(s0 * 32) && part.whole((s0 + part.each) * 32 - 1);
 
-  const float T0 = a.temperature ? a.temperature[b] : 1.f;
+  const float T_given = a.temperature ? a.temperature[b] : 1.f;
+  const float T0 = T_given > kHottest ? kHottest : T_given;  // (NaN stays)
   const int k = a.top_k ? a.top_k[b] : 0;
   const float p = a.top_p ? a.top_p[b] : 1.f;
   const float min_p = a.min_p ? a.min_p[b] : 0.f;
@@ -839,7 +840,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     return;
   }
   const Scale scale = make_scale(top, sh.inverse);
-  weighed = weighed && scale.base == 0.f && top < INFINITY;
+  weighed = weighed && scale.base == 0.f;
   if (weighed) {  // every warp's mass relative to the row's largest logit, as share_kept leaves it
     __syncthreads();
     if (threadIdx.x < warps) {
@@ -873,7 +874,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
   // first CTA then has to itself.  k of the largest logits of quarters of lanes are in the
   // bins up to the one that holds the k-th, so are k tokens; other quarters have none there.
   // Where quarters are not many more than k, all tokens are counted instead.
-  if (by_k && k <= kList / 2) {
+  if (by_k && k <= kList / 2 && top < INFINITY) {
     if (2 * k > min(4 * warps, part.slots) * 32) {
       count_bins(part, top, sh.bins);
     } else {
@@ -942,17 +943,13 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
   }
 
   // --- otherwise what is kept as t and ties, which the limits narrow one after another.
-  float t = top < INFINITY ? -FLT_MAX : top;
-  uint32_t ties = UINT_MAX;
-  if (greedy) {
-    t = top;
-    ties = 1;
-  }
+  float t = greedy || top == INFINITY ? top : -FLT_MAX;
+  uint32_t ties = greedy ? 1 : top == INFINITY ? UINT_MAX - 1 : UINT_MAX;
   // Of the lane's tokens, as far as its warp has any (x > -infinity).
   const auto mass_from = [&](float x) {
     if (!__any_sync(0xffffffffu, lane_top >= x)) return uint64_t{0};
-    return x == -FLT_MAX && scale.least > -FLT_MAX ? weigh_all(part, scale, sh.table)
-                                                   : weigh_from(part, scale, sh.table, x);
+    return x == -FLT_MAX ? weigh_all(part, scale, sh.table)
+                         : weigh_from(part, scale, sh.table, x);
   };
   const auto number_from = [&](float x) {
     return __any_sync(0xffffffffu, lane_top >= x) ? count_from(part, x) : 0u;
@@ -1000,11 +997,20 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     cl.share(warp_sum_u64(m), __reduce_add_sync(0xffffffffu, n));
   };
 
-  if (by_k) halve(static_cast<uint64_t>(k), false);
   bool shared = weighed;  // every CTA has what t and ties keep, by warps
+  if (top == INFINITY && !greedy) {  // each +infinity weighs 1, all else nothing
+    share_kept();
+    shared = true;
+    ties = cl.sum().count;
+    if (by_k) ties = min(ties, static_cast<uint32_t>(k));
+    if (by_p)
+      ties = static_cast<uint32_t>((target_p(uint64_t{ties} << 42) + (uint64_t{1} << 42) - 1) >> 42);
+  } else if (by_k) {
+    halve(static_cast<uint64_t>(k), false);
+  }
   // --- top-p over many tokens: their mass, and a histogram by weight that says near which
   // one the border lies; a list of those bins' tokens then gives it.
-  if (by_p) {
+  if (by_p && top < INFINITY) {
     if (by_k) {  // (the bins have been used)
       for (int i = threadIdx.x; i < kBins; i += kThreads) sh.bins[i] = 0;
       if (threadIdx.x == 0) sh.listed = 0;
@@ -1151,13 +1157,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
       if (!(v[j] >= t) || tie) v[j] = -INFINITY;
     }
     Adder<kPer> sum;
-    if (scale.least > -FLT_MAX) {
+    if (t < INFINITY) {  // (where it is not, ties are all that weighs)
       sum.add(v, scale, sh.table);
       sum.flush();
-    } else {  // (-infinity weighs as much as any)
-#pragma unroll
-      for (int j = 0; j < kPer; ++j)
-        if (v[j] > -INFINITY) sum.mass += weight(v[j], scale, sh.table);
     }
     sum.mass = warp_sum_u64(sum.mass);
     e = __reduce_add_sync(0xffffffffu, e);

@@ -325,6 +325,7 @@ PyObject* layer_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const bool need_dw = PyObject_IsTrue(a[7]);
   TORCH_CHECK_VALUE(!need_dw || m.weight.defined(), "dweight needs weight");
   const int64_t bias_type = integer(a[8]);
+  TORCH_CHECK_VALUE(bias_type <= FLCE_F32, "bias must be bfloat16 or float32");
   TORCH_CHECK_VALUE(bias_type < 0 || !m.weight.defined() || bias_type == m.weight_type,
                     "weight and bias must have the same type");
   if (bias_type >= 0) m.weight_type = static_cast<flce_dtype>(bias_type);

@@ -134,19 +134,20 @@ def layer_norm_backward(dy, h, weight, eps, dh=None):
 def sample(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0):
     """The token of one row, as include/flce.h defines it."""
     l = np.asarray(logits, np.float64)
-    ids = [v for v in range(l.size) if l[v] > -np.inf]  # (NaN is no token)
-    if not ids:
+    ids = np.flatnonzero(l > -np.inf)  # (NaN is no token)
+    if not ids.size:
         return -1
-    ids.sort(key=lambda v: (-l[v], v))
+    ids = ids[np.argsort(-l[ids], kind="stable")]
     if not temperature >= 2.0 ** -64:
-        return ids[0]
+        return int(ids[0])
+    temperature = min(temperature, 2.0 ** 100)
     top = l[ids[0]]
     if top == np.inf:
-        ids = [v for v in ids if l[v] == np.inf]
-        w = np.ones(len(ids))
+        ids = ids[l[ids] == np.inf]
+        w = np.ones(ids.size)
     else:
         w = np.exp((l[ids] - top) / temperature)
-    n = len(ids)
+    n = ids.size
     if 0 < top_k < l.size:
         n = min(n, top_k)
     if top_p < 1:
@@ -155,7 +156,7 @@ def sample(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0):
         n = max(1, int((before < target).sum()))
     if min_p > 0:
         n = max(1, int((w[:n] >= min(min_p, 1.0)).sum()))
-    kept = sorted(zip(ids[:n], w[:n]))
-    mass = np.cumsum([x for _, x in kept])
+    by_id = np.argsort(ids[:n])
+    ids, mass = ids[by_id], np.cumsum(w[by_id])
     u = min(max(0.0 if np.isnan(u) else u, 0.0), 1 - 2.0 ** -24)
-    return kept[int(np.searchsorted(mass, u * mass[-1], side="right"))][0]
+    return int(ids[np.searchsorted(mass, u * mass[-1], side="right")])
