@@ -139,11 +139,10 @@ __device__ __forceinline__ uint64_t weight(float l, const Scale s, const float2*
 }
 
 // Weights being added up.
-template <int PER>
 struct Adder {
   uint64_t mass = 0;
   uint32_t a = 0, b = 0, n = 0;
-  template <bool BASE = true>
+  template <bool BASE = true, int PER>
   __device__ __forceinline__ void add(const float (&l)[PER], const Scale& s, const float2* table) {
 #pragma unroll
     for (int j = 0; j < PER; ++j) {
@@ -460,6 +459,72 @@ __device__ __forceinline__ uint64_t scan_list(uint64_t* w, int n, int threads, u
   return carry;
 }
 
+// Of the n tokens in work, which weigh list[], the largest logit down to which the mass
+// reaches `target`, and the mass above it; `above` is that above hi, and logits are from lo
+// to hi.  Every warp sums up from another key on, so that a round leaves a sixteenth of
+// the keys; after the first, the tokens between alone.  (Up to 2000 tokens: 1.5 us in
+// bf16, whose keys are few, and 3 to 5 in float32, where sorting them takes 3 to 8.)
+struct Border {
+  bool found;
+  float logit;
+  uint64_t above;
+};
+template <class T>
+__device__ __forceinline__ Border find_border(Shared& sh, int n, uint64_t above, uint64_t target,
+                                              float lo, float hi) {
+  static_assert(kWarps == 16 && kList * 2 + kWarps * 16 <= sizeof(sh.weights));
+  constexpr int kShift = 32 + (sizeof(T) == 2 ? 16 : 0);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const auto key_at = [&](int i) { return static_cast<uint32_t>(sh.work[i] >> kShift); };
+  uint16_t* const left = reinterpret_cast<uint16_t*>(sh.weights + 2 * kWarps);
+  uint32_t first = static_cast<uint32_t>(list_entry(lo, 0) >> kShift);
+  uint64_t keys = static_cast<uint32_t>(list_entry(hi, 0) >> kShift) - first + uint64_t{1};
+  if (above >= target) return {false, 0.f, 0};
+  if (threadIdx.x == 0) sh.rank = 0;
+#pragma unroll 1
+  for (int round = 0;; ++round) {
+    const auto from = [&](int w) { return first + static_cast<uint32_t>(keys * w >> 4); };
+    const uint32_t mine = from(warp);
+    uint64_t m = 0;
+    if (round == 0) {
+#pragma unroll 4
+      for (int i = lane; i < n; i += 32)
+        if (key_at(i) >= mine) m += sh.list[i];
+    } else {
+      const uint32_t most = first + static_cast<uint32_t>(keys) - mine;
+#pragma unroll 1
+      for (int i = lane; i < n; i += 32)
+        if (key_at(left[i]) - mine < most) m += sh.list[left[i]];
+    }
+    m = warp_sum_u64(m);
+    uint64_t* const sums = sh.weights + (round & 1) * kWarps;
+    if (lane == 0) sums[warp] = above + m;
+    __syncthreads();
+    const uint64_t s = lane < kWarps ? sums[lane] : 0;
+    const uint32_t reach = __ballot_sync(0xffffffffu, lane < kWarps && s >= target);
+    if (!reach) return {false, 0.f, 0};
+    const int w = 31 - __clz(reach);
+    const uint64_t next = __shfl_sync(0xffffffffu, s, (w + 1) & 31);
+    const uint32_t end = w + 1 < kWarps ? from(w + 1) : first + static_cast<uint32_t>(keys);
+    first = from(w);
+    keys = end - first;  // (a row's first round may have 2^32: less from then on)
+    if (w + 1 < kWarps) above = next;
+    if (keys == 1) break;
+    if (round == 0) {  // from here on the tokens between
+      for (int i = threadIdx.x; i < n; i += kThreads) {
+        const uint32_t k = key_at(i) - first;
+        if (k < keys) left[atomicAdd(&sh.rank, 1)] = static_cast<uint16_t>(i);
+      }
+      __syncthreads();
+      n = static_cast<int>(sh.rank);
+    }
+  }
+  // (a negative bf16's key ends in ones)
+  uint64_t key = static_cast<uint64_t>(first) << kShift;
+  if (sizeof(T) == 2 && !(key >> 63)) key |= uint64_t{0xffff} << 32;
+  return {true, listed_logit(key), above};
+}
+
 // ------------------------------------------------------------------- bins
 // Bins of a token: of its distance from the largest logit, 1/64 of its octave each from
 // 2^-12 on, for counts (a distance of any size lies in one of them); of its weight, 1/64
@@ -485,15 +550,23 @@ __device__ __forceinline__ float step_value(float step, float to, const Scale& s
 // 2^-bits of that: the weight there is 1 within 0.55%, and rounded to a unit, so sums are
 // right to half a unit a token.  A row's tokens in one bin must stay below 2^32.
 __device__ __forceinline__ int unit_bits(int V) { return min(13, __clz(V - 1) - 1); }
-__device__ __forceinline__ uint32_t beside_middle(float l, const Scale& s, float unit, int& bin) {
-  constexpr float kRound = 0x1.8p23f;  // + x: its last bits are x's nearest integer
-  const float d = fmaxf(__fsub_rn(l, s.base), s.least);
+// For logits that weigh 2^(1 - kBins/64) at least.
+struct Beside {
+  float c, shift, a, b, one;
+};
+constexpr float kRound = 0x1.8p23f;  // + x: its last bits are x's nearest integer
+__device__ __forceinline__ Beside beside(const Scale& s, float unit) {
+  constexpr float kStep = 0.010830424696f;  // ln 2 / 64
+  return {-64.f * s.c_hi, 64.f * (kMagic - s.magic), 0.5f * kStep * kStep * unit, -kStep * unit,
+          unit + kRound};
+}
+__device__ __forceinline__ uint32_t beside_middle(float l, const Scale& s, const Beside& m, int& bin) {
   // -64 log2 of the weight
-  const float x = __fmul_rn(64.f, __fmaf_rn(d, -s.c_hi, kMagic - s.magic));
+  const float x = __fmaf_rn(__fsub_rn(l, s.base), m.c, m.shift);
   const float k = __fadd_rn(x, kRound);
-  bin = min(max(__float_as_int(k) - __float_as_int(kRound), 0), kBins - 1);
-  const float y = __fsub_rn(x, __fsub_rn(k, kRound)) * -0.010830424696f;  // (ln 2 / 64)
-  const float n = __fmaf_rn(unit, __fmaf_rn(y, __fmaf_rn(y, 0.5f, 1.f), 1.f), kRound);
+  bin = __float_as_int(k) - __float_as_int(kRound);
+  const float y = __fsub_rn(x, __fsub_rn(k, kRound));
+  const float n = __fmaf_rn(y, __fmaf_rn(y, m.a, m.b), m.one);
   return static_cast<uint32_t>(__float_as_int(n) - __float_as_int(kRound));
 }
 // What n in bin i amounts to; bits: of the unit, or -1 where tokens are counted.
@@ -585,7 +658,7 @@ __device__ __forceinline__ Mass largest_and_mass(const Part<T> part, float2 c,
   constexpr int kPer = Part<T>::kPer;
   Mass all = {-INFINITY, 0};
   Scale s = {0.f, 0.f, c.x, c.y, 0.f};
-  Adder<kPer> sum;
+  Adder sum;
   float shift = -2.f * kLargestShift, next;  // next: the logit that weighs 1
   const auto raise = [&] {
     sum.flush();
@@ -622,7 +695,7 @@ __device__ __forceinline__ uint32_t count_from(const Part<T> part, float x) {
 // Their mass.
 template <class T>
 __device__ __forceinline__ uint64_t weigh_all(const Part<T> part, const Scale s, const float2* table) {
-  Adder<Part<T>::kPer> sum;
+  Adder sum;
   part.template stream<kFew>(
       [&](int, int, const float (&v)[Part<T>::kPer]) { sum.add(v, s, table); });
   sum.flush();
@@ -632,7 +705,7 @@ __device__ __forceinline__ uint64_t weigh_all(const Part<T> part, const Scale s,
 template <class T>
 __device__ __forceinline__ uint64_t weigh_from(const Part<T> part, const Scale s, const float2* table,
                                             float x) {
-  Adder<Part<T>::kPer> sum;
+  Adder sum;
   part.template stream<kFew>([&](int, int, const float (&v)[Part<T>::kPer]) {
     float w[Part<T>::kPer];
     bool some = false;
@@ -659,11 +732,12 @@ __device__ __forceinline__ void count_bins(const Part<T> part, float top, uint32
 template <class T>
 __device__ __forceinline__ void fill_bins(const Part<T> part, const Scale s, float x, float unit,
                                           uint32_t* bins) {
+  const Beside m = beside(s, unit);
   part.template stream<kFew>([&](int, int, const float (&v)[Part<T>::kPer]) {
 #pragma unroll
     for (int j = 0; j < Part<T>::kPer; ++j) {
       int bin;
-      const uint32_t n = beside_middle(v[j], s, unit, bin);
+      const uint32_t n = beside_middle(v[j], s, m, bin);
       if (v[j] >= x) atomicAdd(&bins[bin], n);
     }
   });
@@ -716,17 +790,27 @@ __device__ __forceinline__ void list_from(const Part<T> part, Shared& sh, float 
 template <class T>
 __device__ __forceinline__ uint64_t list_and_weigh(const Part<T> part, const Scale s, Shared& sh,
                                                 float lo, float hi) {
-  Adder<Part<T>::kPer> sum;
+  Adder sum;
   part.template stream<kFew>([&](int, int c, const float (&v)[Part<T>::kPer]) {
+    float most = v[0];
+#pragma unroll
+    for (int j = 1; j < Part<T>::kPer; ++j) most = fmaxf(most, v[j]);
+    if (!__any_sync(0xffffffffu, most >= lo)) return;
     list_unit(sh, c, v, lo, hi);
+    if (!__any_sync(0xffffffffu, most > hi)) return;
     float w[Part<T>::kPer];
-    bool some = false;
+    int over = 0;
 #pragma unroll
     for (int j = 0; j < Part<T>::kPer; ++j) {
-      some = some || v[j] > hi;
+      over += v[j] > hi;
       w[j] = v[j] > hi ? v[j] : -INFINITY;
     }
-    if (__any_sync(0xffffffffu, some)) sum.add(w, s, sh.table);
+    if (__any_sync(0xffffffffu, over > 1)) {
+      sum.add(w, s, sh.table);
+    } else {  // one a lane at most
+      const float one[1] = {over ? most : -INFINITY};
+      sum.add(one, s, sh.table);
+    }
   });
   sum.flush();
   return sum.mass;
@@ -1017,16 +1101,19 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
       __syncthreads();
     }
     const int bits = unit_bits(a.V), unit = 1 << bits;
-    if (__any_sync(0xffffffffu, lane_top >= t)) fill_bins(part, scale, t, unit, sh.bins);
-    share_groups(cl, bits);
-    if (weighed) {
-      cluster_arrive();
-      cluster_wait();
-    } else {
-      share_kept();
-    }
+    if (!weighed) share_kept();
     const Sum s = cl.sum();
-    const uint64_t target = target_p(s.mass + weight(t, scale, sh.table) * min(s.count, ties));
+    const uint64_t all = s.mass + weight(t, scale, sh.table) * min(s.count, ties);
+    const uint64_t target = target_p(all);
+    // Tokens of less than 1 / V of the mass that p leaves out amount to less than that, so
+    // the border is above them.  (In FP32, and where weights are many units.)
+    const float small = static_cast<float>(all - target) / static_cast<float>(a.V) * 0.99f;
+    const float steps = small >= 64.f ? (42.f - log2f(small)) * 64.f : 0x1p30f;
+    const float from = fmaxf(t, step_value(fminf(steps, kBins - 2.f), INFINITY, scale));
+    if (__any_sync(0xffffffffu, lane_top >= from)) fill_bins(part, scale, from, unit, sh.bins);
+    share_groups(cl, bits);
+    cluster_arrive();
+    cluster_wait();
     // the bins' sums are off by half a unit of them, and FP32's rounding
     const uint64_t slack = target / (2 * unit - unit / 16) + kBins;
     const int2 bins =
@@ -1043,36 +1130,21 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
       const Sum in = share_list(cl, warp_sum_u64(mass));
       if (in.count <= kList) {
         pull_lists(cl, in.count);
-        if (threadIdx.x == 0) sh.found[0] = 0;
         cluster_arrive();
         cluster_wait();
-        const int size = list_size(in.count), threads = min(size / 2, kThreads);
         const int n = static_cast<int>(in.count);
-        if (threadIdx.x < threads) {
-          sort_list(sh.work, size, threads);
-          uint64_t* upto = sh.list;  // (all have read it)
-          for (int i = threadIdx.x; i < n; i += threads)
-            upto[i] = weight(listed_logit(sh.work[i]), scale, sh.table);
-          bar_first(threads);
-          scan_list(upto, n, threads, sh.part);
-          for (int i = threadIdx.x; i < n; i += threads)
-            if (in.mass + upto[i] >= target &&
-                (i ? in.mass + upto[i - 1] : in.mass) < target) {  // the border: at most one
-              int equal = i;
-              while (equal > 0 && sh.work[equal - 1] >> 32 == sh.work[i] >> 32) --equal;
-              sh.rank = static_cast<uint32_t>(i - equal + 1);
-              sh.cut = listed_logit(sh.work[i]);
-              sh.found[0] = 1;
-            }
-        }
-        // every warp's mass above the border's logit and tokens equal to it, as
-        // share_kept would leave them
+        for (int i = threadIdx.x; i < n; i += kThreads)  // (all have read the list)
+          sh.list[i] = weight(listed_logit(sh.work[i]), scale, sh.table);
         if (threadIdx.x < warps) sh.count[cl.phase][threadIdx.x] = 0;
         __syncthreads();
-        shared = sh.found[0] == 1;
+        const Border border = find_border<T>(sh, n, in.mass, target, lo, fminf(hi, top));
+        shared = border.found;
         if (shared) {
-          t = sh.cut;
-          ties = sh.rank;
+          // every warp's mass above the border's logit and tokens equal to it, as
+          // share_kept would leave them
+          t = border.logit;
+          const uint64_t w1 = max(weight(t, scale, sh.table), uint64_t{1});
+          ties = static_cast<uint32_t>((target - border.above + w1 - 1) / w1);
           for (int i = threadIdx.x; i < n; i += kThreads) {
             const float l = listed_logit(sh.work[i]);
             if (!(l >= t)) continue;
@@ -1156,7 +1228,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
       e += tie;
       if (!(v[j] >= t) || tie) v[j] = -INFINITY;
     }
-    Adder<kPer> sum;
+    Adder sum;
     if (t < INFINITY) {  // (where it is not, ties are all that weighs)
       sum.add(v, scale, sh.table);
       sum.flush();

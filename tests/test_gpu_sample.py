@@ -155,6 +155,19 @@ def test_edges_of_the_arguments():
     assert got.tolist() == [7, 7, 7]
 
 
+@pytest.mark.parametrize("V", [40, 3000, 40000])
+def test_zeros_of_both_signs_are_equal(V):
+    g = torch.Generator().manual_seed(11)
+    for dt in (BF, F32):
+        l = torch.where(torch.rand(6, V, generator=g) < 0.5, 0.0, -0.0)
+        l[3:] -= (torch.rand(3, V, generator=g) < 0.3).float() * 1e-3
+        l = l.to(dt).cuda()
+        u, k, p = rand(g, 6), ints(g, 6, V), rand(g, 6)
+        for kw in (dict(), dict(top_k=k), dict(top_k=k % 20 + 1), dict(top_p=p),
+                   dict(top_k=k, top_p=p), dict(min_p=p)):
+            check(l, u, **kw)
+
+
 def test_values_that_are_no_numbers():
     V = 700
     g = torch.Generator().manual_seed(6)
