@@ -306,11 +306,6 @@ __device__ __forceinline__ void cluster_wait() {
   __syncwarp();
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// A barrier of the block's first `threads` threads.
-__device__ __forceinline__ void bar_first(int threads) {
-  asm volatile("bar.sync 1, %0;" ::"r"(threads) : "memory");
-}
-
 constexpr int kList = 2048;        // tokens of a list
 constexpr int kBins = 2048;        // of a histogram
 constexpr int kGroups = 32;        // of bins, whose sums the CTAs exchange
@@ -332,15 +327,14 @@ struct Shared {
       uint32_t ties[kMaxSlots];
     } slot;  // of the warp that has the token
   };
-  uint64_t weights[kList / 2];
+  uint64_t weights[kList / 2];  // select_key's
   uint64_t part[kWarps];
   float2 table[32];
   float2 inverse;    // c of the temperature
   float2 log_min_p;  // T ln(min_p)
-  uint64_t before;
+  uint64_t before, border;
   uint32_t listed, rank;
   int found[2];
-  float cut;
 };
 
 struct Sum {
@@ -375,9 +369,6 @@ struct Cluster {
 };
 
 // ------------------------------------------------------- lists in shared memory
-__device__ __forceinline__ int list_size(uint32_t n) {  // a power of two, 64 at least
-  return n <= 64 ? 64 : 2 << (31 - __clz(static_cast<int>(n) - 1));
-}
 __device__ __forceinline__ uint64_t list_entry(float l, int id) {
   const uint32_t key = static_cast<uint32_t>(key_of<float>(l + 0.f)) ^ 0x80000000u;
   return static_cast<uint64_t>(key) << 32 | (static_cast<uint32_t>(id) ^ 0xffffffffu);
@@ -389,140 +380,111 @@ __device__ __forceinline__ int listed_id(uint64_t e) {
   return static_cast<int>(~static_cast<uint32_t>(e));
 }
 
-// Sorts the first n (a power of two, 64 at least) of v, the larger first, with the block's
-// first `threads` = min(n / 2, kThreads) threads, which alone call it.  Bitonic; a warp has
-// 64 neighbours in registers where strides are shorter.
-__device__ __forceinline__ void sort_list(uint64_t* v, int n, int threads) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-#pragma unroll 1
-  for (int size = 64; size <= n; size <<= 1) {
-#pragma unroll 1
-    for (int stride = size / 2; stride > 32; stride >>= 1) {
-      for (int t = threadIdx.x; t < n / 2; t += threads) {
-        const int i = 2 * t - (t & (stride - 1)), k = i + stride;
-        const uint64_t a = v[i], b = v[k];
-        if ((a < b) == ((i & size) == 0)) {
-          v[i] = b;
-          v[k] = a;
-        }
-      }
-      bar_first(threads);
-    }
-    for (int i0 = 64 * warp; i0 < n; i0 += 2 * threads) {
-      uint64_t a = v[i0 + lane], b = v[i0 + lane + 32];
-      const auto exchange = [&](int z, int stride) {
-        const uint64_t x = __shfl_xor_sync(0xffffffffu, a, stride),
-                       y = __shfl_xor_sync(0xffffffffu, b, stride);
-        const bool low = (lane & stride) == 0;
-        if ((a < x) == (low == (((i0 + lane) & z) == 0))) a = x;
-        if ((b < y) == (low == (((i0 + lane + 32) & z) == 0))) b = y;
-      };
-      if (size == 64) {  // from single elements on
-#pragma unroll 1
-        for (int z = 2; z < 64; z <<= 1)
-#pragma unroll 1
-          for (int stride = z / 2; stride > 0; stride >>= 1) exchange(z, stride);
-      }
-      if ((a < b) == ((i0 & size) == 0)) {
-        const uint64_t x = a;
-        a = b;
-        b = x;
-      }
-#pragma unroll 1
-      for (int stride = 16; stride > 0; stride >>= 1) exchange(size, stride);
-      v[i0 + lane] = a;
-      v[i0 + lane + 32] = b;
-    }
-    bar_first(threads);
-  }
+// The block's sum, on every thread.
+__device__ __forceinline__ uint64_t block_sum(Shared& sh, uint64_t v) {
+  const int lane = threadIdx.x & 31;
+  v = warp_sum_u64(v);
+  if (lane == 0) sh.part[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = warp_sum_u64(lane < kWarps ? sh.part[lane] : 0);
+  __syncthreads();
+  return v;
 }
 
-// Sums of w[0 .. n) up to and including each, in place, by the block's first `threads`
-// threads (a multiple of 32), which alone call it; returns the total.
-__device__ __forceinline__ uint64_t scan_list(uint64_t* w, int n, int threads, uint64_t* part) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  uint64_t carry = 0;
-#pragma unroll 1
-  for (int i0 = 0; i0 < n; i0 += threads) {
-    const int i = i0 + threadIdx.x;
-    const uint64_t x = warp_scan(i < n ? w[i] : uint64_t{0});
-    if (lane == 31) part[warp] = x;
-    bar_first(threads);
-    const int warps = threads / 32;
-    const uint64_t p = lane < warps ? part[lane] : 0;
-    const uint64_t upto = warp_scan(p);
-    const uint64_t before = __shfl_sync(0xffffffffu, upto - p, warp);
-    if (i < n) w[i] = carry + before + x;
-    carry += __shfl_sync(0xffffffffu, upto, warps - 1);
-    bar_first(threads);
-  }
-  return carry;
-}
-
-// Of the n tokens in work, which weigh list[], the largest logit down to which the mass
-// reaches `target`, and the mass above it; `above` is that above hi, and logits are from lo
-// to hi.  Every warp sums up from another key on, so that a round leaves a sixteenth of
-// the keys; after the first, the tokens between alone.  (Up to 2000 tokens: 1.5 us in
-// bf16, whose keys are few, and 3 to 5 in float32, where sorting them takes 3 to 8.)
+// Of a list's n tokens (fewer than kList), the key at which the weights of tokens with that
+// key or a larger one reach `target`, as all of them do; and the weight above that key.
+// key(i): from `first` to `last`, or 0 where a token does not count; weight_of(i): at most
+// 2^42.
+//
+// A round adds the weights up in 512 bins of the range (two halves of 21 bits each) and
+// goes on with the tokens of the one that has the border; 64 tokens are compared with one
+// another.  Nothing is sorted: an order by logit and then one by id take 8 us for 1000
+// tokens and 2.5 us for one, these searches 2 and 1.
 struct Border {
-  bool found;
-  float logit;
-  uint64_t above;
+  uint64_t key, above;
 };
-template <class T>
-__device__ __forceinline__ Border find_border(Shared& sh, int n, uint64_t above, uint64_t target,
-                                              float lo, float hi) {
-  static_assert(kWarps == 16 && kList * 2 + kWarps * 16 <= sizeof(sh.weights));
-  constexpr int kShift = 32 + (sizeof(T) == 2 ? 16 : 0);
+template <class K, class W>
+__device__ __forceinline__ Border select_key(Shared& sh, int n, const K& key, const W& weight_of,
+                                               uint64_t first, uint64_t last, uint64_t target) {
+  constexpr int kHalf = 21, kCompared = 64, kEach = kThreads / kCompared;
+  static_assert(sizeof(sh.weights) >= 8 * kThreads + 2 * kList && kList % kThreads == 0);
+  uint32_t* const upper = reinterpret_cast<uint32_t*>(sh.weights);
+  uint32_t* const lower = upper + kThreads;
+  uint16_t* const left = reinterpret_cast<uint16_t*>(lower + kThreads);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const auto key_at = [&](int i) { return static_cast<uint32_t>(sh.work[i] >> kShift); };
-  uint16_t* const left = reinterpret_cast<uint16_t*>(sh.weights + 2 * kWarps);
-  uint32_t first = static_cast<uint32_t>(list_entry(lo, 0) >> kShift);
-  uint64_t keys = static_cast<uint32_t>(list_entry(hi, 0) >> kShift) - first + uint64_t{1};
-  if (above >= target) return {false, 0.f, 0};
-  if (threadIdx.x == 0) sh.rank = 0;
+  bool whole = true;  // (then all are left)
+  const auto at = [&](int q) { return whole ? q : static_cast<int>(left[q]); };
+  uint64_t above = 0;
 #pragma unroll 1
-  for (int round = 0;; ++round) {
-    const auto from = [&](int w) { return first + static_cast<uint32_t>(keys * w >> 4); };
-    const uint32_t mine = from(warp);
-    uint64_t m = 0;
-    if (round == 0) {
-#pragma unroll 4
-      for (int i = lane; i < n; i += 32)
-        if (key_at(i) >= mine) m += sh.list[i];
-    } else {
-      const uint32_t most = first + static_cast<uint32_t>(keys) - mine;
-#pragma unroll 1
-      for (int i = lane; i < n; i += 32)
-        if (key_at(left[i]) - mine < most) m += sh.list[left[i]];
-    }
-    m = warp_sum_u64(m);
-    uint64_t* const sums = sh.weights + (round & 1) * kWarps;
-    if (lane == 0) sums[warp] = above + m;
+  while (n > kCompared && first < last) {
+    const int shift = max(0, 64 - __clzll(static_cast<long long>(last - first)) - 9);
+    upper[threadIdx.x] = lower[threadIdx.x] = 0;
     __syncthreads();
-    const uint64_t s = lane < kWarps ? sums[lane] : 0;
-    const uint32_t reach = __ballot_sync(0xffffffffu, lane < kWarps && s >= target);
-    if (!reach) return {false, 0.f, 0};
-    const int w = 31 - __clz(reach);
-    const uint64_t next = __shfl_sync(0xffffffffu, s, (w + 1) & 31);
-    const uint32_t end = w + 1 < kWarps ? from(w + 1) : first + static_cast<uint32_t>(keys);
-    first = from(w);
-    keys = end - first;  // (a row's first round may have 2^32: less from then on)
-    if (w + 1 < kWarps) above = next;
-    if (keys == 1) break;
-    if (round == 0) {  // from here on the tokens between
-      for (int i = threadIdx.x; i < n; i += kThreads) {
-        const uint32_t k = key_at(i) - first;
-        if (k < keys) left[atomicAdd(&sh.rank, 1)] = static_cast<uint16_t>(i);
-      }
-      __syncthreads();
-      n = static_cast<int>(sh.rank);
+#pragma unroll 1
+    for (int q = threadIdx.x; q < n; q += kThreads) {
+      const int i = at(q);
+      const uint64_t k = key(i);
+      if (k < first || k > last) continue;
+      const uint64_t w = weight_of(i);
+      const uint32_t bin = static_cast<uint32_t>((k - first) >> shift);
+      atomicAdd(&upper[bin], static_cast<uint32_t>(w >> kHalf));
+      atomicAdd(&lower[bin], static_cast<uint32_t>(w) & ((1u << kHalf) - 1));
     }
+    __syncthreads();
+    if (threadIdx.x == 0) sh.listed = 0;
+    const int bin = kThreads - 1 - threadIdx.x;  // larger keys first
+    const uint64_t m = (static_cast<uint64_t>(upper[bin]) << kHalf) + lower[bin];
+    uint64_t upto = warp_scan(m);
+    if (lane == 31) sh.part[warp] = upto;
+    __syncthreads();
+    upto += above + warp_sum_u64(lane < warp ? sh.part[lane] : 0);
+    if (upto >= target && upto - m < target) {
+      sh.before = upto - m;
+      sh.found[0] = bin;
+    }
+    __syncthreads();
+    above = sh.before;
+    first += static_cast<uint64_t>(sh.found[0]) << shift;
+    last = min(last, first + ((uint64_t{1} << shift) - 1));
+    int mine[kList / kThreads];
+#pragma unroll
+    for (int j = 0; j < kList / kThreads; ++j) {
+      const int q = threadIdx.x + j * kThreads;
+      mine[j] = q < n ? at(q) : -1;
+      if (mine[j] >= 0) {
+        const uint64_t k = key(mine[j]);
+        if (k < first || k > last) mine[j] = -1;
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < kList / kThreads; ++j)
+      if (mine[j] >= 0) left[atomicAdd(&sh.listed, 1)] = static_cast<uint16_t>(mine[j]);
+    __syncthreads();
+    n = static_cast<int>(sh.listed);
+    whole = false;
   }
-  // (a negative bf16's key ends in ones)
-  uint64_t key = static_cast<uint64_t>(first) << kShift;
-  if (sizeof(T) == 2 && !(key >> 63)) key |= uint64_t{0xffff} << 32;
-  return {true, listed_logit(key), above};
+  if (first == last) return {first, above};
+  const int q = threadIdx.x / kEach, i = at(min(q, n - 1));
+  const uint64_t k = key(i);
+  uint64_t larger = 0, equal = 0;
+  for (int r = threadIdx.x % kEach; r < n; r += kEach) {
+    const uint64_t x = key(at(r)), w = weight_of(at(r));
+    larger += x > k ? w : 0;
+    equal += x == k ? w : 0;
+  }
+#pragma unroll
+  for (int o = kEach / 2; o > 0; o >>= 1) {
+    larger += __shfl_xor_sync(0xffffffffu, larger, o);
+    equal += __shfl_xor_sync(0xffffffffu, equal, o);
+  }
+  larger += above;
+  if (k != 0 && larger < target && larger + equal >= target) {  // (one key; the same above it)
+    sh.border = k;
+    sh.before = larger;
+  }
+  __syncthreads();
+  return {sh.border, sh.before};
 }
 
 // ------------------------------------------------------------------- bins
@@ -821,8 +783,8 @@ __device__ __forceinline__ Sum share_list(Cluster& cl, uint64_t mass) {
   cl.share(mass, threadIdx.x < 32 ? cl.sh.listed : 0);
   return cl.sum();
 }
-// Every CTA's list into `work`, n tokens in all, padded to list_size(n).
-__device__ __forceinline__ void pull_lists(const Cluster cl, uint32_t n) {
+// Every CTA's list into `work`.
+__device__ __forceinline__ void pull_lists(const Cluster cl) {
   Shared& sh = cl.sh;
   uint32_t most = 0;
   for (int r = 0; r < cl.ctas; ++r) most = max(most, sh.count[cl.phase][r * kWarps]);
@@ -842,8 +804,6 @@ __device__ __forceinline__ void pull_lists(const Cluster cl, uint32_t n) {
       at += c;
     }
   }
-  for (uint32_t i = n + threadIdx.x; i < static_cast<uint32_t>(list_size(n)); i += kThreads)
-    sh.work[i] = 0;
 }
 
 // ------------------------------------------------------------ the kernel
@@ -974,53 +934,44 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     const uint32_t lanes = __ballot_sync(0xffffffffu, lane_top >= cut);
     if (lanes) list_from(part, sh, cut, lanes);
     const uint32_t N = share_list(cl, 0).count;
-    if (N <= kList) {
-      if (cl.rank == 0) pull_lists(cl, N);
+    if (N < kList) {
+      if (cl.rank == 0) pull_lists(cl);
       cluster_arrive();  // the lists have been read
       if (cl.rank != 0) {
         cluster_wait();
         return;
       }
       __syncthreads();
-      const int size = list_size(N), threads = min(size / 2, kThreads);
-      if (threadIdx.x < threads) {
-        sort_list(sh.work, size, threads);
-        int keep = min(static_cast<int>(N), k);
-        for (int i = threadIdx.x; i < keep; i += threads)
-          sh.weights[i] = weight(listed_logit(sh.work[i]), scale, sh.table);
-        bar_first(threads);
-        const uint64_t all = scan_list(sh.weights, keep, threads, sh.part);
-        // p and min_p keep a prefix of these
-        const uint64_t target = by_p ? target_p(all) : UINT64_MAX;
-        uint32_t in = 0;
-        for (int i = threadIdx.x; i < keep; i += threads)
-          in += i == 0 || (sh.weights[i - 1] < target && listed_logit(sh.work[i]) >= least);
-        in = __reduce_add_sync(0xffffffffu, in);
-        if (lane == 0) sh.part[warp] = in;
-        bar_first(threads);
-        keep = 0;
-        for (int w = 0; w < threads / 32; ++w) keep += static_cast<int>(sh.part[w]);
-        const uint64_t kept = sh.weights[keep - 1];
-        // by id: ~id << 32 | place, the larger first
-        const int size2 = list_size(keep), threads2 = min(size2 / 2, kThreads);
-        for (int i = threadIdx.x; i < size2; i += threads)
-          sh.list[i] = i < keep ? sh.work[i] << 32 | i : 0;
-        bar_first(threads);
-        if (threadIdx.x < threads2) {
-          sort_list(sh.list, size2, threads2);
-          uint64_t* by_id = sh.work;
-          for (int i = threadIdx.x; i < keep; i += threads2) {
-            const uint32_t at = static_cast<uint32_t>(sh.list[i]);
-            by_id[i] = sh.weights[at] - (at ? sh.weights[at - 1] : 0);
-          }
-          bar_first(threads2);
-          scan_list(by_id, keep, threads2, sh.part);
-          const uint64_t pick = __umul64hi(part_u, kept);
-          for (int i = threadIdx.x; i < keep; i += threads2)
-            if (by_id[i] > pick && (i == 0 || by_id[i - 1] <= pick))
-              a.out[b] = static_cast<int64_t>(~static_cast<uint32_t>(sh.list[i] >> 32));
-        }
-      }
+      const int n = static_cast<int>(N);
+      for (int i = threadIdx.x; i < n; i += kThreads)
+        sh.list[i] = weight(listed_logit(sh.work[i]), scale, sh.table);
+      __syncthreads();
+      const auto entry = [&](int i) { return sh.work[i]; };
+      const auto mass = [&](int i) { return sh.list[i]; };
+      const auto mass_kept = [&](uint64_t from) {
+        uint64_t m = 0;
+        for (int i = threadIdx.x; i < n; i += kThreads) m += sh.work[i] >= from ? sh.list[i] : 0;
+        return block_sum(sh, m);
+      };
+      // the last entry that is kept
+      const uint64_t last = list_entry(top, 0);
+      uint64_t from = list_entry(cut, 0) >> 32 << 32;
+      if (n > k)
+        from = select_key(sh, n, entry, [](int) { return uint64_t{1}; }, from, last,
+                          static_cast<uint64_t>(k)).key;
+      if (by_p)
+        from = select_key(sh, n, entry, mass, from, last, target_p(mass_kept(from))).key;
+      from = max(from, list_entry(fminf(least, top), 0) >> 32 << 32);
+      // of those, by id
+      const uint64_t pick = __umul64hi(part_u, mass_kept(from));
+      const Border inverse = select_key(
+          sh, n,
+          [&](int i) {
+            const uint64_t e = sh.work[i];
+            return e >= from ? e & 0xffffffffu : uint64_t{0};
+          },
+          mass, 0xffffffffu - (a.V - 1), 0xffffffffu, pick + 1);
+      if (threadIdx.x == 0) a.out[b] = listed_id(inverse.key);
       cluster_wait();
       return;
     }
@@ -1128,8 +1079,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
                                 ? list_and_weigh(part, scale, sh, lo, hi)
                                 : 0;
       const Sum in = share_list(cl, warp_sum_u64(mass));
-      if (in.count <= kList) {
-        pull_lists(cl, in.count);
+      if (in.count < kList) {
+        pull_lists(cl);
         cluster_arrive();
         cluster_wait();
         const int n = static_cast<int>(in.count);
@@ -1137,14 +1088,23 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
           sh.list[i] = weight(listed_logit(sh.work[i]), scale, sh.table);
         if (threadIdx.x < warps) sh.count[cl.phase][threadIdx.x] = 0;
         __syncthreads();
-        const Border border = find_border<T>(sh, n, in.mass, target, lo, fminf(hi, top));
-        shared = border.found;
+        uint64_t m = 0;
+        for (int i = threadIdx.x; i < n; i += kThreads) m += sh.list[i];
+        m = block_sum(sh, m);
+        shared = in.mass < target && in.mass + m >= target;
         if (shared) {
+          constexpr int kShift = 32 + (sizeof(T) == 2 ? 16 : 0);
+          const Border border = select_key(
+              sh, n, [&](int i) { return sh.work[i] >> kShift; }, [&](int i) { return sh.list[i]; },
+              list_entry(lo, 0) >> kShift, list_entry(fminf(hi, top), 0) >> kShift,
+              target - in.mass);
           // every warp's mass above the border's logit and tokens equal to it, as
           // share_kept would leave them
-          t = border.logit;
-          const uint64_t w1 = max(weight(t, scale, sh.table), uint64_t{1});
-          ties = static_cast<uint32_t>((target - border.above + w1 - 1) / w1);
+          uint64_t at = border.key << kShift;
+          if (sizeof(T) == 2 && !(at >> 63)) at |= uint64_t{0xffff} << 32;  // (a negative bf16)
+          t = listed_logit(at);
+          const uint64_t each = max(weight(t, scale, sh.table), uint64_t{1});
+          ties = static_cast<uint32_t>((target - in.mass - border.above + each - 1) / each);
           for (int i = threadIdx.x; i < n; i += kThreads) {
             const float l = listed_logit(sh.work[i]);
             if (!(l >= t)) continue;
