@@ -217,6 +217,11 @@ struct Part {
       else v[i] = __uint_as_float(i % 2 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
     }
   }
+  // f(a unit's column, its logits) for the units of some of the warp's lanes, spread over
+  // all of them where these are few.
+  static constexpr int kFlat = 4;
+  template <int BATCH, class F>
+  __device__ __forceinline__ void stream_of(uint32_t lanes, const F& f) const;
   // f(place in the batch, the unit's column, its logits) for the lane's units, a batch of
   // them loaded at once.
   template <int BATCH, class F>
@@ -254,6 +259,44 @@ struct Part {
     }
   }
 };
+template <class T>
+template <int BATCH, class F>
+__device__ __forceinline__ void Part<T>::stream_of(uint32_t lanes, const F& f) const {
+  constexpr int kHalf = 16;
+  if (__popc(lanes) > kHalf) {
+    stream<BATCH>([&](int, int c, const float (&v)[kPer]) { f(c, v); });
+    return;
+  }
+  const int lane = threadIdx.x & 31, total = __popc(lanes) * each;
+  int place = 0;  // of the lane-th one of them
+  for (int r = 0; lanes; ++r, lanes &= lanes - 1)
+    if (r == lane) place = __ffs(lanes) - 1;
+  // this thread's unit: the slot-th of the which-th lane
+  int which = lane / each, slot = lane - which * each;
+#pragma unroll 1
+  for (int i0 = 0; i0 < total; i0 += 32 * kFlat) {
+    uint4 r[kFlat];
+    int u[kFlat];
+#pragma unroll
+    for (int i = 0; i < kFlat; ++i) {
+      u[i] = u0 - lane + __shfl_sync(0xffffffffu, place, which & 31) + slot * 32;
+      // (past the last one: NaN, which is in no range)
+      r[i] = i0 + i * 32 + lane < total ? load(u[i]) : make_uint4(~0u, ~0u, ~0u, ~0u);
+      slot += 32;
+      while (slot >= each) {
+        slot -= each;
+        ++which;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kFlat; ++i) {
+      if (i0 + i * 32 >= total) break;
+      float v[kPer];
+      floats(r[i], v);
+      f(first(u[i]), v);
+    }
+  }
+}
 constexpr int kWide = 8, kFew = 4;  // batches: of passes that do little, and of those that weigh
 
 // Logits in an order of integers (equal ones, but for the sign of a zero, alike).
@@ -728,32 +771,16 @@ __device__ __forceinline__ void list_unit(Shared& sh, int c, const float (&v)[PE
 // Lists those at or above x.  `lanes`: which of the warp's lanes have one.
 template <class T>
 __device__ __forceinline__ void list_from(const Part<T> part, Shared& sh, float x, uint32_t lanes) {
-  constexpr int kFewLanes = 3;
-  if (__popc(lanes) > kFewLanes) {
-    part.template stream<kWide>([&](int, int c, const float (&v)[Part<T>::kPer]) {
-      list_unit(sh, c, v, x, INFINITY);
-    });
-    return;
-  }
-  const int lane = threadIdx.x & 31;
-#pragma unroll 1
-  for (; lanes; lanes &= lanes - 1) {  // one lane's units, spread over all
-    const int u0 = part.u0 - lane + __ffs(lanes) - 1;
-#pragma unroll 1
-    for (int s = 0; s < part.each; s += 32) {
-      const int u = u0 + (s + lane) * 32;
-      float v[Part<T>::kPer];
-      Part<T>::floats(s + lane < part.each ? part.load(u) : make_uint4(~0u, ~0u, ~0u, ~0u), v);
-      list_unit(sh, part.first(u), v, x, INFINITY);  // (NaN is on no list)
-    }
-  }
+  part.template stream_of<kWide>(lanes, [&](int c, const float (&v)[Part<T>::kPer]) {
+    list_unit(sh, c, v, x, INFINITY);
+  });
 }
-// Lists those from lo to hi; the mass of those above hi.
+// Lists those from lo to hi; the mass of those above hi.  `lanes`: those that have some.
 template <class T>
 __device__ __forceinline__ uint64_t list_and_weigh(const Part<T> part, const Scale s, Shared& sh,
-                                                float lo, float hi) {
+                                                float lo, float hi, uint32_t lanes) {
   Adder sum;
-  part.template stream<kFew>([&](int, int c, const float (&v)[Part<T>::kPer]) {
+  part.template stream_of<kFew>(lanes, [&](int c, const float (&v)[Part<T>::kPer]) {
     float most = v[0];
 #pragma unroll
     for (int j = 1; j < Part<T>::kPer; ++j) most = fmaxf(most, v[j]);
@@ -1075,9 +1102,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
       // a token's step is right to 0.02)
       const float lo = fmaxf(step_value(bins.y + 0.55f, -INFINITY, scale), t);
       const float hi = bins.x == 0 ? INFINITY : step_value(bins.x - 0.55f, INFINITY, scale);
-      const uint64_t mass = __any_sync(0xffffffffu, lane_top >= lo)
-                                ? list_and_weigh(part, scale, sh, lo, hi)
-                                : 0;
+      const uint32_t lanes = __ballot_sync(0xffffffffu, lane_top >= lo);
+      const uint64_t mass = lanes ? list_and_weigh(part, scale, sh, lo, hi, lanes) : 0;
       const Sum in = share_list(cl, warp_sum_u64(mass));
       if (in.count < kList) {
         pull_lists(cl);
