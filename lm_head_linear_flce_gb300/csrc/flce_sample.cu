@@ -9,6 +9,16 @@
 // above t, and the first so many of those equal to t.  The token is then the first, by id,
 // whose cumulative mass among the kept ones exceeds u times their total.
 //
+// What bounds it (GB300, in a graph, inputs past L2, us at 256 x 152064 float32 / 64 x
+// 152064 bf16 / 1 x 152064 bf16; the bytes alone would take 23 / 2.9 / 0.05):
+//     no limits 74 / 22 / 10.8: 37 instructions a token, three quarters of the issue slots
+//     min-p 61 / 20 / 9.3: the same for the kept ones, and a pass for the largest
+//     top-k of 1 to 1000, log-uniform, 72 / 26 / 12.1: a pass for the largest (memory), the
+//         candidates' list, and five to eight steps of about a microsecond each
+//     top-p 175 / 64 / 31: three passes, of 37, 20 and up to 45 instructions a token; the
+//         histogram's atomics; barriers
+// One row takes its steps' latency: launch, pass, cluster barriers of 0.6 to 1 us.
+//
 // Masses are integers.  A token weighs 2^((l - max) / (T ln 2)) in units of 2^-42, off by
 // 2^-31.8 of it (rms, without bias), so that next to a border the cumulative mass is right
 // to some 1e-12, where FP32 sums would be off by 1e-7 on a vocabulary with a border every
@@ -1304,15 +1314,20 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
 }
 
 // ------------------------------------------------------------- launching
-// CTAs a row: as many as one wave of two an SM has for it, two at least; fewer where a
-// warp would have less than three slots of it.
+// CTAs a row: as many as seven eighths of the places (two an SM) have for it, as clusters
+// do not fill all of them; two where rows are long, although they are many; and fewer where
+// a warp would have less than three slots of its row.  us without limits / top-k / top-p:
+//     37 x 152064 bf16       4 CTAs 21 / 22 / 51, 7 18 / 21 / 47, 8 22 / 27 / 47
+//     64 x 152064 bf16       2 CTAs 32 / 31 / 92, 4 22 / 26 / 64, 5 30 / 31 / 70
+//     64 x 32003 float32     1 CTA 17 / 24 / 42, 4 12 / 18 / 28, 8 19 / 31 / 48
+//     256 x 152064 float32   1 CTA 66 / 74 / 193, 2 74 / 72 / 177, 4 81 / 78 / 186
+//     256 x 32003 float32    1 CTA 22 / 33 / 56, 2 29 / 37 / 64
 template <class T>
 cudaError_t run_sample(const SampleArgs& a, int64_t B, int sms, cudaStream_t s) {
   const int64_t slots = a.V / (32 * Part<T>::kPer);
-  int ctas = 1;
-  while (ctas < kMaxCluster && (ctas == 1 || 2 * B * ctas <= 2 * sms) &&
-         slots >= 2 * ctas * kWarps * 3)
-    ctas *= 2;
+  int ctas = static_cast<int>(
+      std::clamp<int64_t>(std::min<int64_t>(7 * sms / (4 * B), slots / (3 * kWarps)), 1, kMaxCluster));
+  if (ctas == 1 && slots >= 2 * kWarps * 16) ctas = 2;
   const cudaError_t e = launch_overlapped(sample_kernel<T>, dim3(static_cast<unsigned>(B * ctas)),
                                           dim3(kThreads), 0, s, ctas, a);
   note_launch();

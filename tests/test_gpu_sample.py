@@ -102,7 +102,7 @@ def test_long_rows(B, V, dt):
         check(l, u, T, top_p=1 - rand(g, B) * 1e-4, min_p=rand(g, B) * 1e-3)
 
 
-@pytest.mark.parametrize("B", [1, 37, 76, 77, 152, 153, 400])
+@pytest.mark.parametrize("B", [1, 37, 44, 53, 66, 76, 77, 88, 133, 152, 153, 400])
 def test_rows_by_one_cta_or_several(B):
     """However many rows there are, each gives what it gives alone."""
     g = torch.Generator().manual_seed(B)
