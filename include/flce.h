@@ -374,9 +374,9 @@ flce_status flce_forward_noalloc(const void* X, const void* W, const int64_t* la
 
 /*
  * ------------------------------------------------------------------------
- * Operators around the LM head: the norm in front of it, 8-bit operands with
- * block scales, the head's product on them, and the processing of its logits
- * before a token is picked.  The conventions above hold (caller's buffers and
+ * Operators around the LM head: the norm in front of it (RMS or layer norm), 8-bit
+ * operands with block scales, the head's product on them, the processing of its
+ * logits and the sampling of a token.  The conventions above hold (caller's buffers and
  * stream, no synchronisation, no state); these entry points report no device
  * error.
  *
@@ -607,7 +607,7 @@ flce_status flce_process_logits(const void* logits, int64_t ld_logits, flce_dtyp
  *            (the lowest id of equals), whatever the limits and u; one above 2^100
  *            is 2^100.  A NaN limit is no limit.
  *   out      device int64 [B]; -1 where the row has no token.
- * Weights are right to 2^-29 of them (a root mean square of 2^-31.8) and 2^-43 of the
+ * Weights are right to 2^-29 of them (a root mean square of 2^-31.6) and 2^-43 of the
  * largest, and are added as integers: a call that is repeated gives the same tokens.
  * B <= 65535, V <= 2^21.
  */

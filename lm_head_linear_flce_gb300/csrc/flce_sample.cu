@@ -11,16 +11,17 @@
 //
 // What bounds it (GB300, in a graph, inputs past L2, us at 256 x 152064 float32 / 64 x
 // 152064 bf16 / 1 x 152064 bf16; the bytes alone would take 23 / 2.9 / 0.05):
-//     no limits 74 / 22 / 10.8: 37 instructions a token, three quarters of the issue slots
-//     min-p 61 / 20 / 9.3: the same for the kept ones, and a pass for the largest
-//     top-k of 1 to 1000, log-uniform, 72 / 26 / 12.1: a pass for the largest (memory), the
+//     no limits 65 / 20 / 10.1: 25 to 30 instructions a token, three quarters of the issue
+//         slots
+//     min-p 57 / 18 / 9.0: the same for the kept ones, and a pass for the largest
+//     top-k of 1 to 1000, log-uniform, 71 / 26 / 12.2: a pass for the largest (memory), the
 //         candidates' list, and five to eight steps of about a microsecond each
-//     top-p 175 / 64 / 31: three passes, of 37, 20 and up to 45 instructions a token; the
+//     top-p 164 / 59 / 29: three passes, of 30, 20 and up to 40 instructions a token; the
 //         histogram's atomics; barriers
 // One row takes its steps' latency: launch, pass, cluster barriers of 0.6 to 1 us.
 //
 // Masses are integers.  A token weighs 2^((l - max) / (T ln 2)) in units of 2^-42, off by
-// 2^-31.8 of it (rms, without bias), so that next to a border the cumulative mass is right
+// 2^-31.6 of it (rms), so that next to a border the cumulative mass is right
 // to some 1e-12, where FP32 sums would be off by 1e-7 on a vocabulary with a border every
 // 1e-5; and sums of integers do not depend on their order.
 #include <cuda_bf16.h>
@@ -111,29 +112,27 @@ __device__ __forceinline__ Scale make_scale(float top, float2 c) {
 
 // A token's weight as a * 2^-21 + b * 2^-42, each as the float that holds its bits above
 // kBitsA and kBitsB.  With x = c (l - base) = k / 32 + f, |f| <= 1/64: 2^x by the table
-// (Tang 1989) times 2^f by its series; f carries the rounding errors of x and of the
-// table's entry.  -infinity and NaN weigh nothing.  Written with intrinsics so that every
-// use rounds alike.  (Two values an instruction cost more registers than they save time.)
+// (Tang 1989) times 2^f by its series, whose f^4 is taken as the multiple of f^2 nearest to
+// it; f carries the rounding error of the table's entry.  -infinity and NaN weigh nothing.
+// Written with intrinsics so that every use rounds alike.  (Two values an instruction cost
+// more registers than they save time.)
 template <bool BASE = true>
 __device__ __forceinline__ void weigh(float l, const Scale& s, const float2* table, uint32_t& a,
                                       uint32_t& b) {
   const float d = fmaxf(BASE ? __fsub_rn(l, s.base) : l, s.least);
-  const float q = __fmul_rn(d, s.c_hi);
-  const float e = __fmaf_rn(d, s.c_lo, __fmaf_rn(d, s.c_hi, -q));
-  const float z = __fadd_rn(q, s.magic);
+  const float z = __fmaf_rn(d, s.c_hi, s.magic);
   const uint32_t k = __float_as_uint(z);
   const float2 t = table[k & 31];
-  const float f = __fadd_rn(__fsub_rn(q, __fsub_rn(z, s.magic)), __fadd_rn(e, t.y));
+  const float f = __fadd_rn(__fmaf_rn(d, s.c_hi, __fsub_rn(s.magic, z)), __fmaf_rn(d, s.c_lo, t.y));
   constexpr float kLn2 = 0.69314718055994531f;
-  float p = __fmaf_rn(f, kLn2 * kLn2 * kLn2 * kLn2 / 24, kLn2 * kLn2 * kLn2 / 6);
-  p = __fmaf_rn(f, p, kLn2 * kLn2 / 2);
+  constexpr float kFourth = kLn2 * kLn2 * kLn2 * kLn2 / 24 * (5.f / 7) / (64 * 64);
+  float p = __fmaf_rn(f, kLn2 * kLn2 * kLn2 / 6, kLn2 * kLn2 / 2 + kFourth);
   p = __fmul_rn(f, __fmaf_rn(f, p, kLn2));
-  // (k's bits above the table's are the exponent; the constant's fall off the top)
-  const float th = __uint_as_float(__float_as_uint(t.x) + ((k & ~31u) << 18));
-  const float v = __fmaf_rn(th, p, th);  // v + rest = th (1 + p)
-  const float rest = __fmaf_rn(th, p, __fsub_rn(th, v));
-  const float fa = __fadd_rn(v, kMagicA);
-  const float fb = __fadd_rn(__fadd_rn(__fsub_rn(v, __fsub_rn(fa, kMagicA)), rest), kMagicB);
+  // (k's bits above the table's are the exponent; the constant's fall off the top, and the
+  // table's entries are less by the others)
+  const float th = __uint_as_float(__float_as_uint(t.x) + (k << 18));
+  const float fa = __fadd_rn(__fmaf_rn(th, p, th), kMagicA);
+  const float fb = __fadd_rn(__fmaf_rn(th, p, __fsub_rn(th, __fsub_rn(fa, kMagicA))), kMagicB);
   a = __float_as_uint(fa);
   b = __float_as_uint(fb);
 }
@@ -873,7 +872,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
   const bool greedy = !(T0 >= kGreedyBelow);
   for (int i = threadIdx.x; i < kBins; i += kThreads) sh.bins[i] = 0;
   if (warp == 0) {
-    sh.table[lane] = kPow2[lane];
+    const float2 entry = kPow2[lane];
+    sh.table[lane] = make_float2(
+        __uint_as_float(__float_as_uint(entry.x) - (static_cast<uint32_t>(lane) << 18)), entry.y);
     if (lane == 0) {
       sh.listed = 0;
       sh.inverse = inverse_of(greedy ? 1.f : T0);

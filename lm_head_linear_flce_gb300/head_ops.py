@@ -1,10 +1,13 @@
-"""Operators around the LM head: the norm in front of it, 8-bit operands with
-block scales and the head's product on them, and the processing of its logits.
+"""Operators around the LM head: the norm in front of it (RMS or layer norm), 8-bit
+operands with block scales and the head's product on them, the processing of its
+logits, and the sampling of a token.
 
-Training:  y, h = rms_norm(x, weight, residual=res); linear_cross_entropy(y, W, labels)
-Serving:   q, s, h = rms_norm_fp8(x, weight, residual=res)
+Training:  y, h = rms_norm(x, weight, residual=res)      # or layer_norm(x, weight, bias, ...)
+           linear_cross_entropy(y, W, labels)
+Serving:   q, s, h = rms_norm_fp8(x, weight, residual=res)      # or layer_norm_fp8
            z = matmul_fp8(q, s, Wq, Ws)          # Wq, Ws = quantize_fp8(W), once
            l = process_logits(z, tokens=..., allowed=...)
+           token = sample_logits(l, u, temperature=..., top_k=..., top_p=..., min_p=...)
 
 Every step runs in the library's kernels on torch's current stream
 (``include/flce.h`` says what each computes); the calls go through a small native
