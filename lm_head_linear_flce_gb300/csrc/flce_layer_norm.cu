@@ -950,17 +950,19 @@ flce_status flce_layer_norm_backward(const void* dy, const void* dh, const void*
       !aligned_to(weight, we) || !aligned_to(dweight, we) || !aligned_to(dbias, we) ||
       !aligned_to(mean, 4) || !aligned_to(rstd, 4))
     return FLCE_ERR_INVALID_ARG;
-  if (dweight || dbias) {
+  if (dweight || dbias) {  // (else it is not used)
     if (!workspace || !aligned_to(workspace, 256)) return FLCE_ERR_INVALID_ARG;
     if (workspace_bytes < flce_layer_norm_workspace_size(N, H))
       return FLCE_ERR_WORKSPACE_TOO_SMALL;
   }
   const size_t nh = span_bytes(N, H, H, e), nw = static_cast<size_t>(H) * we,
                nr = static_cast<size_t>(N) * 4;
-  const Range outs[] = {{dx, nh}, {dweight, nw}, {dbias, nw}};
-  const Range ins[] = {{dy, nh},   {dh, nh},   {h, span_bytes(N, H, ldh, e)}, {weight, nw},
-                       {mean, nr}, {rstd, nr}, {workspace, workspace_bytes}};
-  for (int i = 0; i < 3; ++i) {
+  const bool sums = dweight || dbias;
+  const Range outs[] = {{dx, nh}, {dweight, nw}, {dbias, nw},
+                        {sums ? workspace : nullptr, workspace_bytes}};
+  const Range ins[] = {{dy, nh},     {dh, nh},   {h, span_bytes(N, H, ldh, e)},
+                       {weight, nw}, {mean, nr}, {rstd, nr}};
+  for (int i = 0; i < 4; ++i) {
     for (const Range& r : ins)
       if (ranges_overlap(outs[i], r)) return FLCE_ERR_INVALID_ARG;
     for (int k = 0; k < i; ++k)

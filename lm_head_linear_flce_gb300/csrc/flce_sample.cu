@@ -21,9 +21,9 @@
 // One row takes its steps' latency: launch, pass, cluster barriers of 0.6 to 1 us.
 //
 // Masses are integers.  A token weighs 2^((l - max) / (T ln 2)) in units of 2^-42, off by
-// 2^-31.6 of it (rms), so that next to a border the cumulative mass is right
-// to some 1e-12, where FP32 sums would be off by 1e-7 on a vocabulary with a border every
-// 1e-5; and sums of integers do not depend on their order.
+// 2^-31.6 of it (rms), so that next to a border the cumulative mass is right to 2e-10 or
+// better, where FP32 sums would be off by 1e-7 on a vocabulary with a border every 1e-5;
+// and sums of integers do not depend on their order.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -358,6 +358,7 @@ __device__ __forceinline__ void cluster_wait() {
   __syncwarp();
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+
 constexpr int kList = 2048;        // tokens of a list
 constexpr int kBins = 2048;        // of a histogram
 constexpr int kGroups = 32;        // of bins, whose sums the CTAs exchange
@@ -1098,7 +1099,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     // the border is above them.  (In FP32, and where weights are many units.)
     const float small = static_cast<float>(all - target) / static_cast<float>(a.V) * 0.99f;
     const float steps = small >= 64.f ? (42.f - log2f(small)) * 64.f : 0x1p30f;
-    const float from = fmaxf(t, step_value(fminf(steps, kBins - 2.f), INFINITY, scale));
+    // (a token from there on is in a bin: its step is right to 0.02)
+    const float from =
+        fmaxf(t, fminf(step_value(fminf(steps, kBins - 2.f), INFINITY, scale), top));
     if (__any_sync(0xffffffffu, lane_top >= from)) fill_bins(part, scale, from, unit, sh.bins);
     share_groups(cl, bits);
     cluster_arrive();
@@ -1109,8 +1112,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
         find_bins(cl, bits, 2, warp == 0 ? target - min(slack, target - 1) : target + slack);
     shared = false;
     if (bins.y < kBins - 1) {
-      // logits a little beyond the ends of these bins (|c l| up to kLargestShift, in FP32:
-      // a token's step is right to 0.02)
+      // logits a little beyond the ends of these bins (|c l| up to kLargestShift, in FP32)
       const float lo = fmaxf(step_value(bins.y + 0.55f, -INFINITY, scale), t);
       const float hi = bins.x == 0 ? INFINITY : step_value(bins.x - 0.55f, INFINITY, scale);
       const uint32_t lanes = __ballot_sync(0xffffffffu, lane_top >= lo);

@@ -256,7 +256,9 @@ def layer_norm(x, weight=None, bias=None, eps=1e-5, residual=None):
     may be None.  Without a residual returns y = (x - mean) / sqrt(variance + eps) *
     weight + bias.  With one (as x) returns (y, h): the norm of h = x + residual, and h,
     the new residual stream.  Sums are FP32; y and h are rounded once.  The backward
-    takes h as rounded."""
+    takes h as rounded.  A backward pass that is captured into a CUDA graph while an eager
+    graph of the same leaves lives is flce_layer_norm_backward's: autograd's own waiting for
+    the leaves' stream cannot be captured."""
     return _LayerNorm.apply(x, weight, bias, residual, eps)
 
 

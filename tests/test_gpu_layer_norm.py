@@ -444,6 +444,33 @@ def test_the_captured_backward_beside_a_living_eager_graph():
     assert torch.allclose(q.grad.float(), dw.float(), rtol=2.0 ** -7, atol=1e-4)
 
 
+def test_a_captured_training_step():
+    """Forward and autograd's backward in a graph, after a warm-up on a side stream whose
+    graph is gone; a replay follows new values."""
+    x, res, w, b, a, _ = case(50, 384, F32, F32, seed=18)
+    leaves = [t.clone().requires_grad_() for t in (x, res, w, b)]
+
+    def step():
+        y, h = flce.layer_norm(leaves[0], leaves[2], leaves[3], residual=leaves[1])
+        return torch.autograd.grad((y * a).sum() + h.sum(), leaves)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for _ in range(3):
+            step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    for seed in (19, 20):
+        with torch.no_grad():
+            for t, v in zip(leaves, case(50, 384, F32, F32, seed=seed)):
+                t.copy_(v)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(p, q) for p, q in zip(got, step()))
+
+
 @pytest.mark.parametrize("N,H", [(5, 200), (64, 3584), (700, 4096), (9, 1001)])
 def test_bf16_gradient_against_the_forward_as_it_is(N, H):
     """The forward norms the sum as it is, the backward takes the sum as it was stored,

@@ -230,6 +230,21 @@ def test_a_matrix_past_2_31_elements():
     assert torch.equal(flce.sample_logits(l, u, top_k=k, top_p=u), at)
 
 
+@pytest.mark.parametrize("dt", [BF, F32])
+def test_temperatures_from_end_to_end(dt):
+    g = torch.Generator().manual_seed(12)
+    T = torch.tensor([2.0 ** -63, 1e-15, 1e-9, 1e-7, 1e-6, 1e-5, 1e-4, 1e-3, 1e-2, 0.1, 10.0, 1e3,
+                      1e6, 1e20, 2.0 ** 99, 2.0 ** 101], device="cuda")
+    n = T.numel()
+    for V, scale, shift in ((5000, 3.0, 0.0), (5000, 1e-3, 100.0), (70000, 1e4, -3e4),
+                            (5000, 1e36, 0.0), (5000, 1e-30, 0.0)):
+        l = (torch.randn(1, V, generator=g) * scale + shift).to(dt).cuda().expand(n, V).contiguous()
+        u, k, p = rand(g, n), ints(g, n, 900) + 1, rand(g, n)
+        for kw in (dict(), dict(top_k=k), dict(top_p=p), dict(top_p=1 - p * 1e-5),
+                   dict(top_k=k, top_p=p), dict(min_p=p)):
+            check(l, u, T, **kw)
+
+
 @pytest.mark.parametrize("kw", [dict(), dict(top_k=6), dict(top_p=0.8), dict(min_p=0.2)])
 def test_each_token_takes_its_share_of_u(kw):
     n, V = 4096, 11

@@ -85,7 +85,8 @@ def test_norm_backward_refusals():
                dict(dx=BASE + G), dict(dx=BASE + 2 * G + 2), dict(dw=BASE + 6 * G),
                dict(db=BASE + 7 * G), dict(db=BASE + 9 * G), dict(dw=BASE + 4 * G),
                dict(dx=BASE + 6 * G + 1), dict(db=BASE + 8 * G + 1), dict(mean=BASE + 4 * G + 2),
-               dict(N=-1), dict(H=0)):
+               dict(N=-1), dict(H=0), dict(ws=BASE), dict(ws=BASE + G), dict(ws=BASE + 2 * G),
+               dict(ws=BASE + 3 * G), dict(ws=BASE + 6 * G), dict(ws=BASE + 4 * G - 256)):
         assert call(**kw) == INVALID, kw
     assert call(wsb=need - 1) == SMALL and call(dw=None, wsb=need - 1) == SMALL
     assert call(H=1 << 17, ldh=1 << 17) == SHAPE
