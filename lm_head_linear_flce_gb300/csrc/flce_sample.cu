@@ -1029,14 +1029,19 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     return __any_sync(0xffffffffu, lane_top >= x) ? count_from(part, x) : 0u;
   };
   // Narrows t and ties to the prefix that makes `target` (tokens, or mass): halves the
-  // range of logits from t on, a pass over the row and a barrier each.  For any row; the
+  // range of logits from t to `most`, above which there is `above`, a pass over the row and
+  // a barrier each; `most` (equal logits) and `likely` are tried first.  For any row; the
   // lists are faster where they are long enough.
-  const auto halve = [&](uint64_t target, bool mass) {
-    int lo = key_of<T>(t), hi = key_of<T>(top);
-    uint64_t above = 0;
+  const auto halve = [&](uint64_t target, bool mass, float likely, float most, uint64_t above) {
+    int lo = key_of<T>(t), hi = key_of<T>(most);
+    int first = hi, second = key_of<T>(likely);
 #pragma unroll 1
     while (lo < hi) {
-      const int mid = static_cast<int>(lo + (static_cast<int64_t>(hi) - lo + 1) / 2);
+      const int mid = first > lo && first <= hi
+                          ? first
+                          : static_cast<int>(lo + (static_cast<int64_t>(hi) - lo + 1) / 2);
+      first = second;
+      second = INT_MIN;
       const float x = value_of<T>(mid);
       cl.share(mass ? warp_sum_u64(mass_from(x)) : 0,
                mass ? 0 : __reduce_add_sync(0xffffffffu, number_from(x)));
@@ -1080,7 +1085,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     if (by_p)
       ties = static_cast<uint32_t>((target_p(uint64_t{ties} << 42) + (uint64_t{1} << 42) - 1) >> 42);
   } else if (by_k) {
-    halve(static_cast<uint64_t>(k), false);
+    halve(static_cast<uint64_t>(k), false, t, top, 0);
   }
   // --- top-p over many tokens: their mass, and a histogram by weight that says near which
   // one the border lies; a list of those bins' tokens then gives it.
@@ -1111,6 +1116,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     const int2 bins =
         find_bins(cl, bits, 2, warp == 0 ? target - min(slack, target - 1) : target + slack);
     shared = false;
+    float likely = t, most = top;
+    uint64_t above = 0;
     if (bins.y < kBins - 1) {
       // logits a little beyond the ends of these bins (|c l| up to kLargestShift, in FP32)
       const float lo = fmaxf(step_value(bins.y + 0.55f, -INFINITY, scale), t);
@@ -1118,6 +1125,11 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
       const uint32_t lanes = __ballot_sync(0xffffffffu, lane_top >= lo);
       const uint64_t mass = lanes ? list_and_weigh(part, scale, sh, lo, hi, lanes) : 0;
       const Sum in = share_list(cl, warp_sum_u64(mass));
+      if (in.mass < target) {  // (as it should be)
+        likely = lo;
+        most = fminf(hi, top);
+        above = in.mass;
+      }
       if (in.count < kList) {
         pull_lists(cl);
         cluster_arrive();
@@ -1157,7 +1169,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
         }
       }
     }
-    if (!shared) halve(target, true);
+    if (!shared) halve(target, true, likely, most, above);
   }
   if (least > t) {
     t = least;

@@ -231,6 +231,21 @@ def test_a_matrix_past_2_31_elements():
 
 
 @pytest.mark.parametrize("dt", [BF, F32])
+def test_borders_among_more_tokens_than_a_list_holds(dt):
+    g = torch.Generator().manual_seed(13)
+    V = 60000
+    for l in (torch.randn(5, V, generator=g) * 0.02, torch.randn(5, V, generator=g).round(),
+              -4 + torch.randn(5, V, generator=g).round() / 64, torch.full((5, V), -3.0),
+              torch.randn(5, V, generator=g).sign() * 1e-3):
+        l = l.to(dt).cuda()
+        u, p, T = rand(g, 5), rand(g, 5), rand(g, 5) + 0.5
+        k = torch.tensor([3, 1024, 1025, 5000, V - 1], dtype=torch.int32, device="cuda")
+        for kw in (dict(top_p=p), dict(top_p=1 - p * 1e-3), dict(top_k=k), dict(top_k=k, top_p=p),
+                   dict(top_k=k, top_p=p, min_p=p * 0.9)):
+            check(l, u, T, **kw)
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
 def test_temperatures_from_end_to_end(dt):
     g = torch.Generator().manual_seed(12)
     T = torch.tensor([2.0 ** -63, 1e-15, 1e-9, 1e-7, 1e-6, 1e-5, 1e-4, 1e-3, 1e-2, 0.1, 10.0, 1e3,
