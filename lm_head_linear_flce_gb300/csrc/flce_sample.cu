@@ -360,6 +360,7 @@ __device__ __forceinline__ void cluster_wait() {
 }
 
 constexpr int kList = 2048;        // tokens of a list
+constexpr int kCompared = 64;      // of which are compared with one another
 constexpr int kBins = 2048;        // of a histogram
 constexpr int kGroups = 32;        // of bins, whose sums the CTAs exchange
 constexpr int kGroupBins = kBins / kGroups;
@@ -459,7 +460,7 @@ struct Border {
 template <class K, class W>
 __device__ __forceinline__ Border select_key(Shared& sh, int n, const K& key, const W& weight_of,
                                                uint64_t first, uint64_t last, uint64_t target) {
-  constexpr int kHalf = 21, kCompared = 64, kEach = kThreads / kCompared;
+  constexpr int kHalf = 21, kEach = kThreads / kCompared;
   static_assert(sizeof(sh.weights) >= 8 * kThreads + 2 * kList && kList % kThreads == 0);
   uint32_t* const upper = reinterpret_cast<uint32_t*>(sh.weights);
   uint32_t* const lower = upper + kThreads;
@@ -985,32 +986,64 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
       for (int i = threadIdx.x; i < n; i += kThreads)
         sh.list[i] = weight(listed_logit(sh.work[i]), scale, sh.table);
       __syncthreads();
-      const auto entry = [&](int i) { return sh.work[i]; };
-      const auto mass = [&](int i) { return sh.list[i]; };
-      const auto mass_kept = [&](uint64_t from) {
-        uint64_t m = 0;
-        for (int i = threadIdx.x; i < n; i += kThreads) m += sh.work[i] >= from ? sh.list[i] : 0;
-        return block_sum(sh, m);
-      };
-      // the last entry that is kept
-      const uint64_t last = list_entry(top, 0);
-      uint64_t from = list_entry(cut, 0) >> 32 << 32;
-      if (n > k)
-        from = select_key(sh, n, entry, [](int) { return uint64_t{1}; }, from, last,
-                          static_cast<uint64_t>(k)).key;
-      if (by_p)
-        from = select_key(sh, n, entry, mass, from, last, target_p(mass_kept(from))).key;
-      from = max(from, list_entry(fminf(least, top), 0) >> 32 << 32);
-      // of those, by id
-      const uint64_t pick = __umul64hi(part_u, mass_kept(from));
-      const Border inverse = select_key(
-          sh, n,
-          [&](int i) {
-            const uint64_t e = sh.work[i];
-            return e >= from ? e & 0xffffffffu : uint64_t{0};
-          },
-          mass, 0xffffffffu - (a.V - 1), 0xffffffffu, pick + 1);
-      if (threadIdx.x == 0) a.out[b] = listed_id(inverse.key);
+      if (n <= kCompared) {  // all limits by comparing the tokens with one another
+        constexpr int kEach = kThreads / kCompared;
+        const int q = threadIdx.x / kEach, r = threadIdx.x % kEach;
+        const uint64_t e = q < n ? sh.work[q] : 0, w = q < n && r == 0 ? sh.list[q] : 0;
+        uint32_t rank = 0;
+        uint64_t before = 0;
+        for (int i = r; i < n; i += kEach)
+          if (sh.work[i] > e) {
+            ++rank;
+            before += sh.list[i];
+          }
+#pragma unroll
+        for (int o = kEach / 2; o > 0; o >>= 1) {
+          rank += __shfl_xor_sync(0xffffffffu, rank, o);
+          before += __shfl_xor_sync(0xffffffffu, before, o);
+        }
+        bool keep = q < n && rank < static_cast<uint32_t>(k);
+        if (by_p) {
+          const uint64_t all = block_sum(sh, keep ? w : 0);
+          keep = keep && before < target_p(all);
+        }
+        keep = keep && (rank == 0 || listed_logit(e) >= least);
+        if (r == 0) sh.weights[q] = keep ? w : 0;
+        const uint64_t pick = __umul64hi(part_u, block_sum(sh, keep ? w : 0));
+        uint64_t upto = 0;  // by id
+        for (int i = r; i < n; i += kEach)
+          if (static_cast<uint32_t>(sh.work[i]) >= static_cast<uint32_t>(e)) upto += sh.weights[i];
+#pragma unroll
+        for (int o = kEach / 2; o > 0; o >>= 1) upto += __shfl_xor_sync(0xffffffffu, upto, o);
+        if (keep && r == 0 && upto > pick && upto - w <= pick) a.out[b] = listed_id(e);
+      } else {
+        const auto entry = [&](int i) { return sh.work[i]; };
+        const auto mass = [&](int i) { return sh.list[i]; };
+        const auto mass_kept = [&](uint64_t from) {
+          uint64_t m = 0;
+          for (int i = threadIdx.x; i < n; i += kThreads) m += sh.work[i] >= from ? sh.list[i] : 0;
+          return block_sum(sh, m);
+        };
+        // the last entry that is kept
+        const uint64_t last = list_entry(top, 0);
+        uint64_t from = list_entry(cut, 0) >> 32 << 32;
+        if (n > k)
+          from = select_key(sh, n, entry, [](int) { return uint64_t{1}; }, from, last,
+                            static_cast<uint64_t>(k)).key;
+        if (by_p)
+          from = select_key(sh, n, entry, mass, from, last, target_p(mass_kept(from))).key;
+        from = max(from, list_entry(fminf(least, top), 0) >> 32 << 32);
+        // of those, by id
+        const uint64_t pick = __umul64hi(part_u, mass_kept(from));
+        const Border inverse = select_key(
+            sh, n,
+            [&](int i) {
+              const uint64_t e = sh.work[i];
+              return e >= from ? e & 0xffffffffu : uint64_t{0};
+            },
+            mass, 0xffffffffu - (a.V - 1), 0xffffffffu, pick + 1);
+        if (threadIdx.x == 0) a.out[b] = listed_id(inverse.key);
+      }
       cluster_wait();
       return;
     }
