@@ -14,7 +14,7 @@
 //     no limits 65 / 20 / 10.1: 25 to 30 instructions a token, three quarters of the issue
 //         slots
 //     min-p 57 / 18 / 9.0: the same for the kept ones, and a pass for the largest
-//     top-k of 1 to 1000, log-uniform, 71 / 26 / 12.2: a pass for the largest (memory), the
+//     top-k of 1 to 1000, log-uniform, 72 / 26 / 11.3: a pass for the largest (memory), the
 //         candidates' list, and five to eight steps of about a microsecond each
 //     top-p 164 / 59 / 29: three passes, of 30, 20 and up to 40 instructions a token; the
 //         histogram's atomics; barriers
@@ -452,8 +452,8 @@ __device__ __forceinline__ uint64_t block_sum(Shared& sh, uint64_t v) {
 //
 // A round adds the weights up in 512 bins of the range (two halves of 21 bits each) and
 // goes on with the tokens of the one that has the border; 64 tokens are compared with one
-// another.  Nothing is sorted: an order by logit and then one by id take 8 us for 1000
-// tokens and 2.5 us for one, these searches 2 and 1.
+// another.  Nothing is sorted: an order by logit and then one by id took 17 us for 1200
+// tokens of bf16, two of these searches take 4.
 struct Border {
   uint64_t key, above;
 };

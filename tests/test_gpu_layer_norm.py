@@ -138,7 +138,8 @@ def check_backward(got, dy, h, w, mean, rstd, dh, dt, wdt, bdt):
 # (beside the forward's: with rows enough for every way to split them)
 @pytest.mark.parametrize("dt,wdt", [(BF, BF), (BF, F32), (F32, F32), (F32, BF)])
 @pytest.mark.parametrize("N,H", SHAPES + [(2048, 1001), (2049, 1001), (2500, 1000), (700, 8192),
-                                          (9000, 64), (400, 16384), (130, 16388), (2048, 1024)])
+                                          (9000, 64), (400, 16384), (130, 16388), (2048, 1024),
+                                          (300001, 24)])
 def test_backward(N, H, dt, wdt):
     x, res, w, b, dy, dh = case(N, H, dt, wdt, seed=2, mean=1.0)
     y, h, mean, rstd = flce.flce_layer_norm(x, w, b, eps=EPS, residual=res)
@@ -442,6 +443,30 @@ def test_the_captured_backward_beside_a_living_eager_graph():
     torch.cuda.synchronize()
     assert torch.equal(p.grad, dx)
     assert torch.allclose(q.grad.float(), dw.float(), rtol=2.0 ** -7, atol=1e-4)
+
+
+@pytest.mark.parametrize("N,H", [(33000, 65536), (140000, 16384)])
+def test_matrices_past_2_31_elements(N, H):
+    """The last rows of a matrix are as they are by themselves (dx up to the rounding of
+    sums in another order)."""
+    g = torch.Generator(device="cuda").manual_seed(21)
+    x = torch.randn(N, H, dtype=BF, device="cuda", generator=g)
+    w, b = (torch.randn(H, dtype=BF, device="cuda", generator=g) for _ in range(2))
+    y, h, mean, rstd = flce.flce_layer_norm(x, w, b)
+    for part in (slice(N - 3, N), slice(0, 3)):
+        y3, h3, m3, r3 = flce.flce_layer_norm(x[part].clone(), w, b)
+        assert torch.equal(y[part], y3) and torch.equal(mean[part], m3)
+    dx, dw, db = flce.flce_layer_norm_backward(y, h, w, mean, rstd)
+    for part in (slice(N - 3, N), slice(0, 3)):
+        d3 = flce.flce_layer_norm_backward(y[part].clone(), h[part].clone(), w, mean[part].clone(),
+                                           rstd[part].clone())[0]
+        assert torch.allclose(dx[part].float(), d3.float(), rtol=2.0 ** -7, atol=1e-4)
+    # columns' sums: of the first one in 64 bits
+    col = y[:, 0].double()
+    n = (x[:, 0].double() - mean.double()) * rstd.double()
+    for got, t in ((dw[0], col * n), (db[0], col)):
+        tol = (N / 32 + 80) * U * t.abs().sum().item()
+        assert abs(got.item() - t.sum().item()) <= tol + 1.01 * rnd(BF) * abs(t.sum().item())
 
 
 def test_a_captured_training_step():
