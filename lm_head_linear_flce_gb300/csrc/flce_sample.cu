@@ -547,13 +547,12 @@ __device__ __forceinline__ Border select_key(Shared& sh, int n, const K& key, co
 // of an octave each, for masses.  The last one takes what lies beyond.
 constexpr int kFirstBin = (127 - 12) << 6, kBinShift = 17;
 __device__ __forceinline__ int distance_bin(float l, float top) {
-  const float d = l == top ? 0.f : top - l;
-  const int k = static_cast<int>(__float_as_uint(d) >> kBinShift) - kFirstBin;
+  const int k = static_cast<int>(__float_as_uint(top - l) >> kBinShift) - kFirstBin;
   return min(max(k, 0), kBins - 1);
 }
 // The least logit that may be in bin `last` or one before (or a little less).
 __device__ __forceinline__ float distance_cut(int last, float top) {
-  if (last == kBins - 1 || top == INFINITY) return top == INFINITY ? top : -FLT_MAX;
+  if (last == kBins - 1) return -FLT_MAX;
   const float d = __uint_as_float(static_cast<uint32_t>(last + 1 + kFirstBin) << kBinShift);
   return fmaxf(nextafterf(top - d, -INFINITY), -FLT_MAX);
 }
