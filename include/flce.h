@@ -609,6 +609,7 @@ flce_status flce_process_logits(const void* logits, int64_t ld_logits, flce_dtyp
  *   out      device int64 [B]; -1 where the row has no token.
  * Weights are right to 2^-29 of them (a root mean square of 2^-31.6) and 2^-43 of the
  * largest, and are added as integers: a call that is repeated gives the same tokens.
+ * The logit at which min_p's border lies is right to 2^-29 T.
  * B <= 65535, V <= 2^21.
  */
 flce_status flce_sample_logits(const void* logits, int64_t ld_logits, flce_dtype dtype, int64_t B,

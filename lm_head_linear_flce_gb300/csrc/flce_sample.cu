@@ -77,6 +77,12 @@ __constant__ float2 kPow2[32] = {
     {0x1.cb720ep0f, -0x1.3b49d2p-27f}, {0x1.d5818ep0f, -0x1.2fc81cp-27f}, {0x1.dfc974p0f, -0x1.345598p-25f},
     {0x1.ea4afap0f, 0x1.fda57cp-28f}, {0x1.f50766p0f, -0x1.af2102p-27f}};
 
+// a + b, and what its rounding leaves.
+__device__ __forceinline__ float2 two_sum(float a, float b) {
+  const float s = __fadd_rn(a, b), back = __fsub_rn(s, a);
+  return make_float2(s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, back)), __fsub_rn(b, back)));
+}
+
 // What turns a row's logits into weights.  With c = 1 / (T ln 2) a weight is
 // 2^(c (l - base) - shift): base is the largest logit where |c max| is very large (l - base
 // is then exact for every l that weighs anything), else 0 with shift = ceil(c max), so that
@@ -882,17 +888,24 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     }
     __syncwarp();
     if (min_p > 0.f) {
-      // T ln(min_p) in two floats: FP32's logarithm, corrected by what its exponential
-      // leaves of min_p
-      const float m = fminf(min_p, 1.f), y = logf(m);
-      float rest = 0.f;
-      if (m > 0x1p-30f) {
-        const uint64_t w = weight(y, make_scale(0.f, inverse_of(1.f)), sh.table);
-        rest = static_cast<float>(static_cast<int64_t>(__float2ull_rn(m * 0x1p42f) - w)) /
-               static_cast<float>(w);
-      }
-      const float hi = T0 * y;
-      if (lane == 0) sh.log_min_p = make_float2(hi, fmaf(T0, y, -hi) + T0 * rest);
+      // T ln(min_p) in two floats.  With min_p = f 2^e, e <= 0 and f from 1/2 to 1: FP32's
+      // logarithm of f, corrected by what its exponential leaves of f (a weight has all its
+      // bits there: of a min_p near 2^-29 it has 13), and e ln 2, whose first part is exact.
+      constexpr float kLn2 = 0x1.62e4p-1f, kLn2Rest = 0x1.7f7d1cp-20f;
+      const float m = fminf(min_p, 1.f);
+      int e;
+      frexpf(m, &e);
+      e = min(e, 0);  // (1 stays 1)
+      const float f = ldexpf(m, -e), y = logf(f), n = static_cast<float>(e);
+      const uint64_t w = weight(y, make_scale(0.f, inverse_of(1.f)), sh.table);
+      const float left = static_cast<float>(static_cast<int64_t>(__float2ull_rn(f * 0x1p42f) - w)) /
+                         static_cast<float>(w);
+      const float2 sum = two_sum(__fmul_rn(n, kLn2), y);
+      const float rest = __fadd_rn(__fadd_rn(sum.y, left), __fmul_rn(n, kLn2Rest));
+      const float hi = __fmul_rn(T0, sum.x);
+      if (lane == 0)
+        sh.log_min_p = make_float2(
+            hi, __fadd_rn(__fmaf_rn(T0, sum.x, -hi), __fmul_rn(T0, rest)));
     }
   }
 
@@ -939,11 +952,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
   // what min_p keeps: w >= min_p w_max, l >= max + T ln(min_p), rounded up
   float least = -FLT_MAX;
   if (!greedy && min_p > 0.f && top < INFINITY) {
-    const float2 d = sh.log_min_p;
-    const float sum = __fadd_rn(top, d.x), back = __fsub_rn(sum, top);
-    const float rest = __fadd_rn(
-        __fadd_rn(__fsub_rn(top, __fsub_rn(sum, back)), __fsub_rn(d.x, back)), d.y);
-    least = rest > 0.f ? nextafterf(sum, INFINITY) : sum;
+    // (max and the logarithm may cancel: what the sum leaves is added before it is rounded)
+    const float2 d = sh.log_min_p, first = two_sum(top, d.x);
+    const float2 sum = two_sum(first.x, __fadd_rn(first.y, d.y));
+    least = sum.y > 0.f ? nextafterf(sum.x, INFINITY) : sum.x;
     if (!(least > -FLT_MAX)) least = -FLT_MAX;
   }
   const uint64_t part_p = __float2ull_rz(fmaxf(fminf(p, 0x1.fffffep-1f), 0.f) * 0x1p64f);
