@@ -485,7 +485,9 @@ flce_status flce_layer_norm_fp8(const void* x, int64_t ldx, const void* residual
  *   dy, dh, h, ldh   as in flce_rms_norm_backward (h: h_out, or x without a residual;
  *                    in bf16 the rounded sum).
  *   weight           device [H] of `weight_dtype`, or NULL (1).
- *   mean, rstd       device float [N], as written by the forward.
+ *   mean, rstd       device float [N], as written by the forward.  n is right to FP32 for
+ *                    these, whatever the mean; the rounding of the mean itself leaves up to
+ *                    2^-24 |mean| * rstd in it.
  *   dx               device [N][H] of `dtype`, or NULL.
  *   dweight, dbias   device [H] of `weight_dtype`, each may be NULL.
  *   workspace        device, 256-byte aligned, flce_layer_norm_workspace_size(N, H)

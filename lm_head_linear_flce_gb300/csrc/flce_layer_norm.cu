@@ -212,6 +212,10 @@ __global__ void __launch_bounds__(1024)
 // h is the sum as the forward stored it, in T (in bf16 rounded by up to 2^-8 of h),
 // where mean and rstd are those of the sum before it was rounded.
 //
+// n is formed as (h - mean) rstd: h rstd + (-mean rstd) is an instruction less, but rounds
+// the product for the whole row at once, 6e-5 in every n at a mean of 1000 deviations, where
+// this has 1e-7 beside the mean's own rounding.  It costs 0.6 us of 47 at 8192 x 3584 bf16.
+//
 // Threads hold 16 values where the row has them (two slots of bf16, four of float32) and
 // 128 registers, 512 of them an SM: what a row costs besides its values, two sums and a
 // barrier, is a warp's, so few warps do it fastest.  8192 x 3584 bf16 with dh, dx alone:
@@ -273,7 +277,7 @@ __global__ void __launch_bounds__(THREADS, ln_blocks(P, THREADS))
   float next_r = first < N ? rstd[first] : 0.f, next_m = first < N ? mean[first] : 0.f;
   int stage = 0, phase = 0;
   for (int64_t row = first; row < N; row += step, phase ^= 1) {
-    const F2 r = both(next_r), shift = both(-next_m * next_r);
+    const F2 r = both(next_r), minus_m = both(-next_m);
     const float minus_r = -next_r;
     if (row + step < N) {
       next_r = rstd[row + step];
@@ -308,7 +312,7 @@ __global__ void __launch_bounds__(THREADS, ln_blocks(P, THREADS))
 #pragma unroll
       for (int i = 0; i < kP; ++i) {
         // past the row d is 0, and with it every sum
-        const F2 n = fma2(v[i], r, shift), g = mul2(d[i], w[s][i]);
+        const F2 n = mul2(add2(v[i], minus_m), r), g = mul2(d[i], w[s][i]);
         dw[s][i] = fma2(d[i], n, dw[s][i]);
         db[s][i] = add2(db[s][i], d[i]);
         dot1 = add2(dot1, g);
@@ -326,7 +330,7 @@ __global__ void __launch_bounds__(THREADS, ln_blocks(P, THREADS))
         pairs(1, s, v);
 #pragma unroll
         for (int i = 0; i < kP; ++i) {
-          const F2 n = fma2(v[i], r, shift), g = mul2(d[i], w[s][i]);
+          const F2 n = mul2(add2(v[i], minus_m), r), g = mul2(d[i], w[s][i]);
           d[i] = fma2(g, r, fma2(n, k2, k1));
         }
         if (with_dh) {
@@ -450,7 +454,7 @@ __global__ void __launch_bounds__(kLnSmallThreads)
     const int rows = kLnSmallThreads / tpr, k = threadIdx.x / tpr, t = threadIdx.x % tpr;
     const int64_t row = static_cast<int64_t>(blockIdx.x) * rows + k;
     const bool live = k < rows && row < N;
-    const float r = live ? rstd[row] : 0.f, shift = live ? -mean[row] * r : 0.f;
+    const float r = live ? rstd[row] : 0.f, m = live ? mean[row] : 0.f;
     float g[kLnSmallValues], n[kLnSmallValues], e[kLnSmallValues];
     float2 dot = make_float2(0.f, 0.f);
 #pragma unroll
@@ -458,7 +462,7 @@ __global__ void __launch_bounds__(kLnSmallThreads)
       const int c = t + i * tpr;
       const bool in = live && c < H;
       g[i] = in ? to_f(dy[row * H + c]) : 0.f;
-      n[i] = in ? fmaf(to_f(h[row * ldh + c]), r, shift) : 0.f;
+      n[i] = in ? (to_f(h[row * ldh + c]) - m) * r : 0.f;
       e[i] = in && dh ? to_f(dh[row * H + c]) : 0.f;
       if (in && weight)
         g[i] *= w_f32 ? static_cast<const float*>(weight)[c]
@@ -492,8 +496,8 @@ __global__ void __launch_bounds__(kLnSmallThreads)
   if (c < H) {
 #pragma unroll 8
     for (int i = threadIdx.x / kLnSmallCols; i < N; i += kLnSmallThreads / kLnSmallCols) {
-      const float d = to_f(dy[static_cast<int64_t>(i) * H + c]), r = rstd[i];
-      s.x = fmaf(d, fmaf(to_f(h[i * ldh + c]), r, -mean[i] * r), s.x);
+      const float d = to_f(dy[static_cast<int64_t>(i) * H + c]);
+      s.x = fmaf(d, (to_f(h[i * ldh + c]) - mean[i]) * rstd[i], s.x);
       s.y += d;
     }
   }
@@ -589,18 +593,18 @@ __global__ void __launch_bounds__(kNormThreads)
                      const float* __restrict__ mean, const float* __restrict__ rstd, int H,
                      T* __restrict__ dx) {
   const int64_t row = blockIdx.x;
-  const float r = rstd[row], shift = -mean[row] * r;
+  const float r = rstd[row], m = mean[row];
   float s1 = 0.f, s2 = 0.f;
   for (int c = threadIdx.x; c < H; c += kNormThreads) {
     const float g = to_f(dy[row * H + c]) * param_at(weight, w_f32, 1.f, c);
     s1 += g;
-    s2 = fmaf(g, fmaf(to_f(h[row * ldh + c]), r, shift), s2);
+    s2 = fmaf(g, (to_f(h[row * ldh + c]) - m) * r, s2);
   }
   const float k1 = -r * (block_sum(s1) / static_cast<float>(H));
   const float k2 = -r * (block_sum(s2) / static_cast<float>(H));
   for (int c = threadIdx.x; c < H; c += kNormThreads) {
     const float g = to_f(dy[row * H + c]) * param_at(weight, w_f32, 1.f, c);
-    float v = fmaf(g, r, fmaf(fmaf(to_f(h[row * ldh + c]), r, shift), k2, k1));
+    float v = fmaf(g, r, fmaf((to_f(h[row * ldh + c]) - m) * r, k2, k1));
     if (dh) v += to_f(dh[row * H + c]);
     dx[row * H + c] = from_f<T>(v);
   }
@@ -619,7 +623,7 @@ __global__ void __launch_bounds__(kNormThreads)
   float s = 0.f, b = 0.f;
   for (int64_t n = n0; n < n1; ++n) {
     const float d = to_f(dy[n * H + c]);
-    s = fmaf(d, fmaf(to_f(h[n * ldh + c]), rstd[n], -mean[n] * rstd[n]), s);
+    s = fmaf(d, (to_f(h[n * ldh + c]) - mean[n]) * rstd[n], s);
     b += d;
   }
   float* p = part + static_cast<int64_t>(blockIdx.x) * 2 * H + c;
