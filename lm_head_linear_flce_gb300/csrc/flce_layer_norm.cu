@@ -784,12 +784,24 @@ cudaError_t launch_ln_bwd(const RowPlan& p, bool aligned, int64_t parts, const L
                         : launch(ln_bwd_held_kernel<T, VEC, P, kMost, false>, 0);
 }
 
-// What ln_bwd_small_kernel takes: a column's block adds at most 64 rows a warp, and
-// up to 2^20 values are read twice from L2.  In a graph, us, against the two launches: 64 x
-// 4096 4.2 to 6.5, 256 x 2048 4.2 to 6.2, 1021 x 1001 bf16 7.8 to 8.1 and float32 9.8 to 8.2
-// (from the host 10.0 to 10.5); past it 2048 x 1024 bf16 16.0 to 9.7, float32 15.5 to 12.1.
+// What ln_bwd_small_kernel takes: a column's block adds at most 64 rows a warp, and its
+// inputs are read twice, from L2.  One launch and two, us in a graph over inputs larger than
+// L2 / over inputs that are in L2 / called from the host, bf16 and float32 alike to 0.7:
+//       64 x 4096  bf16      5.6, 7.0 / 5.2, 7.2 / 8.2, 10.0
+//      482 x 1536  float32   8.0, 8.4 / 6.1, 8.1 / 8.6, 10.6
+//     1021 x 1001  float32   9.7, 8.7 / -         / 9.7, 11.1   (1047 rows 8.6, 9.0: its rows
+//                            are added 512 at a time, the last ones of them one by one)
+//      409 x 2560  bf16      9.4, 8.7 / 7.7, 8.3 / 9.6, 11.1
+//      608 x 2048  bf16      8.7, 8.3 / 7.7, 8.2 / 8.9, 10.5   (past the limit)
+//     2097 x 1000  float32  15.7, 12.6 / -       / 16.1, 14.8  (past the limit)
+//      218 x 3584  bf16      8.5, 7.9 / 6.8, 7.8 / 9.0, 10.6
+//      292 x 3584  bf16     11.1, 8.4 / 8.8, 8.3 / 11.2, 10.8  (past the limit)
+//      256 x 4096  float32  10.0, 8.9 / 7.9, 8.2 / 10.1, 10.7  (past the limit)
+// So up to 2^20 values the host's time decides, where the two are close in a graph; from 3584
+// columns on, whose blocks are more than the SMs, one launch falls behind from 3 2^18 on.
 bool small_ln_bwd(int64_t N, int64_t H) {
-  return N <= 2048 && H <= kLnSmallThreads * kLnSmallValues && N * H <= int64_t{1} << 20;
+  return N <= 2048 && H <= kLnSmallThreads * kLnSmallValues &&
+         N * H <= int64_t{H <= 2560 ? 4 : 3} << 18;
 }
 
 template <class T>
