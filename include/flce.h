@@ -610,7 +610,10 @@ flce_status flce_process_logits(const void* logits, int64_t ld_logits, flce_dtyp
  *            is 2^100.  A NaN limit is no limit.
  *   out      device int64 [B]; -1 where the row has no token.
  * Weights are right to 2^-29 of them (a root mean square of 2^-31.6) and 2^-43 of the
- * largest, and are added as integers: a call that is repeated gives the same tokens.
+ * largest, and are added as integers: a call that is repeated gives the same tokens.  With
+ * top_k, or min_p without top_p, a row's token does not depend on the batch around it either;
+ * else all tokens are weighed before the largest is known, and a token next to a border, as
+ * close as weights are right, may be another one at another B or alignment of the row.
  * The logit at which min_p's border lies is right to 2^-29 T.
  * B <= 65535, V <= 2^21.
  */

@@ -23,7 +23,10 @@
 // Masses are integers.  A token weighs 2^((l - max) / (T ln 2)) in units of 2^-42, off by
 // 2^-31.6 of it (rms), so that next to a border the cumulative mass is right to 2e-10 or
 // better, where FP32 sums would be off by 1e-7 on a vocabulary with a border every 1e-5;
-// and sums of integers do not depend on their order.
+// and sums of integers do not depend on their order.  What depends on how a row is split
+// over lanes is the mass that is taken while the largest logit is still looked for (no
+// top-k, and no min-p or top-p too): a lane's sum is rounded as that goes up, to a unit, and
+// the warp's once more.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

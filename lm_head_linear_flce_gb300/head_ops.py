@@ -331,6 +331,8 @@ def sample_logits(logits, u, *, temperature=None, top_k=None, top_p=None, min_p=
     (the first always; 1: all), of these the ones that weigh at least min_p[b] of what the
     first does (0: all).  The result is the first token by id at which the kept ones' mass
     exceeds u[b] of its total.  temperature, top_p and min_p: float32 [B]; any of them may
-    be left out.  A temperature of 0 (below 2^-64) takes the largest logit.  No gradient."""
+    be left out.  A temperature of 0 (below 2^-64) takes the largest logit.  A repeated call
+    gives the same tokens; without top_k, and unless min_p is the only limit, one within 1e-9
+    of a border may be another in a batch of another size.  No gradient."""
     return _ok(_native().sample_logits(logits, u, temperature, top_k, top_p, min_p),
                "flce_sample_logits")[0]
