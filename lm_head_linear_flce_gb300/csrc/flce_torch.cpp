@@ -122,6 +122,12 @@ int64_t integer(PyObject* o) {
   return v;
 }
 
+bool truth(PyObject* o) {
+  const int v = PyObject_IsTrue(o);
+  if (v < 0) throw python_error();
+  return v != 0;
+}
+
 // What the norms share.
 struct Norm {
   Tensor x, weight, bias, residual, h, out;  // out: residual_out, if it is given
@@ -247,8 +253,8 @@ PyObject* rms_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
                     "rstd must be as flce_rms_norm returned it");
   Tensor dx, dw, ws;
   size_t nws = 0;
-  if (PyObject_IsTrue(a[5])) dx = empty(h.sizes(), h, h.scalar_type());
-  if (PyObject_IsTrue(a[6])) {
+  if (truth(a[5])) dx = empty(h.sizes(), h, h.scalar_type());
+  if (truth(a[6])) {
     dw = empty({m.H}, h, m.weight.scalar_type());
     nws = flce_rms_norm_workspace_size(m.N, m.H);
     ws = empty({static_cast<int64_t>(nws)}, h, at::kByte);
@@ -322,7 +328,7 @@ PyObject* layer_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     TORCH_CHECK_VALUE(t.sizes() == h.sizes().slice(0, h.dim() - 1) && t.is_contiguous(), name,
                       " must be as flce_layer_norm returned it");
   }
-  const bool need_dw = PyObject_IsTrue(a[7]);
+  const bool need_dx = truth(a[6]), need_dw = truth(a[7]);
   TORCH_CHECK_VALUE(!need_dw || m.weight.defined(), "dweight needs weight");
   const int64_t bias_type = integer(a[8]);
   TORCH_CHECK_VALUE(bias_type <= FLCE_F32, "bias must be bfloat16 or float32");
@@ -332,7 +338,7 @@ PyObject* layer_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const at::ScalarType wt = m.weight_type == FLCE_F32 ? at::kFloat : at::kBFloat16;
   Tensor dx, dw, db, ws;
   size_t nws = 0;
-  if (PyObject_IsTrue(a[6])) dx = empty(h.sizes(), h, h.scalar_type());
+  if (need_dx) dx = empty(h.sizes(), h, h.scalar_type());
   if (need_dw) dw = empty({m.H}, h, wt);
   if (bias_type >= 0) db = empty({m.H}, h, wt);
   if (need_dw || bias_type >= 0) {
