@@ -20,13 +20,15 @@
 //         histogram's atomics; barriers
 // One row takes its steps' latency: launch, pass, cluster barriers of 0.6 to 1 us.
 //
-// Masses are integers.  A token weighs 2^((l - max) / (T ln 2)) in units of 2^-42, off by
-// 2^-31.6 of it (rms), so that next to a border the cumulative mass is right to 2e-10 or
-// better, where FP32 sums would be off by 1e-7 on a vocabulary with a border every 1e-5;
-// and sums of integers do not depend on their order.  What depends on how a row is split
-// over lanes is the mass that is taken while the largest logit is still looked for (no
-// top-k, and no min-p or top-p too): a lane's sum is rounded as that goes up, to a unit, and
-// the warp's once more.
+// Masses are integers.  A token weighs 2^((l - max) / (T ln 2)) in units of 2^-42 (the
+// largest 2^41 to 2^42 of them), off by 2^-29.3 of it at most (rms 2^-31.6) and by 0.55 of a
+// unit.  Next to a border the cumulative mass is right to 2e-11 on a broad row, to 4e-10
+// between two likely tokens, and on any row to 2^-28 + 1.1 V 2^-42 (the second where many
+// tokens weigh less than a unit), where FP32 sums would be off by 1e-7 on a vocabulary with a
+// border every 1e-5.  Sums of integers do not depend on their order.  What depends on how a
+// row is split over lanes is the mass that is taken while the largest logit is still looked
+// for (no top-k, and no min-p or top-p too): a lane's sum is rounded as that goes up, to a
+// unit, and the warp's once more.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
