@@ -1379,19 +1379,34 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
 
 // ------------------------------------------------------------- launching
 // CTAs a row: as many as seven eighths of the places (two an SM) have for it, as clusters
-// do not fill all of them; two where rows are long, although they are many; and fewer where
-// a warp would have less than three slots of its row.  us without limits / top-k / top-p:
-//     37 x 152064 bf16       4 CTAs 21 / 22 / 51, 7 18 / 21 / 47, 8 22 / 27 / 47
-//     64 x 152064 bf16       2 CTAs 32 / 31 / 92, 4 22 / 26 / 64, 5 30 / 31 / 70
-//     64 x 32003 float32     1 CTA 17 / 24 / 42, 4 12 / 18 / 28, 8 19 / 31 / 48
-//     256 x 152064 float32   1 CTA 66 / 74 / 193, 2 74 / 72 / 177, 4 81 / 78 / 186
-//     256 x 32003 float32    1 CTA 22 / 33 / 56, 2 29 / 37 / 64
+// do not fill all of them, and fewer where a warp would have less than three slots of its
+// row.  Where that is one, two take a long row all the same: with top-k or top-p, whose rows
+// differ in their passes and end at different times; without, as far as an SM has no more than
+// three CTAs to run; with min-p alone where rows are longer.  us in a graph over inputs larger than
+// L2, without limits / top-k / top-p / min-p:
+//     37 x 152064 bf16       4 CTAs 19 / 24 / 48 / 12, 7 17 / 22 / 46 / 13, 8 21 / 28 / 55 / 17
+//     64 x 152064 bf16       2 CTAs 29 / 31 / 89 / 17, 4 20 / 25 / 60 / 13, 5 27 / 31 / 74 / 20
+//     64 x 32003 float32     1 CTA 17 / 25 / 44 / 13, 4 11 / 18 / 28 / 10, 8 18 / 32 / 48 / 18
+//     256 x 32003 float32    1 CTA 19 / 32 / 54 / 16, 2 26 / 36 / 62 / 23
+//     256 x 65536 bf16       1 CTA 26 / 33 / 83 / 19, 2 33 / 36 / 86 / 23
+//     256 x 65536 float32    1 CTA 29 / 43 / 84 / 24, 2 35 / 43 / 88 / 27
+//     256 x 80001 float32    1 CTA - / 54 / 107 / 35, 2 - / 51 / 105 / 35
+//     256 x 100352 bf16      1 CTA 38 / 46 / 122 / 26, 2 45 / 45 / 118 / 29
+//     256 x 128255 bf16      1 CTA 46 / 63 / 166 / 39, 2 52 / 53 / 149 / 35
+//     256 x 152064 float32   1 CTA 56 / 76 / 178 / 56, 2 63 / 73 / 166 / 51
+//     200 x 100352 bf16      1 CTA 36 / 42 / 120 / 26, 2 35 / 40 / 107 / 26
+//     220 x 152064 bf16      1 CTA 50 / 59 / 173 / 33, 2 45 / 49 / 147 / 34
+//     240 x 152064 bf16      1 CTA 51 / 60 / 175 / 43, 2 57 / 52 / 158 / 37
+//     1024 x 128255 bf16     1 CTA 143 / 192 / 617 / 101, 2 169 / 155 / 499 / 112
+constexpr int kLongRow = 80000, kLongerRow = 1 << 17;  // columns
 template <class T>
 cudaError_t run_sample(const SampleArgs& a, int64_t B, int sms, cudaStream_t s) {
   const int64_t slots = a.V / (32 * Part<T>::kPer);
   int ctas = static_cast<int>(
       std::clamp<int64_t>(std::min<int64_t>(7 * sms / (4 * B), slots / (3 * kWarps)), 1, kMaxCluster));
-  if (ctas == 1 && slots >= 2 * kWarps * 16) ctas = 2;
+  if (ctas == 1 && a.V >= kLongRow &&
+      (a.top_k || a.top_p || 2 * B <= 3 * sms || (a.min_p && a.V >= kLongerRow)))
+    ctas = 2;
   const cudaError_t e = launch_overlapped(sample_kernel<T>, dim3(static_cast<unsigned>(B * ctas)),
                                           dim3(kThreads), 0, s, ctas, a);
   note_launch();

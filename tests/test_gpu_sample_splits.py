@@ -87,3 +87,31 @@ def test_either_side_of_a_border_where_all_tokens_are_weighed(V, kind, dt):
     runs = splits(l, u, dt)
     for lead, size, got in runs:
         assert ((got >= first[:got.size]) & (got <= last[:got.size])).all(), (lead, size)
+
+
+@pytest.mark.parametrize("B", [150, 229, 400])
+@pytest.mark.parametrize("V", [79999, 80001, 131072])
+def test_large_batches_of_long_rows(B, V):
+    """By one CTA a row or two, as the limits, the batch and the length have it: the tokens
+    of the same rows alone, and of the definition."""
+    from oracle import head_ops as ref
+    g = torch.Generator(device="cuda").manual_seed(B)
+    l = (torch.randn(B, V, generator=g, device="cuda") * 3).to(BF)
+    u, p = (torch.rand(B, generator=g, device="cuda") for _ in range(2))
+    k = torch.randint(1, 3000, (B,), generator=g, device="cuda").int()
+    some = [0, B // 2, B - 1]
+    for name, limits in (("all", {}), ("k", dict(top_k=k)), ("p", dict(top_p=p)),
+                         ("m", dict(min_p=p * 0.01)), ("kp", dict(top_k=k, top_p=p))):
+        got = flce.sample_logits(l, u, **limits)
+        assert ((got >= 0) & (got < V)).all()
+        for b in some:
+            one = {n: t[b:b + 1] for n, t in limits.items()}
+            alone = flce.sample_logits(l[b:b + 1], u[b:b + 1], **one).item()
+            row, e = l[b].double().cpu().numpy(), 2.0 ** -28 + V * 2.0 ** -41
+            takes = {ref.sample(row, u[b].item() + d, 1.0, int(one["top_k"]) if "top_k" in one
+                                else 0, one["top_p"].item() + q if "top_p" in one else 1.0,
+                                one["min_p"].item() if "min_p" in one else 0.0)
+                     for d in (-e, 0.0, e) for q in (-e, 0.0, e)}
+            assert min(takes) <= got[b].item() <= max(takes), (name, b)
+            if "top_k" in limits or name == "m":
+                assert got[b].item() == alone, (name, b)
