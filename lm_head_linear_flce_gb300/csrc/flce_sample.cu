@@ -9,14 +9,17 @@
 // above t, and the first so many of those equal to t.  The token is then the first, by id,
 // whose cumulative mass among the kept ones exceeds u times their total.
 //
-// What bounds it (GB300, in a graph, inputs past L2, us at 256 x 152064 float32 / 64 x
-// 152064 bf16 / 1 x 152064 bf16; the bytes alone would take 23 / 2.9 / 0.05):
-//     no limits 65 / 20 / 10.1: 25 to 30 instructions a token, three quarters of the issue
-//         slots
-//     min-p 57 / 18 / 9.0: the same for the kept ones, and a pass for the largest
-//     top-k of 1 to 1000, log-uniform, 72 / 26 / 11.3: a pass for the largest (memory), the
-//         candidates' list, and five to eight steps of about a microsecond each
-//     top-p 164 / 59 / 29: three passes, of 30, 20 and up to 40 instructions a token; the
+// What bounds it (GB300, in a graph, inputs past L2, normal logits with forty likely ones a
+// row, us at 256 x 152064 float32 / 64 x 152064 bf16 / 1 x 152064 bf16; the bytes alone would
+// take 23 / 2.9 / 0.05):
+//     no limits 55 / 20 / 9.9: 34 instructions a token in float32 and 31 in bf16, 57 % of the
+//         issue slots (68 % on the SMs that have two of the 256 CTAs)
+//     greedy 42 / 12 / 7.9: a pass for the largest (memory) and the tokens of some warps again
+//     min-p 49 / 14 / 8.7: the same, and the kept ones' weights; 11 instructions a token
+//     top-k of 1 to 1000, log-uniform, 67 / 25 / 11.3: a pass for the largest, the
+//         candidates' list, and five to eight steps of about a microsecond each; 14
+//         instructions a token, a fifth of the issue slots
+//     top-p 166 to 171 / 60 / 30 to 33: three passes, 93 instructions a token in all; the
 //         histogram's atomics; barriers
 // One row takes its steps' latency: launch, pass, cluster barriers of 0.6 to 1 us.
 //
