@@ -611,10 +611,10 @@ flce_status flce_process_logits(const void* logits, int64_t ld_logits, flce_dtyp
  *   out      device int64 [B]; -1 where the row has no token.
  * Weights are right to 2^-29 of them (a root mean square of 2^-31.6) and 1.1 2^-42 of the
  * largest, so that a share of the mass is to 2^-28 + 1.1 V 2^-42 at worst, and are added as
- * integers: a call that is repeated gives the same tokens.  With top_k, or min_p without
- * top_p, a row's token does not depend on the batch around it either; else all tokens are
- * weighed before the largest is known, and a token next to a border, as close as weights are
- * right, may be another one at another B or alignment of the row.
+ * integers: a call that is repeated gives the same tokens.  A row that its top_k limits, or
+ * its min_p and no top_p, gives the same token in any batch, too; the tokens of another are
+ * weighed before the largest is known, and one next to a border, as close as weights are
+ * right, may be another at another B or alignment of the row.
  * The logit at which min_p's border lies is right to 2^-29 T.
  * B <= 65535, V <= 2^21.
  */

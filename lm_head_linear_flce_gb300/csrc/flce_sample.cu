@@ -1384,9 +1384,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
 // CTAs a row: as many as seven eighths of the places (two an SM) have for it, as clusters
 // do not fill all of them, and fewer where a warp would have less than three slots of its
 // row.  Where that is one, two take a long row all the same: with top-k or top-p, whose rows
-// differ in their passes and end at different times; without, as far as an SM has no more than
-// three CTAs to run; with min-p alone where rows are longer.  us in a graph over inputs larger than
-// L2, without limits / top-k / top-p / min-p:
+// differ in their passes and end at different times; without, as far as an SM has no more
+// than three CTAs to run; with min-p alone where rows are longer.  us in a graph over inputs
+// larger than L2, without limits / top-k / top-p / min-p:
 //     37 x 152064 bf16       4 CTAs 19 / 24 / 48 / 12, 7 17 / 22 / 46 / 13, 8 21 / 28 / 55 / 17
 //     64 x 152064 bf16       2 CTAs 29 / 31 / 89 / 17, 4 20 / 25 / 60 / 13, 5 27 / 31 / 74 / 20
 //     64 x 32003 float32     1 CTA 17 / 25 / 44 / 13, 4 11 / 18 / 28 / 10, 8 18 / 32 / 48 / 18

@@ -332,7 +332,7 @@ def sample_logits(logits, u, *, temperature=None, top_k=None, top_p=None, min_p=
     first does (0: all).  The result is the first token by id at which the kept ones' mass
     exceeds u[b] of its total.  temperature, top_p and min_p: float32 [B]; any of them may
     be left out.  A temperature of 0 (below 2^-64) takes the largest logit.  A repeated call
-    gives the same tokens; without top_k, and unless min_p is the only limit, one within 1e-9
-    of a border may be another in a batch of another size.  No gradient."""
+    gives the same tokens; in a row that neither its top_k nor min_p alone limits, one within
+    about 1e-9 of a border may be another in a batch of another size.  No gradient."""
     return _ok(_native().sample_logits(logits, u, temperature, top_k, top_p, min_p),
                "flce_sample_logits")[0]
